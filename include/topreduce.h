@@ -60,7 +60,7 @@
 extern "C" {
 #endif
 
-#define TR_ABI_VERSION 5
+#define TR_ABI_VERSION 6
 
 typedef enum {
     TR_OK = 0,
@@ -310,6 +310,98 @@ tr_status moe_combine_epilogue(int64_t T, int32_t J, int64_t H, tr_dtype dtype,
 tr_status moe_forward_noalloc(const tr_moe_desc* desc, const void* topk_idx, const void* x,
                               const float* topk_weights, const void* w1, const void* w2,
                               void* y, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Router, whole layer, and shared projection with adapters (serving).
+ * ------------------------------------------------------------------------ */
+
+typedef enum { TR_SCORE_SOFTMAX = 0, TR_SCORE_SIGMOID = 1 } tr_score;
+
+/* T rows of x against G experts. */
+typedef struct tr_route_desc {
+    int64_t T;             /* rows, >= 0; T * K < 2^31 */
+    int64_t H;             /* hidden size, a multiple of 8, at most 2^22 */
+    int32_t G;             /* experts, 1..4096 */
+    int32_t K;             /* experts chosen per row, 1..32, at most G */
+    int32_t dtype;         /* tr_dtype of x and w_gate */
+    int32_t idx_dtype;     /* tr_idx_dtype of topk_idx */
+    int32_t score;         /* tr_score */
+    int32_t renorm;        /* 1: the chosen scores are divided by their sum */
+    float scale;           /* factor of the weights, finite */
+    int32_t reserved;      /* 0 */
+} tr_route_desc;
+
+/* Bytes of device workspace of moe_route_topk. 0 and the last error if desc is
+ * invalid. */
+size_t moe_route_topk_workspace(const tr_route_desc* desc);
+
+/* The router: logits[t][g] = x[t] . w_gate[g] (fp32 accumulation), scores p =
+ * softmax over all G experts, or sigmoid; the K experts of the largest keys,
+ * in descending order, ties to the lowest id, NaN below every number; weights
+ * p[idx] * scale, with renorm divided by the sum of the K scores (a sum below
+ * the smallest normal float counts as that). The keys are the logits, or with
+ * bias (fp32 [G], or NULL) p + bias: a balancing bias decides the choice and
+ * stays out of the weights. Deterministic.
+ * x: device [T, H]; w_gate: device [G, H]; topk_idx: device [T, K] of
+ * idx_dtype (global ids, ready for moe_plan); topk_weights: device fp32 [T, K];
+ * ws: device, 256-byte aligned, its contents before and after of no meaning. */
+tr_status moe_route_topk(const tr_route_desc* desc, const void* x, const void* w_gate,
+                         const float* bias, void* topk_idx, float* topk_weights, void* ws,
+                         size_t ws_bytes, hipStream_t stream);
+
+/* A whole layer: router, then the local experts [expert_begin, expert_begin +
+ * E) and their weighted sum. */
+typedef struct tr_layer_desc {
+    tr_route_desc route;
+    int64_t I;             /* SwiGLU intermediate size */
+    int64_t expert_begin;  /* id of local expert 0, 0 <= begin <= begin + E <= G */
+    int32_t E;             /* local experts, 1..1024 */
+    int32_t reserved;      /* 0 */
+} tr_layer_desc;
+
+/* Bytes of device workspace of moe_layer. 0 and the last error if desc is
+ * invalid. */
+size_t moe_layer_workspace(const tr_layer_desc* desc);
+
+/* y[t] = sum over the row's chosen local experts of weight * MLP_e(x[t]); rows
+ * without a local expert are +0. At most 64 rows: the experts' weights are
+ * streamed once against the rows' masks, with no plan and no expanded rows, and
+ * y is rounded once. More rows: moe_route_topk, moe_plan and moe_forward in this
+ * workspace, with their roundings. x: device [T, H]; w_gate, bias: as
+ * moe_route_topk; w1, w2: as moe_forward; y: device [T, H], may alias x.
+ * topk_idx (of route.idx_dtype) and topk_weights: device [T, K], written.
+ * ws: device, 256-byte aligned, its contents before and after of no meaning. */
+tr_status moe_layer(const tr_layer_desc* desc, const void* x, const void* w_gate,
+                    const float* bias, const void* w1, const void* w2, void* y, void* topk_idx,
+                    float* topk_weights, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* A projection that all rows share, with a low-rank adapter of each row's
+ * request beside it. */
+typedef struct tr_adapter_desc {
+    int64_t T;             /* rows, >= 0, < 2^31 */
+    int64_t H;             /* input size, a multiple of 8, at most 2^22 */
+    int64_t N;             /* output size, 1..2^22 */
+    int32_t R;             /* rank, 1..256 (adapters of lower rank: zero rows) */
+    int32_t A;             /* adapters, 1..2^20 */
+    int32_t dtype;         /* tr_dtype of x, w, a, b and y */
+    int32_t reserved;      /* 0 */
+} tr_adapter_desc;
+
+/* Bytes of device workspace of moe_adapter_linear. 0 and the last error if
+ * desc is invalid. */
+size_t moe_adapter_linear_workspace(const tr_adapter_desc* desc);
+
+/* y[t] = w x[t] + scales[i] * b[i] (a[i] x[t]) with i = ids[t]; rows whose id is
+ * outside [0, A) (-1, say) have no adapter and read none. Accumulation is
+ * fp32; with more than 64 bf16 rows the low-rank product a x is rounded to
+ * bf16. x: device [T, H]; w: device [N, H]; a: device [A, R, H]; b: device
+ * [A, N, R]; ids: device int32 [T]; scales: device fp32 [A] or NULL (1);
+ * y: device [T, N], must not overlap x; ws: device, 256-byte aligned, its
+ * contents before and after of no meaning. */
+tr_status moe_adapter_linear(const tr_adapter_desc* desc, const void* x, const void* w,
+                             const void* a, const void* b, const int32_t* ids,
+                             const float* scales, void* y, void* ws, size_t ws_bytes,
+                             hipStream_t stream);
 
 /* Copies stats to host_out[4] = {R, rows with a local route, ignored slots,
  * empty experts} and synchronises `stream` (opt-in host sync, the counterpart

@@ -17,6 +17,11 @@ gathering x, ``grouped_gemm_down_y`` writing single-slot rows to y),
 and ``plan_stats``. ``FLAG_NO_XE`` plans without the expanded-row buffer.
 ``forward_noalloc`` is plan + forward in the library's own static workspace,
 for callers that cannot allocate device memory.
+
+Before and beside the expert path: ``route_topk`` (the router: logits, top-k,
+gate weights), ``layer`` (the whole layer from hidden rows, router included)
+and ``adapter_linear`` (a projection all rows share, with a low-rank adapter
+of each row's request), each with its ``*_workspace_size``.
 """
 
 from ._binding import (  # noqa: F401
@@ -29,6 +34,8 @@ from ._binding import (  # noqa: F401
     NOALLOC_SCRATCH_BYTES,
     MoePlan,
     TopReduceError,
+    adapter_linear,
+    adapter_workspace_size,
     combine_epilogue,
     compact_rows,
     combine_reduce,
@@ -41,10 +48,14 @@ from ._binding import (  # noqa: F401
     grouped_gemm_down_y,
     grouped_gemm_up,
     grouped_gemm_up_x,
+    layer,
+    layer_workspace_size,
     lib_path,
     load_library,
     make_desc,
     plan,
     plan_stats,
+    route_topk,
+    route_workspace_size,
     workspace_size,
 )

@@ -18,7 +18,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libtopreduce.so"
 
-ABI_VERSION = 5
+ABI_VERSION = 6
 BF16, F32 = 0, 1
 IDX_I32, IDX_I64 = 0, 1
 FLAG_GEMM_FORCE_TILED = 0x1
@@ -51,6 +51,22 @@ class PlanStruct(C.Structure):
                 ("scan_rows_per_block", C.c_int32), ("row_dst", C.c_void_p),
                 ("tok_rest", C.c_void_p), ("block_rows", C.c_int32), ("reserved2", C.c_int32),
                 ("block_counts", C.c_void_p)]
+
+
+class RouteDesc(C.Structure):
+    _fields_ = [("T", C.c_int64), ("H", C.c_int64), ("G", C.c_int32), ("K", C.c_int32),
+                ("dtype", C.c_int32), ("idx_dtype", C.c_int32), ("score", C.c_int32),
+                ("renorm", C.c_int32), ("scale", C.c_float), ("reserved", C.c_int32)]
+
+
+class LayerDesc(C.Structure):
+    _fields_ = [("route", RouteDesc), ("I", C.c_int64), ("expert_begin", C.c_int64),
+                ("E", C.c_int32), ("reserved", C.c_int32)]
+
+
+class AdapterDesc(C.Structure):
+    _fields_ = [("T", C.c_int64), ("H", C.c_int64), ("N", C.c_int64), ("R", C.c_int32),
+                ("A", C.c_int32), ("dtype", C.c_int32), ("reserved", C.c_int32)]
 
 
 _lib = None
@@ -106,6 +122,20 @@ def load_library():
                                          C.c_int64, vp, vp]
     lib.moe_forward_noalloc.restype = st
     lib.moe_forward_noalloc.argtypes = [C.POINTER(Desc), vp, vp, vp, vp, vp, vp, vp]
+    lib.moe_route_topk_workspace.restype = C.c_size_t
+    lib.moe_route_topk_workspace.argtypes = [C.POINTER(RouteDesc)]
+    lib.moe_route_topk.restype = st
+    lib.moe_route_topk.argtypes = [C.POINTER(RouteDesc), vp, vp, vp, vp, vp, vp, C.c_size_t, vp]
+    lib.moe_layer_workspace.restype = C.c_size_t
+    lib.moe_layer_workspace.argtypes = [C.POINTER(LayerDesc)]
+    lib.moe_layer.restype = st
+    lib.moe_layer.argtypes = [C.POINTER(LayerDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp, C.c_size_t,
+                              vp]
+    lib.moe_adapter_linear_workspace.restype = C.c_size_t
+    lib.moe_adapter_linear_workspace.argtypes = [C.POINTER(AdapterDesc)]
+    lib.moe_adapter_linear.restype = st
+    lib.moe_adapter_linear.argtypes = [C.POINTER(AdapterDesc), vp, vp, vp, vp, vp, vp, vp, vp,
+                                       C.c_size_t, vp]
     lib.moe_plan_stats.restype = st
     lib.moe_plan_stats.argtypes = [C.POINTER(PlanStruct), C.POINTER(C.c_int32), vp]
     lib.moe_last_error.restype = C.c_char_p
@@ -457,6 +487,190 @@ def compact_rows(src: torch.Tensor, block_rows: int, block_counts: torch.Tensor,
                                            1 if to_padded else 0, C.c_void_p(np_ or None),
                                            _stream_ptr(stream, dev)))
     return dst
+
+
+# ---------------------------------------------------------------------------
+# Router, whole layer, shared projection with adapters
+# ---------------------------------------------------------------------------
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _need(query, desc) -> int:
+    n = query(C.byref(desc))
+    if n == 0:
+        _check(-1)
+    return int(n)
+
+
+def _workspace(ws: Optional[torch.Tensor], need: int, device) -> torch.Tensor:
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    _dev_tensor(ws, "ws", torch.uint8)
+    return ws
+
+
+def _on_device(device, **tensors):
+    """Every tensor of a call is on x's device."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, x on {device}")
+
+
+def _route_desc(x, w_gate, K, score, renorm, scale, idx_dtype) -> RouteDesc:
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a [T, H] tensor")
+    if not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 2:
+        raise ValueError("w_gate must be a [G, H] tensor")
+    if score not in _SCORES:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid' (got {score!r})")
+    if idx_dtype not in (torch.int32, torch.int64):
+        raise TypeError("idx_dtype must be torch.int32 or torch.int64")
+    return RouteDesc(T=x.shape[0], H=x.shape[1], G=w_gate.shape[0], K=K,
+                     dtype=_dtype_code(x.dtype),
+                     idx_dtype=IDX_I64 if idx_dtype == torch.int64 else IDX_I32,
+                     score=_SCORES[score], renorm=1 if renorm else 0, scale=scale, reserved=0)
+
+
+def _route_buffers(d: RouteDesc, x, w_gate, bias, idx, weights, idx_dtype):
+    """Checks the router's tensors; returns the outputs (allocated if None)."""
+    dev = x.device
+    _dev_tensor(x, "x")
+    _dev_tensor(w_gate, "w_gate", x.dtype, (d.G, d.H))
+    if bias is not None:
+        _dev_tensor(bias, "bias", torch.float32, (d.G,))
+    if idx is None:
+        idx = torch.empty((d.T, d.K), dtype=idx_dtype, device=dev)
+    else:
+        _dev_tensor(idx, "idx", idx_dtype, (d.T, d.K))
+    if weights is None:
+        weights = torch.empty((d.T, d.K), dtype=torch.float32, device=dev)
+    else:
+        _dev_tensor(weights, "weights", torch.float32, (d.T, d.K))
+    _on_device(dev, w_gate=w_gate, bias=bias, idx=idx, weights=weights)
+    return idx, weights
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr() or None
+
+
+def route_workspace_size(T: int, H: int, G: int, K: int, dtype=torch.bfloat16) -> int:
+    """Bytes of ws for route_topk of these sizes."""
+    d = RouteDesc(T=T, H=H, G=G, K=K, dtype=_dtype_code(dtype), idx_dtype=IDX_I64, scale=1.0)
+    return _need(load_library().moe_route_topk_workspace, d)
+
+
+def route_topk(x: torch.Tensor, w_gate: torch.Tensor, K: int, bias: Optional[torch.Tensor] = None,
+               score: str = "softmax", renorm: bool = True, scale: float = 1.0,
+               idx_dtype=torch.int64, idx: Optional[torch.Tensor] = None,
+               weights: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """moe_route_topk: (idx [T, K], weights fp32 [T, K]) of x [T, H] against the
+    experts' rows w_gate [G, H].
+
+    Scores are the softmax of the logits over all G experts, or their sigmoid.
+    The K best are chosen in descending order, ties to the lowest id; with a
+    bias (fp32 [G]) by score + bias. The weights are the scores, divided by
+    their sum with renorm, times scale. idx is what plan() takes."""
+    d = _route_desc(x, w_gate, K, score, renorm, scale, idx_dtype)
+    lib = load_library()
+    need = _need(lib.moe_route_topk_workspace, d)
+    idx, weights = _route_buffers(d, x, w_gate, bias, idx, weights, idx_dtype)
+    ws = _workspace(ws, need, x.device)
+    _on_device(x.device, ws=ws)
+    _check(lib.moe_route_topk(C.byref(d), _ptr(x), _ptr(w_gate), _ptr(bias), _ptr(idx),
+                              _ptr(weights), _ptr(ws), ws.numel(), _stream_ptr(stream, x.device)))
+    return idx, weights
+
+
+def _layer_desc(x, w_gate, w1, K, score, renorm, scale, idx_dtype, expert_begin) -> LayerDesc:
+    if not isinstance(w1, torch.Tensor) or w1.dim() != 3 or w1.shape[1] % 2:
+        raise ValueError("w1 must be an [E, 2I, H] tensor")
+    return LayerDesc(route=_route_desc(x, w_gate, K, score, renorm, scale, idx_dtype),
+                     I=w1.shape[1] // 2, expert_begin=expert_begin, E=w1.shape[0], reserved=0)
+
+
+def layer_workspace_size(T: int, H: int, I: int, E: int, G: int, K: int,
+                         dtype=torch.bfloat16) -> int:
+    """Bytes of ws for layer of these sizes."""
+    d = LayerDesc(route=RouteDesc(T=T, H=H, G=G, K=K, dtype=_dtype_code(dtype), idx_dtype=IDX_I64,
+                                  scale=1.0), I=I, expert_begin=0, E=E)
+    return _need(load_library().moe_layer_workspace, d)
+
+
+def layer(x: torch.Tensor, w_gate: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor, K: int,
+          bias: Optional[torch.Tensor] = None, score: str = "softmax", renorm: bool = True,
+          scale: float = 1.0, expert_begin: int = 0, idx_dtype=torch.int64,
+          y: Optional[torch.Tensor] = None, idx: Optional[torch.Tensor] = None,
+          weights: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+          stream: Optional[torch.cuda.Stream] = None
+          ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """moe_layer: (y [T, H], idx [T, K], weights [T, K]), the router as in
+    route_topk and then the local experts [expert_begin, expert_begin + E)
+    (w1 [E, 2I, H] gate | up, w2 [E, H, I]) and their weighted sum. Rows
+    without a local expert are +0. y may be x."""
+    d = _layer_desc(x, w_gate, w1, K, score, renorm, scale, idx_dtype, expert_begin)
+    lib = load_library()
+    need = _need(lib.moe_layer_workspace, d)
+    r = d.route
+    idx, weights = _route_buffers(r, x, w_gate, bias, idx, weights, idx_dtype)
+    _dev_tensor(w1, "w1", x.dtype, (d.E, 2 * d.I, r.H))
+    _dev_tensor(w2, "w2", x.dtype, (d.E, r.H, d.I))
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _dev_tensor(y, "y", x.dtype, (r.T, r.H))
+    ws = _workspace(ws, need, x.device)
+    _on_device(x.device, w1=w1, w2=w2, y=y, ws=ws)
+    _check(lib.moe_layer(C.byref(d), _ptr(x), _ptr(w_gate), _ptr(bias), _ptr(w1), _ptr(w2),
+                         _ptr(y), _ptr(idx), _ptr(weights), _ptr(ws), ws.numel(),
+                         _stream_ptr(stream, x.device)))
+    return y, idx, weights
+
+
+def adapter_workspace_size(T: int, H: int, N: int, R: int, A: int, dtype=torch.bfloat16) -> int:
+    """Bytes of ws for adapter_linear of these sizes."""
+    return _need(load_library().moe_adapter_linear_workspace,
+                 AdapterDesc(T=T, H=H, N=N, R=R, A=A, dtype=_dtype_code(dtype)))
+
+
+def adapter_linear(x: torch.Tensor, w: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
+                   ids: torch.Tensor, scales: Optional[torch.Tensor] = None,
+                   y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """moe_adapter_linear: y [T, N] = x w^T + scales[i] (x a[i]^T) b[i]^T with
+    i = ids[t] (int32 [T]; outside [0, A): no adapter). x [T, H], w [N, H],
+    a [A, R, H], b [A, N, R], scales fp32 [A] or None for 1."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a [T, H] tensor")
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("w must be an [N, H] tensor")
+    if not isinstance(a, torch.Tensor) or a.dim() != 3:
+        raise ValueError("a must be an [A, R, H] tensor")
+    T, H = x.shape
+    N = w.shape[0]
+    n, R = a.shape[0], a.shape[1]
+    dev, dt = x.device, x.dtype
+    d = AdapterDesc(T=T, H=H, N=N, R=R, A=n, dtype=_dtype_code(dt), reserved=0)
+    lib = load_library()
+    need = _need(lib.moe_adapter_linear_workspace, d)
+    _dev_tensor(x, "x")
+    _dev_tensor(w, "w", dt, (N, H))
+    _dev_tensor(a, "a", dt, (n, R, H))
+    _dev_tensor(b, "b", dt, (n, N, R))
+    _dev_tensor(ids, "ids", torch.int32, (T,))
+    if scales is not None:
+        _dev_tensor(scales, "scales", torch.float32, (n,))
+    if y is None:
+        y = torch.empty((T, N), dtype=dt, device=dev)
+    else:
+        _dev_tensor(y, "y", dt, (T, N))
+    ws = _workspace(ws, need, dev)
+    _on_device(dev, w=w, a=a, b=b, ids=ids, scales=scales, y=y, ws=ws)
+    _check(lib.moe_adapter_linear(C.byref(d), _ptr(x), _ptr(w), _ptr(a), _ptr(b), _ptr(ids),
+                                  _ptr(scales), _ptr(y), _ptr(ws), ws.numel(),
+                                  _stream_ptr(stream, dev)))
+    return y
 
 
 def plan_stats(p: MoePlan, stream=None) -> Tuple[int, int, int, int]:

@@ -8,6 +8,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "tr_device.h"
 #include "tr_internal.h"
 
 namespace {
@@ -474,6 +475,213 @@ tr_status moe_forward_noalloc(const tr_moe_desc* desc, const void* topk_idx, con
   tr_moe_plan p;
   if ((s = plan_rows(&d, topk_idx, 0, nullptr, ws, need, stream, &p)) != TR_OK) return s;
   return moe_forward(&p, x, topk_weights, w1, w2, y, stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Router, whole layer, shared projection with adapters
+// ---------------------------------------------------------------------------
+namespace {
+
+tr_status check_route_desc(const tr_route_desc* d) {
+  if (!d) return fail(TR_EINVAL, "desc is NULL");
+  if (d->T < 0) return fail(TR_EINVAL, "T must be >= 0 (got %lld)", (long long)d->T);
+  if (d->H < 1) return fail(TR_EINVAL, "H must be >= 1 (got %lld)", (long long)d->H);
+  if (d->G < 1) return fail(TR_EINVAL, "G must be >= 1 (got %d)", d->G);
+  if (d->K < 1 || d->K > tr::kMaxK || d->K > d->G)
+    return fail(TR_EINVAL, "K must be in [1, %d] and at most G (got %d)", tr::kMaxK, d->K);
+  if (d->dtype != TR_BF16 && d->dtype != TR_F32) return fail(TR_EINVAL, "unknown dtype %d", d->dtype);
+  if (d->idx_dtype != TR_IDX_I32 && d->idx_dtype != TR_IDX_I64)
+    return fail(TR_EINVAL, "unknown idx_dtype %d", d->idx_dtype);
+  if (d->score != TR_SCORE_SOFTMAX && d->score != TR_SCORE_SIGMOID)
+    return fail(TR_EINVAL, "unknown score %d", d->score);
+  if (d->renorm != 0 && d->renorm != 1) return fail(TR_EINVAL, "renorm must be 0 or 1");
+  if (!(d->scale - d->scale == 0.0f)) return fail(TR_EINVAL, "scale must be finite");
+  if (d->reserved != 0) return fail(TR_EINVAL, "reserved must be 0");
+  if (d->G > tr::kMaxGates) return fail(TR_EUNSUPPORTED, "G must be at most %d (got %d)", tr::kMaxGates, d->G);
+  // rows move in 16-byte pieces; a tile of rows is addressed with 32 bits
+  if (d->H % 8 || d->H > (int64_t{1} << 22))
+    return fail(TR_EUNSUPPORTED, "H must be a multiple of 8, at most 2^22 (got %lld)", (long long)d->H);
+  if (d->T > ((int64_t{1} << 31) - 1) / d->K) return fail(TR_EUNSUPPORTED, "T*K must be < 2^31");
+  return TR_OK;
+}
+
+tr_status check_layer_desc(const tr_layer_desc* d) {
+  if (!d) return fail(TR_EINVAL, "desc is NULL");
+  tr_status s = check_route_desc(&d->route);
+  if (s != TR_OK) return s;
+  if (d->E < 1 || d->E > tr::kMaxE) return fail(TR_EINVAL, "E must be in [1, %d] (got %d)", tr::kMaxE, d->E);
+  if (d->I < 1) return fail(TR_EINVAL, "I must be >= 1");
+  if (d->expert_begin < 0 || d->expert_begin > d->route.G - d->E)
+    return fail(TR_EINVAL, "local experts [%lld, +%d) must lie in [0, %d)", (long long)d->expert_begin,
+                d->E, d->route.G);
+  if (d->reserved != 0) return fail(TR_EINVAL, "reserved must be 0");
+  if (d->I > (1 << 22) || 2 * d->route.H * d->I >= (int64_t(1) << 31))
+    return fail(TR_EUNSUPPORTED, "I must be <= 2^22 and 2*H*I < 2^31");
+  return TR_OK;
+}
+
+tr_status check_adapter_desc(const tr_adapter_desc* d) {
+  if (!d) return fail(TR_EINVAL, "desc is NULL");
+  if (d->T < 0) return fail(TR_EINVAL, "T must be >= 0 (got %lld)", (long long)d->T);
+  if (d->H < 1 || d->N < 1) return fail(TR_EINVAL, "H and N must be >= 1");
+  if (d->R < 1) return fail(TR_EINVAL, "R must be >= 1 (got %d)", d->R);
+  if (d->A < 1) return fail(TR_EINVAL, "A must be >= 1 (got %d)", d->A);
+  if (d->dtype != TR_BF16 && d->dtype != TR_F32) return fail(TR_EINVAL, "unknown dtype %d", d->dtype);
+  if (d->reserved != 0) return fail(TR_EINVAL, "reserved must be 0");
+  if (d->R > tr::kMaxRank) return fail(TR_EUNSUPPORTED, "R must be at most %d (got %d)", tr::kMaxRank, d->R);
+  if (d->A > (1 << 20)) return fail(TR_EUNSUPPORTED, "A must be at most 2^20 (got %d)", d->A);
+  if (d->T >= (int64_t{1} << 31)) return fail(TR_EUNSUPPORTED, "T must be < 2^31");
+  if (d->H % 8 || d->H > (int64_t{1} << 22))
+    return fail(TR_EUNSUPPORTED, "H must be a multiple of 8, at most 2^22 (got %lld)", (long long)d->H);
+  if (d->N > (int64_t{1} << 22)) return fail(TR_EUNSUPPORTED, "N must be at most 2^22");
+  // 128-row tiles are numbered with 32 bits
+  if (tr::cdiv(d->T, 128) * tr::cdiv(d->N, 128) >= (int64_t{1} << 30))
+    return fail(TR_EUNSUPPORTED, "T * N must be below 2^44");
+  return TR_OK;
+}
+
+tr_status check_ws(const void* ws, size_t bytes, size_t need) {
+  if (!ws) return fail(TR_EINVAL, "workspace is NULL");
+  if (!aligned(ws, kAlign)) return fail(TR_EINVAL, "workspace must be %zu-byte aligned", kAlign);
+  if (bytes < need) return fail(TR_EWORKSPACE, "workspace has %zu bytes, needs %zu", bytes, need);
+  return TR_OK;
+}
+
+tr_status check_route_buffers(const tr_route_desc& d, const void* x, const void* w_gate,
+                              const float* bias, const void* topk_idx, const float* topk_weights) {
+  tr_status s;
+  if ((s = check_buf(x, "x", true)) != TR_OK) return s;
+  if ((s = check_buf(w_gate, "w_gate", true)) != TR_OK) return s;
+  if (bias && !aligned(bias, 4)) return fail(TR_EINVAL, "bias misaligned");
+  if (!topk_idx || !aligned(topk_idx, d.idx_dtype == TR_IDX_I64 ? 8 : 4))
+    return fail(TR_EINVAL, "topk_idx must be non-NULL and aligned");
+  if (!topk_weights || !aligned(topk_weights, 4))
+    return fail(TR_EINVAL, "topk_weights must be non-NULL and 4-byte aligned");
+  return TR_OK;
+}
+
+// Workspace of moe_layer: the router's, then the experts' (at most kFewTokens
+// rows) or the plan's.
+struct LayerLayout {
+  size_t experts, total;
+  tr_moe_desc plan;
+};
+
+tr_status layer_layout(const tr_layer_desc& d, LayerLayout* L) {
+  L->experts = up(tr::route_workspace(d.route));
+  if (d.route.T <= tr::kFewTokens) {
+    L->total = L->experts + tr::few_workspace(d);
+    return TR_OK;
+  }
+  tr_moe_desc& m = L->plan;
+  memset(&m, 0, sizeof m);
+  m.T = d.route.T;
+  m.K = d.route.K;
+  m.E = d.E;
+  m.expert_begin = d.expert_begin;
+  m.H = d.route.H;
+  m.I = d.I;
+  m.dtype = d.route.dtype;
+  m.idx_dtype = d.route.idx_dtype;
+  if (tr::gemm_can_gather(m)) m.flags |= TR_FLAG_NO_XE;
+  const tr_status s = check_desc(&m);
+  if (s != TR_OK) return s;
+  L->total = L->experts + layout(m).total;
+  return TR_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_route_topk_workspace(const tr_route_desc* desc) {
+  if (check_route_desc(desc) != TR_OK) return 0;
+  ok();
+  const size_t n = tr::route_workspace(*desc);
+  return n ? n : kAlign;
+}
+
+tr_status moe_route_topk(const tr_route_desc* desc, const void* x, const void* w_gate,
+                         const float* bias, void* topk_idx, float* topk_weights, void* ws,
+                         size_t ws_bytes, hipStream_t stream) {
+  tr_status s = check_route_desc(desc);
+  if (s != TR_OK) return s;
+  if ((s = check_ws(ws, ws_bytes, tr::route_workspace(*desc))) != TR_OK) return s;
+  if (desc->T == 0) return ok();
+  if ((s = check_route_buffers(*desc, x, w_gate, bias, topk_idx, topk_weights)) != TR_OK) return s;
+  return hip_status(tr::route_topk(*desc, x, w_gate, bias, topk_idx, topk_weights, ws, stream),
+                    "moe_route_topk launch");
+}
+
+size_t moe_layer_workspace(const tr_layer_desc* desc) {
+  LayerLayout L;
+  if (check_layer_desc(desc) != TR_OK || layer_layout(*desc, &L) != TR_OK) return 0;
+  ok();
+  return L.total;
+}
+
+tr_status moe_layer(const tr_layer_desc* desc, const void* x, const void* w_gate,
+                    const float* bias, const void* w1, const void* w2, void* y, void* topk_idx,
+                    float* topk_weights, void* ws, size_t ws_bytes, hipStream_t stream) {
+  tr_status s = check_layer_desc(desc);
+  if (s != TR_OK) return s;
+  LayerLayout L;
+  if ((s = layer_layout(*desc, &L)) != TR_OK) return s;
+  if ((s = check_ws(ws, ws_bytes, L.total)) != TR_OK) return s;
+  if (desc->route.T == 0) return ok();
+  if ((s = check_route_buffers(desc->route, x, w_gate, bias, topk_idx, topk_weights)) != TR_OK) return s;
+  if ((s = check_buf(w1, "w1", true)) != TR_OK) return s;
+  if ((s = check_buf(w2, "w2", true)) != TR_OK) return s;
+  if ((s = check_buf(y, "y", true)) != TR_OK) return s;
+  char* ews = static_cast<char*>(ws) + L.experts;
+  if (desc->route.T <= tr::kFewTokens) {
+    const tr::FewRoutes f = tr::few_routes(*desc, ews);
+    if ((s = hip_status(tr::route_topk(desc->route, x, w_gate, bias, topk_idx, topk_weights, ws,
+                                       stream, &f),
+                        "moe_layer router launch")) != TR_OK)
+      return s;
+    return hip_status(tr::few_experts(*desc, x, w1, w2, topk_weights, y, ews, stream),
+                      "moe_layer experts launch");
+  }
+  if ((s = hip_status(tr::route_topk(desc->route, x, w_gate, bias, topk_idx, topk_weights, ws, stream),
+                      "moe_layer router launch")) != TR_OK)
+    return s;
+  tr_moe_plan p;
+  if ((s = plan_rows(&L.plan, topk_idx, 0, nullptr, ews, L.total - L.experts, stream, &p)) != TR_OK)
+    return s;
+  return moe_forward(&p, x, topk_weights, w1, w2, y, stream);
+}
+
+size_t moe_adapter_linear_workspace(const tr_adapter_desc* desc) {
+  if (check_adapter_desc(desc) != TR_OK) return 0;
+  ok();
+  return tr::adapter_workspace(*desc);
+}
+
+tr_status moe_adapter_linear(const tr_adapter_desc* desc, const void* x, const void* w,
+                             const void* a, const void* b, const int32_t* ids,
+                             const float* scales, void* y, void* ws, size_t ws_bytes,
+                             hipStream_t stream) {
+  tr_status s = check_adapter_desc(desc);
+  if (s != TR_OK) return s;
+  if ((s = check_ws(ws, ws_bytes, tr::adapter_workspace(*desc))) != TR_OK) return s;
+  if (desc->T == 0) return ok();
+  if ((s = check_buf(x, "x", true)) != TR_OK) return s;
+  if ((s = check_buf(w, "w", true)) != TR_OK) return s;
+  if ((s = check_buf(a, "a", true)) != TR_OK) return s;
+  if ((s = check_buf(b, "b", true)) != TR_OK) return s;
+  if ((s = check_buf(y, "y", true)) != TR_OK) return s;
+  if (!ids || !aligned(ids, 4)) return fail(TR_EINVAL, "ids must be non-NULL and 4-byte aligned");
+  if (scales && !aligned(scales, 4)) return fail(TR_EINVAL, "scales misaligned");
+  const size_t es = desc->dtype == TR_BF16 ? 2 : 4;
+  const char* x0 = static_cast<const char*>(x);
+  const char* y0 = static_cast<const char*>(y);
+  if (x0 < y0 + es * desc->T * desc->N && y0 < x0 + es * desc->T * desc->H)
+    return fail(TR_EINVAL, "y must not overlap x");
+  return hip_status(tr::adapter_linear(*desc, x, w, a, b, ids, scales, y, ws, stream),
+                    "moe_adapter_linear launch");
 }
 
 tr_status moe_plan_stats(const tr_moe_plan* plan, int32_t* host_out, hipStream_t stream) {

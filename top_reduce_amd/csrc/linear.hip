@@ -1,0 +1,711 @@
+// Projections y = x W^T of rows of x: the router's logits and the projection
+// that all requests share, with each token's low-rank adapter beside it.
+//
+//   logits[t, g] = x[t] . Wg[g]
+//   y[t, n] = x[t] . W[n] + s[a] sum_j (x[t] . A[a][j]) B[a][n, j],  a = ids[t]
+//
+// Three forms, by the number of tokens T (the same code for bf16 and fp32, see
+// tr_chunk.h):
+//  - stream_partial (T <= 64): bound by reading W. Weight rows go from memory
+//    straight into MFMA operands, the tokens ride in the other operand, and
+//    the reduction dimension is split over the waves of a block and over
+//    blocks, so that a few hundred rows still occupy every compute unit. The
+//    sums of a block's part go to fp32 partials; the kernel that follows
+//    (router selection, adapter_few) adds them in a fixed order.
+//    The adapters' low-rank products x A^T are units of the same launch.
+//  - linear_tile (more tokens): 128 x 128 tiles staged through LDS.
+//  - adapter_shrink + linear_tile with the adapters in its epilogue.
+#include "tr_chunk.h"
+#include "tr_internal.h"
+
+namespace tr {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kU = 8;   // 64-byte k-blocks of one batch of loads
+
+// --------------------------------------------------------------------------
+// A few tokens
+// --------------------------------------------------------------------------
+struct StreamArgs {
+  const char* x;         // [T, H]
+  const char* w;         // [N, H]
+  float* part;           // [S, T, Np] sums of each part of the reduction
+  int64_t row_bytes;     // bytes of a row of x and of w
+  int T, N, Np;
+  int tiles;             // ceil(N / 16)
+  // adapters (NULL ids: none)
+  const int32_t* ids;    // [T]
+  const char* a;         // [A, R, H]
+  float* vpart;          // [S, T, Rp]
+  int A, R, Rp, rank_tiles;
+  // memory that the next kernel wants zeroed
+  uint32_t* zero;
+  int n_zero;
+};
+
+// Block (tile, s): 16 weight rows against every token over part s of the
+// reduction, which its waves share. Tiles past the weight's are adapter tiles:
+// unit (slot, rank tile) takes 16 rows of the slot-th different adapter among
+// the tokens' ids, and keeps the sums of that adapter's tokens.
+template <bool kF32, int NQ>
+__global__ __launch_bounds__(kThreads) void stream_partial(StreamArgs p) {
+  __shared__ floatx4 red[kWaves][NQ][kWave];
+  const int tid = threadIdx.x;
+  const int lane = tid & 63, wave = tid >> 6;
+  const int g = lane >> 4, r = lane & 15;
+  const int tile = blockIdx.x, s = blockIdx.y, S = gridDim.y;
+
+  const int64_t z = (static_cast<int64_t>(s) * gridDim.x + tile) * kThreads + tid;
+  if (z < p.n_zero) p.zero[z] = 0;
+
+  const bool is_w = tile < p.tiles;
+  uint64_t mask = p.T == 64 ? ~0ull : (1ull << p.T) - 1;   // tokens of this tile
+  const char* wp;
+  int rt = 0;
+  if (is_w) {
+    wp = p.w + static_cast<int64_t>(min(tile * 16 + r, p.N - 1)) * p.row_bytes;
+  } else {
+    const int u = tile - p.tiles, slot = u / p.rank_tiles;
+    rt = u % p.rank_tiles;
+    const int id = lane < p.T ? p.ids[lane] : -1;
+    uint64_t todo = __ballot(id >= 0 && id < p.A);
+    int aid = 0;
+    mask = 0;
+    for (int i = 0; i <= slot && todo; ++i) {
+      aid = __builtin_amdgcn_readlane(id, __ffsll(static_cast<unsigned long long>(todo)) - 1);
+      mask = __ballot(id == aid);
+      todo &= ~mask;
+      if (i < slot) mask = 0;
+    }
+    if (mask == 0) return;   // fewer different adapters (the same in every wave)
+    wp = p.a + (static_cast<int64_t>(aid) * p.R + min(rt * 16 + r, p.R - 1)) * p.row_bytes;
+  }
+
+  // A lane whose token is not of this tile reads the first one's row: its sums
+  // are never stored, and the columns of an MFMA do not mix.
+  const int first = __ffsll(static_cast<unsigned long long>(mask)) - 1;
+  const char* xp[NQ];
+  bool on[NQ];
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) {
+    const int t = q * 16 + r;
+    on[q] = (mask >> (16 * q)) & 0xffff;
+    xp[q] = p.x + static_cast<int64_t>(t < 64 && ((mask >> t) & 1) ? t : first) * p.row_bytes + g * 16;
+  }
+  wp += g * 16;
+
+  // this wave's 64-byte blocks; the last one of a row may be short
+  const int nkb = static_cast<int>((p.row_bytes + 63) >> 6);
+  const int nfull = static_cast<int>(p.row_bytes >> 6);
+  const int part = s * kWaves + wave, parts = S * kWaves;
+  int kb = static_cast<int>(static_cast<int64_t>(part) * nkb / parts);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(part + 1) * nkb / parts);
+  const int kbf = min(kb1, nfull);
+  floatx4 acc[NQ];
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) acc[q] = floatx4{0, 0, 0, 0};
+  for (; kb + kU <= kbf; kb += kU) {
+    u32x4 wa[kU];
+#pragma unroll
+    for (int j = 0; j < kU; ++j) wa[j] = load16(wp + (kb + j) * 64);
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      if (!on[q]) continue;
+      u32x4 xb[kU];
+#pragma unroll
+      for (int j = 0; j < kU; ++j) xb[j] = load16(xp[q] + (kb + j) * 64);
+#pragma unroll
+      for (int j = 0; j < kU; ++j) acc[q] = mma16<kF32>(wa[j], xb[j], acc[q]);
+    }
+  }
+  for (; kb < kb1; ++kb) {
+    const bool in = kb * 64 + g * 16 < p.row_bytes;
+    const u32x4 wa = in ? load16(wp + kb * 64) : u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      if (!on[q]) continue;
+      const u32x4 xb = in ? load16(xp[q] + kb * 64) : u32x4{0, 0, 0, 0};
+      acc[q] = mma16<kF32>(wa, xb, acc[q]);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) red[wave][q][lane] = acc[q];
+  __syncthreads();
+  for (int q = wave; q < NQ; q += kWaves) {
+    const int t = q * 16 + r;
+    if (t >= p.T || !((mask >> t) & 1)) continue;
+    floatx4 v = red[0][q][lane];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) v += red[w][q][lane];
+    const int64_t row = static_cast<int64_t>(s) * p.T + t;
+    float* dst = is_w ? p.part + row * p.Np + tile * 16 + 4 * g
+                      : p.vpart + row * p.Rp + rt * 16 + 4 * g;
+    *reinterpret_cast<floatx4*>(dst) = v;
+  }
+}
+
+struct ExpandArgs {
+  const float* part;     // [S, T, Np]
+  const float* vpart;    // [S, T, Rp]
+  const int32_t* ids;
+  const float* scales;   // [A] or NULL
+  const void* b;         // [A, N, R]
+  void* y;               // [T, N]
+  int S, T, N, Np, A, R, Rp;
+};
+
+// y[t, n] = the sum of the parts + s[a] sum_j v[t, j] B[a][n, j]. One block:
+// 256 columns of one token, one column a thread, which reads its row of B
+// whole (neighbouring threads' rows are neighbours in memory). The low-rank
+// sums of the token stay in LDS. fp32 throughout, rounded once.
+template <bool kF32>
+__global__ __launch_bounds__(kThreads) void adapter_few(ExpandArgs p) {
+  typedef typename Elem<kF32>::type E;
+  constexpr int kC = Elem<kF32>::kChunk;
+  __shared__ float v_s[kMaxRank + 8];
+  const int t = blockIdx.y;
+  const int n = blockIdx.x * kThreads + threadIdx.x;
+  const int aid = p.ids[t];
+  const bool has = aid >= 0 && aid < p.A;
+  const int64_t nT = p.T;
+  float acc = 0.0f;
+  if (n < p.N)
+    for (int s = 0; s < p.S; ++s) acc += p.part[(s * nT + t) * p.Np + n];
+  if (has) {   // the same for the whole block
+    const float sc = p.scales ? p.scales[aid] : 1.0f;
+    for (int j = threadIdx.x; j < kMaxRank + 8; j += kThreads) {
+      float v = 0.0f;
+      if (j < p.R)
+        for (int s = 0; s < p.S; ++s) v += p.vpart[(s * nT + t) * p.Rp + j];
+      v_s[j] = v * sc;
+    }
+    __syncthreads();
+    if (n < p.N) {
+      const E* row = static_cast<const E*>(p.b) + (static_cast<int64_t>(aid) * p.N + n) * p.R;
+      const bool vec = (p.R % kC) == 0;
+      float d = 0.0f;
+#pragma unroll 4
+      for (int j = 0; j < p.R; j += kC) {
+        const u32x4 c = vec ? load16(reinterpret_cast<const char*>(row + j))
+                            : load16_any<kF32>(row, j, p.R);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (kF32) {
+            d = fmaf(v_s[j + i], __uint_as_float(c[i]), d);
+          } else {
+            d = fmaf(v_s[j + 2 * i], bf16_bits_to_f32(c[i] & 0xffffu), d);
+            d = fmaf(v_s[j + 2 * i + 1], __uint_as_float(c[i] & 0xffff0000u), d);
+          }
+        }
+      }
+      acc += d;
+    }
+  }
+  if (n < p.N) {
+    if constexpr (kF32) static_cast<float*>(p.y)[static_cast<int64_t>(t) * p.N + n] = acc;
+    else
+      static_cast<uint16_t*>(p.y)[static_cast<int64_t>(t) * p.N + n] =
+          static_cast<uint16_t>(f32_to_bf16_bits(acc));
+  }
+}
+
+// --------------------------------------------------------------------------
+// Many tokens: the adapters' low-rank products
+// --------------------------------------------------------------------------
+struct ShrinkArgs {
+  const char* x;
+  const char* a;
+  const int32_t* ids;
+  const float* scales;
+  void* v;               // [T, Rq] in the storage type, zero past R
+  int64_t row_bytes;
+  int64_t T;
+  int A, R, Rq;
+};
+
+// v[t, j] = s[a] x[t] . A[a][j] for a group of 16 tokens, one after another
+// for the different adapters among them (one or two where tokens of a request
+// are neighbours); up to 64 rows of A at a time, the waves sharing the
+// reduction. v is rounded to the storage type, to be an MFMA operand of the
+// tile's epilogue: its error is that of one rounding of the adapter's part.
+template <bool kF32>
+__global__ __launch_bounds__(kThreads) void adapter_shrink(ShrinkArgs p) {
+  typedef typename Elem<kF32>::type E;
+  constexpr int kRT = 4;   // rank tiles of 16 at a time
+  __shared__ floatx4 red[kWaves][kRT][kWave];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int g = lane >> 4, r = lane & 15;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 16 + r;
+  const int id = t < p.T ? p.ids[t] : -1;
+  uint32_t todo = static_cast<uint32_t>(__ballot(id >= 0 && id < p.A)) & 0xffffu;
+  const int nkb = static_cast<int>((p.row_bytes + 63) >> 6);
+  const int nfull = static_cast<int>(p.row_bytes >> 6);
+  const int kb0 = wave * nkb / kWaves, kb1 = (wave + 1) * nkb / kWaves;
+  const int kbf = min(kb1, nfull);
+  while (todo) {
+    const int first = __ffs(todo) - 1;
+    const int aid = __builtin_amdgcn_readlane(id, first);
+    const bool mine = id == aid;
+    todo &= ~static_cast<uint32_t>(__ballot(mine));
+    const char* xp =
+        p.x + (mine ? t : static_cast<int64_t>(blockIdx.x) * 16 + first) * p.row_bytes + g * 16;
+    const float sc = p.scales ? p.scales[aid] : 1.0f;
+    for (int j0 = 0; j0 < p.R; j0 += 16 * kRT) {
+      const char* ap[kRT];
+#pragma unroll
+      for (int c = 0; c < kRT; ++c)
+        ap[c] = p.a + (static_cast<int64_t>(aid) * p.R + min(j0 + c * 16 + r, p.R - 1)) * p.row_bytes + g * 16;
+      const int nc = min(kRT, (p.R - j0 + 15) / 16);
+      floatx4 acc[kRT];
+#pragma unroll
+      for (int c = 0; c < kRT; ++c) acc[c] = floatx4{0, 0, 0, 0};
+      int kb = kb0;
+      for (; kb + kU <= kbf; kb += kU) {
+        u32x4 xb[kU];
+#pragma unroll
+        for (int j = 0; j < kU; ++j) xb[j] = load16(xp + (kb + j) * 64);
+#pragma unroll
+        for (int c = 0; c < kRT; ++c) {
+          if (c >= nc) continue;
+          u32x4 wa[kU];
+#pragma unroll
+          for (int j = 0; j < kU; ++j) wa[j] = load16(ap[c] + (kb + j) * 64);
+#pragma unroll
+          for (int j = 0; j < kU; ++j) acc[c] = mma16<kF32>(wa[j], xb[j], acc[c]);
+        }
+      }
+      for (; kb < kb1; ++kb) {
+        const bool in = kb * 64 + g * 16 < p.row_bytes;
+        const u32x4 xb = in ? load16(xp + kb * 64) : u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < kRT; ++c) {
+          if (c >= nc) continue;
+          const u32x4 wa = in ? load16(ap[c] + kb * 64) : u32x4{0, 0, 0, 0};
+          acc[c] = mma16<kF32>(wa, xb, acc[c]);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < kRT; ++c) red[wave][c][lane] = acc[c];
+      __syncthreads();
+      // wave c: rank tile c; columns past R are zero
+      const int col = j0 + wave * 16 + 4 * g;
+      if (mine && col < p.Rq) {
+        floatx4 v = red[0][wave][lane];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) v += red[w][wave][lane];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = col + i < p.R ? v[i] * sc : 0.0f;
+        store4<kF32>(static_cast<E*>(p.v) + t * p.Rq, col, p.Rq, true, v);
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// --------------------------------------------------------------------------
+// Many tokens: 128 x 128 tiles
+// --------------------------------------------------------------------------
+constexpr int kTile = 128;                    // tokens and weight rows of a tile
+constexpr int kLine = 8;                      // 16-byte chunks of a k-tile's row
+constexpr int kStage = kTile * kLine;
+constexpr int kBufferFlags = 0x00020000;      // raw buffer, 32-bit data format
+constexpr uint32_t kPast = 0x80000000u;       // an offset past every buffer here
+
+struct TileArgs {
+  const char* x;         // [T, H]
+  const char* w;         // [N, H]
+  int64_t row_bytes;
+  int64_t T;
+  int N;
+  int m_tiles, n_tiles;
+  float* part;           // [S, T, Np] fp32 sums (router), or NULL: y
+  int Np;
+  void* y;               // [T, N]
+  const int32_t* ids;    // adapters (NULL: none)
+  const void* v;         // [T, Rq]
+  const void* b;         // [A, N, R]
+  int A, R, Rq;
+};
+
+typedef __attribute__((address_space(3))) void lds_ptr;
+
+// Two stages of a token half and a weight half each: distinct objects, so that
+// reads of one are not taken to wait for DMA into another. Row i of a stage
+// keeps its chunk c at c ^ (i & 7) ^ ((i >> 3) & 1): the 16 rows of a fragment
+// read lie in different banks.
+__shared__ u32x4 t_x0[kStage], t_w0[kStage], t_x1[kStage], t_w1[kStage];
+
+#if defined(__HIP_DEVICE_COMPILE__)
+template <int S>
+__device__ __forceinline__ u32x4* stage_x() { return S == 0 ? t_x0 : t_x1; }
+template <int S>
+__device__ __forceinline__ u32x4* stage_w() { return S == 0 ? t_w0 : t_w1; }
+
+struct TileLoad {
+  __amdgpu_buffer_rsrc_t xr, wr;
+  uint32_t xo[4], wo[4];   // this lane's byte offsets in its four pieces; kPast: zeros
+  uint32_t chunk[2];       // the lane's byte in a k-tile's row, even and odd pieces
+  uint32_t row_bytes;
+};
+
+// Pieces of 8 rows x 128 bytes, 4 + 4 a wave. Rows past T or N and bytes past
+// the row are given an offset past the buffer, whose DMA writes zeros.
+template <int S>
+__device__ __forceinline__ void tile_dma(const TileLoad& l, int wave, int kt) {
+  const uint32_t k = static_cast<uint32_t>(kt) * 128;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t c = l.chunk[j & 1];
+    const bool in = k + c < l.row_bytes;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        l.xr, (lds_ptr*)(stage_x<S>() + (wave * 4 + j) * 8 * kLine), 16,
+        in ? l.xo[j] + k : kPast, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        l.wr, (lds_ptr*)(stage_w<S>() + (wave * 4 + j) * 8 * kLine), 16,
+        in ? l.wo[j] + k : kPast, 0, 0, 0);
+  }
+}
+
+template <bool kF32, int S>
+__device__ __forceinline__ void tile_mma(int wm, int wn, const int (&frag)[2], floatx4 (&acc)[4][4]) {
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    u32x4 fx[4], fw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      fx[i] = stage_x<S>()[(wm * 64 + i * 16) * kLine + frag[s]];
+      fw[i] = stage_w<S>()[(wn * 64 + i * 16) * kLine + frag[s]];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = mma16<kF32>(fw[j], fx[i], acc[i][j]);
+  }
+}
+
+__device__ __forceinline__ void dma_wait_barrier() {
+  __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) and lgkmcnt(0)
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+#endif  // __HIP_DEVICE_COMPILE__
+
+// Tile (m, n) over the k-tiles of part blockIdx.y. Each wave has a 64 x 64
+// quarter. kAdapt: the epilogue adds each token's adapter, v B^T, one different
+// adapter of a 16-token group after another.
+template <bool kF32, bool kAdapt>
+__global__ __launch_bounds__(kThreads) void linear_tile(TileArgs p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef typename Elem<kF32>::type E;
+  constexpr int kC = Elem<kF32>::kChunk;
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int g = lane >> 4, r = lane & 15;
+
+  // blocks are dealt round-robin to the 8 XCDs: each XCD gets a run of the
+  // order (n fastest: a run shares tokens)
+  const int total = p.m_tiles * p.n_tiles;
+  int pos = blockIdx.x;
+  const int per = gridDim.x >> 3;
+  pos = (pos & 7) * per + (pos >> 3);   // the grid is a multiple of 8
+  if (pos >= total) return;
+  const int mt = pos / p.n_tiles, nt = pos % p.n_tiles;
+  const int64_t t0 = static_cast<int64_t>(mt) * kTile;
+  const int n0 = nt * kTile;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(kTile), p.T - t0));
+  const int cols = min(kTile, p.N - n0);
+
+  const int nkt = static_cast<int>((p.row_bytes + 127) >> 7);
+  const int S = gridDim.y, s = blockIdx.y;
+  const int k0 = static_cast<int>(static_cast<int64_t>(s) * nkt / S);
+  const int k1 = static_cast<int>(static_cast<int64_t>(s + 1) * nkt / S);
+
+  TileLoad l;
+  l.row_bytes = static_cast<uint32_t>(p.row_bytes);
+  // 128 rows of at most 2^24 bytes: within the 2^31 that an offset reaches
+  l.xr = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p.x + t0 * p.row_bytes), 0,
+                                           static_cast<int>(rows * l.row_bytes), kBufferFlags);
+  l.wr = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<char*>(p.w + static_cast<int64_t>(n0) * p.row_bytes), 0,
+      static_cast<int>(cols * l.row_bytes), kBufferFlags);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) l.chunk[j] = ((lane & 7) ^ (lane >> 3) ^ j) * 16;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int row = (wave * 4 + j) * 8 + (lane >> 3);
+    l.xo[j] = row < rows ? row * l.row_bytes + l.chunk[j & 1] : kPast;
+    l.wo[j] = row < cols ? row * l.row_bytes + l.chunk[j & 1] : kPast;
+  }
+  int frag[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) frag[q] = r * kLine + ((4 * q + g) ^ (r & 7) ^ ((r >> 3) & 1));
+
+  floatx4 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = floatx4{0, 0, 0, 0};
+
+  if (k0 < k1) tile_dma<0>(l, wave, k0);
+  int kt = k0;
+  for (; kt + 1 < k1; kt += 2) {
+    dma_wait_barrier();
+    tile_dma<1>(l, wave, kt + 1);
+    tile_mma<kF32, 0>(wm, wn, frag, acc);
+    dma_wait_barrier();
+    if (kt + 2 < k1) tile_dma<0>(l, wave, kt + 2);
+    tile_mma<kF32, 1>(wm, wn, frag, acc);
+  }
+  if (kt < k1) {
+    dma_wait_barrier();
+    tile_mma<kF32, 0>(wm, wn, frag, acc);
+  }
+
+  // lane (g, r): columns n0 + 64 wn + 16 j + 4 g .. + 3 of token 64 wm + 16 i + r
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int lt = wm * 64 + i * 16 + r;
+    const int64_t t = t0 + lt;
+    if constexpr (kAdapt) {
+      const int id = lt < rows ? p.ids[t] : -1;
+      uint32_t todo = static_cast<uint32_t>(__ballot(id >= 0 && id < p.A)) & 0xffffu;
+      const bool vec = (p.R % kC) == 0;
+      while (todo) {
+        const int lead = __ffs(todo) - 1;
+        const int aid = __builtin_amdgcn_readlane(id, lead);
+        const bool mine = id == aid;
+        todo &= ~static_cast<uint32_t>(__ballot(mine));
+        const E* vrow = static_cast<const E*>(p.v) + (mine ? t : t0 + wm * 64 + i * 16 + lead) * p.Rq;
+        floatx4 d[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] = floatx4{0, 0, 0, 0};
+        for (int j0 = 0; j0 < p.R; j0 += 4 * kC) {
+          const int k = j0 + g * kC;
+          const u32x4 fv = load16(reinterpret_cast<const char*>(vrow + k));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int n = min(n0 + wn * 64 + j * 16 + r, p.N - 1);
+            const E* row = static_cast<const E*>(p.b) + (static_cast<int64_t>(aid) * p.N + n) * p.R;
+            u32x4 fb = {0, 0, 0, 0};
+            if (k < p.R)
+              fb = vec ? load16(reinterpret_cast<const char*>(row + k)) : load16_any<kF32>(row, k, p.R);
+            d[j] = mma16<kF32>(fb, fv, d[j]);
+          }
+        }
+        // added to its own tokens only: an adapter's infinities reach no other
+        if (mine) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] += d[j];
+        }
+      }
+    }
+    if (lt >= rows) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = n0 + wn * 64 + j * 16 + 4 * g;
+      if (n >= p.N) continue;
+      if constexpr (kAdapt)
+        store4<kF32>(static_cast<E*>(p.y) + t * p.N, n, p.N, (p.N & 3) == 0, acc[i][j]);
+      else
+        *reinterpret_cast<floatx4*>(p.part + (s * p.T + t) * p.Np + n) = acc[i][j];
+    }
+  }
+#endif  // __HIP_DEVICE_COMPILE__
+}
+
+template <bool kF32>
+hipError_t launch_stream(const StreamArgs& a, int tiles, int S, hipStream_t st) {
+  const dim3 grid(tiles, S);
+  if (a.T <= 16)
+    hipLaunchKernelGGL((stream_partial<kF32, 1>), grid, dim3(kThreads), 0, st, a);
+  else if (a.T <= 32)
+    hipLaunchKernelGGL((stream_partial<kF32, 2>), grid, dim3(kThreads), 0, st, a);
+  else
+    hipLaunchKernelGGL((stream_partial<kF32, 4>), grid, dim3(kThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+template <bool kF32, bool kAdapt>
+hipError_t launch_tile(const TileArgs& a, int S, hipStream_t st) {
+  const int64_t total = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
+  hipLaunchKernelGGL((linear_tile<kF32, kAdapt>), dim3(static_cast<unsigned>(cdiv(total, 8) * 8), S),
+                     dim3(kThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+// Parts of the reduction for `tiles` tiles of a few tokens: about two blocks a
+// CU, and four 64-byte blocks for each of a part's waves.
+int stream_parts(int64_t tiles, int64_t row_bytes) {
+  const int64_t want = cdiv(2 * static_cast<int64_t>(kPlanCus), tiles);
+  const int64_t most = cdiv(row_bytes, 64) / (4 * kWaves);
+  return static_cast<int>(want < 1 || most < 1 ? 1 : want < most ? (want < 16 ? want : 16)
+                                                                 : (most < 16 ? most : 16));
+}
+
+int64_t up16(int64_t v) { return cdiv(v, 16) * 16; }
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+}  // namespace
+
+// ---- the router's logits --------------------------------------------------
+LogitsLayout logits_layout(int64_t T, int64_t H, int N, bool f32) {
+  LogitsLayout L{};
+  const int64_t row_bytes = H * (f32 ? 4 : 2);
+  L.pitch = static_cast<int>(up16(N));
+  if (T <= kFewTokens) {
+    L.parts = stream_parts(cdiv(N, 16), row_bytes);
+  } else {
+    const int64_t tiles = cdiv(T, kTile) * cdiv(N, kTile);
+    const int64_t want = cdiv(2 * static_cast<int64_t>(kPlanCus), tiles), most = cdiv(row_bytes, 128) / 8;
+    L.parts = static_cast<int>(want < 1 || most < 1 ? 1 : want < most ? (want < 8 ? want : 8)
+                                                                      : (most < 8 ? most : 8));
+  }
+  L.bytes = up256(sizeof(float) * static_cast<size_t>(L.parts) * T * L.pitch);
+  return L;
+}
+
+hipError_t logits(int64_t T, int64_t H, int N, bool f32, const void* x, const void* w, float* part,
+                  uint32_t* zero, int n_zero, hipStream_t st) {
+  const LogitsLayout L = logits_layout(T, H, N, f32);
+  const int64_t row_bytes = H * (f32 ? 4 : 2);
+  if (T <= kFewTokens) {
+    StreamArgs a{};
+    a.x = static_cast<const char*>(x);
+    a.w = static_cast<const char*>(w);
+    a.part = part;
+    a.row_bytes = row_bytes;
+    a.T = static_cast<int>(T);
+    a.N = N;
+    a.Np = L.pitch;
+    a.tiles = static_cast<int>(cdiv(N, 16));
+    a.zero = zero;
+    a.n_zero = n_zero;
+    return f32 ? launch_stream<true>(a, a.tiles, L.parts, st)
+               : launch_stream<false>(a, a.tiles, L.parts, st);
+  }
+  TileArgs a{};
+  a.x = static_cast<const char*>(x);
+  a.w = static_cast<const char*>(w);
+  a.row_bytes = row_bytes;
+  a.T = T;
+  a.N = N;
+  a.m_tiles = static_cast<int>(cdiv(T, kTile));
+  a.n_tiles = static_cast<int>(cdiv(N, kTile));
+  a.part = part;
+  a.Np = L.pitch;
+  return f32 ? launch_tile<true, false>(a, L.parts, st) : launch_tile<false, false>(a, L.parts, st);
+}
+
+// ---- the shared projection with adapters ------------------------------------
+namespace {
+struct AdapterLayout {
+  int parts, Np, Rp, Rq;
+  size_t part, vpart, v, total;
+};
+AdapterLayout adapter_layout(const tr_adapter_desc& d) {
+  AdapterLayout L{};
+  const bool f32 = d.dtype == TR_F32;
+  const int64_t row_bytes = d.H * (f32 ? 4 : 2);
+  L.Np = static_cast<int>(up16(d.N));
+  L.Rp = static_cast<int>(up16(d.R));
+  L.Rq = static_cast<int>(f32 ? up16(d.R) : cdiv(d.R, 32) * 32);
+  if (d.T <= kFewTokens) {
+    L.parts = stream_parts(cdiv(d.N, 16), row_bytes);
+    L.vpart = up256(sizeof(float) * static_cast<size_t>(L.parts) * d.T * L.Np);
+    L.total = L.vpart + up256(sizeof(float) * static_cast<size_t>(L.parts) * d.T * L.Rp);
+  } else {
+    L.total = up256(static_cast<size_t>(d.T) * L.Rq * (f32 ? 4 : 2));
+  }
+  if (L.total == 0) L.total = 256;
+  return L;
+}
+}  // namespace
+
+size_t adapter_workspace(const tr_adapter_desc& d) { return adapter_layout(d).total; }
+
+hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w, const void* a,
+                          const void* b, const int32_t* ids, const float* scales, void* y, void* ws,
+                          hipStream_t st) {
+  const AdapterLayout L = adapter_layout(d);
+  const bool f32 = d.dtype == TR_F32;
+  const int64_t row_bytes = d.H * (f32 ? 4 : 2);
+  hipError_t e;
+  if (d.T <= kFewTokens) {
+    StreamArgs s{};
+    s.x = static_cast<const char*>(x);
+    s.w = static_cast<const char*>(w);
+    s.part = static_cast<float*>(ws);
+    s.row_bytes = row_bytes;
+    s.T = static_cast<int>(d.T);
+    s.N = static_cast<int>(d.N);
+    s.Np = L.Np;
+    s.tiles = static_cast<int>(cdiv(d.N, 16));
+    s.ids = ids;
+    s.a = static_cast<const char*>(a);
+    s.vpart = reinterpret_cast<float*>(static_cast<char*>(ws) + L.vpart);
+    s.A = d.A;
+    s.R = d.R;
+    s.Rp = L.Rp;
+    s.rank_tiles = L.Rp / 16;
+    const int slots = static_cast<int>(d.T < d.A ? d.T : d.A);
+    const int tiles = s.tiles + slots * s.rank_tiles;
+    e = f32 ? launch_stream<true>(s, tiles, L.parts, st) : launch_stream<false>(s, tiles, L.parts, st);
+    if (e != hipSuccess) return e;
+    ExpandArgs p{};
+    p.part = s.part;
+    p.vpart = s.vpart;
+    p.ids = ids;
+    p.scales = scales;
+    p.b = b;
+    p.y = y;
+    p.S = L.parts;
+    p.T = s.T;
+    p.N = s.N;
+    p.Np = L.Np;
+    p.A = d.A;
+    p.R = d.R;
+    p.Rp = L.Rp;
+    const dim3 grid(static_cast<unsigned>(cdiv(d.N, kThreads)), static_cast<unsigned>(d.T));
+    if (f32) hipLaunchKernelGGL(adapter_few<true>, grid, dim3(kThreads), 0, st, p);
+    else hipLaunchKernelGGL(adapter_few<false>, grid, dim3(kThreads), 0, st, p);
+    return hipGetLastError();
+  }
+  ShrinkArgs s{};
+  s.x = static_cast<const char*>(x);
+  s.a = static_cast<const char*>(a);
+  s.ids = ids;
+  s.scales = scales;
+  s.v = ws;
+  s.row_bytes = row_bytes;
+  s.T = d.T;
+  s.A = d.A;
+  s.R = d.R;
+  s.Rq = L.Rq;
+  const unsigned groups = static_cast<unsigned>(cdiv(d.T, 16));
+  if (f32) hipLaunchKernelGGL(adapter_shrink<true>, dim3(groups), dim3(kThreads), 0, st, s);
+  else hipLaunchKernelGGL(adapter_shrink<false>, dim3(groups), dim3(kThreads), 0, st, s);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  TileArgs t{};
+  t.x = s.x;
+  t.w = static_cast<const char*>(w);
+  t.row_bytes = row_bytes;
+  t.T = d.T;
+  t.N = static_cast<int>(d.N);
+  t.m_tiles = static_cast<int>(cdiv(d.T, kTile));
+  t.n_tiles = static_cast<int>(cdiv(d.N, kTile));
+  t.y = y;
+  t.ids = ids;
+  t.v = ws;
+  t.b = b;
+  t.A = d.A;
+  t.R = d.R;
+  t.Rq = L.Rq;
+  return f32 ? launch_tile<true, true>(t, 1, st) : launch_tile<false, true>(t, 1, st);
+}
+
+}  // namespace tr

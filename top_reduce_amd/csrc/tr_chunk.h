@@ -1,0 +1,110 @@
+// 16-byte pieces of operand rows, alike for bf16 and fp32 (gfx950, wave64).
+//
+// Every product here is "NT": activation rows and weight rows both run along
+// the reduction dimension. A lane holds one 16-byte chunk of a row: lane l the
+// row l % 16 and, of four neighbouring chunks, chunk l / 16. For bf16 that is
+// the operand of one 16x16x32 MFMA. For fp32 the four elements of the chunk
+// feed four 16x16x4 MFMAs: MFMA s takes element s of every lane, so the four
+// cover the 16 k of the chunks once each (in another order, the same for both
+// operands). Either way lane (g, r) = (l / 16, l % 16) ends with
+// sum_k A[4 g + i][k] B[r][k], i = 0..3.
+#pragma once
+
+#include "tr_device.h"
+
+namespace tr {
+
+template <bool kF32>
+struct Elem;
+template <>
+struct Elem<false> {
+  typedef uint16_t type;
+  static constexpr int kBytes = 2, kChunk = 8;   // elements in 16 bytes
+};
+template <>
+struct Elem<true> {
+  typedef float type;
+  static constexpr int kBytes = 4, kChunk = 4;
+};
+
+template <bool kF32>
+__device__ __forceinline__ floatx4 mma16(const u32x4& a, const u32x4& b, floatx4 c) {
+  if constexpr (kF32) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[s]), __uint_as_float(b[s]), c, 0,
+                                               0, 0);
+    return c;
+  } else {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+}
+
+__device__ __forceinline__ u32x4 load16(const char* p) {
+  return *reinterpret_cast<const u32x4*>(p);
+}
+
+// The 16 bytes at element k of a row of n elements that need not start on 16
+// bytes; zero past n.
+template <bool kF32>
+__device__ __forceinline__ u32x4 load16_any(const typename Elem<kF32>::type* row, int k, int n) {
+  u32x4 v = {0, 0, 0, 0};
+  if constexpr (kF32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (k + i < n) v[i] = __float_as_uint(row[k + i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = k + 2 * i < n ? row[k + 2 * i] : 0;
+      const uint32_t hi = k + 2 * i + 1 < n ? row[k + 2 * i + 1] : 0;
+      v[i] = lo | (hi << 16);
+    }
+  }
+  return v;
+}
+
+// Two floats rounded to bf16 (nearest even) by one hardware conversion; lo in
+// bits 0..15.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  const bf16x2 v = {static_cast<__bf16>(lo), static_cast<__bf16>(hi)};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+// silu(g) * u in fp32. bf16 results take the hardware exponential and
+// reciprocal (about 1 ulp of fp32 each, far below their own rounding); fp32
+// results the exact division.
+template <bool kF32>
+__device__ __forceinline__ float swiglu(float g, float u) {
+  if constexpr (kF32) return g / (1.0f + expf(-g)) * u;
+  return g * u * __builtin_amdgcn_rcpf(1.0f + __expf(-g));
+}
+
+// Stores the four neighbouring outputs v of a row at column col, those below
+// n only; `vec`: the row's start and col allow one wide store.
+template <bool kF32>
+__device__ __forceinline__ void store4(typename Elem<kF32>::type* row, int64_t col, int64_t n,
+                                       bool vec, const floatx4& v) {
+  if constexpr (kF32) {
+    if (vec && col + 4 <= n) {
+      *reinterpret_cast<floatx4*>(row + col) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (col + i < n) row[col + i] = v[i];
+    }
+  } else {
+    const uint32_t p[2] = {cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
+    if (vec && col + 4 <= n) {
+      *reinterpret_cast<uint2*>(row + col) = uint2{p[0], p[1]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (col + i < n) row[col + i] = static_cast<uint16_t>(p[i >> 1] >> (16 * (i & 1)));
+    }
+  }
+}
+
+}  // namespace tr

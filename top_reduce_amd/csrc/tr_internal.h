@@ -63,5 +63,47 @@ hipError_t compact_rows(int64_t T, int B, const int* counts, int64_t row_bytes, 
 
 // Compute units of the current device (cached per device).
 int device_cu_count();
+// Compute units that a workspace's layout is planned for (a layout must not
+// depend on the device that is current).
+constexpr int kPlanCus = 256;
+
+// --- router, few-token layer, shared projection with adapters ---------------
+// Batches of at most this many tokens take the weight-streaming kernels (their
+// tokens are the bits of one 64-bit mask).
+constexpr int kFewTokens = 64;
+constexpr int kMaxGates = 4096;   // experts a router chooses from
+constexpr int kMaxRank = 256;     // of an adapter
+
+// Logits x w^T as fp32 parts [parts, T, pitch]; their sum is the logits.
+struct LogitsLayout {
+  int parts, pitch;
+  size_t bytes;
+};
+LogitsLayout logits_layout(int64_t T, int64_t H, int N, bool f32);
+// Few tokens only: also zeroes n_zero words at `zero` (n_zero at most 2048).
+hipError_t logits(int64_t T, int64_t H, int N, bool f32, const void* x, const void* w, float* part,
+                  uint32_t* zero, int n_zero, hipStream_t st);
+
+// Local routes of at most kFewTokens tokens, written by the router's selection.
+struct FewRoutes {
+  unsigned long long* masks;   // [E] the tokens that chose each local expert
+  uint8_t* slots;              // [E, 64] the token's slot that names it
+  int64_t begin;
+  int E;
+};
+size_t route_workspace(const tr_route_desc& d);
+hipError_t route_topk(const tr_route_desc& d, const void* x, const void* w_gate, const float* bias,
+                      void* idx, float* w, void* ws, hipStream_t st, const FewRoutes* few = nullptr);
+
+size_t few_workspace(const tr_layer_desc& d);
+FewRoutes few_routes(const tr_layer_desc& d, void* ws);
+// The local experts of the routes in ws (few_routes): y, complete.
+hipError_t few_experts(const tr_layer_desc& d, const void* x, const void* w1, const void* w2,
+                       const float* w, void* y, void* ws, hipStream_t st);
+
+size_t adapter_workspace(const tr_adapter_desc& d);
+hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w, const void* a,
+                          const void* b, const int32_t* ids, const float* scales, void* y, void* ws,
+                          hipStream_t st);
 
 }  // namespace tr
