@@ -39,10 +39,11 @@ struct FewArgs {
 };
 
 // The experts with a token, in ascending order, in LDS; returns how many.
+template <int kBlock>
 __device__ __forceinline__ int active_experts(const FewArgs& a, int* list, uint64_t* mask_s,
                                               int* tmp) {
-  constexpr int kPer = kMaxE / kThreads;
-  const int per = (a.E + kThreads - 1) / kThreads;
+  constexpr int kPer = kMaxE / kBlock;
+  const int per = (a.E + kBlock - 1) / kBlock;
   uint64_t m[kPer];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
@@ -52,7 +53,7 @@ __device__ __forceinline__ int active_experts(const FewArgs& a, int* list, uint6
   int n = 0, total = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) n += m[j] != 0;
-  int at = block_exclusive_scan<kThreads>(n, tmp, &total);
+  int at = block_exclusive_scan<kBlock>(n, tmp, &total);
 #pragma unroll
   for (int j = 0; j < kPer; ++j)
     if (m[j]) {
@@ -72,7 +73,7 @@ __global__ __launch_bounds__(kThreads) void few_up(FewArgs a) {
   __shared__ uint64_t mask_s[kMaxE];
   __shared__ int tmp[kWaves];
   __shared__ floatx4 red[kWaves][NQ][2][kWave];
-  const int n_act = active_experts(a, list, mask_s, tmp);
+  const int n_act = active_experts<kThreads>(a, list, mask_s, tmp);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, r = lane & 15;
   const int upe = static_cast<int>(a.Ip / 16);
@@ -99,35 +100,39 @@ __global__ __launch_bounds__(kThreads) void few_up(FewArgs a) {
       xp[i] = a.x + ((mask >> t) & 1 ? t : first) * row_bytes + g * 16;
       ag[i] = au[i] = floatx4{0, 0, 0, 0};
     }
-    int kb = kb0;
-    for (; kb + kU <= kbf; kb += kU) {
+    // Batches of kU blocks. A share's last batch may be short: its loads
+    // re-read the last whole block and the products are skipped.
+    for (int kb = kb0; kb < kbf; kb += kU) {
       u32x4 vg[kU], vu[kU];
 #pragma unroll
       for (int j = 0; j < kU; ++j) {
-        vg[j] = load16(wg + (kb + j) * 64);
-        vu[j] = load16(wu + (kb + j) * 64);
+        vg[j] = load16(wg + min(kb + j, kbf - 1) * 64);
+        vu[j] = load16(wu + min(kb + j, kbf - 1) * 64);
       }
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
-        if (!on[i]) continue;
+        if (NQ > 1 && !on[i]) continue;
         u32x4 xb[kU];
 #pragma unroll
-        for (int j = 0; j < kU; ++j) xb[j] = load16(xp[i] + (kb + j) * 64);
+        for (int j = 0; j < kU; ++j) xb[j] = load16(xp[i] + min(kb + j, kbf - 1) * 64);
+        // every load of the batch is out before the first product
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < kU; ++j) {
-          ag[i] = mma16<kF32>(vg[j], xb[j], ag[i]);
-          au[i] = mma16<kF32>(vu[j], xb[j], au[i]);
-        }
+        for (int j = 0; j < kU; ++j)
+          if (kb + j < kbf) {
+            ag[i] = mma16<kF32>(vg[j], xb[j], ag[i]);
+            au[i] = mma16<kF32>(vu[j], xb[j], au[i]);
+          }
       }
     }
-    for (; kb < kb1; ++kb) {
-      const bool in = kb * 64 + g * 16 < row_bytes;
+    if (kb1 > nfull) {   // the short block at the end of the rows
+      const bool in = nfull * 64 + g * 16 < row_bytes;
       const u32x4 z = {0, 0, 0, 0};
-      const u32x4 vg = in ? load16(wg + kb * 64) : z, vu = in ? load16(wu + kb * 64) : z;
+      const u32x4 vg = in ? load16(wg + nfull * 64) : z, vu = in ? load16(wu + nfull * 64) : z;
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
         if (!on[i]) continue;
-        const u32x4 xb = in ? load16(xp[i] + kb * 64) : z;
+        const u32x4 xb = in ? load16(xp[i] + nfull * 64) : z;
         ag[i] = mma16<kF32>(vg, xb, ag[i]);
         au[i] = mma16<kF32>(vu, xb, au[i]);
       }
@@ -174,85 +179,114 @@ __global__ __launch_bounds__(kThreads) void few_up(FewArgs a) {
 }
 
 // A unit: 16 output columns of every token; the (expert, batch of k) pairs of
-// the sum are shared by the block's waves. kVec: rows of w2 start on 16 bytes.
+// the sum are shared by the block's waves, each a run of them. kVec: rows of w2
+// start on 16 bytes.
+constexpr int kDownThreads = 512;
+constexpr int kDownWaves = kDownThreads / kWave;
+
 template <bool kF32, int NQ, bool kVec>
-__global__ __launch_bounds__(kThreads) void few_down(FewArgs a) {
+__global__ __launch_bounds__(kDownThreads) void few_down(FewArgs a) {
   typedef typename Elem<kF32>::type E;
   constexpr int kC = Elem<kF32>::kChunk, kB = Elem<kF32>::kBytes;
   constexpr int kParts = kF32 ? 1 : 2;
   __shared__ int list[kMaxE];
   __shared__ uint64_t mask_s[kMaxE];
-  __shared__ int tmp[kWaves];
-  __shared__ floatx4 red[kWaves][NQ][kWave];
-  const int n_act = active_experts(a, list, mask_s, tmp);
+  __shared__ int tmp[kDownWaves];
+  __shared__ floatx4 red[kDownWaves][NQ][kWave];
+  const int n_act = active_experts<kDownThreads>(a, list, mask_s, tmp);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, r = lane & 15;
-  const int I = static_cast<int>(a.I);
+  const int I = static_cast<int>(a.I), Ip = static_cast<int>(a.Ip);
   const int nkb = (I * kB + 63) >> 6;             // 64-byte blocks of a row
   const int nb = (nkb + kU - 1) / kU;             // batches of an expert
-  const int64_t items = static_cast<int64_t>(n_act) * nb;
-  const int i0 = static_cast<int>(wave * items / kWaves);
-  const int i1 = static_cast<int>((wave + 1) * items / kWaves);
+  const int items = n_act * nb;
+  const int i0 = static_cast<int>(static_cast<int64_t>(wave) * items / kDownWaves);
+  const int i1 = static_cast<int>(static_cast<int64_t>(wave + 1) * items / kDownWaves);
   const int units = static_cast<int>((a.H + 15) / 16);
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
     const int64_t n = min(static_cast<int64_t>(u * 16 + r), a.H - 1);
     floatx4 acc[NQ], cur[NQ];   // over the experts; of the expert at hand
 #pragma unroll
     for (int i = 0; i < NQ; ++i) acc[i] = cur[i] = floatx4{0, 0, 0, 0};
-    for (int it = i0; it < i1; ++it) {
-      const int q = it / nb, b = it % nb;
-      const int e = list[q];
+    int q = i0 / nb, b = i0 % nb;
+    for (int it = i0; it < i1;) {
+      // expert q: this wave's batches of it
+      const int e = __builtin_amdgcn_readfirstlane(list[q]);
       const uint64_t mask = mask_s[q];
       const E* wrow = static_cast<const E*>(a.w2) + (e * a.H + n) * a.I;
-      u32x4 wv[kU];
-#pragma unroll
-      for (int j = 0; j < kU; ++j) {
-        const int k = (b * kU + j) * 4 * kC + g * kC;
-        wv[j] = u32x4{0, 0, 0, 0};
-        if (k < I) {
-          if constexpr (kVec) wv[j] = load16(reinterpret_cast<const char*>(wrow + k));
-          else wv[j] = load16_any<kF32>(wrow, k, I);
-        }
-      }
+      const char* hp[NQ];
+      bool on[NQ];
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
-        if (!((mask >> (16 * i)) & 0xffff)) continue;
         const int t = i * 16 + r;
-        const bool mine = (mask >> t) & 1;
-        const int at = mine ? t : __ffsll(static_cast<unsigned long long>(mask)) - 1;
-        const int slot = at * a.K + a.slots[e * 64 + at];
-        const char* hp = a.h + static_cast<int64_t>(slot) * kParts * a.Ip * kB;
+        const int at = (mask >> t) & 1 ? t : __ffsll(static_cast<unsigned long long>(mask)) - 1;
+        on[i] = (mask >> (16 * i)) & 0xffff;
+        hp[i] = a.h + static_cast<int64_t>(at * a.K + a.slots[e * 64 + at]) * kParts * Ip * kB;
+      }
+      const int b1 = min(nb, b + i1 - it);
+      it += b1 - b;
+      for (; b < b1; ++b) {
+        u32x4 wv[kU];
+        const int k0 = b * kU * 4 * kC + g * kC;
+        const bool whole = (b + 1) * kU * 4 * kC <= I;   // the same in every lane
+        if (kVec && whole) {
 #pragma unroll
-        for (int part = 0; part < kParts; ++part) {
-          u32x4 hv[kU];
+          for (int j = 0; j < kU; ++j) wv[j] = load16(reinterpret_cast<const char*>(wrow + k0 + j * 4 * kC));
+        } else {
 #pragma unroll
           for (int j = 0; j < kU; ++j) {
-            const int k = (b * kU + j) * 4 * kC + g * kC;
-            hv[j] = k < I ? load16(hp + (part * a.Ip + k) * kB) : u32x4{0, 0, 0, 0};
+            const int k = k0 + j * 4 * kC;
+            wv[j] = u32x4{0, 0, 0, 0};
+            if (k < I) {
+              if constexpr (kVec) wv[j] = load16(reinterpret_cast<const char*>(wrow + k));
+              else wv[j] = load16_any<kF32>(wrow, k, I);
+            }
           }
-#pragma unroll
-          for (int j = 0; j < kU; ++j) cur[i] = mma16<kF32>(wv[j], hv[j], cur[i]);
         }
-      }
-      if (b + 1 == nb || it + 1 == i1) {
-        // the expert's sums go to its own tokens only: infinities in its
-        // weights reach no other
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
-          if ((mask >> (i * 16 + r)) & 1) acc[i] += cur[i];
-          cur[i] = floatx4{0, 0, 0, 0};
+          if (NQ > 1 && !on[i]) continue;
+          // past I both operands are zero (h has zeros from I to Ip)
+          u32x4 hv[kParts][kU];
+#pragma unroll
+          for (int part = 0; part < kParts; ++part)
+#pragma unroll
+            for (int j = 0; j < kU; ++j)
+              hv[part][j] = load16(hp[i] + (part * Ip + min(k0 + j * 4 * kC, Ip - kC)) * kB);
+          if (!whole) {
+#pragma unroll
+            for (int part = 0; part < kParts; ++part)
+#pragma unroll
+              for (int j = 0; j < kU; ++j)
+                if (k0 + j * 4 * kC >= Ip) hv[part][j] = u32x4{0, 0, 0, 0};
+          }
+          // every load of the batch is out before the first product
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int part = 0; part < kParts; ++part)
+#pragma unroll
+            for (int j = 0; j < kU; ++j) cur[i] = mma16<kF32>(wv[j], hv[part][j], cur[i]);
         }
       }
+      // the expert's sums go to its own tokens only: infinities in its weights
+      // reach no other
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        if ((mask >> (i * 16 + r)) & 1) acc[i] += cur[i];
+        cur[i] = floatx4{0, 0, 0, 0};
+      }
+      ++q;
+      b = 0;
     }
 #pragma unroll
     for (int i = 0; i < NQ; ++i) red[wave][i][lane] = acc[i];
     __syncthreads();
-    for (int i = wave; i < NQ; i += kWaves) {
+    for (int i = wave; i < NQ; i += kDownWaves) {
       const int t = i * 16 + r;
       if (t >= a.T) continue;
       floatx4 v = red[0][i][lane];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) v += red[w][i][lane];
+      for (int w = 1; w < kDownWaves; ++w) v += red[w][i][lane];
       store4<kF32>(static_cast<E*>(a.y) + t * a.H, u * 16 + 4 * g, a.H, true, v);
     }
     __syncthreads();
@@ -270,9 +304,9 @@ hipError_t launch_few(const FewArgs& a, hipStream_t st) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (a.I % Elem<kF32>::kChunk == 0)
-    hipLaunchKernelGGL((few_down<kF32, NQ, true>), dim3(g2), dim3(kThreads), 0, st, a);
+    hipLaunchKernelGGL((few_down<kF32, NQ, true>), dim3(g2), dim3(kDownThreads), 0, st, a);
   else
-    hipLaunchKernelGGL((few_down<kF32, NQ, false>), dim3(g2), dim3(kThreads), 0, st, a);
+    hipLaunchKernelGGL((few_down<kF32, NQ, false>), dim3(g2), dim3(kDownThreads), 0, st, a);
   return hipGetLastError();
 }
 

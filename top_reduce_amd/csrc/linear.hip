@@ -48,17 +48,14 @@ struct StreamArgs {
 // Block (tile, s): 16 weight rows against every token over part s of the
 // reduction, which its waves share. Tiles past the weight's are adapter tiles:
 // unit (slot, rank tile) takes 16 rows of the slot-th different adapter among
-// the tokens' ids, and keeps the sums of that adapter's tokens.
+// the tokens' ids, and keeps the sums of that adapter's tokens. red: LDS of
+// kWaves * NQ * kWave floatx4.
 template <bool kF32, int NQ>
-__global__ __launch_bounds__(kThreads) void stream_partial(StreamArgs p) {
-  __shared__ floatx4 red[kWaves][NQ][kWave];
+__device__ __forceinline__ void stream_unit(const StreamArgs& p, int tile, int s, int S,
+                                            floatx4* red) {
   const int tid = threadIdx.x;
   const int lane = tid & 63, wave = tid >> 6;
   const int g = lane >> 4, r = lane & 15;
-  const int tile = blockIdx.x, s = blockIdx.y, S = gridDim.y;
-
-  const int64_t z = (static_cast<int64_t>(s) * gridDim.x + tile) * kThreads + tid;
-  if (z < p.n_zero) p.zero[z] = 0;
 
   const bool is_w = tile < p.tiles;
   uint64_t mask = p.T == 64 ? ~0ull : (1ull << p.T) - 1;   // tokens of this tile
@@ -106,39 +103,43 @@ __global__ __launch_bounds__(kThreads) void stream_partial(StreamArgs p) {
   floatx4 acc[NQ];
 #pragma unroll
   for (int q = 0; q < NQ; ++q) acc[q] = floatx4{0, 0, 0, 0};
-  for (; kb + kU <= kbf; kb += kU) {
+  // Batches of kU blocks. A part's last batch may be short: its loads re-read
+  // the last whole block and the products are skipped, so that it costs one
+  // wait like the others and not one a block.
+  for (; kb < kbf; kb += kU) {
     u32x4 wa[kU];
 #pragma unroll
-    for (int j = 0; j < kU; ++j) wa[j] = load16(wp + (kb + j) * 64);
+    for (int j = 0; j < kU; ++j) wa[j] = load16(wp + min(kb + j, kbf - 1) * 64);
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
       if (!on[q]) continue;
       u32x4 xb[kU];
 #pragma unroll
-      for (int j = 0; j < kU; ++j) xb[j] = load16(xp[q] + (kb + j) * 64);
+      for (int j = 0; j < kU; ++j) xb[j] = load16(xp[q] + min(kb + j, kbf - 1) * 64);
 #pragma unroll
-      for (int j = 0; j < kU; ++j) acc[q] = mma16<kF32>(wa[j], xb[j], acc[q]);
+      for (int j = 0; j < kU; ++j)
+        if (kb + j < kbf) acc[q] = mma16<kF32>(wa[j], xb[j], acc[q]);
     }
   }
-  for (; kb < kb1; ++kb) {
-    const bool in = kb * 64 + g * 16 < p.row_bytes;
-    const u32x4 wa = in ? load16(wp + kb * 64) : u32x4{0, 0, 0, 0};
+  if (kb1 > nfull) {   // the short block at the end of the rows
+    const bool in = nfull * 64 + g * 16 < p.row_bytes;
+    const u32x4 wa = in ? load16(wp + nfull * 64) : u32x4{0, 0, 0, 0};
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
       if (!on[q]) continue;
-      const u32x4 xb = in ? load16(xp[q] + kb * 64) : u32x4{0, 0, 0, 0};
+      const u32x4 xb = in ? load16(xp[q] + nfull * 64) : u32x4{0, 0, 0, 0};
       acc[q] = mma16<kF32>(wa, xb, acc[q]);
     }
   }
 #pragma unroll
-  for (int q = 0; q < NQ; ++q) red[wave][q][lane] = acc[q];
+  for (int q = 0; q < NQ; ++q) red[(wave * NQ + q) * kWave + lane] = acc[q];
   __syncthreads();
   for (int q = wave; q < NQ; q += kWaves) {
     const int t = q * 16 + r;
     if (t >= p.T || !((mask >> t) & 1)) continue;
-    floatx4 v = red[0][q][lane];
+    floatx4 v = red[q * kWave + lane];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) v += red[w][q][lane];
+    for (int w = 1; w < kWaves; ++w) v += red[(w * NQ + q) * kWave + lane];
     const int64_t row = static_cast<int64_t>(s) * p.T + t;
     float* dst = is_w ? p.part + row * p.Np + tile * 16 + 4 * g
                       : p.vpart + row * p.Rp + rt * 16 + 4 * g;
@@ -158,50 +159,65 @@ struct ExpandArgs {
 
 // y[t, n] = the sum of the parts + s[a] sum_j v[t, j] B[a][n, j]. One block:
 // 256 columns of one token, one column a thread, which reads its row of B
-// whole (neighbouring threads' rows are neighbours in memory). The low-rank
-// sums of the token stay in LDS. fp32 throughout, rounded once.
+// whole (neighbouring threads' rows are neighbours in memory); the first of it
+// is asked for before the token's low-rank sums, which stay in LDS, are made.
+// fp32 throughout, rounded once.
 template <bool kF32>
 __global__ __launch_bounds__(kThreads) void adapter_few(ExpandArgs p) {
   typedef typename Elem<kF32>::type E;
   constexpr int kC = Elem<kF32>::kChunk;
-  __shared__ float v_s[kMaxRank + 8];
+  constexpr int kAhead = 8;   // chunks of B's row at a time
+  __shared__ float v_s[kMaxRank + kAhead * 8];
   const int t = blockIdx.y;
   const int n = blockIdx.x * kThreads + threadIdx.x;
+  const int nc = min(n, p.N - 1);
   const int aid = p.ids[t];
-  const bool has = aid >= 0 && aid < p.A;
+  const bool has = aid >= 0 && aid < p.A;   // the same for the whole block
   const int64_t nT = p.T;
+  const E* row = static_cast<const E*>(p.b) + (static_cast<int64_t>(has ? aid : 0) * p.N + nc) * p.R;
+  const bool vec = (p.R % kC) == 0;
+  auto chunk = [&](int j) -> u32x4 {
+    if (vec) return load16(reinterpret_cast<const char*>(row + min(j, p.R - kC)));
+    return load16_any<kF32>(row, j, p.R);
+  };
+  u32x4 c[kAhead];
+  if (has) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) c[i] = chunk(i * kC);
+  }
   float acc = 0.0f;
-  if (n < p.N)
-    for (int s = 0; s < p.S; ++s) acc += p.part[(s * nT + t) * p.Np + n];
-  if (has) {   // the same for the whole block
+  for (int s = 0; s < p.S; ++s) acc += p.part[(s * nT + t) * p.Np + nc];
+  if (has) {
     const float sc = p.scales ? p.scales[aid] : 1.0f;
-    for (int j = threadIdx.x; j < kMaxRank + 8; j += kThreads) {
+    for (int j = threadIdx.x; j < kMaxRank + kAhead * 8; j += kThreads) {
       float v = 0.0f;
       if (j < p.R)
         for (int s = 0; s < p.S; ++s) v += p.vpart[(s * nT + t) * p.Rp + j];
       v_s[j] = v * sc;
     }
     __syncthreads();
-    if (n < p.N) {
-      const E* row = static_cast<const E*>(p.b) + (static_cast<int64_t>(aid) * p.N + n) * p.R;
-      const bool vec = (p.R % kC) == 0;
-      float d = 0.0f;
-#pragma unroll 4
-      for (int j = 0; j < p.R; j += kC) {
-        const u32x4 c = vec ? load16(reinterpret_cast<const char*>(row + j))
-                            : load16_any<kF32>(row, j, p.R);
+    float d = 0.0f;
+    for (int j0 = 0; j0 < p.R; j0 += kAhead * kC) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kAhead; ++i) {
+        const int j = j0 + i * kC;
+        if (j >= p.R) continue;   // a chunk past the row: read again, not used
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
           if constexpr (kF32) {
-            d = fmaf(v_s[j + i], __uint_as_float(c[i]), d);
+            d = fmaf(v_s[j + q], __uint_as_float(c[i][q]), d);
           } else {
-            d = fmaf(v_s[j + 2 * i], bf16_bits_to_f32(c[i] & 0xffffu), d);
-            d = fmaf(v_s[j + 2 * i + 1], __uint_as_float(c[i] & 0xffff0000u), d);
+            d = fmaf(v_s[j + 2 * q], bf16_bits_to_f32(c[i][q] & 0xffffu), d);
+            d = fmaf(v_s[j + 2 * q + 1], __uint_as_float(c[i][q] & 0xffff0000u), d);
           }
         }
       }
-      acc += d;
+      if (j0 + kAhead * kC < p.R) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) c[i] = chunk(j0 + (kAhead + i) * kC);
+      }
     }
+    acc += d;
   }
   if (n < p.N) {
     if constexpr (kF32) static_cast<float*>(p.y)[static_cast<int64_t>(t) * p.N + n] = acc;
@@ -305,11 +321,9 @@ __global__ __launch_bounds__(kThreads) void adapter_shrink(ShrinkArgs p) {
 }
 
 // --------------------------------------------------------------------------
-// Many tokens: 128 x 128 tiles
+// Tiles staged through LDS
 // --------------------------------------------------------------------------
-constexpr int kTile = 128;                    // tokens and weight rows of a tile
 constexpr int kLine = 8;                      // 16-byte chunks of a k-tile's row
-constexpr int kStage = kTile * kLine;
 constexpr int kBufferFlags = 0x00020000;      // raw buffer, 32-bit data format
 constexpr uint32_t kPast = 0x80000000u;       // an offset past every buffer here
 
@@ -319,8 +333,8 @@ struct TileArgs {
   int64_t row_bytes;
   int64_t T;
   int N;
-  int m_tiles, n_tiles;
-  float* part;           // [S, T, Np] fp32 sums (router), or NULL: y
+  int m_tiles, n_tiles, parts;
+  float* part;           // [parts, T, Np] fp32 sums, or NULL: y
   int Np;
   void* y;               // [T, N]
   const int32_t* ids;    // adapters (NULL: none)
@@ -329,150 +343,173 @@ struct TileArgs {
   int A, R, Rq;
 };
 
+// A tile's shape: WM x WN waves of MS x NS blocks of 16 x 16, kStages k-tiles
+// of 128 bytes a row in LDS.
+template <int WM, int WN, int MS, int NS, int kStages_>
+struct Shape {
+  static constexpr int kWm = WM, kWn = WN, kMs = MS, kNs = NS, kStages = kStages_;
+  static constexpr int kM = 16 * WM * MS, kN = 16 * WN * NS;
+  static constexpr int kBlock = WM * WN * kWave;
+  // 1 KiB pieces (8 rows) of a stage that a wave loads
+  static constexpr int kXp = kM / 8 / (WM * WN), kWp = kN / 8 / (WM * WN);
+  static_assert(kXp * 8 * WM * WN == kM && kWp * 8 * WM * WN == kN, "whole pieces a wave");
+  static_assert((kStages - 2) * (kXp + kWp) <= 63, "vmcnt range");
+};
+
 typedef __attribute__((address_space(3))) void lds_ptr;
 
-// Two stages of a token half and a weight half each: distinct objects, so that
-// reads of one are not taken to wait for DMA into another. Row i of a stage
-// keeps its chunk c at c ^ (i & 7) ^ ((i >> 3) & 1): the 16 rows of a fragment
-// read lie in different banks.
-__shared__ u32x4 t_x0[kStage], t_w0[kStage], t_x1[kStage], t_w1[kStage];
-
 #if defined(__HIP_DEVICE_COMPILE__)
-template <int S>
-__device__ __forceinline__ u32x4* stage_x() { return S == 0 ? t_x0 : t_x1; }
-template <int S>
-__device__ __forceinline__ u32x4* stage_w() { return S == 0 ? t_w0 : t_w1; }
+// Stage S's token half and weight half: distinct objects, so that reads of one
+// are not taken to wait for DMA into another.
+template <typename C, int S>
+__device__ __forceinline__ u32x4* stage_x() {
+  __shared__ u32x4 lds[C::kM * kLine];
+  return lds;
+}
+template <typename C, int S>
+__device__ __forceinline__ u32x4* stage_w() {
+  __shared__ u32x4 lds[C::kN * kLine];
+  return lds;
+}
 
+template <typename C>
 struct TileLoad {
   __amdgpu_buffer_rsrc_t xr, wr;
-  uint32_t xo[4], wo[4];   // this lane's byte offsets in its four pieces; kPast: zeros
-  uint32_t chunk[2];       // the lane's byte in a k-tile's row, even and odd pieces
+  uint32_t xo[C::kXp], wo[C::kWp];   // this lane's byte offsets in its pieces; kPast: zeros
+  uint32_t xc[C::kXp], wc[C::kWp];   // its byte in the k-tile's row
   uint32_t row_bytes;
 };
 
-// Pieces of 8 rows x 128 bytes, 4 + 4 a wave. Rows past T or N and bytes past
-// the row are given an offset past the buffer, whose DMA writes zeros.
-template <int S>
-__device__ __forceinline__ void tile_dma(const TileLoad& l, int wave, int kt) {
-  const uint32_t k = static_cast<uint32_t>(kt) * 128;
+// k-tile kt into stage S. Row i of a stage keeps its chunk c at c ^ (i & 7) ^
+// ((i >> 3) & 1): the 16 rows of a fragment read lie in different banks. Rows
+// past T or N, bytes past the row and k-tiles from k1 on are given an offset
+// past the buffer, whose DMA writes zeros.
+template <typename C, int S>
+__device__ __forceinline__ void tile_dma(const TileLoad<C>& l, int wave, int kt, int k1) {
+  const uint32_t k = kt < k1 ? static_cast<uint32_t>(kt) * 128 : l.row_bytes;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t c = l.chunk[j & 1];
-    const bool in = k + c < l.row_bytes;
+  for (int j = 0; j < C::kXp; ++j)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        l.xr, (lds_ptr*)(stage_x<S>() + (wave * 4 + j) * 8 * kLine), 16,
-        in ? l.xo[j] + k : kPast, 0, 0, 0);
+        l.xr, (lds_ptr*)(stage_x<C, S>() + (wave * C::kXp + j) * 8 * kLine), 16,
+        k + l.xc[j] < l.row_bytes ? l.xo[j] + k : kPast, 0, 0, 0);
+#pragma unroll
+  for (int j = 0; j < C::kWp; ++j)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        l.wr, (lds_ptr*)(stage_w<S>() + (wave * 4 + j) * 8 * kLine), 16,
-        in ? l.wo[j] + k : kPast, 0, 0, 0);
-  }
+        l.wr, (lds_ptr*)(stage_w<C, S>() + (wave * C::kWp + j) * 8 * kLine), 16,
+        k + l.wc[j] < l.row_bytes ? l.wo[j] + k : kPast, 0, 0, 0);
 }
 
-template <bool kF32, int S>
-__device__ __forceinline__ void tile_mma(int wm, int wn, const int (&frag)[2], floatx4 (&acc)[4][4]) {
+template <bool kF32, typename C, int S>
+__device__ __forceinline__ void tile_mma(int wm, int wn, const int (&frag)[2],
+                                         floatx4 (&acc)[C::kMs][C::kNs]) {
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    u32x4 fx[4], fw[4];
+    u32x4 fx[C::kMs], fw[C::kNs];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      fx[i] = stage_x<S>()[(wm * 64 + i * 16) * kLine + frag[s]];
-      fw[i] = stage_w<S>()[(wn * 64 + i * 16) * kLine + frag[s]];
-    }
+    for (int i = 0; i < C::kMs; ++i)
+      fx[i] = stage_x<C, S>()[(wm * C::kMs + i) * 16 * kLine + frag[s]];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < C::kNs; ++j)
+      fw[j] = stage_w<C, S>()[(wn * C::kNs + j) * 16 * kLine + frag[s]];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = mma16<kF32>(fw[j], fx[i], acc[i][j]);
+    for (int i = 0; i < C::kMs; ++i)
+#pragma unroll
+      for (int j = 0; j < C::kNs; ++j) acc[i][j] = mma16<kF32>(fw[j], fx[i], acc[i][j]);
   }
 }
 
-__device__ __forceinline__ void dma_wait_barrier() {
-  __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) and lgkmcnt(0)
+// Step kt of the ring: its k-tile has landed once at most the DMA of the
+// kStages - 2 after it is in flight; after the barrier every wave has finished
+// with the k-tile before it, whose stage takes k-tile kt + kStages - 1.
+template <bool kF32, typename C, int S>
+__device__ __forceinline__ void tile_step(const TileLoad<C>& l, int wave, int wm, int wn, int kt,
+                                          int k1, const int (&frag)[2],
+                                          floatx4 (&acc)[C::kMs][C::kNs]) {
+  constexpr int kLeft = (C::kStages - 2) * (C::kXp + C::kWp);
+  // s_waitcnt: vmcnt(kLeft), lgkmcnt(0), no wait for exports
+  __builtin_amdgcn_s_waitcnt((kLeft & 15) | ((kLeft >> 4) << 14) | 0x70);
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+  tile_dma<C, (S + C::kStages - 1) % C::kStages>(l, wave, kt + C::kStages - 1, k1);
+  tile_mma<kF32, C, S>(wm, wn, frag, acc);
 }
-#endif  // __HIP_DEVICE_COMPILE__
 
-// Tile (m, n) over the k-tiles of part blockIdx.y. Each wave has a 64 x 64
-// quarter. kAdapt: the epilogue adds each token's adapter, v B^T, one different
-// adapter of a 16-token group after another.
-template <bool kF32, bool kAdapt>
-__global__ __launch_bounds__(kThreads) void linear_tile(TileArgs p) {
-#if defined(__HIP_DEVICE_COMPILE__)
+// Block `block` of m_tiles x n_tiles x parts: a tile over one part of the
+// reduction.
+template <bool kF32, typename C, bool kAdapt>
+__device__ __forceinline__ void tile_unit(const TileArgs& p, int block) {
   typedef typename Elem<kF32>::type E;
   constexpr int kC = Elem<kF32>::kChunk;
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 1, wn = wave & 1;
+  const int wm = wave / C::kWn, wn = wave % C::kWn;
   const int g = lane >> 4, r = lane & 15;
 
-  // blocks are dealt round-robin to the 8 XCDs: each XCD gets a run of the
-  // order (n fastest: a run shares tokens)
   const int total = p.m_tiles * p.n_tiles;
-  int pos = blockIdx.x;
-  const int per = gridDim.x >> 3;
-  pos = (pos & 7) * per + (pos >> 3);   // the grid is a multiple of 8
-  if (pos >= total) return;
+  const int s = block / total, pos = block % total;
   const int mt = pos / p.n_tiles, nt = pos % p.n_tiles;
-  const int64_t t0 = static_cast<int64_t>(mt) * kTile;
-  const int n0 = nt * kTile;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(kTile), p.T - t0));
-  const int cols = min(kTile, p.N - n0);
+  const int64_t t0 = static_cast<int64_t>(mt) * C::kM;
+  const int n0 = nt * C::kN;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(C::kM), p.T - t0));
+  const int cols = min(C::kN, p.N - n0);
 
   const int nkt = static_cast<int>((p.row_bytes + 127) >> 7);
-  const int S = gridDim.y, s = blockIdx.y;
-  const int k0 = static_cast<int>(static_cast<int64_t>(s) * nkt / S);
-  const int k1 = static_cast<int>(static_cast<int64_t>(s + 1) * nkt / S);
+  const int k0 = static_cast<int>(static_cast<int64_t>(s) * nkt / p.parts);
+  const int k1 = static_cast<int>(static_cast<int64_t>(s + 1) * nkt / p.parts);
 
-  TileLoad l;
+  TileLoad<C> l;
   l.row_bytes = static_cast<uint32_t>(p.row_bytes);
-  // 128 rows of at most 2^24 bytes: within the 2^31 that an offset reaches
+  // at most 128 (256) rows of 2^24 (2^23) bytes: within the 2^31 that an offset
+  // reaches
   l.xr = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p.x + t0 * p.row_bytes), 0,
                                            static_cast<int>(rows * l.row_bytes), kBufferFlags);
   l.wr = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<char*>(p.w + static_cast<int64_t>(n0) * p.row_bytes), 0,
       static_cast<int>(cols * l.row_bytes), kBufferFlags);
 #pragma unroll
-  for (int j = 0; j < 2; ++j) l.chunk[j] = ((lane & 7) ^ (lane >> 3) ^ j) * 16;
+  for (int j = 0; j < C::kXp; ++j) {
+    const int pc = wave * C::kXp + j, row = pc * 8 + (lane >> 3);
+    l.xc[j] = ((lane & 7) ^ (lane >> 3) ^ (pc & 1)) * 16;
+    l.xo[j] = row < rows ? row * l.row_bytes + l.xc[j] : kPast;
+  }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int row = (wave * 4 + j) * 8 + (lane >> 3);
-    l.xo[j] = row < rows ? row * l.row_bytes + l.chunk[j & 1] : kPast;
-    l.wo[j] = row < cols ? row * l.row_bytes + l.chunk[j & 1] : kPast;
+  for (int j = 0; j < C::kWp; ++j) {
+    const int pc = wave * C::kWp + j, row = pc * 8 + (lane >> 3);
+    l.wc[j] = ((lane & 7) ^ (lane >> 3) ^ (pc & 1)) * 16;
+    l.wo[j] = row < cols ? row * l.row_bytes + l.wc[j] : kPast;
   }
   int frag[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) frag[q] = r * kLine + ((4 * q + g) ^ (r & 7) ^ ((r >> 3) & 1));
 
-  floatx4 acc[4][4];
+  floatx4 acc[C::kMs][C::kNs];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < C::kMs; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = floatx4{0, 0, 0, 0};
+    for (int j = 0; j < C::kNs; ++j) acc[i][j] = floatx4{0, 0, 0, 0};
 
-  if (k0 < k1) tile_dma<0>(l, wave, k0);
-  int kt = k0;
-  for (; kt + 1 < k1; kt += 2) {
-    dma_wait_barrier();
-    tile_dma<1>(l, wave, kt + 1);
-    tile_mma<kF32, 0>(wm, wn, frag, acc);
-    dma_wait_barrier();
-    if (kt + 2 < k1) tile_dma<0>(l, wave, kt + 2);
-    tile_mma<kF32, 1>(wm, wn, frag, acc);
+  tile_dma<C, 0>(l, wave, k0, k1);
+  if constexpr (C::kStages > 2) tile_dma<C, 1>(l, wave, k0 + 1, k1);
+  if constexpr (C::kStages > 3) tile_dma<C, 2>(l, wave, k0 + 2, k1);
+  for (int kt = k0; kt < k1; kt += C::kStages) {
+    tile_step<kF32, C, 0>(l, wave, wm, wn, kt, k1, frag, acc);
+    if (kt + 1 < k1) tile_step<kF32, C, 1>(l, wave, wm, wn, kt + 1, k1, frag, acc);
+    if constexpr (C::kStages > 2)
+      if (kt + 2 < k1) tile_step<kF32, C, 2>(l, wave, wm, wn, kt + 2, k1, frag, acc);
+    if constexpr (C::kStages > 3)
+      if (kt + 3 < k1) tile_step<kF32, C, 3>(l, wave, wm, wn, kt + 3, k1, frag, acc);
   }
-  if (kt < k1) {
-    dma_wait_barrier();
-    tile_mma<kF32, 0>(wm, wn, frag, acc);
-  }
+  __builtin_amdgcn_s_waitcnt(0x0070);   // the DMA past the last k-tile
 
-  // lane (g, r): columns n0 + 64 wn + 16 j + 4 g .. + 3 of token 64 wm + 16 i + r
+  // lane (g, r): columns n0 + 16 (wn NS + j) + 4 g .. + 3 of token 16 (wm MS + i) + r
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int lt = wm * 64 + i * 16 + r;
-    const int64_t t = t0 + lt;
+  for (int i = 0; i < C::kMs; ++i) {
+    const int lt0 = (wm * C::kMs + i) * 16;
+    const int64_t t = t0 + lt0 + r;
     if constexpr (kAdapt) {
-      const int id = lt < rows ? p.ids[t] : -1;
+      const int id = lt0 + r < rows ? p.ids[t] : -1;
       uint32_t todo = static_cast<uint32_t>(__ballot(id >= 0 && id < p.A)) & 0xffffu;
       const bool vec = (p.R % kC) == 0;
       while (todo) {
@@ -480,16 +517,16 @@ __global__ __launch_bounds__(kThreads) void linear_tile(TileArgs p) {
         const int aid = __builtin_amdgcn_readlane(id, lead);
         const bool mine = id == aid;
         todo &= ~static_cast<uint32_t>(__ballot(mine));
-        const E* vrow = static_cast<const E*>(p.v) + (mine ? t : t0 + wm * 64 + i * 16 + lead) * p.Rq;
-        floatx4 d[4];
+        const E* vrow = static_cast<const E*>(p.v) + (mine ? t : t0 + lt0 + lead) * p.Rq;
+        floatx4 d[C::kNs];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) d[j] = floatx4{0, 0, 0, 0};
+        for (int j = 0; j < C::kNs; ++j) d[j] = floatx4{0, 0, 0, 0};
         for (int j0 = 0; j0 < p.R; j0 += 4 * kC) {
           const int k = j0 + g * kC;
           const u32x4 fv = load16(reinterpret_cast<const char*>(vrow + k));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int n = min(n0 + wn * 64 + j * 16 + r, p.N - 1);
+          for (int j = 0; j < C::kNs; ++j) {
+            const int n = min(n0 + (wn * C::kNs + j) * 16 + r, p.N - 1);
             const E* row = static_cast<const E*>(p.b) + (static_cast<int64_t>(aid) * p.N + n) * p.R;
             u32x4 fb = {0, 0, 0, 0};
             if (k < p.R)
@@ -500,14 +537,14 @@ __global__ __launch_bounds__(kThreads) void linear_tile(TileArgs p) {
         // added to its own tokens only: an adapter's infinities reach no other
         if (mine) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] += d[j];
+          for (int j = 0; j < C::kNs; ++j) acc[i][j] += d[j];
         }
       }
     }
-    if (lt >= rows) continue;
+    if (lt0 + r >= rows) continue;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + wn * 64 + j * 16 + 4 * g;
+    for (int j = 0; j < C::kNs; ++j) {
+      const int n = n0 + (wn * C::kNs + j) * 16 + 4 * g;
       if (n >= p.N) continue;
       if constexpr (kAdapt)
         store4<kF32>(static_cast<E*>(p.y) + t * p.N, n, p.N, (p.N & 3) == 0, acc[i][j]);
@@ -515,36 +552,83 @@ __global__ __launch_bounds__(kThreads) void linear_tile(TileArgs p) {
         *reinterpret_cast<floatx4*>(p.part + (s * p.T + t) * p.Np + n) = acc[i][j];
     }
   }
+}
 #endif  // __HIP_DEVICE_COMPILE__
+
+// kAdapt: the epilogue adds each token's adapter, v B^T, one different adapter
+// of a 16-token group after another, and writes y; otherwise fp32 parts.
+template <bool kF32, typename C, bool kAdapt>
+__global__ __launch_bounds__(C::kBlock) void linear_tile(TileArgs p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  // blocks are dealt round-robin to the 8 XCDs: each XCD gets a run of the
+  // order (weight tiles fastest: a run shares tokens); the grid is a multiple
+  // of 8
+  const int per = gridDim.x >> 3;
+  const int block = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if (block < p.m_tiles * p.n_tiles * p.parts) tile_unit<kF32, C, kAdapt>(p, block);
+#endif
 }
 
+// At most 16 tokens: block (tile, s) of the weight's and then the adapters'
+// tiles.
 template <bool kF32>
-hipError_t launch_stream(const StreamArgs& a, int tiles, int S, hipStream_t st) {
-  const dim3 grid(tiles, S);
-  if (a.T <= 16)
-    hipLaunchKernelGGL((stream_partial<kF32, 1>), grid, dim3(kThreads), 0, st, a);
-  else if (a.T <= 32)
-    hipLaunchKernelGGL((stream_partial<kF32, 2>), grid, dim3(kThreads), 0, st, a);
+__global__ __launch_bounds__(kThreads) void stream_partial(StreamArgs p) {
+  const int64_t z = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
+  if (z < p.n_zero) p.zero[z] = 0;
+  __shared__ floatx4 red[kWaves * kWave];
+  stream_unit<kF32, 1>(p, blockIdx.x, blockIdx.y, gridDim.y, red);
+}
+
+// 17 to 64 tokens: blocks below `tiles` are weight tiles of 64 tokens x 128
+// rows (every token beside each weight byte, so that x is read once a tile and
+// not once for 16 rows), the others units of the adapters' low-rank products.
+typedef Shape<1, 4, 4, 2, 3> FewShape;
+template <bool kF32>
+__global__ __launch_bounds__(kThreads) void few_linear(TileArgs p, StreamArgs q, int tiles) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const int b = blockIdx.x;
+  const int64_t z = static_cast<int64_t>(b) * kThreads + threadIdx.x;
+  if (z < q.n_zero) q.zero[z] = 0;
+  // (the units' sums meet in the tiles' LDS: two blocks fit a CU)
+  static_assert(sizeof(u32x4) * FewShape::kN * kLine >= sizeof(floatx4) * kWaves * 4 * kWave, "");
+  if (b < tiles)
+    tile_unit<kF32, FewShape, false>(p, b);
   else
-    hipLaunchKernelGGL((stream_partial<kF32, 4>), grid, dim3(kThreads), 0, st, a);
+    stream_unit<kF32, 4>(q, (b - tiles) / p.parts, (b - tiles) % p.parts, p.parts,
+                         reinterpret_cast<floatx4*>(stage_w<FewShape, 0>()));
+#endif
+}
+
+typedef Shape<2, 2, 2, 2, 4> SmallShape;   // 64 x 64
+typedef Shape<2, 2, 4, 4, 2> MidShape;     // 128 x 128
+typedef Shape<2, 4, 4, 4, 3> WideShape;    // 128 x 256, eight waves
+
+template <bool kF32, typename C, bool kAdapt>
+hipError_t launch_tile(TileArgs a, hipStream_t st) {
+  a.m_tiles = static_cast<int>(cdiv(a.T, C::kM));
+  a.n_tiles = static_cast<int>(cdiv(a.N, C::kN));
+  const int64_t total = static_cast<int64_t>(a.m_tiles) * a.n_tiles * a.parts;
+  hipLaunchKernelGGL((linear_tile<kF32, C, kAdapt>), dim3(static_cast<unsigned>(cdiv(total, 8) * 8)),
+                     dim3(C::kBlock), 0, st, a);
   return hipGetLastError();
 }
 
-template <bool kF32, bool kAdapt>
-hipError_t launch_tile(const TileArgs& a, int S, hipStream_t st) {
-  const int64_t total = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
-  hipLaunchKernelGGL((linear_tile<kF32, kAdapt>), dim3(static_cast<unsigned>(cdiv(total, 8) * 8), S),
-                     dim3(kThreads), 0, st, a);
-  return hipGetLastError();
+// Parts of the reduction for n tiles of `ksteps` steps: enough for two blocks
+// a CU, at least `least` steps each.
+int parts_for(int64_t n, int64_t ksteps, int64_t least, int64_t most) {
+  int64_t want = cdiv(2 * static_cast<int64_t>(kPlanCus), n);
+  if (want > ksteps / least) want = ksteps / least;
+  if (want > most) want = most;
+  return static_cast<int>(want < 1 ? 1 : want);
 }
 
-// Parts of the reduction for `tiles` tiles of a few tokens: about two blocks a
-// CU, and four 64-byte blocks for each of a part's waves.
+// At most 16 tokens: one batch of loads for each of a part's waves, or a few
+// where that already gives four blocks a CU.
 int stream_parts(int64_t tiles, int64_t row_bytes) {
-  const int64_t want = cdiv(2 * static_cast<int64_t>(kPlanCus), tiles);
-  const int64_t most = cdiv(row_bytes, 64) / (4 * kWaves);
-  return static_cast<int>(want < 1 || most < 1 ? 1 : want < most ? (want < 16 ? want : 16)
-                                                                 : (most < 16 ? most : 16));
+  const int64_t batches = cdiv(cdiv(row_bytes, 64), kU * kWaves);
+  int64_t each = 1;
+  while (each < batches && tiles * cdiv(batches, each + 1) >= 4 * kPlanCus) ++each;
+  return static_cast<int>(cdiv(batches, each));
 }
 
 int64_t up16(int64_t v) { return cdiv(v, 16) * 16; }
@@ -553,18 +637,28 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 }  // namespace
 
 // ---- the router's logits --------------------------------------------------
+namespace {
+// Shapes of the logits' tiles: 128 x 256 where that leaves a tile for every
+// fourth CU or more, so that four parts fill them all; else 64 x 64.
+bool wide_logits(int64_t T, int64_t row_bytes, int N) {
+  return N > 128 && row_bytes <= (int64_t{1} << 23) &&
+         cdiv(T, WideShape::kM) * cdiv(N, WideShape::kN) >= kPlanCus / 4;
+}
+}  // namespace
+
 LogitsLayout logits_layout(int64_t T, int64_t H, int N, bool f32) {
   LogitsLayout L{};
-  const int64_t row_bytes = H * (f32 ? 4 : 2);
+  const int64_t row_bytes = H * (f32 ? 4 : 2), ktiles = cdiv(row_bytes, 128);
   L.pitch = static_cast<int>(up16(N));
-  if (T <= kFewTokens) {
+  if (T <= 16)
     L.parts = stream_parts(cdiv(N, 16), row_bytes);
-  } else {
-    const int64_t tiles = cdiv(T, kTile) * cdiv(N, kTile);
-    const int64_t want = cdiv(2 * static_cast<int64_t>(kPlanCus), tiles), most = cdiv(row_bytes, 128) / 8;
-    L.parts = static_cast<int>(want < 1 || most < 1 ? 1 : want < most ? (want < 8 ? want : 8)
-                                                                      : (most < 8 ? most : 8));
-  }
+  else if (T <= kFewTokens)
+    L.parts = parts_for(cdiv(N, FewShape::kN), ktiles, 3, 16);
+  else if (wide_logits(T, row_bytes, N))
+    // one block of these a CU
+    L.parts = parts_for(2 * cdiv(T, WideShape::kM) * cdiv(N, WideShape::kN), ktiles, 6, 4);
+  else
+    L.parts = parts_for(cdiv(T, SmallShape::kM) * cdiv(N, SmallShape::kN), ktiles, 4, 16);
   L.bytes = up256(sizeof(float) * static_cast<size_t>(L.parts) * T * L.pitch);
   return L;
 }
@@ -573,32 +667,42 @@ hipError_t logits(int64_t T, int64_t H, int N, bool f32, const void* x, const vo
                   uint32_t* zero, int n_zero, hipStream_t st) {
   const LogitsLayout L = logits_layout(T, H, N, f32);
   const int64_t row_bytes = H * (f32 ? 4 : 2);
-  if (T <= kFewTokens) {
-    StreamArgs a{};
-    a.x = static_cast<const char*>(x);
-    a.w = static_cast<const char*>(w);
-    a.part = part;
-    a.row_bytes = row_bytes;
-    a.T = static_cast<int>(T);
-    a.N = N;
-    a.Np = L.pitch;
-    a.tiles = static_cast<int>(cdiv(N, 16));
-    a.zero = zero;
-    a.n_zero = n_zero;
-    return f32 ? launch_stream<true>(a, a.tiles, L.parts, st)
-               : launch_stream<false>(a, a.tiles, L.parts, st);
-  }
-  TileArgs a{};
+  StreamArgs a{};
   a.x = static_cast<const char*>(x);
   a.w = static_cast<const char*>(w);
-  a.row_bytes = row_bytes;
-  a.T = T;
-  a.N = N;
-  a.m_tiles = static_cast<int>(cdiv(T, kTile));
-  a.n_tiles = static_cast<int>(cdiv(N, kTile));
   a.part = part;
+  a.row_bytes = row_bytes;
+  a.T = static_cast<int>(T);
+  a.N = N;
   a.Np = L.pitch;
-  return f32 ? launch_tile<true, false>(a, L.parts, st) : launch_tile<false, false>(a, L.parts, st);
+  a.tiles = static_cast<int>(cdiv(N, 16));
+  a.zero = zero;
+  a.n_zero = n_zero;
+  if (T <= 16) {
+    if (f32) hipLaunchKernelGGL(stream_partial<true>, dim3(a.tiles, L.parts), dim3(kThreads), 0, st, a);
+    else hipLaunchKernelGGL(stream_partial<false>, dim3(a.tiles, L.parts), dim3(kThreads), 0, st, a);
+    return hipGetLastError();
+  }
+  TileArgs t{};
+  t.x = a.x;
+  t.w = a.w;
+  t.row_bytes = row_bytes;
+  t.T = T;
+  t.N = N;
+  t.part = part;
+  t.Np = L.pitch;
+  t.parts = L.parts;
+  if (T <= kFewTokens) {
+    t.m_tiles = 1;
+    t.n_tiles = static_cast<int>(cdiv(N, FewShape::kN));
+    const int tiles = t.n_tiles * t.parts;
+    if (f32) hipLaunchKernelGGL(few_linear<true>, dim3(tiles), dim3(kThreads), 0, st, t, a, tiles);
+    else hipLaunchKernelGGL(few_linear<false>, dim3(tiles), dim3(kThreads), 0, st, t, a, tiles);
+    return hipGetLastError();
+  }
+  if (wide_logits(T, row_bytes, N))
+    return f32 ? launch_tile<true, WideShape, false>(t, st) : launch_tile<false, WideShape, false>(t, st);
+  return f32 ? launch_tile<true, SmallShape, false>(t, st) : launch_tile<false, SmallShape, false>(t, st);
 }
 
 // ---- the shared projection with adapters ------------------------------------
@@ -615,7 +719,8 @@ AdapterLayout adapter_layout(const tr_adapter_desc& d) {
   L.Rp = static_cast<int>(up16(d.R));
   L.Rq = static_cast<int>(f32 ? up16(d.R) : cdiv(d.R, 32) * 32);
   if (d.T <= kFewTokens) {
-    L.parts = stream_parts(cdiv(d.N, 16), row_bytes);
+    L.parts = d.T <= 16 ? stream_parts(cdiv(d.N, 16), row_bytes)
+                        : parts_for(cdiv(d.N, FewShape::kN), cdiv(row_bytes, 128), 3, 16);
     L.vpart = up256(sizeof(float) * static_cast<size_t>(L.parts) * d.T * L.Np);
     L.total = L.vpart + up256(sizeof(float) * static_cast<size_t>(L.parts) * d.T * L.Rp);
   } else {
@@ -653,9 +758,29 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
     s.Rp = L.Rp;
     s.rank_tiles = L.Rp / 16;
     const int slots = static_cast<int>(d.T < d.A ? d.T : d.A);
-    const int tiles = s.tiles + slots * s.rank_tiles;
-    e = f32 ? launch_stream<true>(s, tiles, L.parts, st) : launch_stream<false>(s, tiles, L.parts, st);
-    if (e != hipSuccess) return e;
+    if (d.T <= 16) {
+      const dim3 grid(s.tiles + slots * s.rank_tiles, L.parts);
+      if (f32) hipLaunchKernelGGL(stream_partial<true>, grid, dim3(kThreads), 0, st, s);
+      else hipLaunchKernelGGL(stream_partial<false>, grid, dim3(kThreads), 0, st, s);
+    } else {
+      TileArgs t{};
+      t.x = s.x;
+      t.w = s.w;
+      t.row_bytes = row_bytes;
+      t.T = d.T;
+      t.N = s.N;
+      t.part = s.part;
+      t.Np = L.Np;
+      t.parts = L.parts;
+      t.m_tiles = 1;
+      t.n_tiles = static_cast<int>(cdiv(d.N, FewShape::kN));
+      s.tiles = 0;   // its units: the adapters' only
+      const int tiles = t.n_tiles * t.parts;
+      const int units = tiles + slots * s.rank_tiles * t.parts;
+      if (f32) hipLaunchKernelGGL(few_linear<true>, dim3(units), dim3(kThreads), 0, st, t, s, tiles);
+      else hipLaunchKernelGGL(few_linear<false>, dim3(units), dim3(kThreads), 0, st, t, s, tiles);
+    }
+    if ((e = hipGetLastError()) != hipSuccess) return e;
     ExpandArgs p{};
     p.part = s.part;
     p.vpart = s.vpart;
@@ -696,8 +821,7 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
   t.row_bytes = row_bytes;
   t.T = d.T;
   t.N = static_cast<int>(d.N);
-  t.m_tiles = static_cast<int>(cdiv(d.T, kTile));
-  t.n_tiles = static_cast<int>(cdiv(d.N, kTile));
+  t.parts = 1;
   t.y = y;
   t.ids = ids;
   t.v = ws;
@@ -705,7 +829,9 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
   t.A = d.A;
   t.R = d.R;
   t.Rq = L.Rq;
-  return f32 ? launch_tile<true, true>(t, 1, st) : launch_tile<false, true>(t, 1, st);
+  if (cdiv(d.T, MidShape::kM) * cdiv(d.N, MidShape::kN) >= kPlanCus)
+    return f32 ? launch_tile<true, MidShape, true>(t, st) : launch_tile<false, MidShape, true>(t, st);
+  return f32 ? launch_tile<true, SmallShape, true>(t, st) : launch_tile<false, SmallShape, true>(t, st);
 }
 
 }  // namespace tr

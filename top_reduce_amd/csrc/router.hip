@@ -12,6 +12,8 @@
 // below everything, so that every row yields K different valid ids. Each of
 // the K rounds reduces one integer over the lanes. Bound: latency of the
 // rounds for one token, the logits' bytes for many.
+#include <type_traits>
+
 #include "tr_chunk.h"
 #include "tr_internal.h"
 
@@ -46,15 +48,32 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+// Reductions over the 64 lanes by row operations: lanes swapped within rows of
+// 16 by DPP, then rows 0 and 2 into 1 and 3 and row 1 into 3; lane 63 holds the
+// result. A round of the selection waits for this chain.
+template <typename F>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, uint32_t neutral, F op) {
+  auto dpp = [&](auto ctrl, auto rows) {
+    v = op(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(
+                  static_cast<int>(neutral), static_cast<int>(v), decltype(ctrl)::value,
+                  decltype(rows)::value, 0xf, false)));
+  };
+  using All = std::integral_constant<int, 0xf>;
+  dpp(std::integral_constant<int, 0xb1>{}, All{});    // lanes 1 0 3 2
+  dpp(std::integral_constant<int, 0x4e>{}, All{});    // lanes 2 3 0 1
+  dpp(std::integral_constant<int, 0x141>{}, All{});   // mirrored in 8 lanes
+  dpp(std::integral_constant<int, 0x140>{}, All{});   // mirrored in 16 lanes
+  dpp(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xa>{});
+  dpp(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xc>{});
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
+}
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) v = max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), d, kWave)));
-  return v;
+  return wave_reduce(v, 0u, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) v += __shfl_xor(v, d, kWave);
-  return v;
+  return __uint_as_float(wave_reduce(__float_as_uint(v), 0u, [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
 }
 
 // NR registers of logits a lane: G <= 64 NR.
@@ -63,90 +82,100 @@ __global__ __launch_bounds__(kThreads) void route_select(SelectArgs a) {
   const int lane = threadIdx.x & 63;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 6) + (threadIdx.x >> 6);
   if (t >= a.T) return;
-  float p[NR];
+  // v: the logits, and with a bias (which needs every score) the scores
+  float v[NR];
   uint32_t key[NR];
 #pragma unroll
-  for (int i = 0; i < NR; ++i) p[i] = 0.0f;
-  for (int s = 0; s < a.S; ++s) {
-    const float* row = a.part + (s * a.T + t) * a.pitch;
+  for (int i = 0; i < NR; ++i) v[i] = 0.0f;
+  {
+    // four parts' loads at a time, unconditional (indices clamped into the
+    // row) so that all go out before the first wait
+    constexpr int kB = NR <= 4 ? 4 : NR <= 16 ? 2 : 1;
+    int col[NR];
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      const int e = i * kWave + lane;
-      if (e < a.G) p[i] += row[e];
+    for (int i = 0; i < NR; ++i) col[i] = min(i * kWave + lane, a.G - 1);
+    for (int s0 = 0; s0 < a.S; s0 += kB) {
+      float ld[kB][NR];
+#pragma unroll
+      for (int b = 0; b < kB; ++b) {
+        const float* row = a.part + (min(s0 + b, a.S - 1) * a.T + t) * a.pitch;
+#pragma unroll
+        for (int i = 0; i < NR; ++i) ld[b][i] = row[col[i]];
+      }
+#pragma unroll
+      for (int b = 0; b < kB; ++b)
+        if (s0 + b < a.S) {
+#pragma unroll
+          for (int i = 0; i < NR; ++i) v[i] += ld[b][i];
+        }
     }
   }
-  // the logits' keys; the largest logit (of those that are numbers)
-  uint32_t best = kUsed;
 #pragma unroll
-  for (int i = 0; i < NR; ++i) {
-    key[i] = i * kWave + lane < a.G ? order_key(p[i]) : kUsed;
-    best = max(best, key[i]);
-  }
-  // scores
-  if (a.sigmoid) {
+  for (int i = 0; i < NR; ++i) key[i] = i * kWave + lane < a.G ? order_key(v[i]) : kUsed;
+  float m = 0.0f, sum = 1.0f;
+  if (!a.sigmoid) {
+    // the largest logit (of those that are numbers), the sum of exp
+    uint32_t best = kUsed;
 #pragma unroll
-    for (int i = 0; i < NR; ++i) p[i] = 1.0f / (1.0f + expf(-p[i]));
-  } else {
+    for (int i = 0; i < NR; ++i) best = max(best, key[i]);
     const uint32_t mk = wave_max(best);
-    const float m = __uint_as_float((mk & 0x80000000u) ? mk & 0x7fffffffu : ~mk);
-    float sum = 0.0f;
+    m = __uint_as_float((mk & 0x80000000u) ? mk & 0x7fffffffu : ~mk);
+    sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      p[i] = i * kWave + lane < a.G ? expf(p[i] - m) : 0.0f;
-      sum += p[i];
-    }
+    for (int i = 0; i < NR; ++i) sum += i * kWave + lane < a.G ? expf(v[i] - m) : 0.0f;
     sum = wave_sum(sum);
-#pragma unroll
-    for (int i = 0; i < NR; ++i) p[i] /= sum;
   }
+  auto score = [&](float l) { return a.sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - m) / sum; };
   if (a.bias) {
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
       const int e = i * kWave + lane;
-      if (e < a.G) key[i] = order_key(p[i] + a.bias[e]);
+      v[i] = score(v[i]);
+      if (e < a.G) key[i] = order_key(v[i] + a.bias[e]);
     }
   }
 
-  // K rounds; lane k keeps the k-th expert and its score
+  // K rounds; lane k keeps the k-th expert and its value. Every lane offers its
+  // largest key (the lowest register among equals).
   int my_e = 0;
-  float my_p = 0.0f;
+  float my_v = 0.0f;
   for (int k = 0; k < a.K; ++k) {
-    uint32_t lb = kUsed;
+    uint32_t lb = key[0];
     int li = 0;
+    float lv = v[0];
 #pragma unroll
-    for (int i = 0; i < NR; ++i)
-      if (key[i] > lb) { lb = key[i]; li = i; }
-    const uint32_t top = wave_max(lb);
-    // the lowest id among the lanes that hold the largest key
-    uint32_t cand = lb == top ? ~static_cast<uint32_t>(li * kWave + lane) : 0u;
-    uint64_t hit = __ballot(lb == top);
-    int e;
-    if (__popcll(hit) == 1) {
-      const int l = __ffsll(static_cast<unsigned long long>(hit)) - 1;
-      e = __builtin_amdgcn_readlane(li, l) * kWave + l;
-    } else {
-      e = static_cast<int>(~wave_max(cand));
-    }
-    const int owner = e & 63, reg = e >> 6;
-    float pe = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-      if (i == reg) {
-        pe = p[i];
-        if (lane == owner) key[i] = kUsed;
+    for (int i = 1; i < NR; ++i)
+      if (key[i] > lb) {
+        lb = key[i];
+        li = i;
+        lv = v[i];
       }
-    pe = __shfl(pe, owner, kWave);
+    const uint32_t top = wave_max(lb);
+    const uint64_t hit = __ballot(lb == top);
+    int owner = __ffsll(static_cast<unsigned long long>(hit)) - 1;
+    if (hit & (hit - 1)) {
+      // several lanes: the lowest id among them
+      const uint32_t e = ~wave_max(lb == top ? ~static_cast<uint32_t>(li * kWave + lane) : 0u);
+      owner = static_cast<int>(e & 63);
+    }
+    const int e = __builtin_amdgcn_readlane(li, owner) * kWave + owner;
+    const float ev = __uint_as_float(static_cast<uint32_t>(
+        __builtin_amdgcn_readlane(static_cast<int>(__float_as_uint(lv)), owner)));
     if (lane == k) {
       my_e = e;
-      my_p = pe;
+      my_v = ev;
     }
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+      if (lane == owner && i == li) key[i] = kUsed;
   }
+  const float my_p = a.bias ? my_v : score(my_v);
   float w = my_p;
   if (a.renorm) {
-    const float sum = wave_sum(lane < a.K ? my_p : 0.0f);
+    const float all = wave_sum(lane < a.K ? my_p : 0.0f);
     // a sum below the smallest normal float (all scores 0) divides by that
     // instead: weights 0, not NaN
-    w = my_p / (sum < 1.17549435e-38f ? 1.17549435e-38f : sum);
+    w = my_p / (all < 1.17549435e-38f ? 1.17549435e-38f : all);
   }
   w *= a.scale;
   if (lane < a.K) {
