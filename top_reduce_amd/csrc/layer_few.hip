@@ -1,15 +1,16 @@
 // The local experts of a mixture-of-experts layer for at most 64 tokens, from
 // the router's choice to the output, in two launches:
 //
-//   few_up:    h[t, k] = w[t, k] silu(W1g[e] x[t]) * (W1u[e] x[t])   e = idx[t, k]
-//   few_down:  y[t]    = sum over the token's local experts e: W2[e] h[t, k(e)]
+//   few_up:    h[t, e] = w[t, e] silu(W1g[e] x[t]) * (W1u[e] x[t])
+//   few_down:  y[t]    = sum over the token's local experts e: W2[e] h[t, e]
 //
 // Bound: reading the weights of the experts that some token chose, once. The
-// tokens of an expert are a 64-bit mask, so there is no expanded row order and
-// no route scan: in few_up the tokens ride in MFMA columns in groups of 16
-// (groups without a token of the expert are skipped), and few_down adds a
-// column's sum over an expert to the token's total where the token chose it,
-// experts ascending, so that the weighted sum over experts stays in registers.
+// tokens of an expert are a 64-bit mask, so there is no route scan and no
+// expanded copy of x: 16 of an expert's tokens (in most decode batches all of
+// them) are the columns of one MFMA operand, weight rows go from memory into
+// the other, and a row of h has its place by the expert's tokens before it.
+// Both kernels keep two batches of loads per wave, one in flight while the
+// other's products run, with a batch small enough that 16 waves fit a CU.
 //
 // The gate weight is folded into h. bf16: h is kept as two bf16 numbers whose
 // sum has 16 significant bits, and few_down multiplies both; the MFMA units
@@ -23,7 +24,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kU = 8;   // 64-byte k-blocks of one batch of loads
+constexpr int kDownThreads = 256;
+constexpr int kDownWaves = kDownThreads / kWave;
+constexpr int kU = 4;   // 64-byte k-blocks of one batch of loads
+// groups of 16 tokens of an expert: one for each expert with a token, and one
+// more for every 16 routes at most
+constexpr int kMaxGroups = kMaxE + kFewTokens * kMaxK / 16;
 
 struct FewArgs {
   const char* x;                     // [T, H]
@@ -32,17 +38,24 @@ struct FewArgs {
   const unsigned long long* masks;   // [E] tokens of each local expert
   const uint8_t* slots;              // [E, 64] slot of token t that names expert e
   const float* w;                    // [T, K] gate weights
-  char* h;                           // [T * K][parts][Ip]
+  char* h;                           // [routes][parts][Ip]
   void* y;                           // [T, H]
   int T, K, E;
   int64_t H, I, Ip;
 };
 
-// The experts with a token, in ascending order, in LDS; returns how many.
+// Groups in LDS, experts ascending.
+struct Groups {
+  uint64_t mask[kMaxGroups];   // the expert's tokens
+  int expert[kMaxGroups];
+  int row[kMaxGroups];         // row of h of the group's first token
+  int rank[kMaxGroups];        // that token's rank among the expert's
+};
+
+// Fills `s`; returns the number of groups. tmp: LDS of kBlock / 64 ints.
 template <int kBlock>
-__device__ __forceinline__ int active_experts(const FewArgs& a, int* list, uint64_t* mask_s,
-                                              int* tmp) {
-  constexpr int kPer = kMaxE / kBlock;
+__device__ __forceinline__ int find_groups(const FewArgs& a, Groups& s, int* tmp) {
+  constexpr int kPer = (kMaxE + kBlock - 1) / kBlock;
   const int per = (a.E + kBlock - 1) / kBlock;
   uint64_t m[kPer];
 #pragma unroll
@@ -50,116 +63,159 @@ __device__ __forceinline__ int active_experts(const FewArgs& a, int* list, uint6
     const int e = static_cast<int>(threadIdx.x) * per + j;
     m[j] = j < per && e < a.E ? a.masks[e] : 0;
   }
+  // routes and groups of the experts before: one scan of both (at most 2048
+  // routes and 1152 groups)
   int n = 0, total = 0;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) n += m[j] != 0;
+  for (int j = 0; j < kPer; ++j) {
+    const int c = __popcll(m[j]);
+    n += c | ((c + 15) / 16) << 16;
+  }
   int at = block_exclusive_scan<kBlock>(n, tmp, &total);
+  int row = at & 0xffff, g = at >> 16;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    if (m[j]) {
-      list[at] = static_cast<int>(threadIdx.x) * per + j;
-      mask_s[at] = m[j];
-      ++at;
+  for (int j = 0; j < kPer; ++j) {
+    const int c = __popcll(m[j]);
+    for (int k = 0; k < c; k += 16) {
+      s.mask[g] = m[j];
+      s.expert[g] = static_cast<int>(threadIdx.x) * per + j;
+      s.row[g] = row + k;
+      s.rank[g] = k;
+      ++g;
     }
+    row += c;
+  }
   __syncthreads();
-  return total;
+  return total >> 16;
 }
 
-// A unit: 16 gate rows and the matching 16 up rows of one expert, the
+// Lane l's token: the one of rank `rank` + l % 16 in `mask` (for ranks past the
+// last, the group's first token). mask and rank are the same in every lane.
+__device__ __forceinline__ int group_token(uint64_t mask, int rank, int n) {
+  const int lane = lane_id();
+  // lane t of the mask sends t to the lane of its rank
+  const int to = (mask >> lane) & 1 ? popc_below(mask) : 63;
+  int by_rank = __builtin_amdgcn_ds_permute(to * 4, lane);
+  // (64 tokens: lane 63 is its own rank; fewer: what lane 63 gets is not used)
+  const int r = lane & 15;
+  return __shfl(by_rank, rank + (r < n ? r : 0), kWave);
+}
+
+// A unit: 16 gate rows and the matching 16 up rows of one group's expert, the
 // reduction over the block's waves.
-template <bool kF32, int NQ>
-__global__ __launch_bounds__(kThreads) void few_up(FewArgs a) {
-  __shared__ int list[kMaxE];
-  __shared__ uint64_t mask_s[kMaxE];
+template <bool kF32>
+__global__ __launch_bounds__(kThreads, 3) void few_up(FewArgs a) {
+  __shared__ Groups s;
   __shared__ int tmp[kWaves];
-  __shared__ floatx4 red[kWaves][NQ][2][kWave];
-  const int n_act = active_experts<kThreads>(a, list, mask_s, tmp);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ floatx4 red[kWaves][2][kWave];
+  const int n_groups = find_groups<kThreads>(a, s, tmp);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int g = lane >> 4, r = lane & 15;
   const int upe = static_cast<int>(a.Ip / 16);
-  const int total = n_act * upe;
+  const int total = n_groups * upe;
   const int64_t row_bytes = a.H * Elem<kF32>::kBytes;
   const int nkb = static_cast<int>((row_bytes + 63) >> 6), nfull = static_cast<int>(row_bytes >> 6);
   const int kb0 = wave * nkb / kWaves, kb1 = (wave + 1) * nkb / kWaves;
   const int kbf = min(kb1, nfull);
   for (int u = blockIdx.x; u < total; u += gridDim.x) {
     const int q = u / upe, c = u % upe;
-    const int e = list[q];
-    const uint64_t mask = mask_s[q];
-    const int first = __ffsll(static_cast<unsigned long long>(mask)) - 1;
-    const int64_t col = min(static_cast<int64_t>(c * 16 + r), a.I - 1);
-    const char* wg = static_cast<const char*>(a.w1) + (2 * e * a.I + col) * row_bytes + g * 16;
+    const int e = __builtin_amdgcn_readfirstlane(s.expert[q]);
+    const uint64_t mask = s.mask[q];
+    const int rank = s.rank[q];
+    const int n = min(16, __popcll(mask) - rank);   // tokens of the group
+    const int t = group_token(mask, rank, n);
+    // addresses: a start that is the same for the wave, 32-bit offsets in it.
+    // Rows past I (the last units fill h up to Ip with zeros) read the last row.
+    const int64_t c0 = min(static_cast<int64_t>(c * 16), a.I - 1);
+    const char* wg = static_cast<const char*>(a.w1) + (2 * e * a.I + c0) * row_bytes;
     const char* wu = wg + a.I * row_bytes;
-    const char* xp[NQ];
-    bool on[NQ];
-    floatx4 ag[NQ], au[NQ];
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      const int t = i * 16 + r;
-      on[i] = (mask >> (16 * i)) & 0xffff;
-      xp[i] = a.x + ((mask >> t) & 1 ? t : first) * row_bytes + g * 16;
-      ag[i] = au[i] = floatx4{0, 0, 0, 0};
-    }
-    // Batches of kU blocks. A share's last batch may be short: its loads
-    // re-read the last whole block and the products are skipped.
-    for (int kb = kb0; kb < kbf; kb += kU) {
-      u32x4 vg[kU], vu[kU];
+    const uint32_t wo = static_cast<uint32_t>(min(static_cast<int64_t>(r), a.I - 1 - c0)) *
+                            static_cast<uint32_t>(row_bytes) + g * 16;
+    const uint32_t xo = static_cast<uint32_t>(t) * static_cast<uint32_t>(row_bytes) + g * 16;
+    floatx4 ag = {0, 0, 0, 0}, au = {0, 0, 0, 0};
+
+    struct Batch {
+      u32x4 wg[kU], wu[kU], x[kU];
+    } b0, b1;
+    // a share's last batch starts early enough to end with it; the products of
+    // blocks that it reads again are skipped
+    auto start = [&](int kb) { return min(kb, max(kbf - kU, 0)); };
+    auto load = [&](Batch& b, int kb) {
+      const uint32_t k = static_cast<uint32_t>(start(kb)) * 64;
 #pragma unroll
       for (int j = 0; j < kU; ++j) {
-        vg[j] = load16(wg + min(kb + j, kbf - 1) * 64);
-        vu[j] = load16(wu + min(kb + j, kbf - 1) * 64);
+        b.wg[j] = load16(wg + (wo + k) + j * 64);
+        b.wu[j] = load16(wu + (wo + k) + j * 64);
+        b.x[j] = load16(a.x + (xo + k) + j * 64);
       }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto mma = [&](const Batch& b, int kb) {
+      const int k = start(kb);
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        if (NQ > 1 && !on[i]) continue;
-        u32x4 xb[kU];
-#pragma unroll
-        for (int j = 0; j < kU; ++j) xb[j] = load16(xp[i] + min(kb + j, kbf - 1) * 64);
-        // every load of the batch is out before the first product
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int j = 0; j < kU; ++j)
-          if (kb + j < kbf) {
-            ag[i] = mma16<kF32>(vg[j], xb[j], ag[i]);
-            au[i] = mma16<kF32>(vu[j], xb[j], au[i]);
-          }
+      for (int j = 0; j < kU; ++j)
+        if (k + j >= kb && k + j < kbf) {
+          ag = mma16<kF32>(b.wg[j], b.x[j], ag);
+          au = mma16<kF32>(b.wu[j], b.x[j], au);
+        }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    if (nfull >= kU) {
+      // (no load below is under a condition inside the loop: a load that may not
+      // have been made would turn the waits for the batch before it into waits
+      // for everything)
+      if (kb0 < kbf) {
+        load(b0, kb0);
+        int kb = kb0;
+        for (; kb + 2 * kU < kbf; kb += 2 * kU) {
+          load(b1, kb + kU);
+          mma(b0, kb);
+          load(b0, kb + 2 * kU);
+          mma(b1, kb + kU);
+        }
+        if (kb + kU < kbf) {
+          load(b1, kb + kU);
+          mma(b0, kb);
+          mma(b1, kb + kU);
+        } else {
+          mma(b0, kb);
+        }
+      }
+    } else {   // rows of fewer blocks than a batch has
+      for (int kb = kb0; kb < kbf; ++kb) {
+        const u32x4 vx = load16(a.x + xo + kb * 64);
+        ag = mma16<kF32>(load16(wg + wo + kb * 64), vx, ag);
+        au = mma16<kF32>(load16(wu + wo + kb * 64), vx, au);
       }
     }
     if (kb1 > nfull) {   // the short block at the end of the rows
       const bool in = nfull * 64 + g * 16 < row_bytes;
       const u32x4 z = {0, 0, 0, 0};
-      const u32x4 vg = in ? load16(wg + nfull * 64) : z, vu = in ? load16(wu + nfull * 64) : z;
-#pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        if (!on[i]) continue;
-        const u32x4 xb = in ? load16(xp[i] + nfull * 64) : z;
-        ag[i] = mma16<kF32>(vg, xb, ag[i]);
-        au[i] = mma16<kF32>(vu, xb, au[i]);
-      }
+      const u32x4 vg = in ? load16(wg + wo + nfull * 64) : z;
+      const u32x4 vu = in ? load16(wu + wo + nfull * 64) : z;
+      const u32x4 vx = in ? load16(a.x + xo + nfull * 64) : z;
+      ag = mma16<kF32>(vg, vx, ag);
+      au = mma16<kF32>(vu, vx, au);
     }
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      red[wave][i][0][lane] = ag[i];
-      red[wave][i][1][lane] = au[i];
-    }
+    red[wave][0][lane] = ag;
+    red[wave][1][lane] = au;
     __syncthreads();
-    for (int i = wave; i < NQ; i += kWaves) {
-      const int t = i * 16 + r;
-      if (!((mask >> t) & 1)) continue;
-      floatx4 vg = red[0][i][0][lane], vu = red[0][i][1][lane];
+    if (wave == 0 && r < n) {
+      floatx4 vg = red[0][0][lane], vu = red[0][1][lane];
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) {
-        vg += red[w][i][0][lane];
-        vu += red[w][i][1][lane];
+        vg += red[w][0][lane];
+        vu += red[w][1][lane];
       }
-      const int slot = t * a.K + a.slots[e * 64 + t];
-      const float wt = a.w[slot];
-      const int64_t c0 = c * 16 + 4 * g;
+      const float wt = a.w[t * a.K + a.slots[e * 64 + t]];
+      const int64_t col = c * 16 + 4 * g;
+      const int64_t row = s.row[q] + r;
       floatx4 v;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = c0 + j < a.I ? wt * swiglu<kF32>(vg[j], vu[j]) : 0.0f;
+      for (int j = 0; j < 4; ++j) v[j] = col + j < a.I ? wt * swiglu<kF32>(vg[j], vu[j]) : 0.0f;
       if constexpr (kF32) {
-        *reinterpret_cast<floatx4*>(a.h + (slot * a.Ip + c0) * 4) = v;
+        *reinterpret_cast<floatx4*>(a.h + (row * a.Ip + col) * 4) = v;
       } else {
         const uint32_t h0 = cvt_bf16x2(v[0], v[1]), h1 = cvt_bf16x2(v[2], v[3]);
         // the rest of a number past bf16's range (or of a NaN) is 0, not NaN
@@ -168,145 +224,191 @@ __global__ __launch_bounds__(kThreads) void few_up(FewArgs a) {
         float lo[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) lo[j] = fabsf(hf[j]) <= 3.3895314e38f ? v[j] - hf[j] : 0.0f;
-        const uint32_t l0 = cvt_bf16x2(lo[0], lo[1]), l1 = cvt_bf16x2(lo[2], lo[3]);
-        char* row = a.h + (slot * 2 * a.Ip + c0) * 2;
-        *reinterpret_cast<uint2*>(row) = uint2{h0, h1};
-        *reinterpret_cast<uint2*>(row + a.Ip * 2) = uint2{l0, l1};
+        char* dst = a.h + (row * 2 * a.Ip + col) * 2;
+        *reinterpret_cast<uint2*>(dst) = uint2{h0, h1};
+        *reinterpret_cast<uint2*>(dst + a.Ip * 2) = uint2{cvt_bf16x2(lo[0], lo[1]), cvt_bf16x2(lo[2], lo[3])};
       }
     }
     __syncthreads();
   }
 }
 
-// A unit: 16 output columns of every token; the (expert, batch of k) pairs of
-// the sum are shared by the block's waves, each a run of them. kVec: rows of w2
-// start on 16 bytes.
-constexpr int kDownThreads = 512;
-constexpr int kDownWaves = kDownThreads / kWave;
+// A wave's place in the (group, batch) pairs of few_down.
+struct Item {
+  int q, b;
+  __device__ __forceinline__ void next(int nb) {
+    if (++b == nb) {
+      b = 0;
+      ++q;
+    }
+  }
+};
 
-template <bool kF32, int NQ, bool kVec>
-__global__ __launch_bounds__(kDownThreads) void few_down(FewArgs a) {
+// A unit: 16 output columns of every token; the block's waves share the
+// reduction. A wave adds a group's sums to its tokens' totals, which it keeps
+// in LDS, experts ascending, so an expert's infinities reach its own tokens
+// only; then the waves' totals are added.
+// kVec: rows of w2 start on 16 bytes.
+template <bool kF32, bool kVec>
+__global__ __launch_bounds__(kDownThreads, 3) void few_down(FewArgs a) {
   typedef typename Elem<kF32>::type E;
   constexpr int kC = Elem<kF32>::kChunk, kB = Elem<kF32>::kBytes;
   constexpr int kParts = kF32 ? 1 : 2;
-  __shared__ int list[kMaxE];
-  __shared__ uint64_t mask_s[kMaxE];
+  __shared__ Groups s;
   __shared__ int tmp[kDownWaves];
-  __shared__ floatx4 red[kDownWaves][NQ][kWave];
-  const int n_act = active_experts<kDownThreads>(a, list, mask_s, tmp);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ floatx4 sum[kDownWaves][kFewTokens][4];
+  const int n_groups = find_groups<kDownThreads>(a, s, tmp);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int g = lane >> 4, r = lane & 15;
   const int I = static_cast<int>(a.I), Ip = static_cast<int>(a.Ip);
-  const int nkb = (I * kB + 63) >> 6;             // 64-byte blocks of a row
-  const int nb = (nkb + kU - 1) / kU;             // batches of an expert
-  const int items = n_act * nb;
-  const int i0 = static_cast<int>(static_cast<int64_t>(wave) * items / kDownWaves);
-  const int i1 = static_cast<int>(static_cast<int64_t>(wave + 1) * items / kDownWaves);
+  // This wave's 64-byte blocks of every row of h and w2 (the same for every
+  // expert, so that a token's sums do not depend on the other tokens), in
+  // batches of kU: whole blocks by wide loads, the last of which start early
+  // enough to end with the share; then what is left of the row's end.
+  const int nkb = (I * kB + 63) >> 6;
+  const int nfull = kVec && (I * kB >> 6) >= kU ? I * kB >> 6 : 0;
+  const int kb0 = wave * nkb / kDownWaves, kb1 = (wave + 1) * nkb / kDownWaves;
+  const int kbf = max(min(kb1, nfull), kb0);
+  const int nbf = (kbf - kb0 + kU - 1) / kU;
+  const int items = n_groups * nbf;
   const int units = static_cast<int>((a.H + 15) / 16);
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    const int64_t n = min(static_cast<int64_t>(u * 16 + r), a.H - 1);
-    floatx4 acc[NQ], cur[NQ];   // over the experts; of the expert at hand
+    // (H is a multiple of 8: the last unit may have 8 columns)
+    const uint32_t lr = static_cast<uint32_t>(min(static_cast<int64_t>(r), a.H - 1 - u * 16));
+    const uint32_t wo = lr * static_cast<uint32_t>(I * kB) + g * 16;
+    for (int t = lane; t < a.T * 4; t += kWave) sum[wave][t >> 2][t & 3] = floatx4{0, 0, 0, 0};
+    floatx4 acc = {0, 0, 0, 0};
+
+    struct Batch {
+      u32x4 w[kU], h[kParts][kU];
+    } b0, b1;
+    auto start = [&](int b) { return min(kb0 + b * kU, max(kbf - kU, 0)); };
+    auto w_at = [&](int q) {
+      const int e = __builtin_amdgcn_readfirstlane(s.expert[q]);
+      return static_cast<const char*>(a.w2) + (e * a.H + u * 16) * a.I * kB;
+    };
+    auto h_at = [&](int q) {
+      const int row = __builtin_amdgcn_readfirstlane(s.row[q]);
+      return a.h + static_cast<int64_t>(row) * kParts * Ip * kB;
+    };
+    // the lane's row of h; past the group's last token its first one's
+    auto h_off = [&](int q) {
+      const int n = __popcll(s.mask[q]) - s.rank[q];
+      return static_cast<uint32_t>(r < n ? r : 0) * kParts * Ip * kB + g * 16;
+    };
+    auto load = [&](Batch& v, const Item& it) {
+      const char* w0 = w_at(it.q);
+      const char* h0 = h_at(it.q);
+      const uint32_t k = static_cast<uint32_t>(start(it.b)) * 64, ho = h_off(it.q) + k;
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) acc[i] = cur[i] = floatx4{0, 0, 0, 0};
-    int q = i0 / nb, b = i0 % nb;
-    for (int it = i0; it < i1;) {
-      // expert q: this wave's batches of it
-      const int e = __builtin_amdgcn_readfirstlane(list[q]);
-      const uint64_t mask = mask_s[q];
-      const E* wrow = static_cast<const E*>(a.w2) + (e * a.H + n) * a.I;
-      const char* hp[NQ];
-      bool on[NQ];
+      for (int j = 0; j < kU; ++j) {
+        v.w[j] = load16(w0 + (wo + k) + j * 64);
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        const int t = i * 16 + r;
-        const int at = (mask >> t) & 1 ? t : __ffsll(static_cast<unsigned long long>(mask)) - 1;
-        on[i] = (mask >> (16 * i)) & 0xffff;
-        hp[i] = a.h + static_cast<int64_t>(at * a.K + a.slots[e * 64 + at]) * kParts * Ip * kB;
+        for (int part = 0; part < kParts; ++part) v.h[part][j] = load16(h0 + part * Ip * kB + ho + j * 64);
       }
-      const int b1 = min(nb, b + i1 - it);
-      it += b1 - b;
-      for (; b < b1; ++b) {
-        u32x4 wv[kU];
-        const int k0 = b * kU * 4 * kC + g * kC;
-        const bool whole = (b + 1) * kU * 4 * kC <= I;   // the same in every lane
-        if (kVec && whole) {
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    // the group's sums to its tokens
+    auto add = [&](int q) {
+      const uint64_t mask = s.mask[q];
+      const int rank = s.rank[q];
+      const int n = __popcll(mask) - rank;
+      const int t = group_token(mask, rank, n);
+      if (r < n) sum[wave][t][g] += acc;
+      acc = floatx4{0, 0, 0, 0};
+    };
+    auto mma = [&](const Batch& v, Item& it) {
+      // products of blocks that a batch reads again are skipped
+      const int k = start(it.b), kb = kb0 + it.b * kU;
 #pragma unroll
-          for (int j = 0; j < kU; ++j) wv[j] = load16(reinterpret_cast<const char*>(wrow + k0 + j * 4 * kC));
-        } else {
+      for (int j = 0; j < kU; ++j)
+        if (k + j >= kb && k + j < kbf) {
+#pragma unroll
+          for (int part = 0; part < kParts; ++part) acc = mma16<kF32>(v.w[j], v.h[part][j], acc);
+        }
+      __builtin_amdgcn_sched_barrier(0);
+      if (it.b + 1 == nbf) add(it.q);
+      it.next(nbf);
+    };
+    if (items > 0) {   // as in few_up: no load under a condition
+      Item at{0, 0}, ahead{0, 0};   // of the products, of the loads
+      load(b0, ahead);
+      int i = 0;
+      for (; i + 2 < items; i += 2) {
+        ahead.next(nbf);
+        load(b1, ahead);
+        mma(b0, at);
+        ahead.next(nbf);
+        load(b0, ahead);
+        mma(b1, at);
+      }
+      if (i + 1 < items) {
+        ahead.next(nbf);
+        load(b1, ahead);
+        mma(b0, at);
+        mma(b1, at);
+      } else {
+        mma(b0, at);
+      }
+    }
+    if (kbf < kb1) {
+      // what is left of the rows: past I both operands are zero (h has zeros from
+      // I to Ip)
+      for (int q = 0; q < n_groups; ++q) {
+        const E* wrow = reinterpret_cast<const E*>(w_at(q) + lr * static_cast<uint32_t>(I * kB));
+        const char* hrow = h_at(q) + h_off(q);
+        for (int kb = kbf; kb < kb1; kb += kU) {
+          u32x4 w[kU], h[kParts][kU];
 #pragma unroll
           for (int j = 0; j < kU; ++j) {
-            const int k = k0 + j * 4 * kC;
-            wv[j] = u32x4{0, 0, 0, 0};
-            if (k < I) {
-              if constexpr (kVec) wv[j] = load16(reinterpret_cast<const char*>(wrow + k));
-              else wv[j] = load16_any<kF32>(wrow, k, I);
+            const int k = (kb + j) * 4 * kC + g * kC;
+            const bool in = kb + j < kb1;
+            w[j] = u32x4{0, 0, 0, 0};
+            if (in && k < I) {
+              if constexpr (kVec) w[j] = load16(reinterpret_cast<const char*>(wrow + k));
+              else w[j] = load16_any<kF32>(wrow, k, I);
             }
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-          if (NQ > 1 && !on[i]) continue;
-          // past I both operands are zero (h has zeros from I to Ip)
-          u32x4 hv[kParts][kU];
-#pragma unroll
-          for (int part = 0; part < kParts; ++part)
-#pragma unroll
-            for (int j = 0; j < kU; ++j)
-              hv[part][j] = load16(hp[i] + (part * Ip + min(k0 + j * 4 * kC, Ip - kC)) * kB);
-          if (!whole) {
 #pragma unroll
             for (int part = 0; part < kParts; ++part)
-#pragma unroll
-              for (int j = 0; j < kU; ++j)
-                if (k0 + j * 4 * kC >= Ip) hv[part][j] = u32x4{0, 0, 0, 0};
+              h[part][j] = in && k < Ip ? load16(hrow + part * Ip * kB + (kb + j) * 64)
+                                        : u32x4{0, 0, 0, 0};
           }
-          // every load of the batch is out before the first product
-          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
           for (int part = 0; part < kParts; ++part)
 #pragma unroll
-            for (int j = 0; j < kU; ++j) cur[i] = mma16<kF32>(wv[j], hv[part][j], cur[i]);
+            for (int j = 0; j < kU; ++j) acc = mma16<kF32>(w[j], h[part][j], acc);
         }
+        add(q);
       }
-      // the expert's sums go to its own tokens only: infinities in its weights
-      // reach no other
-#pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        if ((mask >> (i * 16 + r)) & 1) acc[i] += cur[i];
-        cur[i] = floatx4{0, 0, 0, 0};
-      }
-      ++q;
-      b = 0;
     }
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) red[wave][i][lane] = acc[i];
     __syncthreads();
-    for (int i = wave; i < NQ; i += kDownWaves) {
-      const int t = i * 16 + r;
-      if (t >= a.T) continue;
-      floatx4 v = red[0][i][lane];
+    for (int i = threadIdx.x; i < a.T * 4; i += kDownThreads) {
+      const int t = i >> 2, gg = i & 3;
+      floatx4 v = sum[0][t][gg];
 #pragma unroll
-      for (int w = 1; w < kDownWaves; ++w) v += red[w][i][lane];
-      store4<kF32>(static_cast<E*>(a.y) + t * a.H, u * 16 + 4 * g, a.H, true, v);
+      for (int w = 1; w < kDownWaves; ++w) v += sum[w][t][gg];
+      store4<kF32>(static_cast<E*>(a.y) + t * a.H, u * 16 + 4 * gg, a.H, true, v);
     }
     __syncthreads();
   }
 }
 
-template <bool kF32, int NQ>
+template <bool kF32>
 hipError_t launch_few(const FewArgs& a, hipStream_t st) {
   const int cus = device_cu_count();
-  const int64_t most = static_cast<int64_t>(a.T) * a.K < a.E ? static_cast<int64_t>(a.T) * a.K : a.E;
+  const int64_t most = static_cast<int64_t>(a.T) * a.K < a.E ? static_cast<int64_t>(a.T) * a.K
+                                                             : a.E + static_cast<int64_t>(a.T) * a.K / 16;
   const int64_t u1 = most * (a.Ip / 16), u2 = cdiv(a.H, 16);
   const unsigned g1 = static_cast<unsigned>(u1 < 4 * cus ? u1 : 4 * cus);
-  const unsigned g2 = static_cast<unsigned>(u2 < 4 * cus ? u2 : 4 * cus);
-  hipLaunchKernelGGL((few_up<kF32, NQ>), dim3(g1), dim3(kThreads), 0, st, a);
+  const unsigned g2 = static_cast<unsigned>(u2 < 2 * cus ? u2 : 2 * cus);
+  hipLaunchKernelGGL(few_up<kF32>, dim3(g1), dim3(kThreads), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (a.I % Elem<kF32>::kChunk == 0)
-    hipLaunchKernelGGL((few_down<kF32, NQ, true>), dim3(g2), dim3(kDownThreads), 0, st, a);
+    hipLaunchKernelGGL((few_down<kF32, true>), dim3(g2), dim3(kDownThreads), 0, st, a);
   else
-    hipLaunchKernelGGL((few_down<kF32, NQ, false>), dim3(g2), dim3(kDownThreads), 0, st, a);
+    hipLaunchKernelGGL((few_down<kF32, false>), dim3(g2), dim3(kDownThreads), 0, st, a);
   return hipGetLastError();
 }
 
@@ -359,10 +461,7 @@ hipError_t few_experts(const tr_layer_desc& d, const void* x, const void* w1, co
   a.H = d.route.H;
   a.I = d.I;
   a.Ip = L.Ip;
-  const bool f32 = d.route.dtype == TR_F32;
-  if (a.T <= 16) return f32 ? launch_few<true, 1>(a, st) : launch_few<false, 1>(a, st);
-  if (a.T <= 32) return f32 ? launch_few<true, 2>(a, st) : launch_few<false, 2>(a, st);
-  return f32 ? launch_few<true, 4>(a, st) : launch_few<false, 4>(a, st);
+  return d.route.dtype == TR_F32 ? launch_few<true>(a, st) : launch_few<false>(a, st);
 }
 
 }  // namespace tr

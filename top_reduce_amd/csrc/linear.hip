@@ -185,14 +185,25 @@ __global__ __launch_bounds__(kThreads) void adapter_few(ExpandArgs p) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) c[i] = chunk(i * kC);
   }
-  float acc = 0.0f;
-  for (int s = 0; s < p.S; ++s) acc += p.part[(s * nT + t) * p.Np + nc];
+  // eight parts' loads at a time, unconditional (the last is read again) so
+  // that they go out together
+  auto sum = [&](const float* base, int64_t pitch) {
+    float total = 0.0f;
+    for (int s0 = 0; s0 < p.S; s0 += 8) {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = base[min(s0 + i, p.S - 1) * pitch];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (s0 + i < p.S) total += f[i];
+    }
+    return total;
+  };
+  float acc = sum(p.part + static_cast<int64_t>(t) * p.Np + nc, nT * p.Np);
   if (has) {
     const float sc = p.scales ? p.scales[aid] : 1.0f;
     for (int j = threadIdx.x; j < kMaxRank + kAhead * 8; j += kThreads) {
-      float v = 0.0f;
-      if (j < p.R)
-        for (int s = 0; s < p.S; ++s) v += p.vpart[(s * nT + t) * p.Rp + j];
+      const float v = j < p.R ? sum(p.vpart + static_cast<int64_t>(t) * p.Rp + j, nT * p.Rp) : 0.0f;
       v_s[j] = v * sc;
     }
     __syncthreads();
@@ -241,79 +252,98 @@ struct ShrinkArgs {
   int A, R, Rq;
 };
 
-// v[t, j] = s[a] x[t] . A[a][j] for a group of 16 tokens, one after another
+// v[t, j] = s[a] x[t] . A[a][j] for a group of 16 NG tokens, one after another
 // for the different adapters among them (one or two where tokens of a request
-// are neighbours); up to 64 rows of A at a time, the waves sharing the
+// are neighbours); up to 32 rows of A at a time, the waves sharing the
 // reduction. v is rounded to the storage type, to be an MFMA operand of the
 // tile's epilogue: its error is that of one rounding of the adapter's part.
-template <bool kF32>
-__global__ __launch_bounds__(kThreads) void adapter_shrink(ShrinkArgs p) {
+constexpr int kShrinkThreads = 512;
+constexpr int kShrinkWaves = kShrinkThreads / kWave;
+
+template <bool kF32, int NG>
+__global__ __launch_bounds__(kShrinkThreads) void adapter_shrink(ShrinkArgs p) {
   typedef typename Elem<kF32>::type E;
-  constexpr int kRT = 4;   // rank tiles of 16 at a time
-  __shared__ floatx4 red[kWaves][kRT][kWave];
+  constexpr int kRT = 2;   // rank tiles of 16 at a time
+  __shared__ floatx4 red[kShrinkWaves][kRT][NG][kWave];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, r = lane & 15;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 16 + r;
-  const int id = t < p.T ? p.ids[t] : -1;
-  uint32_t todo = static_cast<uint32_t>(__ballot(id >= 0 && id < p.A)) & 0xffffu;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * 16 * NG;
+  const int id = lane < 16 * NG && t0 + lane < p.T ? p.ids[t0 + lane] : -1;
+  uint64_t todo = __ballot(id >= 0 && id < p.A);
   const int nkb = static_cast<int>((p.row_bytes + 63) >> 6);
   const int nfull = static_cast<int>(p.row_bytes >> 6);
-  const int kb0 = wave * nkb / kWaves, kb1 = (wave + 1) * nkb / kWaves;
+  const int kb0 = wave * nkb / kShrinkWaves, kb1 = (wave + 1) * nkb / kShrinkWaves;
   const int kbf = min(kb1, nfull);
   while (todo) {
-    const int first = __ffs(todo) - 1;
+    const int first = __ffsll(static_cast<unsigned long long>(todo)) - 1;
     const int aid = __builtin_amdgcn_readlane(id, first);
-    const bool mine = id == aid;
-    todo &= ~static_cast<uint32_t>(__ballot(mine));
-    const char* xp =
-        p.x + (mine ? t : static_cast<int64_t>(blockIdx.x) * 16 + first) * p.row_bytes + g * 16;
+    const uint64_t mask = __ballot(id == aid);
+    todo &= ~mask;
+    // a token of another adapter reads the first one's row: not stored
+    const char* xp[NG];
+#pragma unroll
+    for (int q = 0; q < NG; ++q)
+      xp[q] = p.x + (t0 + ((mask >> (16 * q + r)) & 1 ? 16 * q + r : first)) * p.row_bytes + g * 16;
     const float sc = p.scales ? p.scales[aid] : 1.0f;
-    for (int j0 = 0; j0 < p.R; j0 += 16 * kRT) {
+    for (int j0 = 0; j0 < p.Rq; j0 += 16 * kRT) {
       const char* ap[kRT];
 #pragma unroll
       for (int c = 0; c < kRT; ++c)
         ap[c] = p.a + (static_cast<int64_t>(aid) * p.R + min(j0 + c * 16 + r, p.R - 1)) * p.row_bytes + g * 16;
-      const int nc = min(kRT, (p.R - j0 + 15) / 16);
-      floatx4 acc[kRT];
+      floatx4 acc[kRT][NG];
 #pragma unroll
-      for (int c = 0; c < kRT; ++c) acc[c] = floatx4{0, 0, 0, 0};
-      int kb = kb0;
-      for (; kb + kU <= kbf; kb += kU) {
-        u32x4 xb[kU];
+      for (int c = 0; c < kRT; ++c)
 #pragma unroll
-        for (int j = 0; j < kU; ++j) xb[j] = load16(xp + (kb + j) * 64);
+        for (int q = 0; q < NG; ++q) acc[c][q] = floatx4{0, 0, 0, 0};
+      // the last batch may be short: it reads the last whole block again, and
+      // skips the products
+      for (int kb = kb0; kb < kbf; kb += kU) {
+        u32x4 xb[NG][kU], wa[kRT][kU];
+#pragma unroll
+        for (int q = 0; q < NG; ++q)
+#pragma unroll
+          for (int j = 0; j < kU; ++j) xb[q][j] = load16(xp[q] + min(kb + j, kbf - 1) * 64);
+#pragma unroll
+        for (int c = 0; c < kRT; ++c)
+#pragma unroll
+          for (int j = 0; j < kU; ++j) wa[c][j] = load16(ap[c] + min(kb + j, kbf - 1) * 64);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < kU; ++j)
+          if (kb + j < kbf) {
+#pragma unroll
+            for (int c = 0; c < kRT; ++c)
+#pragma unroll
+              for (int q = 0; q < NG; ++q) acc[c][q] = mma16<kF32>(wa[c][j], xb[q][j], acc[c][q]);
+          }
+      }
+      if (kb1 > nfull) {   // the short block at the end of the rows
+        const bool in = nfull * 64 + g * 16 < p.row_bytes;
 #pragma unroll
         for (int c = 0; c < kRT; ++c) {
-          if (c >= nc) continue;
-          u32x4 wa[kU];
+          const u32x4 wa = in ? load16(ap[c] + nfull * 64) : u32x4{0, 0, 0, 0};
 #pragma unroll
-          for (int j = 0; j < kU; ++j) wa[j] = load16(ap[c] + (kb + j) * 64);
-#pragma unroll
-          for (int j = 0; j < kU; ++j) acc[c] = mma16<kF32>(wa[j], xb[j], acc[c]);
-        }
-      }
-      for (; kb < kb1; ++kb) {
-        const bool in = kb * 64 + g * 16 < p.row_bytes;
-        const u32x4 xb = in ? load16(xp + kb * 64) : u32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int c = 0; c < kRT; ++c) {
-          if (c >= nc) continue;
-          const u32x4 wa = in ? load16(ap[c] + kb * 64) : u32x4{0, 0, 0, 0};
-          acc[c] = mma16<kF32>(wa, xb, acc[c]);
+          for (int q = 0; q < NG; ++q) {
+            const u32x4 xb = in ? load16(xp[q] + nfull * 64) : u32x4{0, 0, 0, 0};
+            acc[c][q] = mma16<kF32>(wa, xb, acc[c][q]);
+          }
         }
       }
 #pragma unroll
-      for (int c = 0; c < kRT; ++c) red[wave][c][lane] = acc[c];
+      for (int c = 0; c < kRT; ++c)
+#pragma unroll
+        for (int q = 0; q < NG; ++q) red[wave][c][q][lane] = acc[c][q];
       __syncthreads();
-      // wave c: rank tile c; columns past R are zero
-      const int col = j0 + wave * 16 + 4 * g;
-      if (mine && col < p.Rq) {
-        floatx4 v = red[0][wave][lane];
+      // wave c + kRT q: rank tile c of token group q; columns past R are zero
+      const int c = wave % kRT, q = wave / kRT;
+      const int col = j0 + c * 16 + 4 * g;
+      if (q < NG && ((mask >> (16 * q + r)) & 1) && col < p.Rq) {
+        floatx4 v = red[0][c][q][lane];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) v += red[w][wave][lane];
+        for (int w = 1; w < kShrinkWaves; ++w) v += red[w][c][q][lane];
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = col + i < p.R ? v[i] * sc : 0.0f;
-        store4<kF32>(static_cast<E*>(p.v) + t * p.Rq, col, p.Rq, true, v);
+        store4<kF32>(static_cast<E*>(p.v) + (t0 + 16 * q + r) * p.Rq, col, p.Rq, true, v);
       }
       __syncthreads();
     }
@@ -399,28 +429,11 @@ __device__ __forceinline__ void tile_dma(const TileLoad<C>& l, int wave, int kt,
         k + l.wc[j] < l.row_bytes ? l.wo[j] + k : kPast, 0, 0, 0);
 }
 
-template <bool kF32, typename C, int S>
-__device__ __forceinline__ void tile_mma(int wm, int wn, const int (&frag)[2],
-                                         floatx4 (&acc)[C::kMs][C::kNs]) {
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    u32x4 fx[C::kMs], fw[C::kNs];
-#pragma unroll
-    for (int i = 0; i < C::kMs; ++i)
-      fx[i] = stage_x<C, S>()[(wm * C::kMs + i) * 16 * kLine + frag[s]];
-#pragma unroll
-    for (int j = 0; j < C::kNs; ++j)
-      fw[j] = stage_w<C, S>()[(wn * C::kNs + j) * 16 * kLine + frag[s]];
-#pragma unroll
-    for (int i = 0; i < C::kMs; ++i)
-#pragma unroll
-      for (int j = 0; j < C::kNs; ++j) acc[i][j] = mma16<kF32>(fw[j], fx[i], acc[i][j]);
-  }
-}
-
 // Step kt of the ring: its k-tile has landed once at most the DMA of the
 // kStages - 2 after it is in flight; after the barrier every wave has finished
-// with the k-tile before it, whose stage takes k-tile kt + kStages - 1.
+// with the k-tile before it, whose stage takes k-tile kt + kStages - 1. The
+// fragments of both 64-byte halves are asked for first, so that the second
+// half's reads and the DMA run beside the first half's products.
 template <bool kF32, typename C, int S>
 __device__ __forceinline__ void tile_step(const TileLoad<C>& l, int wave, int wm, int wn, int kt,
                                           int k1, const int (&frag)[2],
@@ -431,8 +444,25 @@ __device__ __forceinline__ void tile_step(const TileLoad<C>& l, int wave, int wm
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+  u32x4 fx[2][C::kMs], fw[2][C::kNs];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+#pragma unroll
+    for (int i = 0; i < C::kMs; ++i)
+      fx[s][i] = stage_x<C, S>()[(wm * C::kMs + i) * 16 * kLine + frag[s]];
+#pragma unroll
+    for (int j = 0; j < C::kNs; ++j)
+      fw[s][j] = stage_w<C, S>()[(wn * C::kNs + j) * 16 * kLine + frag[s]];
+  }
+  __builtin_amdgcn_sched_barrier(0);
   tile_dma<C, (S + C::kStages - 1) % C::kStages>(l, wave, kt + C::kStages - 1, k1);
-  tile_mma<kF32, C, S>(wm, wn, frag, acc);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int i = 0; i < C::kMs; ++i)
+#pragma unroll
+      for (int j = 0; j < C::kNs; ++j) acc[i][j] = mma16<kF32>(fw[s][j], fx[s][i], acc[i][j]);
 }
 
 // Block `block` of m_tiles x n_tiles x parts: a tile over one part of the
@@ -811,9 +841,13 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
   s.A = d.A;
   s.R = d.R;
   s.Rq = L.Rq;
-  const unsigned groups = static_cast<unsigned>(cdiv(d.T, 16));
-  if (f32) hipLaunchKernelGGL(adapter_shrink<true>, dim3(groups), dim3(kThreads), 0, st, s);
-  else hipLaunchKernelGGL(adapter_shrink<false>, dim3(groups), dim3(kThreads), 0, st, s);
+  // 32 tokens a block read A half as often; 16 where that leaves CUs without one
+  const bool pairs = cdiv(d.T, 32) >= kPlanCus / 2;
+  const dim3 groups(static_cast<unsigned>(cdiv(d.T, pairs ? 32 : 16)));
+  if (f32 && pairs) hipLaunchKernelGGL((adapter_shrink<true, 2>), groups, dim3(kShrinkThreads), 0, st, s);
+  else if (f32) hipLaunchKernelGGL((adapter_shrink<true, 1>), groups, dim3(kShrinkThreads), 0, st, s);
+  else if (pairs) hipLaunchKernelGGL((adapter_shrink<false, 2>), groups, dim3(kShrinkThreads), 0, st, s);
+  else hipLaunchKernelGGL((adapter_shrink<false, 1>), groups, dim3(kShrinkThreads), 0, st, s);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   TileArgs t{};
   t.x = s.x;

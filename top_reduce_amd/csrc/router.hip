@@ -76,6 +76,15 @@ __device__ __forceinline__ float wave_sum(float v) {
   }));
 }
 
+// f(0), f(1), .. f(N - 1) with constants.
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void each_group(F f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    each_group<N, I + 1>(f);
+  }
+}
+
 // NR registers of logits a lane: G <= 64 NR.
 template <int NR>
 __global__ __launch_bounds__(kThreads) void route_select(SelectArgs a) {
@@ -136,19 +145,36 @@ __global__ __launch_bounds__(kThreads) void route_select(SelectArgs a) {
   }
 
   // K rounds; lane k keeps the k-th expert and its value. Every lane offers its
-  // largest key (the lowest register among equals).
+  // largest key (the lowest register among equals), the largest of the maxima
+  // of its groups of registers: a round marks one register of one lane, so it
+  // renews one group's maximum only (register and group are the same for the
+  // whole wave).
+  constexpr int kGrp = NR <= 4 ? 1 : NR <= 16 ? 4 : 8;
+  constexpr int kPer = NR / kGrp;
+  uint32_t gk[kGrp];   // a group's largest key, and its register
+  int gi[kGrp];
+  auto renew = [&](auto grp) {
+    constexpr int q = decltype(grp)::value;
+    gk[q] = key[q * kPer];
+    gi[q] = q * kPer;
+#pragma unroll
+    for (int i = q * kPer + 1; i < (q + 1) * kPer; ++i)
+      if (key[i] > gk[q]) {
+        gk[q] = key[i];
+        gi[q] = i;
+      }
+  };
+  each_group<kGrp>(renew);
   int my_e = 0;
   float my_v = 0.0f;
   for (int k = 0; k < a.K; ++k) {
-    uint32_t lb = key[0];
-    int li = 0;
-    float lv = v[0];
+    uint32_t lb = gk[0];
+    int li = gi[0];
 #pragma unroll
-    for (int i = 1; i < NR; ++i)
-      if (key[i] > lb) {
-        lb = key[i];
-        li = i;
-        lv = v[i];
+    for (int q = 1; q < kGrp; ++q)
+      if (gk[q] > lb) {
+        lb = gk[q];
+        li = gi[q];
       }
     const uint32_t top = wave_max(lb);
     const uint64_t hit = __ballot(lb == top);
@@ -158,16 +184,24 @@ __global__ __launch_bounds__(kThreads) void route_select(SelectArgs a) {
       const uint32_t e = ~wave_max(lb == top ? ~static_cast<uint32_t>(li * kWave + lane) : 0u);
       owner = static_cast<int>(e & 63);
     }
-    const int e = __builtin_amdgcn_readlane(li, owner) * kWave + owner;
-    const float ev = __uint_as_float(static_cast<uint32_t>(
-        __builtin_amdgcn_readlane(static_cast<int>(__float_as_uint(lv)), owner)));
+    const int reg = __builtin_amdgcn_readlane(li, owner);
+    float ev = 0.0f;
+    each_group<kGrp>([&](auto grp) {
+      constexpr int q = decltype(grp)::value;
+      if (reg / kPer != q) return;
+#pragma unroll
+      for (int i = q * kPer; i < (q + 1) * kPer; ++i)
+        if (i == reg) {
+          ev = __uint_as_float(static_cast<uint32_t>(
+              __builtin_amdgcn_readlane(static_cast<int>(__float_as_uint(v[i])), owner)));
+          if (lane == owner) key[i] = kUsed;
+        }
+      renew(grp);
+    });
     if (lane == k) {
-      my_e = e;
+      my_e = reg * kWave + owner;
       my_v = ev;
     }
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-      if (lane == owner && i == li) key[i] = kUsed;
   }
   const float my_p = a.bias ? my_v : score(my_v);
   float w = my_p;
