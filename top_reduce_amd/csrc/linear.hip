@@ -33,7 +33,8 @@ struct StreamArgs {
   const char* w;         // [N, H]
   float* part;           // [S, T, Np] sums of each part of the reduction
   int64_t row_bytes;     // bytes of a row of x and of w
-  int T, N, Np;
+  int64_t T;
+  int N, Np;
   int tiles;             // ceil(N / 16)
   // adapters (NULL ids: none)
   const int32_t* ids;    // [T]
@@ -45,20 +46,41 @@ struct StreamArgs {
   int n_zero;
 };
 
-// Block (tile, s): 16 weight rows against every token over part s of the
-// reduction, which its waves share. Tiles past the weight's are adapter tiles:
+// Lane t: the tokens (of n, lane t's id in `id`) with the same id as t.
+__device__ __forceinline__ uint64_t same_id(int id, int n) {
+  uint32_t lo = 0, hi = 0;
+  for (int j = 0; j < min(n, 32); ++j) lo |= (id == __builtin_amdgcn_readlane(id, j) ? 1u : 0u) << j;
+  for (int j = 32; j < n; ++j) hi |= (id == __builtin_amdgcn_readlane(id, j) ? 1u : 0u) << (j - 32);
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
+// Lane `from`'s v, in every lane.
+__device__ __forceinline__ uint64_t lane_u64(uint64_t v, int from) {
+  return static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v >> 32), from))) << 32 |
+         static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), from));
+}
+// The u-th set bit of m (the same in every lane), or -1.
+__device__ __forceinline__ int nth_bit(uint64_t m, int u) {
+  const uint64_t hit = __ballot(((m >> lane_id()) & 1) && popc_below(m) == u);
+  return __ffsll(static_cast<unsigned long long>(hit)) - 1;
+}
+
+// Unit (chunk, tile, s): 16 weight rows against the chunk's tokens (64, the last
+// chunk the rest) over part s of the reduction, which its waves share. Tiles past the weight's are adapter tiles:
 // unit (slot, rank tile) takes 16 rows of the slot-th different adapter among
 // the tokens' ids, and keeps the sums of that adapter's tokens. red: LDS of
 // kWaves * NQ * kWave floatx4.
 template <bool kF32, int NQ>
-__device__ __forceinline__ void stream_unit(const StreamArgs& p, int tile, int s, int S,
+__device__ __forceinline__ void stream_unit(const StreamArgs& p, int chunk, int tile, int s, int S,
                                             floatx4* red) {
+  const int64_t t0 = static_cast<int64_t>(chunk) * kFewTokens;
+  const int n_tok = static_cast<int>(min(static_cast<int64_t>(kFewTokens), p.T - t0));
+  const char* x0 = p.x + t0 * p.row_bytes;
   const int tid = threadIdx.x;
   const int lane = tid & 63, wave = tid >> 6;
   const int g = lane >> 4, r = lane & 15;
 
   const bool is_w = tile < p.tiles;
-  uint64_t mask = p.T == 64 ? ~0ull : (1ull << p.T) - 1;   // tokens of this tile
+  uint64_t mask = n_tok == 64 ? ~0ull : (1ull << n_tok) - 1;   // tokens of this tile
   const char* wp;
   int rt = 0;
   if (is_w) {
@@ -66,17 +88,13 @@ __device__ __forceinline__ void stream_unit(const StreamArgs& p, int tile, int s
   } else {
     const int u = tile - p.tiles, slot = u / p.rank_tiles;
     rt = u % p.rank_tiles;
-    const int id = lane < p.T ? p.ids[lane] : -1;
-    uint64_t todo = __ballot(id >= 0 && id < p.A);
-    int aid = 0;
-    mask = 0;
-    for (int i = 0; i <= slot && todo; ++i) {
-      aid = __builtin_amdgcn_readlane(id, __ffsll(static_cast<unsigned long long>(todo)) - 1);
-      mask = __ballot(id == aid);
-      todo &= ~mask;
-      if (i < slot) mask = 0;
-    }
-    if (mask == 0) return;   // fewer different adapters (the same in every wave)
+    const int id = lane < n_tok ? p.ids[t0 + lane] : -1;
+    // the first tokens of the different adapters
+    const uint64_t same = same_id(id, n_tok);
+    const int lead = nth_bit(__ballot(id >= 0 && id < p.A && (same & ((1ull << lane) - 1)) == 0), slot);
+    if (lead < 0) return;   // fewer different adapters (the same in every wave)
+    const int aid = __builtin_amdgcn_readlane(id, lead);
+    mask = lane_u64(same, lead);
     wp = p.a + (static_cast<int64_t>(aid) * p.R + min(rt * 16 + r, p.R - 1)) * p.row_bytes;
   }
 
@@ -89,7 +107,7 @@ __device__ __forceinline__ void stream_unit(const StreamArgs& p, int tile, int s
   for (int q = 0; q < NQ; ++q) {
     const int t = q * 16 + r;
     on[q] = (mask >> (16 * q)) & 0xffff;
-    xp[q] = p.x + static_cast<int64_t>(t < 64 && ((mask >> t) & 1) ? t : first) * p.row_bytes + g * 16;
+    xp[q] = x0 + ((mask >> t) & 1 ? t : first) * p.row_bytes + g * 16;
   }
   wp += g * 16;
 
@@ -136,11 +154,11 @@ __device__ __forceinline__ void stream_unit(const StreamArgs& p, int tile, int s
   __syncthreads();
   for (int q = wave; q < NQ; q += kWaves) {
     const int t = q * 16 + r;
-    if (t >= p.T || !((mask >> t) & 1)) continue;
+    if (!((mask >> t) & 1)) continue;
     floatx4 v = red[q * kWave + lane];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) v += red[(w * NQ + q) * kWave + lane];
-    const int64_t row = static_cast<int64_t>(s) * p.T + t;
+    const int64_t row = s * p.T + t0 + t;
     float* dst = is_w ? p.part + row * p.Np + tile * 16 + 4 * g
                       : p.vpart + row * p.Rp + rt * 16 + 4 * g;
     *reinterpret_cast<floatx4*>(dst) = v;
@@ -154,87 +172,174 @@ struct ExpandArgs {
   const float* scales;   // [A] or NULL
   const void* b;         // [A, N, R]
   void* y;               // [T, N]
-  int S, T, N, Np, A, R, Rp;
+  int64_t T;
+  int S, N, Np, A, R, Rp;
 };
 
 // y[t, n] = the sum of the parts + s[a] sum_j v[t, j] B[a][n, j]. One block:
-// 256 columns of one token, one column a thread, which reads its row of B
-// whole (neighbouring threads' rows are neighbours in memory); the first of it
-// is asked for before the token's low-rank sums, which stay in LDS, are made.
-// fp32 throughout, rounded once.
+// 256 columns of up to 16 tokens of one adapter (unit blockIdx.y of the 64
+// tokens of chunk blockIdx.z), 64 columns a wave. Rows of B are one MFMA
+// operand, read whole and once for all of the adapter's tokens, the low-rank
+// sums the other: for bf16 as two bf16 numbers each (16 significant bits), so
+// that y is rounded once. Bound by latency: the loads of B and of the parts go
+// out before the low-rank sums are made.
 template <bool kF32>
 __global__ __launch_bounds__(kThreads) void adapter_few(ExpandArgs p) {
   typedef typename Elem<kF32>::type E;
   constexpr int kC = Elem<kF32>::kChunk;
-  constexpr int kAhead = 8;   // chunks of B's row at a time
-  __shared__ float v_s[kMaxRank + kAhead * 8];
-  const int t = blockIdx.y;
-  const int n = blockIdx.x * kThreads + threadIdx.x;
-  const int nc = min(n, p.N - 1);
-  const int aid = p.ids[t];
-  const bool has = aid >= 0 && aid < p.A;   // the same for the whole block
-  const int64_t nT = p.T;
-  const E* row = static_cast<const E*>(p.b) + (static_cast<int64_t>(has ? aid : 0) * p.N + nc) * p.R;
-  const bool vec = (p.R % kC) == 0;
-  auto chunk = [&](int j) -> u32x4 {
-    if (vec) return load16(reinterpret_cast<const char*>(row + min(j, p.R - kC)));
-    return load16_any<kF32>(row, j, p.R);
-  };
-  u32x4 c[kAhead];
-  if (has) {
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) c[i] = chunk(i * kC);
-  }
-  // eight parts' loads at a time, unconditional (the last is read again) so
-  // that they go out together
-  auto sum = [&](const float* base, int64_t pitch) {
-    float total = 0.0f;
-    for (int s0 = 0; s0 < p.S; s0 += 8) {
-      float f[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = base[min(s0 + i, p.S - 1) * pitch];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (s0 + i < p.S) total += f[i];
+  constexpr int kV = kF32 ? 1 : 2;       // numbers that make up a low-rank sum
+  constexpr int kTok = 16, kNs = 4, kKb = 2;
+  constexpr int kPitch = kMaxRank + kC;  // (a pad: rows in other banks)
+  __shared__ E v_s[kV][kTok][kPitch];
+  __shared__ int unit_s[2 + kTok];   // adapter, tokens, which
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int g = lane >> 4, r = lane & 15;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.z) * kFewTokens;
+  const int n_tok = static_cast<int>(min(static_cast<int64_t>(kFewTokens), p.T - t0));
+  if (wave == 0) {
+    // each adapter's tokens by sixteens (tokens without one are alike): every
+    // sixteenth of them leads a unit
+    int id = lane < n_tok ? p.ids[t0 + lane] : -1;
+    if (id < 0 || id >= p.A) id = -1;
+    const uint64_t same = same_id(id, n_tok);
+    const int rank = __popcll(same & ((1ull << lane) - 1));
+    const int found = nth_bit(__ballot(lane < n_tok && rank % kTok == 0), blockIdx.y);
+    const int lead = max(found, 0);
+    const uint64_t tokens = lane_u64(same, lead);
+    const int first = __builtin_amdgcn_readlane(rank, lead);
+    // lane t of the adapter's tokens: its place in the unit
+    const int at = popc_below(tokens) - first;
+    const int n = min(kTok, __popcll(tokens) - first);
+    if (lane == 0) {
+      unit_s[0] = __builtin_amdgcn_readlane(id, lead);
+      unit_s[1] = found < 0 ? 0 : n;
     }
-    return total;
+    if (((tokens >> lane) & 1) && at >= 0 && at < n) unit_s[2 + at] = lane;
+  }
+  __syncthreads();
+  const int aid = __builtin_amdgcn_readfirstlane(unit_s[0]);
+  const int n = __builtin_amdgcn_readfirstlane(unit_s[1]);
+  if (n == 0) return;   // fewer units
+  const int64_t t = t0 + unit_s[2 + min(r, n - 1)];   // this lane's token
+  const bool has = aid >= 0;   // the same for the whole block
+  const int col0 = blockIdx.x * kThreads + wave * 64;
+
+  // rows of B: lane r's column of each 16, chunk g of a k-block
+  const E* row[kNs];
+#pragma unroll
+  for (int j = 0; j < kNs; ++j)
+    row[j] = static_cast<const E*>(p.b) +
+             (static_cast<int64_t>(max(aid, 0)) * p.N + min(col0 + j * 16 + r, p.N - 1)) * p.R;
+  const bool vec = (p.R % kC) == 0;
+  auto b_chunk = [&](int j, int kb) -> u32x4 {
+    const int k = kb * 4 * kC + g * kC;
+    if (k >= p.R) return u32x4{0, 0, 0, 0};
+    return vec ? load16(reinterpret_cast<const char*>(row[j] + k)) : load16_any<kF32>(row[j], k, p.R);
   };
-  float acc = sum(p.part + static_cast<int64_t>(t) * p.Np + nc, nT * p.Np);
+  u32x4 bv[kKb][kNs];
   if (has) {
-    const float sc = p.scales ? p.scales[aid] : 1.0f;
-    for (int j = threadIdx.x; j < kMaxRank + kAhead * 8; j += kThreads) {
-      const float v = j < p.R ? sum(p.vpart + static_cast<int64_t>(t) * p.Rp + j, nT * p.Rp) : 0.0f;
-      v_s[j] = v * sc;
+#pragma unroll
+    for (int kb = 0; kb < kKb; ++kb)
+#pragma unroll
+      for (int j = 0; j < kNs; ++j) bv[kb][j] = b_chunk(j, kb);
+  }
+  // The parts' sums, four parts' loads at a time (the last is read again), and
+  // this thread's first low-rank sum: all of these loads go out together.
+  const int Rk = (p.R + 4 * kC - 1) / (4 * kC) * (4 * kC);   // v_s: zero from R to Rk
+  const float sc = has && p.scales ? p.scales[aid] : 1.0f;
+  const int n_v = has ? n * Rk : 0;
+  auto v_at = [&](int i) {
+    const int k = i / Rk, j = i - k * Rk;
+    return p.vpart + (t0 + unit_s[2 + min(k, n - 1)]) * p.Rp + min(j, p.R - 1);
+  };
+  floatx4 acc[kNs];
+#pragma unroll
+  for (int j = 0; j < kNs; ++j) acc[j] = floatx4{0, 0, 0, 0};
+  floatx4 f[4][kNs];
+  auto load_parts = [&](int s0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < kNs; ++j)
+        f[i][j] = *reinterpret_cast<const floatx4*>(
+            p.part + (min(s0 + i, p.S - 1) * p.T + t) * p.Np + min(col0 + j * 16, p.Np - 16) + 4 * g);
+  };
+  auto add_parts = [&](int s0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (s0 + i < p.S) {
+#pragma unroll
+        for (int j = 0; j < kNs; ++j) acc[j] += f[i][j];
+      }
+  };
+  float fv[4];
+  auto load_v = [&](const float* v, int s0) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) fv[q] = v[min(s0 + q, p.S - 1) * p.T * p.Rp];
+  };
+  const float* v0 = p.vpart;
+  load_parts(0);
+  if (has) {
+    v0 = v_at(min(static_cast<int>(threadIdx.x), n_v - 1));
+    load_v(v0, 0);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  add_parts(0);
+  for (int s0 = 4; s0 < p.S; s0 += 4) {
+    load_parts(s0);
+    add_parts(s0);
+  }
+  if (has) {
+    for (int i = threadIdx.x; i < n_v; i += kThreads) {
+      if (i >= kThreads) {
+        v0 = v_at(i);
+        load_v(v0, 0);
+      }
+      float total = 0.0f;
+      for (int s0 = 0; s0 < p.S; s0 += 4) {
+        if (s0 > 0) load_v(v0, s0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (s0 + q < p.S) total += fv[q];
+      }
+      const int k = i / Rk, j = i - k * Rk;
+      total = j < p.R ? total * sc : 0.0f;
+      if constexpr (kF32) {
+        v_s[0][k][j] = total;
+      } else {
+        const uint32_t hi = cvt_bf16x2(total, 0.0f) & 0xffffu;
+        const float hf = bf16_bits_to_f32(hi);
+        // (the rest of an infinity is 0, not NaN)
+        v_s[0][k][j] = static_cast<uint16_t>(hi);
+        v_s[1][k][j] = static_cast<uint16_t>(
+            cvt_bf16x2(fabsf(hf) <= 3.3895314e38f ? total - hf : 0.0f, 0.0f) & 0xffffu);
+      }
     }
     __syncthreads();
-    float d = 0.0f;
-    for (int j0 = 0; j0 < p.R; j0 += kAhead * kC) {
+    for (int kb0 = 0; kb0 < Rk / (4 * kC); kb0 += kKb) {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int j = j0 + i * kC;
-        if (j >= p.R) continue;   // a chunk past the row: read again, not used
+      for (int kb = 0; kb < kKb; ++kb) {
+        if ((kb0 + kb) * 4 * kC >= Rk) continue;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if constexpr (kF32) {
-            d = fmaf(v_s[j + q], __uint_as_float(c[i][q]), d);
-          } else {
-            d = fmaf(v_s[j + 2 * q], bf16_bits_to_f32(c[i][q] & 0xffffu), d);
-            d = fmaf(v_s[j + 2 * q + 1], __uint_as_float(c[i][q] & 0xffff0000u), d);
-          }
+        for (int q = 0; q < kV; ++q) {
+          const u32x4 vv = *reinterpret_cast<const u32x4*>(&v_s[q][r][(kb0 + kb) * 4 * kC + g * kC]);
+#pragma unroll
+          for (int j = 0; j < kNs; ++j) acc[j] = mma16<kF32>(bv[kb][j], vv, acc[j]);
         }
       }
-      if (j0 + kAhead * kC < p.R) {
+      if ((kb0 + kKb) * 4 * kC < Rk) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) c[i] = chunk(j0 + (kAhead + i) * kC);
+        for (int kb = 0; kb < kKb; ++kb)
+#pragma unroll
+          for (int j = 0; j < kNs; ++j) bv[kb][j] = b_chunk(j, kb0 + kKb + kb);
       }
     }
-    acc += d;
   }
-  if (n < p.N) {
-    if constexpr (kF32) static_cast<float*>(p.y)[static_cast<int64_t>(t) * p.N + n] = acc;
-    else
-      static_cast<uint16_t*>(p.y)[static_cast<int64_t>(t) * p.N + n] =
-          static_cast<uint16_t>(f32_to_bf16_bits(acc));
+  if (r >= n) return;
+#pragma unroll
+  for (int j = 0; j < kNs; ++j) {
+    const int col = col0 + j * 16 + 4 * g;
+    if (col < p.N) store4<kF32>(static_cast<E*>(p.y) + t * p.N, col, p.N, (p.N & 3) == 0, acc[j]);
   }
 }
 
@@ -606,26 +711,31 @@ __global__ __launch_bounds__(kThreads) void stream_partial(StreamArgs p) {
   const int64_t z = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
   if (z < p.n_zero) p.zero[z] = 0;
   __shared__ floatx4 red[kWaves * kWave];
-  stream_unit<kF32, 1>(p, blockIdx.x, blockIdx.y, gridDim.y, red);
+  stream_unit<kF32, 1>(p, 0, blockIdx.x, blockIdx.y, gridDim.y, red);
 }
 
-// 17 to 64 tokens: blocks below `tiles` are weight tiles of 64 tokens x 128
-// rows (every token beside each weight byte, so that x is read once a tile and
-// not once for 16 rows), the others units of the adapters' low-rank products.
+// More tokens: the first `tiles` blocks are weight tiles of 64 tokens x 128 rows
+// (every token beside each weight byte, so that x is read once a tile and not
+// once for 16 rows), the others units of the adapters' low-rank products,
+// `units` for each 64 tokens (first they would fill the CUs' LDS: 43 us against
+// 32 us for 64 tokens and a 7168 x 7168 weight).
 typedef Shape<1, 4, 4, 2, 3> FewShape;
 template <bool kF32>
-__global__ __launch_bounds__(kThreads) void few_linear(TileArgs p, StreamArgs q, int tiles) {
+__global__ __launch_bounds__(kThreads) void few_linear(TileArgs p, StreamArgs q, int tiles, int units) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  const int b = blockIdx.x;
+  int b = blockIdx.x;
   const int64_t z = static_cast<int64_t>(b) * kThreads + threadIdx.x;
   if (z < q.n_zero) q.zero[z] = 0;
   // (the units' sums meet in the tiles' LDS: two blocks fit a CU)
   static_assert(sizeof(u32x4) * FewShape::kN * kLine >= sizeof(floatx4) * kWaves * 4 * kWave, "");
-  if (b < tiles)
+  if (b < tiles) {
     tile_unit<kF32, FewShape, false>(p, b);
-  else
-    stream_unit<kF32, 4>(q, (b - tiles) / p.parts, (b - tiles) % p.parts, p.parts,
+  } else {
+    b -= tiles;
+    const int u = b / p.parts;
+    stream_unit<kF32, 4>(q, u / units, u % units, b % p.parts, p.parts,
                          reinterpret_cast<floatx4*>(stage_w<FewShape, 0>()));
+  }
 #endif
 }
 
@@ -643,13 +753,20 @@ hipError_t launch_tile(TileArgs a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Parts of the reduction for n tiles of `ksteps` steps: enough for two blocks
-// a CU, at least `least` steps each.
-int parts_for(int64_t n, int64_t ksteps, int64_t least, int64_t most) {
-  int64_t want = cdiv(2 * static_cast<int64_t>(kPlanCus), n);
+// Parts of the reduction for n tiles of `ksteps` steps: enough for `per_cu`
+// blocks a CU, at least `least` steps each.
+int parts_for(int per_cu, int64_t n, int64_t ksteps, int64_t least, int64_t most) {
+  int64_t want = cdiv(static_cast<int64_t>(per_cu) * kPlanCus, n);
   if (want > ksteps / least) want = ksteps / least;
   if (want > most) want = most;
   return static_cast<int>(want < 1 ? 1 : want);
+}
+
+// For n 64 x 128 tiles: one block a CU, in four parts where that leaves seven
+// in eight CUs with one (adapter_few reads four parts in one go).
+int few_parts(int64_t n, int64_t row_bytes) {
+  const int64_t ktiles = cdiv(row_bytes, 128);
+  return parts_for(1, n, ktiles, 3, 4 * n >= kPlanCus * 7 / 8 ? 4 : 16);
 }
 
 // At most 16 tokens: one batch of loads for each of a part's waves, or a few
@@ -683,12 +800,11 @@ LogitsLayout logits_layout(int64_t T, int64_t H, int N, bool f32) {
   if (T <= 16)
     L.parts = stream_parts(cdiv(N, 16), row_bytes);
   else if (T <= kFewTokens)
-    L.parts = parts_for(cdiv(N, FewShape::kN), ktiles, 3, 16);
+    L.parts = parts_for(1, cdiv(N, FewShape::kN), ktiles, 3, 16);
   else if (wide_logits(T, row_bytes, N))
-    // one block of these a CU
-    L.parts = parts_for(2 * cdiv(T, WideShape::kM) * cdiv(N, WideShape::kN), ktiles, 6, 4);
+    L.parts = parts_for(1, cdiv(T, WideShape::kM) * cdiv(N, WideShape::kN), ktiles, 6, 4);
   else
-    L.parts = parts_for(cdiv(T, SmallShape::kM) * cdiv(N, SmallShape::kN), ktiles, 4, 16);
+    L.parts = parts_for(2, cdiv(T, SmallShape::kM) * cdiv(N, SmallShape::kN), ktiles, 4, 16);
   L.bytes = up256(sizeof(float) * static_cast<size_t>(L.parts) * T * L.pitch);
   return L;
 }
@@ -702,7 +818,7 @@ hipError_t logits(int64_t T, int64_t H, int N, bool f32, const void* x, const vo
   a.w = static_cast<const char*>(w);
   a.part = part;
   a.row_bytes = row_bytes;
-  a.T = static_cast<int>(T);
+  a.T = T;
   a.N = N;
   a.Np = L.pitch;
   a.tiles = static_cast<int>(cdiv(N, 16));
@@ -726,8 +842,8 @@ hipError_t logits(int64_t T, int64_t H, int N, bool f32, const void* x, const vo
     t.m_tiles = 1;
     t.n_tiles = static_cast<int>(cdiv(N, FewShape::kN));
     const int tiles = t.n_tiles * t.parts;
-    if (f32) hipLaunchKernelGGL(few_linear<true>, dim3(tiles), dim3(kThreads), 0, st, t, a, tiles);
-    else hipLaunchKernelGGL(few_linear<false>, dim3(tiles), dim3(kThreads), 0, st, t, a, tiles);
+    if (f32) hipLaunchKernelGGL(few_linear<true>, dim3(tiles), dim3(kThreads), 0, st, t, a, tiles, 0);
+    else hipLaunchKernelGGL(few_linear<false>, dim3(tiles), dim3(kThreads), 0, st, t, a, tiles, 0);
     return hipGetLastError();
   }
   if (wide_logits(T, row_bytes, N))
@@ -737,6 +853,11 @@ hipError_t logits(int64_t T, int64_t H, int N, bool f32, const void* x, const vo
 
 // ---- the shared projection with adapters ------------------------------------
 namespace {
+// Whether the projection goes through fp32 parts: a few tokens, or too few
+// 64 x 128 tiles to occupy the CUs without dividing the reduction.
+bool adapter_in_parts(const tr_adapter_desc& d) {
+  return cdiv(d.T, FewShape::kM) * cdiv(d.N, FewShape::kN) < kPlanCus;
+}
 struct AdapterLayout {
   int parts, Np, Rp, Rq;
   size_t part, vpart, v, total;
@@ -748,9 +869,9 @@ AdapterLayout adapter_layout(const tr_adapter_desc& d) {
   L.Np = static_cast<int>(up16(d.N));
   L.Rp = static_cast<int>(up16(d.R));
   L.Rq = static_cast<int>(f32 ? up16(d.R) : cdiv(d.R, 32) * 32);
-  if (d.T <= kFewTokens) {
+  if (adapter_in_parts(d)) {
     L.parts = d.T <= 16 ? stream_parts(cdiv(d.N, 16), row_bytes)
-                        : parts_for(cdiv(d.N, FewShape::kN), cdiv(row_bytes, 128), 3, 16);
+                        : few_parts(cdiv(d.T, FewShape::kM) * cdiv(d.N, FewShape::kN), row_bytes);
     L.vpart = up256(sizeof(float) * static_cast<size_t>(L.parts) * d.T * L.Np);
     L.total = L.vpart + up256(sizeof(float) * static_cast<size_t>(L.parts) * d.T * L.Rp);
   } else {
@@ -770,16 +891,15 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
   const bool f32 = d.dtype == TR_F32;
   const int64_t row_bytes = d.H * (f32 ? 4 : 2);
   hipError_t e;
-  if (d.T <= kFewTokens) {
+  if (adapter_in_parts(d)) {
     StreamArgs s{};
     s.x = static_cast<const char*>(x);
     s.w = static_cast<const char*>(w);
     s.part = static_cast<float*>(ws);
     s.row_bytes = row_bytes;
-    s.T = static_cast<int>(d.T);
+    s.T = d.T;
     s.N = static_cast<int>(d.N);
     s.Np = L.Np;
-    s.tiles = static_cast<int>(cdiv(d.N, 16));
     s.ids = ids;
     s.a = static_cast<const char*>(a);
     s.vpart = reinterpret_cast<float*>(static_cast<char*>(ws) + L.vpart);
@@ -787,8 +907,11 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
     s.R = d.R;
     s.Rp = L.Rp;
     s.rank_tiles = L.Rp / 16;
-    const int slots = static_cast<int>(d.T < d.A ? d.T : d.A);
+    const int64_t chunk = d.T < kFewTokens ? d.T : kFewTokens;
+    const int slots = static_cast<int>(chunk < d.A ? chunk : d.A);   // adapters among 64 tokens
+    const int chunks = static_cast<int>(cdiv(d.T, kFewTokens));
     if (d.T <= 16) {
+      s.tiles = static_cast<int>(cdiv(d.N, 16));
       const dim3 grid(s.tiles + slots * s.rank_tiles, L.parts);
       if (f32) hipLaunchKernelGGL(stream_partial<true>, grid, dim3(kThreads), 0, st, s);
       else hipLaunchKernelGGL(stream_partial<false>, grid, dim3(kThreads), 0, st, s);
@@ -802,13 +925,13 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
       t.part = s.part;
       t.Np = L.Np;
       t.parts = L.parts;
-      t.m_tiles = 1;
+      t.m_tiles = chunks;
       t.n_tiles = static_cast<int>(cdiv(d.N, FewShape::kN));
-      s.tiles = 0;   // its units: the adapters' only
-      const int tiles = t.n_tiles * t.parts;
-      const int units = tiles + slots * s.rank_tiles * t.parts;
-      if (f32) hipLaunchKernelGGL(few_linear<true>, dim3(units), dim3(kThreads), 0, st, t, s, tiles);
-      else hipLaunchKernelGGL(few_linear<false>, dim3(units), dim3(kThreads), 0, st, t, s, tiles);
+      const int tiles = t.m_tiles * t.n_tiles * t.parts;
+      const int units = slots * s.rank_tiles;   // (s.tiles is 0: the adapters' only)
+      const dim3 grid(tiles + chunks * units * t.parts);
+      if (f32) hipLaunchKernelGGL(few_linear<true>, grid, dim3(kThreads), 0, st, t, s, tiles, units);
+      else hipLaunchKernelGGL(few_linear<false>, grid, dim3(kThreads), 0, st, t, s, tiles, units);
     }
     if ((e = hipGetLastError()) != hipSuccess) return e;
     ExpandArgs p{};
@@ -825,7 +948,11 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
     p.A = d.A;
     p.R = d.R;
     p.Rp = L.Rp;
-    const dim3 grid(static_cast<unsigned>(cdiv(d.N, kThreads)), static_cast<unsigned>(d.T));
+    // units of 64 tokens: one for each adapter (and for none), one more for every
+    // 16 tokens
+    const int64_t units = d.A + 1 + chunk / 16;
+    const dim3 grid(static_cast<unsigned>(cdiv(d.N, kThreads)),
+                    static_cast<unsigned>(units < chunk ? units : chunk), static_cast<unsigned>(chunks));
     if (f32) hipLaunchKernelGGL(adapter_few<true>, grid, dim3(kThreads), 0, st, p);
     else hipLaunchKernelGGL(adapter_few<false>, grid, dim3(kThreads), 0, st, p);
     return hipGetLastError();
