@@ -42,6 +42,26 @@ def test_against_the_formula(T, H, N, R, A, run, dtype):
         S.check(y, ref, bound, f"scales {s is not None}")
 
 
+@pytest.mark.parametrize("T,H,N,R,A,run", [
+    (4096, 128, 8192, 8, 5, 1000), (4090, 256, 8192, 16, 3, 256), (8191, 128, 4096, 40, 6, 333),
+    (16385, 256, 2048, 64, 40, 1), (8000, 384, 4352, 24, 2, 31), (33000, 128, 1024, 256, 4, 5000),
+])
+def test_large_tiles_against_the_formula(T, H, N, R, A, run):
+    """Shapes of the 256 x 256 tiles: row blocks of one adapter, of several, of
+    none, and a short last tile. Checked on the first and last rows, on the rows
+    around every 256th, and on some others."""
+    say(f"adapter tiles T={T} H={H} N={N} R={R} A={A} run={run}")
+    x, w, a, b, ids, scales = make(T + N, T, H, N, R, A, BF, run)
+    y = tr.adapter_linear(x.cuda(), w.cuda(), a.cuda(), b.cuda(), ids.cuda(), scales=scales.cuda())
+    rows = {0, 1, T - 2, T - 1} | {t + d for t in range(256, T - 1, 1792) for d in (-1, 0, 31, 32, 127)}
+    g = torch.Generator().manual_seed(T)
+    rows |= set(torch.randint(0, T, (150,), generator=g).tolist())
+    rows = torch.tensor(sorted(t for t in rows if t < T))
+    # (the row sample is past 64 rows, so the bound has the low-rank product's rounding)
+    ref, bound = S.adapter(x[rows], w, a, b, ids[rows], scales)
+    S.check(y[rows.cuda()], ref, bound, "y")
+
+
 @pytest.mark.parametrize("T", [5, 64, 100, 700])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_adapters_that_no_row_names_are_not_read(T, dtype):
@@ -56,6 +76,19 @@ def test_adapters_that_no_row_names_are_not_read(T, dtype):
     y3 = tr.adapter_linear(x.cuda(), w.cuda(), a.cuda(), b.cuda(), ids.cuda(), scales=scales.cuda())
     mine = (ids == 3).cuda()
     assert torch.equal(y[~mine], y3[~mine]) and torch.isnan(y3[mine]).all()
+
+
+@pytest.mark.parametrize("run", [1, 50, 300])
+def test_an_adapter_of_infinities_in_the_large_tiles(run):
+    T, H, N, R, A = 4100, 128, 8192, 16, 4
+    x, w, a, b, ids, scales = make(run, T, H, N, R, A, BF, run)
+    call = lambda: tr.adapter_linear(x.cuda(), w.cuda(), a.cuda(), b.cuda(), ids.cuda())  # noqa: E731
+    y = call()
+    b[1], a[2] = float("inf"), float("nan")
+    y2 = call()
+    theirs = ((ids == 1) | (ids == 2)).cuda()
+    assert torch.equal(y[~theirs], y2[~theirs])
+    assert not torch.isfinite(y2[theirs]).any()
 
 
 @pytest.mark.parametrize("T", [20, 200])

@@ -74,6 +74,15 @@ struct GemmArgs {
   const int* n_take;
 };
 
+// The low-rank adapters of a shared projection (adapter_tiled): row t of the
+// output gets v[t] . B[ids[t]][n] on top.
+struct AdaptArgs {
+  const int* ids;       // [rows]; outside [0, n): none
+  const uint16_t* v;    // [rows, Rq] low-rank products, scaled; zero past R
+  const uint16_t* b;    // [n, Nc, R]
+  int n, R, Rq;         // R a multiple of 8
+};
+
 // Builds in LDS the exclusive prefix of `units(e)` over experts; returns the
 // total. `pre` has E+1 entries, `tmp` kBlock/64; E <= 4 kBlock.
 template <int kBlock = kThreads, typename F>
@@ -497,10 +506,13 @@ __device__ __forceinline__ int early_down_tiles(int total_m, int NT1, int NT2, i
 // The tile loop of gemm_tiles (below). pre / cnt_s / off_s: the LDS tables
 // of gemm_prologue. kFused (GEMM2 only): the reduce folded into the epilogue
 // for the rows the plan's row_dst names (a.dst non-NULL).
-template <bool kSwiglu, bool kGather, bool kFused>
+// kAdapt (a shared projection: one "expert", no SwiGLU): the adapters `ad` of
+// the rows.
+template <bool kSwiglu, bool kGather, bool kFused, bool kAdapt = false>
 __device__ __forceinline__ void gemm_tiles_impl(const GemmArgs& a, int I, const int* pre,
                                                 const int* cnt_s, const int* off_s, int total_m,
-                                                int begin, int end, int slot, int nslots) {
+                                                int begin, int end, int slot, int nslots,
+                                                const AdaptArgs* ad = nullptr) {
   constexpr int kOutCols = kSwiglu ? BN / 2 : BN;   // output columns per tile
   const int NT = (a.Nc + kOutCols - 1) / kOutCols;
   const int tid = threadIdx.x;
@@ -672,6 +684,63 @@ __device__ __forceinline__ void gemm_tiles_impl(const GemmArgs& a, int I, const 
       kt += 2;
     } while (kt < nk);
 
+    // Adapters. A wave's row block of 32 rows that all have one adapter takes
+    // its product in the accumulators: the rows of B are loaded once for every
+    // row block with that adapter (in prompts mostly all four). Row blocks with several adapters, or with rows that have none, are
+    // marked in `mixed` and take theirs in the epilogue.
+    int aid[4];
+    uint32_t mixed = 0;
+    if constexpr (kAdapt) {
+      uint32_t todo = 0;   // row blocks of one adapter
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = wm * 128 + i * 32 + (lane & 31);
+        aid[i] = row < t.rows_valid ? ad->ids[t.row0 + row] : -1;
+        if (aid[i] < 0 || aid[i] >= ad->n) aid[i] = -1;
+        const int lead = __builtin_amdgcn_readfirstlane(aid[i]);   // (row 0 of the block)
+        const uint64_t in = __ballot(row < t.rows_valid), same = __ballot(aid[i] == lead);
+        if ((in & ~same) != 0) mixed |= 1u << i;
+        else if (lead >= 0) todo |= 1u << i;
+      }
+      while (todo) {
+        int which = -1;
+#pragma unroll
+        for (int i = 3; i >= 0; --i)
+          if ((todo >> i) & 1) which = __builtin_amdgcn_readfirstlane(aid[i]);
+        uint32_t now = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (((todo >> i) & 1) && __builtin_amdgcn_readfirstlane(aid[i]) == which) now |= 1u << i;
+        todo &= ~now;
+        const uint16_t* brow = ad->b + (static_cast<int64_t>(which) * a.Nc + t.n0 + wn * 128 + (lane & 31)) * ad->R;
+        const uint16_t* vrow = ad->v + static_cast<int64_t>(t.row0 + wm * 128 + (lane & 31)) * ad->Rq;
+#pragma clang loop unroll(disable)
+        for (int k0 = 0; k0 < ad->R; k0 += 16) {
+          const int k = k0 + (lane >> 5) * 8;
+          u32x4 vf[4], bf[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            bf[j] = vf[j] = u32x4{0, 0, 0, 0};
+            if (k < ad->R) {
+              bf[j] = *reinterpret_cast<const u32x4*>(brow + j * 32 * ad->R + k);
+              // (rows past the last are not read)
+              if (wm * 128 + j * 32 + (lane & 31) < t.rows_valid)
+                vf[j] = *reinterpret_cast<const u32x4*>(vrow + j * 32 * ad->Rq + k);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((now >> i) & 1) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                f.acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    __builtin_bit_cast(bf16x8, bf[j]), __builtin_bit_cast(bf16x8, vf[i]),
+                    f.acc[i][j], 0, 0, 0);
+            }
+        }
+      }
+    }
+
     // The accumulators stay in accumulation registers up to their block's
     // turn in the epilogue.
 #pragma unroll
@@ -718,6 +787,40 @@ __device__ __forceinline__ void gemm_tiles_impl(const GemmArgs& a, int I, const 
         if (kSwiglu) {
           xu = f.acc[i][j + 2];
           asm volatile("" : "+v"(xu));
+        }
+        if constexpr (kAdapt) {
+          if ((mixed >> i) & 1) {
+            // one different adapter after another, added to its own rows only:
+            // its infinities reach no other
+            uint32_t todo = static_cast<uint32_t>(__ballot(aid[i] >= 0));
+            const int row = wm * 128 + i * 32 + (lane & 31);
+            while (todo) {
+              const int lead = __ffs(todo) - 1;
+              const int which = __builtin_amdgcn_readlane(aid[i], lead);
+              const bool mine = aid[i] == which;
+              todo &= ~static_cast<uint32_t>(__ballot(mine));
+              const uint16_t* brow =
+                  ad->b + (static_cast<int64_t>(which) * a.Nc + t.n0 + wn * 128 + j * 32 + (lane & 31)) * ad->R;
+              const uint16_t* vrow =
+                  ad->v + static_cast<int64_t>(t.row0 + (mine ? row : wm * 128 + i * 32 + lead)) * ad->Rq;
+              floatx16 d = {};
+#pragma clang loop unroll(disable)
+              for (int k0 = 0; k0 < ad->R; k0 += 16) {
+                const int k = k0 + (lane >> 5) * 8;
+                u32x4 bf = {0, 0, 0, 0}, vf = {0, 0, 0, 0};
+                if (k < ad->R) {
+                  bf = *reinterpret_cast<const u32x4*>(brow + k);
+                  vf = *reinterpret_cast<const u32x4*>(vrow + k);
+                }
+                d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, bf),
+                                                            __builtin_bit_cast(bf16x8, vf), d, 0, 0, 0);
+              }
+              if (mine) {
+#pragma unroll
+                for (int q = 0; q < 16; ++q) xg[q] += d[q];
+              }
+            }
+          }
         }
         uint32_t d[4][2];   // [column group q'][pair]: bf16 pairs of 4 columns
 #pragma unroll
@@ -826,6 +929,24 @@ __global__ __launch_bounds__(kThreads) void gemm_tiled(GemmArgs a, int I, int pa
     begin = early_down_tiles(total_m, (a.Kd + BN / 2 - 1) / (BN / 2), NT, a.Nc / a.Kd, g_split);
   gemm_tiles<kSwiglu, kGather>(a, I, pre, cnt_s, off_s, total_m, begin, end, blockIdx.x,
                                gridDim.x);
+#endif  // __HIP_DEVICE_COMPILE__
+}
+
+// A projection that all rows share, with the rows' adapters: the tile loop over
+// one "expert" whose segment is every row.
+__global__ __launch_bounds__(kThreads) void adapter_tiled(GemmArgs a, AdaptArgs ad) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ int pre[2], cnt_s[1], off_s[1];
+  const int total_m = static_cast<int>((a.T + BM - 1) / BM);
+  if (threadIdx.x == 0) {
+    pre[0] = 0;
+    pre[1] = total_m;
+    cnt_s[0] = static_cast<int>(a.T);
+    off_s[0] = 0;
+  }
+  __syncthreads();
+  gemm_tiles_impl<false, false, false, true>(a, 0, pre, cnt_s, off_s, total_m, 0,
+                                             total_m * (a.Nc / BN), blockIdx.x, gridDim.x, &ad);
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
@@ -1579,6 +1700,28 @@ __global__ __launch_bounds__(kThreads) void gemm_any(GemmArgs a, int I) {
 
 bool gemm_can_gather(const tr_moe_desc& d) {
   return d.dtype == TR_BF16 && d.T * d.H * 2 <= 0x7fffffffLL;
+}
+
+bool adapter_can_tile(const tr_adapter_desc& d) {
+  return d.dtype == TR_BF16 && d.H % (2 * BK) == 0 && d.N % BN == 0 && d.R % 8 == 0 &&
+         d.H * d.N < (int64_t{1} << 30) &&
+         cdiv(d.T, BM) * (d.N / BN) >= 2 * static_cast<int64_t>(kPlanCus);
+}
+
+hipError_t adapter_tiles(const tr_adapter_desc& d, const void* x, const void* w, const void* b,
+                         const int32_t* ids, const void* v, int Rq, void* y, hipStream_t st) {
+  GemmArgs a{};
+  a.A = x;
+  a.B = w;
+  a.C = y;
+  a.E = 1;
+  a.Kd = static_cast<int>(d.H);
+  a.Nc = static_cast<int>(d.N);
+  a.a_rows = d.T;
+  a.T = d.T;
+  const AdaptArgs ad{ids, static_cast<const uint16_t*>(v), static_cast<const uint16_t*>(b), d.A, d.R, Rq};
+  hipLaunchKernelGGL(adapter_tiled, dim3(device_cu_count()), dim3(kThreads), 0, st, a, ad);
+  return hipGetLastError();
 }
 
 hipError_t grouped_gemm(const tr_moe_plan& p, const void* w1, const void* w2, int parts,

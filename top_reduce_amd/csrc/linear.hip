@@ -976,6 +976,7 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
   else if (pairs) hipLaunchKernelGGL((adapter_shrink<false, 2>), groups, dim3(kShrinkThreads), 0, st, s);
   else hipLaunchKernelGGL((adapter_shrink<false, 1>), groups, dim3(kShrinkThreads), 0, st, s);
   if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (adapter_can_tile(d)) return adapter_tiles(d, x, w, b, ids, ws, L.Rq, y, st);
   TileArgs t{};
   t.x = s.x;
   t.w = static_cast<const char*>(w);

@@ -101,6 +101,12 @@ FewRoutes few_routes(const tr_layer_desc& d, void* ws);
 hipError_t few_experts(const tr_layer_desc& d, const void* x, const void* w1, const void* w2,
                        const float* w, void* y, void* ws, hipStream_t st);
 
+// The shared projection on the grouped GEMM's 256 x 256 tiles: whether its shape
+// allows that and gives at least two tiles a CU (bf16; v: low-rank products as
+// adapter_linear makes them, rows of Rq).
+bool adapter_can_tile(const tr_adapter_desc& d);
+hipError_t adapter_tiles(const tr_adapter_desc& d, const void* x, const void* w, const void* b,
+                         const int32_t* ids, const void* v, int Rq, void* y, hipStream_t st);
 size_t adapter_workspace(const tr_adapter_desc& d);
 hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w, const void* a,
                           const void* b, const int32_t* ids, const float* scales, void* y, void* ws,
