@@ -357,92 +357,138 @@ struct ShrinkArgs {
   int A, R, Rq;
 };
 
-// v[t, j] = s[a] x[t] . A[a][j] for a group of 16 NG tokens, one after another
-// for the different adapters among them (one or two where tokens of a request
-// are neighbours); up to 32 rows of A at a time, the waves sharing the
-// reduction. v is rounded to the storage type, to be an MFMA operand of the
-// tile's epilogue: its error is that of one rounding of the adapter's part.
-constexpr int kShrinkThreads = 512;
+// v[t, j] = s[a] x[t] . A[a][j] for a group of 32 tokens: up to 32 rows of A at
+// a time, the waves sharing the reduction, two batches of loads in flight.
+// Bound by x from memory and A from L2 (16 tokens a group, which read A twice
+// as often, took 58 us for 8192 x 7168 and rank 32, of which 41 us were A's
+// loads alone; x alone takes 25 us). The different adapters among the tokens (one where tokens of a request are
+// neighbours) are dealt to kSlots blocks, so that a group at the border of two
+// requests takes no longer than the others. v is rounded to the storage type,
+// to be an MFMA operand of the tile's epilogue: its error is that of one
+// rounding of the adapter's part.
+constexpr int kSlots = 2;
+constexpr int kShrinkThreads = 384;   // two blocks a CU
 constexpr int kShrinkWaves = kShrinkThreads / kWave;
 
-template <bool kF32, int NG>
-__global__ __launch_bounds__(kShrinkThreads) void adapter_shrink(ShrinkArgs p) {
+template <bool kF32>
+__global__ __launch_bounds__(kShrinkThreads, 3) void adapter_shrink(ShrinkArgs p) {
   typedef typename Elem<kF32>::type E;
   constexpr int kRT = 2;   // rank tiles of 16 at a time
-  __shared__ floatx4 red[kShrinkWaves][kRT][NG][kWave];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int kNG = 2;   // groups of 16 tokens
+  constexpr int kB = 3;    // 64-byte blocks of a batch (4: registers spill, 42 us; 2: 50 us; 3: 39 us)
+  __shared__ floatx4 red[kShrinkWaves][kRT][kNG][kWave];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int g = lane >> 4, r = lane & 15;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * 16 * NG;
-  const int id = lane < 16 * NG && t0 + lane < p.T ? p.ids[t0 + lane] : -1;
-  uint64_t todo = __ballot(id >= 0 && id < p.A);
-  const int nkb = static_cast<int>((p.row_bytes + 63) >> 6);
-  const int nfull = static_cast<int>(p.row_bytes >> 6);
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * 16 * kNG;
+  const int id = lane < 16 * kNG && t0 + lane < p.T ? p.ids[t0 + lane] : -1;
+  uint32_t todo = static_cast<uint32_t>(__ballot(id >= 0 && id < p.A));
+  const char* x0 = p.x + t0 * p.row_bytes;
+  const uint32_t row_bytes = static_cast<uint32_t>(p.row_bytes);
+  const int nkb = static_cast<int>((row_bytes + 63) >> 6);
+  const int nfull = static_cast<int>(row_bytes >> 6);
   const int kb0 = wave * nkb / kShrinkWaves, kb1 = (wave + 1) * nkb / kShrinkWaves;
   const int kbf = min(kb1, nfull);
-  while (todo) {
-    const int first = __ffsll(static_cast<unsigned long long>(todo)) - 1;
+  for (int slot = 0; todo; ++slot) {
+    const int first = __ffs(todo) - 1;
     const int aid = __builtin_amdgcn_readlane(id, first);
-    const uint64_t mask = __ballot(id == aid);
+    const uint32_t mask = static_cast<uint32_t>(__ballot(id == aid));
     todo &= ~mask;
+    if (slot % kSlots != static_cast<int>(blockIdx.y)) continue;
     // a token of another adapter reads the first one's row: not stored
-    const char* xp[NG];
+    uint32_t xo[kNG];
 #pragma unroll
-    for (int q = 0; q < NG; ++q)
-      xp[q] = p.x + (t0 + ((mask >> (16 * q + r)) & 1 ? 16 * q + r : first)) * p.row_bytes + g * 16;
+    for (int q = 0; q < kNG; ++q)
+      xo[q] = ((mask >> (16 * q + r)) & 1 ? 16 * q + r : first) * row_bytes + g * 16;
     const float sc = p.scales ? p.scales[aid] : 1.0f;
     for (int j0 = 0; j0 < p.Rq; j0 += 16 * kRT) {
-      const char* ap[kRT];
+      // rows past R read the last one: zeros are stored for them
+      const int base = min(j0, p.R - 1);
+      const char* a0 = p.a + (static_cast<int64_t>(aid) * p.R + base) * p.row_bytes;
+      uint32_t ao[kRT];
+#pragma unroll
+      for (int c = 0; c < kRT; ++c) ao[c] = min(c * 16 + r, p.R - 1 - base) * row_bytes + g * 16;
+      floatx4 acc[kRT][kNG];
 #pragma unroll
       for (int c = 0; c < kRT; ++c)
-        ap[c] = p.a + (static_cast<int64_t>(aid) * p.R + min(j0 + c * 16 + r, p.R - 1)) * p.row_bytes + g * 16;
-      floatx4 acc[kRT][NG];
 #pragma unroll
-      for (int c = 0; c < kRT; ++c)
+        for (int q = 0; q < kNG; ++q) acc[c][q] = floatx4{0, 0, 0, 0};
+      struct Batch {
+        u32x4 x[kNG][kB], a[kRT][kB];
+      } b0, b1;
+      // a share's last batch starts early enough to end with it; the products of
+      // blocks that it reads again are skipped
+      auto start = [&](int kb) { return min(kb, max(kbf - kB, 0)); };
+      auto load = [&](Batch& b, int kb) {
+        const uint32_t k = static_cast<uint32_t>(start(kb)) * 64;
 #pragma unroll
-        for (int q = 0; q < NG; ++q) acc[c][q] = floatx4{0, 0, 0, 0};
-      // the last batch may be short: it reads the last whole block again, and
-      // skips the products
-      for (int kb = kb0; kb < kbf; kb += kU) {
-        u32x4 xb[NG][kU], wa[kRT][kU];
+        for (int j = 0; j < kB; ++j) {
 #pragma unroll
-        for (int q = 0; q < NG; ++q)
+          for (int q = 0; q < kNG; ++q) b.x[q][j] = load16(x0 + (xo[q] + k) + j * 64);
 #pragma unroll
-          for (int j = 0; j < kU; ++j) xb[q][j] = load16(xp[q] + min(kb + j, kbf - 1) * 64);
-#pragma unroll
-        for (int c = 0; c < kRT; ++c)
-#pragma unroll
-          for (int j = 0; j < kU; ++j) wa[c][j] = load16(ap[c] + min(kb + j, kbf - 1) * 64);
+          for (int c = 0; c < kRT; ++c) b.a[c][j] = load16(a0 + (ao[c] + k) + j * 64);
+        }
         __builtin_amdgcn_sched_barrier(0);
+      };
+      auto mma = [&](const Batch& b, int kb) {
+        const int k = start(kb);
 #pragma unroll
-        for (int j = 0; j < kU; ++j)
-          if (kb + j < kbf) {
+        for (int j = 0; j < kB; ++j)
+          if (k + j >= kb && k + j < kbf) {
 #pragma unroll
             for (int c = 0; c < kRT; ++c)
 #pragma unroll
-              for (int q = 0; q < NG; ++q) acc[c][q] = mma16<kF32>(wa[c][j], xb[q][j], acc[c][q]);
+              for (int q = 0; q < kNG; ++q) acc[c][q] = mma16<kF32>(b.a[c][j], b.x[q][j], acc[c][q]);
+          }
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      if (nfull >= kB) {
+        if (kb0 < kbf) {
+          load(b0, kb0);
+          int kb = kb0;
+          for (; kb + 2 * kB < kbf; kb += 2 * kB) {
+            load(b1, kb + kB);
+            mma(b0, kb);
+            load(b0, kb + 2 * kB);
+            mma(b1, kb + kB);
+          }
+          if (kb + kB < kbf) {
+            load(b1, kb + kB);
+            mma(b0, kb);
+            mma(b1, kb + kB);
+          } else {
+            mma(b0, kb);
+          }
+        }
+      } else {   // rows of fewer blocks than a batch has
+        for (int kb = kb0; kb < kbf; ++kb)
+#pragma unroll
+          for (int q = 0; q < kNG; ++q) {
+            const u32x4 xv = load16(x0 + xo[q] + kb * 64);
+#pragma unroll
+            for (int c = 0; c < kRT; ++c)
+              acc[c][q] = mma16<kF32>(load16(a0 + ao[c] + kb * 64), xv, acc[c][q]);
           }
       }
       if (kb1 > nfull) {   // the short block at the end of the rows
-        const bool in = nfull * 64 + g * 16 < p.row_bytes;
+        const bool in = nfull * 64u + g * 16 < row_bytes;
 #pragma unroll
-        for (int c = 0; c < kRT; ++c) {
-          const u32x4 wa = in ? load16(ap[c] + nfull * 64) : u32x4{0, 0, 0, 0};
+        for (int q = 0; q < kNG; ++q) {
+          const u32x4 xv = in ? load16(x0 + xo[q] + nfull * 64) : u32x4{0, 0, 0, 0};
 #pragma unroll
-          for (int q = 0; q < NG; ++q) {
-            const u32x4 xb = in ? load16(xp[q] + nfull * 64) : u32x4{0, 0, 0, 0};
-            acc[c][q] = mma16<kF32>(wa, xb, acc[c][q]);
-          }
+          for (int c = 0; c < kRT; ++c)
+            acc[c][q] = mma16<kF32>(in ? load16(a0 + ao[c] + nfull * 64) : u32x4{0, 0, 0, 0}, xv, acc[c][q]);
         }
       }
 #pragma unroll
       for (int c = 0; c < kRT; ++c)
 #pragma unroll
-        for (int q = 0; q < NG; ++q) red[wave][c][q][lane] = acc[c][q];
+        for (int q = 0; q < kNG; ++q) red[wave][c][q][lane] = acc[c][q];
       __syncthreads();
-      // wave c + kRT q: rank tile c of token group q; columns past R are zero
+      // wave c + kRT q: rank tile c of token group q
       const int c = wave % kRT, q = wave / kRT;
       const int col = j0 + c * 16 + 4 * g;
-      if (q < NG && ((mask >> (16 * q + r)) & 1) && col < p.Rq) {
+      if (q < kNG && ((mask >> (16 * q + r)) & 1) && col < p.Rq) {
         floatx4 v = red[0][c][q][lane];
 #pragma unroll
         for (int w = 1; w < kShrinkWaves; ++w) v += red[w][c][q][lane];
@@ -488,7 +534,7 @@ struct Shape {
   // 1 KiB pieces (8 rows) of a stage that a wave loads
   static constexpr int kXp = kM / 8 / (WM * WN), kWp = kN / 8 / (WM * WN);
   static_assert(kXp * 8 * WM * WN == kM && kWp * 8 * WM * WN == kN, "whole pieces a wave");
-  static_assert((kStages - 2) * (kXp + kWp) <= 63, "vmcnt range");
+  static_assert((kStages - 1) * (kXp + kWp) <= 63, "vmcnt range");
 };
 
 typedef __attribute__((address_space(3))) void lds_ptr;
@@ -534,40 +580,55 @@ __device__ __forceinline__ void tile_dma(const TileLoad<C>& l, int wave, int kt,
         k + l.wc[j] < l.row_bytes ? l.wo[j] + k : kPast, 0, 0, 0);
 }
 
-// Step kt of the ring: its k-tile has landed once at most the DMA of the
-// kStages - 2 after it is in flight; after the barrier every wave has finished
-// with the k-tile before it, whose stage takes k-tile kt + kStages - 1. The
-// fragments of both 64-byte halves are asked for first, so that the second
-// half's reads and the DMA run beside the first half's products.
-template <bool kF32, typename C, int S>
-__device__ __forceinline__ void tile_step(const TileLoad<C>& l, int wave, int wm, int wn, int kt,
-                                          int k1, const int (&frag)[2],
-                                          floatx4 (&acc)[C::kMs][C::kNs]) {
-  constexpr int kLeft = (C::kStages - 2) * (C::kXp + C::kWp);
-  // s_waitcnt: vmcnt(kLeft), lgkmcnt(0), no wait for exports
-  __builtin_amdgcn_s_waitcnt((kLeft & 15) | ((kLeft >> 4) << 14) | 0x70);
+// A wave's fragments of half of a k-tile (64 bytes of every row).
+template <typename C>
+struct Frags {
+  u32x4 x[C::kMs], w[C::kNs];
+};
+template <typename C, int S>
+__device__ __forceinline__ void tile_read(Frags<C>& f, int wm, int wn, int frag) {
+#pragma unroll
+  for (int i = 0; i < C::kMs; ++i) f.x[i] = stage_x<C, S>()[(wm * C::kMs + i) * 16 * kLine + frag];
+#pragma unroll
+  for (int j = 0; j < C::kNs; ++j) f.w[j] = stage_w<C, S>()[(wn * C::kNs + j) * 16 * kLine + frag];
+  __builtin_amdgcn_sched_barrier(0);
+}
+template <bool kF32, typename C>
+__device__ __forceinline__ void tile_mma(const Frags<C>& f, floatx4 (&acc)[C::kMs][C::kNs]) {
+#pragma unroll
+  for (int i = 0; i < C::kMs; ++i)
+#pragma unroll
+    for (int j = 0; j < C::kNs; ++j) acc[i][j] = mma16<kF32>(f.w[j], f.x[i], acc[i][j]);
+  __builtin_amdgcn_sched_barrier(0);
+}
+// At most n DMA of this wave in flight, its LDS reads done; then every wave.
+template <int n>
+__device__ __forceinline__ void tile_wait() {
+  // s_waitcnt: vmcnt(n), lgkmcnt(0), no wait for exports
+  __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | 0x70);
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-  u32x4 fx[2][C::kMs], fw[2][C::kNs];
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-#pragma unroll
-    for (int i = 0; i < C::kMs; ++i)
-      fx[s][i] = stage_x<C, S>()[(wm * C::kMs + i) * 16 * kLine + frag[s]];
-#pragma unroll
-    for (int j = 0; j < C::kNs; ++j)
-      fw[s][j] = stage_w<C, S>()[(wn * C::kNs + j) * 16 * kLine + frag[s]];
-  }
+}
+
+// Step kt of the ring (stage S), its first half's fragments in f0. Fragments
+// are read half a k-tile ahead of their products, so that the LDS reads of all
+// waves run beside products and not before them. After the barrier in the
+// middle k-tile kt + 1 has landed (the DMA of the kStages - 2 after it may be in
+// flight) and every wave has read all of k-tile kt, whose stage takes k-tile
+// kt + kStages.
+template <bool kF32, typename C, int S>
+__device__ __forceinline__ void tile_step(const TileLoad<C>& l, int wave, int wm, int wn, int kt,
+                                          int k1, const int (&frag)[2], Frags<C>& f0,
+                                          floatx4 (&acc)[C::kMs][C::kNs]) {
+  Frags<C> f1;
+  tile_read<C, S>(f1, wm, wn, frag[1]);
+  tile_mma<kF32, C>(f0, acc);
+  tile_wait<(C::kStages - 2) * (C::kXp + C::kWp)>();
+  tile_read<C, (S + 1) % C::kStages>(f0, wm, wn, frag[0]);
+  tile_dma<C, S>(l, wave, kt + C::kStages, k1);
   __builtin_amdgcn_sched_barrier(0);
-  tile_dma<C, (S + C::kStages - 1) % C::kStages>(l, wave, kt + C::kStages - 1, k1);
-  __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-#pragma unroll
-    for (int i = 0; i < C::kMs; ++i)
-#pragma unroll
-      for (int j = 0; j < C::kNs; ++j) acc[i][j] = mma16<kF32>(fw[s][j], fx[s][i], acc[i][j]);
+  tile_mma<kF32, C>(f1, acc);
 }
 
 // Block `block` of m_tiles x n_tiles x parts: a tile over one part of the
@@ -626,15 +687,29 @@ __device__ __forceinline__ void tile_unit(const TileArgs& p, int block) {
     for (int j = 0; j < C::kNs; ++j) acc[i][j] = floatx4{0, 0, 0, 0};
 
   tile_dma<C, 0>(l, wave, k0, k1);
-  if constexpr (C::kStages > 2) tile_dma<C, 1>(l, wave, k0 + 1, k1);
-  if constexpr (C::kStages > 3) tile_dma<C, 2>(l, wave, k0 + 2, k1);
-  for (int kt = k0; kt < k1; kt += C::kStages) {
-    tile_step<kF32, C, 0>(l, wave, wm, wn, kt, k1, frag, acc);
-    if (kt + 1 < k1) tile_step<kF32, C, 1>(l, wave, wm, wn, kt + 1, k1, frag, acc);
+  tile_dma<C, 1>(l, wave, k0 + 1, k1);
+  if constexpr (C::kStages > 2) tile_dma<C, 2>(l, wave, k0 + 2, k1);
+  if constexpr (C::kStages > 3) tile_dma<C, 3>(l, wave, k0 + 3, k1);
+  tile_wait<(C::kStages - 1) * (C::kXp + C::kWp)>();
+  Frags<C> f0;
+  tile_read<C, 0>(f0, wm, wn, frag[0]);
+  // (whole turns of the ring in a loop without conditions, then the rest: a
+  // step that may not have run would make the compiler wait for every DMA)
+  int kt = k0;
+  for (; kt + C::kStages <= k1; kt += C::kStages) {
+    tile_step<kF32, C, 0>(l, wave, wm, wn, kt, k1, frag, f0, acc);
+    tile_step<kF32, C, 1>(l, wave, wm, wn, kt + 1, k1, frag, f0, acc);
+    if constexpr (C::kStages > 2) tile_step<kF32, C, 2>(l, wave, wm, wn, kt + 2, k1, frag, f0, acc);
+    if constexpr (C::kStages > 3) tile_step<kF32, C, 3>(l, wave, wm, wn, kt + 3, k1, frag, f0, acc);
+  }
+  if (kt < k1) {
+    tile_step<kF32, C, 0>(l, wave, wm, wn, kt, k1, frag, f0, acc);
     if constexpr (C::kStages > 2)
-      if (kt + 2 < k1) tile_step<kF32, C, 2>(l, wave, wm, wn, kt + 2, k1, frag, acc);
-    if constexpr (C::kStages > 3)
-      if (kt + 3 < k1) tile_step<kF32, C, 3>(l, wave, wm, wn, kt + 3, k1, frag, acc);
+      if (kt + 1 < k1) {
+        tile_step<kF32, C, 1>(l, wave, wm, wn, kt + 1, k1, frag, f0, acc);
+        if constexpr (C::kStages > 3)
+          if (kt + 2 < k1) tile_step<kF32, C, 2>(l, wave, wm, wn, kt + 2, k1, frag, f0, acc);
+      }
   }
   __builtin_amdgcn_s_waitcnt(0x0070);   // the DMA past the last k-tile
 
@@ -968,13 +1043,9 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
   s.A = d.A;
   s.R = d.R;
   s.Rq = L.Rq;
-  // 32 tokens a block read A half as often; 16 where that leaves CUs without one
-  const bool pairs = cdiv(d.T, 32) >= kPlanCus / 2;
-  const dim3 groups(static_cast<unsigned>(cdiv(d.T, pairs ? 32 : 16)));
-  if (f32 && pairs) hipLaunchKernelGGL((adapter_shrink<true, 2>), groups, dim3(kShrinkThreads), 0, st, s);
-  else if (f32) hipLaunchKernelGGL((adapter_shrink<true, 1>), groups, dim3(kShrinkThreads), 0, st, s);
-  else if (pairs) hipLaunchKernelGGL((adapter_shrink<false, 2>), groups, dim3(kShrinkThreads), 0, st, s);
-  else hipLaunchKernelGGL((adapter_shrink<false, 1>), groups, dim3(kShrinkThreads), 0, st, s);
+  const dim3 groups(static_cast<unsigned>(cdiv(d.T, 32)), kSlots);
+  if (f32) hipLaunchKernelGGL(adapter_shrink<true>, groups, dim3(kShrinkThreads), 0, st, s);
+  else hipLaunchKernelGGL(adapter_shrink<false>, groups, dim3(kShrinkThreads), 0, st, s);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if (adapter_can_tile(d)) return adapter_tiles(d, x, w, b, ids, ws, L.Rq, y, st);
   TileArgs t{};
