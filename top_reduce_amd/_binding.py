@@ -9,6 +9,7 @@ torch uint8 tensor; the library itself allocates nothing.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import math
 import os
 from typing import Optional, Tuple
@@ -492,6 +493,10 @@ def compact_rows(src: torch.Tensor, block_rows: int, block_counts: torch.Tensor,
 # ---------------------------------------------------------------------------
 # Router, whole layer, shared projection with adapters
 # ---------------------------------------------------------------------------
+# These calls run in a few microseconds on the GPU, so their own checks are kept
+# cheap: descriptors and workspace sizes are made once for each set of sizes, and
+# a tensor is compared with what its argument must be in one expression before
+# the error is worked out.
 _SCORES = {"softmax": 0, "sigmoid": 1}
 
 
@@ -502,62 +507,71 @@ def _need(query, desc) -> int:
     return int(n)
 
 
-def _workspace(ws: Optional[torch.Tensor], need: int, device) -> torch.Tensor:
+def _arg(t: torch.Tensor, name: str, dtype, shape, device) -> int:
+    """The address of a contiguous tensor of that type, shape and device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+        _dev_tensor(t, name, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, x on {device}")
+    return t.data_ptr()
+
+
+def _x_arg(x) -> torch.device:
+    """Checks the rows x that a call's other tensors go by; returns their device."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a [T, H] tensor")
+    if not x.is_cuda or not x.is_contiguous():
+        _dev_tensor(x, "x")
+    return x.device
+
+
+def _ws_arg(ws: Optional[torch.Tensor], need: int, device) -> torch.Tensor:
     if ws is None:
         return torch.empty(need, dtype=torch.uint8, device=device)
     _dev_tensor(ws, "ws", torch.uint8)
+    if ws.device != device:
+        raise ValueError(f"ws is on {ws.device}, x on {device}")
     return ws
 
 
-def _on_device(device, **tensors):
-    """Every tensor of a call is on x's device."""
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, x on {device}")
+def _raw_stream(stream, device) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _route_desc(x, w_gate, K, score, renorm, scale, idx_dtype) -> RouteDesc:
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        raise ValueError("x must be a [T, H] tensor")
-    if not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 2:
-        raise ValueError("w_gate must be a [G, H] tensor")
+def _route_sizes(T, H, G, K, dtype, score, renorm, scale, idx_dtype) -> RouteDesc:
     if score not in _SCORES:
         raise ValueError(f"score must be 'softmax' or 'sigmoid' (got {score!r})")
     if idx_dtype not in (torch.int32, torch.int64):
         raise TypeError("idx_dtype must be torch.int32 or torch.int64")
-    return RouteDesc(T=x.shape[0], H=x.shape[1], G=w_gate.shape[0], K=K,
-                     dtype=_dtype_code(x.dtype),
+    return RouteDesc(T=T, H=H, G=G, K=K, dtype=_dtype_code(dtype),
                      idx_dtype=IDX_I64 if idx_dtype == torch.int64 else IDX_I32,
                      score=_SCORES[score], renorm=1 if renorm else 0, scale=scale, reserved=0)
 
 
-def _route_buffers(d: RouteDesc, x, w_gate, bias, idx, weights, idx_dtype):
-    """Checks the router's tensors; returns the outputs (allocated if None)."""
-    dev = x.device
-    _dev_tensor(x, "x")
-    _dev_tensor(w_gate, "w_gate", x.dtype, (d.G, d.H))
-    if bias is not None:
-        _dev_tensor(bias, "bias", torch.float32, (d.G,))
-    if idx is None:
-        idx = torch.empty((d.T, d.K), dtype=idx_dtype, device=dev)
-    else:
-        _dev_tensor(idx, "idx", idx_dtype, (d.T, d.K))
-    if weights is None:
-        weights = torch.empty((d.T, d.K), dtype=torch.float32, device=dev)
-    else:
-        _dev_tensor(weights, "weights", torch.float32, (d.T, d.K))
-    _on_device(dev, w_gate=w_gate, bias=bias, idx=idx, weights=weights)
-    return idx, weights
+@functools.lru_cache(maxsize=512)
+def _route_plan(*sizes):
+    d = _route_sizes(*sizes)
+    return d, C.byref(d), _need(load_library().moe_route_topk_workspace, d)
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr() or None
+@functools.lru_cache(maxsize=512)
+def _layer_plan(E, I, expert_begin, *sizes):
+    d = LayerDesc(route=_route_sizes(*sizes), I=I, expert_begin=expert_begin, E=E, reserved=0)
+    return d, C.byref(d), _need(load_library().moe_layer_workspace, d)
+
+
+@functools.lru_cache(maxsize=512)
+def _adapter_plan(T, H, N, R, A, dtype):
+    d = AdapterDesc(T=T, H=H, N=N, R=R, A=A, dtype=_dtype_code(dtype), reserved=0)
+    return d, C.byref(d), _need(load_library().moe_adapter_linear_workspace, d)
 
 
 def route_workspace_size(T: int, H: int, G: int, K: int, dtype=torch.bfloat16) -> int:
     """Bytes of ws for route_topk of these sizes."""
-    d = RouteDesc(T=T, H=H, G=G, K=K, dtype=_dtype_code(dtype), idx_dtype=IDX_I64, scale=1.0)
-    return _need(load_library().moe_route_topk_workspace, d)
+    return _route_plan(T, H, G, K, dtype, "softmax", True, 1.0, torch.int64)[2]
 
 
 def route_topk(x: torch.Tensor, w_gate: torch.Tensor, K: int, bias: Optional[torch.Tensor] = None,
@@ -572,30 +586,32 @@ def route_topk(x: torch.Tensor, w_gate: torch.Tensor, K: int, bias: Optional[tor
     The K best are chosen in descending order, ties to the lowest id; with a
     bias (fp32 [G]) by score + bias. The weights are the scores, divided by
     their sum with renorm, times scale. idx is what plan() takes."""
-    d = _route_desc(x, w_gate, K, score, renorm, scale, idx_dtype)
-    lib = load_library()
-    need = _need(lib.moe_route_topk_workspace, d)
-    idx, weights = _route_buffers(d, x, w_gate, bias, idx, weights, idx_dtype)
-    ws = _workspace(ws, need, x.device)
-    _on_device(x.device, ws=ws)
-    _check(lib.moe_route_topk(C.byref(d), _ptr(x), _ptr(w_gate), _ptr(bias), _ptr(idx),
-                              _ptr(weights), _ptr(ws), ws.numel(), _stream_ptr(stream, x.device)))
+    dev = _x_arg(x)
+    if not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 2:
+        raise ValueError("w_gate must be a [G, H] tensor")
+    T, H = x.shape
+    G, dt = w_gate.shape[0], x.dtype
+    _, desc, need = _route_plan(T, H, G, K, dt, score, renorm, scale, idx_dtype)
+    gp = _arg(w_gate, "w_gate", dt, (G, H), dev)
+    bp = None if bias is None else _arg(bias, "bias", torch.float32, (G,), dev)
+    if idx is None:
+        idx = torch.empty((T, K), dtype=idx_dtype, device=dev)
+    if weights is None:
+        weights = torch.empty((T, K), dtype=torch.float32, device=dev)
+    ip = _arg(idx, "idx", idx_dtype, (T, K), dev)
+    wp = _arg(weights, "weights", torch.float32, (T, K), dev)
+    ws = _ws_arg(ws, need, dev)
+    status = _lib.moe_route_topk(desc, x.data_ptr(), gp, bp, ip, wp, ws.data_ptr(), ws.numel(),
+                                 _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return idx, weights
-
-
-def _layer_desc(x, w_gate, w1, K, score, renorm, scale, idx_dtype, expert_begin) -> LayerDesc:
-    if not isinstance(w1, torch.Tensor) or w1.dim() != 3 or w1.shape[1] % 2:
-        raise ValueError("w1 must be an [E, 2I, H] tensor")
-    return LayerDesc(route=_route_desc(x, w_gate, K, score, renorm, scale, idx_dtype),
-                     I=w1.shape[1] // 2, expert_begin=expert_begin, E=w1.shape[0], reserved=0)
 
 
 def layer_workspace_size(T: int, H: int, I: int, E: int, G: int, K: int,
                          dtype=torch.bfloat16) -> int:
     """Bytes of ws for layer of these sizes."""
-    d = LayerDesc(route=RouteDesc(T=T, H=H, G=G, K=K, dtype=_dtype_code(dtype), idx_dtype=IDX_I64,
-                                  scale=1.0), I=I, expert_begin=0, E=E)
-    return _need(load_library().moe_layer_workspace, d)
+    return _layer_plan(E, I, 0, T, H, G, K, dtype, "softmax", True, 1.0, torch.int64)[2]
 
 
 def layer(x: torch.Tensor, w_gate: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor, K: int,
@@ -609,29 +625,39 @@ def layer(x: torch.Tensor, w_gate: torch.Tensor, w1: torch.Tensor, w2: torch.Ten
     route_topk and then the local experts [expert_begin, expert_begin + E)
     (w1 [E, 2I, H] gate | up, w2 [E, H, I]) and their weighted sum. Rows
     without a local expert are +0. y may be x."""
-    d = _layer_desc(x, w_gate, w1, K, score, renorm, scale, idx_dtype, expert_begin)
-    lib = load_library()
-    need = _need(lib.moe_layer_workspace, d)
-    r = d.route
-    idx, weights = _route_buffers(r, x, w_gate, bias, idx, weights, idx_dtype)
-    _dev_tensor(w1, "w1", x.dtype, (d.E, 2 * d.I, r.H))
-    _dev_tensor(w2, "w2", x.dtype, (d.E, r.H, d.I))
+    dev = _x_arg(x)
+    if not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 2:
+        raise ValueError("w_gate must be a [G, H] tensor")
+    if not isinstance(w1, torch.Tensor) or w1.dim() != 3 or w1.shape[1] % 2:
+        raise ValueError("w1 must be an [E, 2I, H] tensor")
+    T, H = x.shape
+    G, dt = w_gate.shape[0], x.dtype
+    E, I = w1.shape[0], w1.shape[1] // 2
+    _, desc, need = _layer_plan(E, I, expert_begin, T, H, G, K, dt, score, renorm, scale, idx_dtype)
+    gp = _arg(w_gate, "w_gate", dt, (G, H), dev)
+    bp = None if bias is None else _arg(bias, "bias", torch.float32, (G,), dev)
+    w1p = _arg(w1, "w1", dt, (E, 2 * I, H), dev)
+    w2p = _arg(w2, "w2", dt, (E, H, I), dev)
+    if idx is None:
+        idx = torch.empty((T, K), dtype=idx_dtype, device=dev)
+    if weights is None:
+        weights = torch.empty((T, K), dtype=torch.float32, device=dev)
     if y is None:
         y = torch.empty_like(x)
-    else:
-        _dev_tensor(y, "y", x.dtype, (r.T, r.H))
-    ws = _workspace(ws, need, x.device)
-    _on_device(x.device, w1=w1, w2=w2, y=y, ws=ws)
-    _check(lib.moe_layer(C.byref(d), _ptr(x), _ptr(w_gate), _ptr(bias), _ptr(w1), _ptr(w2),
-                         _ptr(y), _ptr(idx), _ptr(weights), _ptr(ws), ws.numel(),
-                         _stream_ptr(stream, x.device)))
+    ip = _arg(idx, "idx", idx_dtype, (T, K), dev)
+    wp = _arg(weights, "weights", torch.float32, (T, K), dev)
+    yp = _arg(y, "y", dt, (T, H), dev)
+    ws = _ws_arg(ws, need, dev)
+    status = _lib.moe_layer(desc, x.data_ptr(), gp, bp, w1p, w2p, yp, ip, wp, ws.data_ptr(),
+                            ws.numel(), _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return y, idx, weights
 
 
 def adapter_workspace_size(T: int, H: int, N: int, R: int, A: int, dtype=torch.bfloat16) -> int:
     """Bytes of ws for adapter_linear of these sizes."""
-    return _need(load_library().moe_adapter_linear_workspace,
-                 AdapterDesc(T=T, H=H, N=N, R=R, A=A, dtype=_dtype_code(dtype)))
+    return _adapter_plan(T, H, N, R, A, dtype)[2]
 
 
 def adapter_linear(x: torch.Tensor, w: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
@@ -641,35 +667,28 @@ def adapter_linear(x: torch.Tensor, w: torch.Tensor, a: torch.Tensor, b: torch.T
     """moe_adapter_linear: y [T, N] = x w^T + scales[i] (x a[i]^T) b[i]^T with
     i = ids[t] (int32 [T]; outside [0, A): no adapter). x [T, H], w [N, H],
     a [A, R, H], b [A, N, R], scales fp32 [A] or None for 1."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        raise ValueError("x must be a [T, H] tensor")
+    dev = _x_arg(x)
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("w must be an [N, H] tensor")
     if not isinstance(a, torch.Tensor) or a.dim() != 3:
         raise ValueError("a must be an [A, R, H] tensor")
     T, H = x.shape
-    N = w.shape[0]
-    n, R = a.shape[0], a.shape[1]
-    dev, dt = x.device, x.dtype
-    d = AdapterDesc(T=T, H=H, N=N, R=R, A=n, dtype=_dtype_code(dt), reserved=0)
-    lib = load_library()
-    need = _need(lib.moe_adapter_linear_workspace, d)
-    _dev_tensor(x, "x")
-    _dev_tensor(w, "w", dt, (N, H))
-    _dev_tensor(a, "a", dt, (n, R, H))
-    _dev_tensor(b, "b", dt, (n, N, R))
-    _dev_tensor(ids, "ids", torch.int32, (T,))
-    if scales is not None:
-        _dev_tensor(scales, "scales", torch.float32, (n,))
+    N, dt = w.shape[0], x.dtype
+    A, R = a.shape[0], a.shape[1]
+    _, desc, need = _adapter_plan(T, H, N, R, A, dt)
+    wp = _arg(w, "w", dt, (N, H), dev)
+    ap = _arg(a, "a", dt, (A, R, H), dev)
+    bp = _arg(b, "b", dt, (A, N, R), dev)
+    ip = _arg(ids, "ids", torch.int32, (T,), dev)
+    sp = None if scales is None else _arg(scales, "scales", torch.float32, (A,), dev)
     if y is None:
         y = torch.empty((T, N), dtype=dt, device=dev)
-    else:
-        _dev_tensor(y, "y", dt, (T, N))
-    ws = _workspace(ws, need, dev)
-    _on_device(dev, w=w, a=a, b=b, ids=ids, scales=scales, y=y, ws=ws)
-    _check(lib.moe_adapter_linear(C.byref(d), _ptr(x), _ptr(w), _ptr(a), _ptr(b), _ptr(ids),
-                                  _ptr(scales), _ptr(y), _ptr(ws), ws.numel(),
-                                  _stream_ptr(stream, dev)))
+    yp = _arg(y, "y", dt, (T, N), dev)
+    ws = _ws_arg(ws, need, dev)
+    status = _lib.moe_adapter_linear(desc, x.data_ptr(), wp, ap, bp, ip, sp, yp, ws.data_ptr(),
+                                     ws.numel(), _raw_stream(stream, dev))
+    if status:
+        _check(status)
     return y
 
 

@@ -637,13 +637,9 @@ tr_status moe_layer(const tr_layer_desc* desc, const void* x, const void* w_gate
   if ((s = check_buf(y, "y", true)) != TR_OK) return s;
   char* ews = static_cast<char*>(ws) + L.experts;
   if (desc->route.T <= tr::kFewTokens) {
-    const tr::FewRoutes f = tr::few_routes(*desc, ews);
-    if ((s = hip_status(tr::route_topk(desc->route, x, w_gate, bias, topk_idx, topk_weights, ws,
-                                       stream, &f),
-                        "moe_layer router launch")) != TR_OK)
-      return s;
-    return hip_status(tr::few_experts(*desc, x, w1, w2, topk_weights, y, ews, stream),
-                      "moe_layer experts launch");
+    return hip_status(tr::few_layer(*desc, x, w_gate, bias, w1, w2, y, topk_idx, topk_weights, ws, ews,
+                                    stream),
+                      "moe_layer launch");
   }
   if ((s = hip_status(tr::route_topk(desc->route, x, w_gate, bias, topk_idx, topk_weights, ws, stream),
                       "moe_layer router launch")) != TR_OK)

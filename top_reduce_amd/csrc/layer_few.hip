@@ -1,7 +1,9 @@
 // The local experts of a mixture-of-experts layer for at most 64 tokens, from
-// the router's choice to the output, in two launches:
+// the router's logits to the output, in two launches:
 //
-//   few_up:    h[t, e] = w[t, e] silu(W1g[e] x[t]) * (W1u[e] x[t])
+//   few_up:    the choice, where it is little work for every block to make it
+//              (else it is there already, from a launch of its own)
+//              h[t, e] = w[t, e] silu(W1g[e] x[t]) * (W1u[e] x[t])
 //   few_down:  y[t]    = sum over the token's local experts e: W2[e] h[t, e]
 //
 // Bound: reading the weights of the experts that some token chose, once. The
@@ -18,6 +20,7 @@
 // if h had never been rounded.
 #include "tr_chunk.h"
 #include "tr_internal.h"
+#include "tr_select.h"
 
 namespace tr {
 namespace {
@@ -35,7 +38,7 @@ struct FewArgs {
   const char* x;                     // [T, H]
   const void* w1;                    // [E, 2 I, H]
   const void* w2;                    // [E, H, I]
-  const unsigned long long* masks;   // [E] tokens of each local expert
+  unsigned long long* masks;         // [E] tokens of each local expert
   const uint8_t* slots;              // [E, 64] slot of token t that names expert e
   const float* w;                    // [T, K] gate weights
   char* h;                           // [routes][parts][Ip]
@@ -52,16 +55,17 @@ struct Groups {
   int rank[kMaxGroups];        // that token's rank among the expert's
 };
 
-// Fills `s`; returns the number of groups. tmp: LDS of kBlock / 64 ints.
+// Fills `s` from masks (E of them); returns the number of groups. tmp: LDS of
+// kBlock / 64 ints.
 template <int kBlock>
-__device__ __forceinline__ int find_groups(const FewArgs& a, Groups& s, int* tmp) {
+__device__ __forceinline__ int find_groups(const unsigned long long* masks, int E, Groups& s, int* tmp) {
   constexpr int kPer = (kMaxE + kBlock - 1) / kBlock;
-  const int per = (a.E + kBlock - 1) / kBlock;
+  const int per = (E + kBlock - 1) / kBlock;
   uint64_t m[kPer];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int e = static_cast<int>(threadIdx.x) * per + j;
-    m[j] = j < per && e < a.E ? a.masks[e] : 0;
+    m[j] = j < per && e < E ? masks[e] : 0;
   }
   // routes and groups of the experts before: one scan of both (at most 2048
   // routes and 1152 groups)
@@ -101,14 +105,42 @@ __device__ __forceinline__ int group_token(uint64_t mask, int rank, int n) {
   return __shfl(by_rank, rank + (r < n ? r : 0), kWave);
 }
 
+// Up to this many tokens (one a wave) and experts few_up makes the choice: every
+// block repeats it, 2.5 us, which is less than the launch that it saves (about
+// 5 us on the GPU, 3 on the host). Two tokens a wave cost as much as the launch,
+// four more (16 tokens of 8 experts: 11.1 us instead of 5.6 + 3.2).
+constexpr int kChooseTokens = kWaves;
+constexpr int kChooseGates = 256;
+
 // A unit: 16 gate rows and the matching 16 up rows of one group's expert, the
-// reduction over the block's waves.
-template <bool kF32>
-__global__ __launch_bounds__(kThreads, 3) void few_up(FewArgs a) {
+// reduction over the block's waves. NR > 0: every block makes the tokens'
+// choice from the logits' parts (NR registers a lane); block 0 stores it.
+template <bool kF32, int NR>
+__global__ __launch_bounds__(kThreads, 3) void few_up(FewArgs a, SelectArgs sel, int64_t begin) {
   __shared__ Groups s;
   __shared__ int tmp[kWaves];
   __shared__ floatx4 red[kWaves][2][kWave];
-  const int n_groups = find_groups<kThreads>(a, s, tmp);
+  __shared__ unsigned long long mask_s[NR ? kChooseGates : 1];
+  __shared__ float w_s[NR ? kChooseGates * kChooseTokens : 1];   // [local expert][token]
+  __shared__ SelectScratch scratch[NR ? kWaves : 1];
+  if constexpr (NR > 0) {
+    for (int e = threadIdx.x; e < a.E; e += kThreads) mask_s[e] = 0;
+    __syncthreads();
+    const int t = threadIdx.x >> 6;
+    if (t < a.T) {
+      const Chosen c = choose<NR>(sel, t, scratch[t]);
+      if (blockIdx.x == 0) store_chosen(sel, t, c);
+      const int64_t e = c.e - begin;
+      if (c.rank >= 0 && e >= 0 && e < a.E) {
+        atomicOr(&mask_s[e], 1ull << t);
+        w_s[e * a.T + t] = c.w;
+      }
+    }
+    __syncthreads();
+    if (blockIdx.x == 0)
+      for (int e = threadIdx.x; e < a.E; e += kThreads) a.masks[e] = mask_s[e];
+  }
+  const int n_groups = find_groups<kThreads>(NR ? mask_s : a.masks, a.E, s, tmp);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int g = lane >> 4, r = lane & 15;
@@ -208,7 +240,7 @@ __global__ __launch_bounds__(kThreads, 3) void few_up(FewArgs a) {
         vg += red[w][0][lane];
         vu += red[w][1][lane];
       }
-      const float wt = a.w[t * a.K + a.slots[e * 64 + t]];
+      const float wt = NR ? w_s[e * a.T + t] : a.w[t * a.K + a.slots[e * 64 + t]];
       const int64_t col = c * 16 + 4 * g;
       const int64_t row = s.row[q] + r;
       floatx4 v;
@@ -257,7 +289,7 @@ __global__ __launch_bounds__(kDownThreads, 3) void few_down(FewArgs a) {
   __shared__ Groups s;
   __shared__ int tmp[kDownWaves];
   __shared__ floatx4 sum[kDownWaves][kFewTokens][4];
-  const int n_groups = find_groups<kDownThreads>(a, s, tmp);
+  const int n_groups = find_groups<kDownThreads>(a.masks, a.E, s, tmp);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int g = lane >> 4, r = lane & 15;
@@ -395,14 +427,20 @@ __global__ __launch_bounds__(kDownThreads, 3) void few_down(FewArgs a) {
 }
 
 template <bool kF32>
-hipError_t launch_few(const FewArgs& a, hipStream_t st) {
+hipError_t launch_few(const FewArgs& a, const SelectArgs* sel, int64_t begin, hipStream_t st) {
   const int cus = device_cu_count();
   const int64_t most = static_cast<int64_t>(a.T) * a.K < a.E ? static_cast<int64_t>(a.T) * a.K
                                                              : a.E + static_cast<int64_t>(a.T) * a.K / 16;
   const int64_t u1 = most * (a.Ip / 16), u2 = cdiv(a.H, 16);
-  const unsigned g1 = static_cast<unsigned>(u1 < 4 * cus ? u1 : 4 * cus);
+  // as many blocks as fit at once
+  const unsigned g1 = static_cast<unsigned>(u1 < 3 * cus ? u1 : 3 * cus);
   const unsigned g2 = static_cast<unsigned>(u2 < 2 * cus ? u2 : 2 * cus);
-  hipLaunchKernelGGL(few_up<kF32>, dim3(g1), dim3(kThreads), 0, st, a);
+  if (!sel)
+    hipLaunchKernelGGL((few_up<kF32, 0>), dim3(g1), dim3(kThreads), 0, st, a, SelectArgs{}, begin);
+  else if (sel->G <= 64)
+    hipLaunchKernelGGL((few_up<kF32, 1>), dim3(g1), dim3(kThreads), 0, st, a, *sel, begin);
+  else
+    hipLaunchKernelGGL((few_up<kF32, 4>), dim3(g1), dim3(kThreads), 0, st, a, *sel, begin);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (a.I % Elem<kF32>::kChunk == 0)
@@ -435,17 +473,19 @@ FewLayout few_layout(const tr_layer_desc& d) {
 
 size_t few_workspace(const tr_layer_desc& d) { return few_layout(d).total; }
 
-FewRoutes few_routes(const tr_layer_desc& d, void* ws) {
+hipError_t few_layer(const tr_layer_desc& d, const void* x, const void* w_gate, const float* bias,
+                     const void* w1, const void* w2, void* y, void* idx, float* w, void* route_ws,
+                     void* ws, hipStream_t st) {
   const FewLayout L = few_layout(d);
+  const tr_route_desc& r = d.route;
+  const bool f32 = r.dtype == TR_F32;
   char* b = static_cast<char*>(ws);
-  return FewRoutes{reinterpret_cast<unsigned long long*>(b + L.masks),
-                   reinterpret_cast<uint8_t*>(b + L.slots), d.expert_begin, d.E};
-}
-
-hipError_t few_experts(const tr_layer_desc& d, const void* x, const void* w1, const void* w2,
-                       const float* w, void* y, void* ws, hipStream_t st) {
-  const FewLayout L = few_layout(d);
-  const FewRoutes f = few_routes(d, ws);
+  const FewRoutes f{reinterpret_cast<unsigned long long*>(b + L.masks),
+                    reinterpret_cast<uint8_t*>(b + L.slots), d.expert_begin, d.E};
+  const bool fused = r.T <= kChooseTokens && r.G <= kChooseGates;
+  hipError_t e = fused ? logits(r.T, r.H, r.G, f32, x, w_gate, static_cast<float*>(route_ws), nullptr, 0, st)
+                       : route_topk(r, x, w_gate, bias, idx, w, route_ws, st, &f);
+  if (e != hipSuccess) return e;
   FewArgs a{};
   a.x = static_cast<const char*>(x);
   a.w1 = w1;
@@ -453,15 +493,17 @@ hipError_t few_experts(const tr_layer_desc& d, const void* x, const void* w1, co
   a.masks = f.masks;
   a.slots = f.slots;
   a.w = w;
-  a.h = static_cast<char*>(ws) + L.h;
+  a.h = b + L.h;
   a.y = y;
-  a.T = static_cast<int>(d.route.T);
-  a.K = d.route.K;
+  a.T = static_cast<int>(r.T);
+  a.K = r.K;
   a.E = d.E;
-  a.H = d.route.H;
+  a.H = r.H;
   a.I = d.I;
   a.Ip = L.Ip;
-  return d.route.dtype == TR_F32 ? launch_few<true>(a, st) : launch_few<false>(a, st);
+  const SelectArgs sel = select_args(r, bias, idx, w, route_ws);
+  return f32 ? launch_few<true>(a, fused ? &sel : nullptr, d.expert_begin, st)
+             : launch_few<false>(a, fused ? &sel : nullptr, d.expert_begin, st);
 }
 
 }  // namespace tr

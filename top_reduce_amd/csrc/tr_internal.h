@@ -95,11 +95,15 @@ size_t route_workspace(const tr_route_desc& d);
 hipError_t route_topk(const tr_route_desc& d, const void* x, const void* w_gate, const float* bias,
                       void* idx, float* w, void* ws, hipStream_t st, const FewRoutes* few = nullptr);
 
+struct SelectArgs;   // tr_select.h
+SelectArgs select_args(const tr_route_desc& d, const float* bias, void* idx, float* w, const void* ws);
+
+// A whole layer of at most kFewTokens rows. route_ws: route_workspace bytes; ws:
+// few_workspace bytes.
 size_t few_workspace(const tr_layer_desc& d);
-FewRoutes few_routes(const tr_layer_desc& d, void* ws);
-// The local experts of the routes in ws (few_routes): y, complete.
-hipError_t few_experts(const tr_layer_desc& d, const void* x, const void* w1, const void* w2,
-                       const float* w, void* y, void* ws, hipStream_t st);
+hipError_t few_layer(const tr_layer_desc& d, const void* x, const void* w_gate, const float* bias,
+                     const void* w1, const void* w2, void* y, void* idx, float* w, void* route_ws,
+                     void* ws, hipStream_t st);
 
 // The shared projection on the grouped GEMM's 256 x 256 tiles: whether its shape
 // allows that and gives at least two tiles a CU (bf16; v: low-rank products as
