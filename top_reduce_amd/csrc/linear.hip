@@ -645,7 +645,12 @@ __device__ __forceinline__ void tile_unit(const TileArgs& p, int block) {
 
   const int total = p.m_tiles * p.n_tiles;
   const int s = block / total, pos = block % total;
-  const int mt = pos / p.n_tiles, nt = pos % p.n_tiles;
+  // groups of 1024 tokens, token tiles fastest: the tiles that an XCD runs at a
+  // time share rows of both operands in its L2
+  constexpr int kGroup = 1024 / C::kM;
+  const int group = pos / (kGroup * p.n_tiles), in = pos - group * kGroup * p.n_tiles;
+  const int gm = min(kGroup, p.m_tiles - group * kGroup);
+  const int mt = group * kGroup + in % gm, nt = in / gm;
   const int64_t t0 = static_cast<int64_t>(mt) * C::kM;
   const int n0 = nt * C::kN;
   const int rows = static_cast<int>(min(static_cast<int64_t>(C::kM), p.T - t0));
@@ -771,8 +776,7 @@ template <bool kF32, typename C, bool kAdapt>
 __global__ __launch_bounds__(C::kBlock) void linear_tile(TileArgs p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   // blocks are dealt round-robin to the 8 XCDs: each XCD gets a run of the
-  // order (weight tiles fastest: a run shares tokens); the grid is a multiple
-  // of 8
+  // order; the grid is a multiple of 8
   const int per = gridDim.x >> 3;
   const int block = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
   if (block < p.m_tiles * p.n_tiles * p.parts) tile_unit<kF32, C, kAdapt>(p, block);
@@ -1062,6 +1066,11 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
   t.A = d.A;
   t.R = d.R;
   t.Rq = L.Rq;
+  // the largest tiles of which there is one for each CU: 8192 x 7160 x 7000 takes
+  // 1035 us on the wide ones and 1189 us on the middle ones, 1000 x 5000 x 6001
+  // (376 middle tiles) 140 us on the middle and 181 us on the small ones
+  if (cdiv(d.T, WideShape::kM) * cdiv(d.N, WideShape::kN) >= kPlanCus && row_bytes <= (int64_t{1} << 23))
+    return f32 ? launch_tile<true, WideShape, true>(t, st) : launch_tile<false, WideShape, true>(t, st);
   if (cdiv(d.T, MidShape::kM) * cdiv(d.N, MidShape::kN) >= kPlanCus)
     return f32 ? launch_tile<true, MidShape, true>(t, st) : launch_tile<false, MidShape, true>(t, st);
   return f32 ? launch_tile<true, SmallShape, true>(t, st) : launch_tile<false, SmallShape, true>(t, st);

@@ -9,12 +9,13 @@
 // Expert 64 i + lane is in register i. Keys are compared as integers that order
 // like the floats, NaN below everything, so that every token gets K different
 // valid ids. The K-th largest of the lanes' largest keys is a bound that at
-// least K keys reach; the keys that reach it, seldom many more than K, are
-// gathered into one register, lowest id first, and each one's place is the
-// number of keys before it. That is two counting loops of independent steps
-// instead of K rounds of a reduction over the wave: choosing 16 of 896 took
-// 3.9 us in rounds of 0.25 us. Where over 64 keys reach the bound (many equal
-// ones) the rounds are taken.
+// least K keys reach (for K up to 8 a lower one that is quicker to find serves:
+// the least of eight groups' largest keys). The keys that reach it, seldom many
+// more than K, are gathered into one register, lowest id first, and each one's
+// place is the number of keys before it. These are counting loops of independent
+// steps, not K rounds of a reduction over the wave: choosing 16 of 896 took
+// 3.9 us in rounds of 0.25 us (the whole kernel 8.3 us, now 5.2). Where over 64
+// keys reach the bound (many equal ones) the rounds are taken.
 #pragma once
 
 #include <type_traits>
@@ -55,6 +56,13 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t u = __float_as_uint(v);
   if ((u & 0x7fffffffu) > 0x7f800000u) return kNan;
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+// Lanes moved within rows of 16 by DPP.
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp_move(uint32_t v) {
+  return static_cast<uint32_t>(
+      __builtin_amdgcn_update_dpp(0, static_cast<int>(v), kCtrl, 0xf, 0xf, false));
 }
 
 // Reductions over the 64 lanes by row operations: lanes swapped within rows of
@@ -168,9 +176,20 @@ __device__ __forceinline__ Chosen choose(const SelectArgs& a, int64_t t, SelectS
   int c_id = lane, c_n = a.G;
   float c_v = v[0];
   if constexpr (NR > 1) {
-    // the lanes with fewer than K larger lane maxima; the least of their maxima
-    const int larger = count_larger(best, kWave);
-    const uint32_t bound = wave_min(larger < a.K ? best : ~0u);
+    uint32_t bound;
+    if (a.K <= 8) {
+      // the least of the maxima of 8 groups of 8 lanes: it takes about 8 (1 + 1/2
+      // + .. + 1/8) = 22 of the largest keys, dealt to 8 groups, to reach them all
+      uint32_t g = best;
+      g = max(g, dpp_move<0xb1>(g));
+      g = max(g, dpp_move<0x4e>(g));
+      g = max(g, dpp_move<0x141>(g));
+      bound = wave_min(g);
+    } else {
+      // the least of the lane maxima with fewer than K larger ones
+      const int larger = count_larger(best, kWave);
+      bound = wave_min(larger < a.K ? best : ~0u);
+    }
     c_n = 0;
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
