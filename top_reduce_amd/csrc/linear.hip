@@ -28,6 +28,13 @@ constexpr int kU = 8;   // 64-byte k-blocks of one batch of loads
 // --------------------------------------------------------------------------
 // A few tokens
 // --------------------------------------------------------------------------
+// Up to 16 of a chunk's 64 tokens that have one adapter, or none (aid -1);
+// n = 0: no unit.
+struct AdapterUnit {
+  int aid, n;
+  int tok[16];   // in the chunk
+};
+
 struct StreamArgs {
   const char* x;         // [T, H]
   const char* w;         // [N, H]
@@ -41,17 +48,24 @@ struct StreamArgs {
   const char* a;         // [A, R, H]
   float* vpart;          // [S, T, Rp]
   int A, R, Rp, rank_tiles;
+  AdapterUnit* units;    // [chunks, n_units], for the kernel that follows
+  int n_units, chunks;
   // memory that the next kernel wants zeroed
   uint32_t* zero;
   int n_zero;
 };
 
-// Lane t: the tokens (of n, lane t's id in `id`) with the same id as t.
+// Lane t: the lanes with the same id as t (lanes without a token have an id
+// that no token has; n: the lanes that count, rounded up to 8).
 __device__ __forceinline__ uint64_t same_id(int id, int n) {
-  uint32_t lo = 0, hi = 0;
-  for (int j = 0; j < min(n, 32); ++j) lo |= (id == __builtin_amdgcn_readlane(id, j) ? 1u : 0u) << j;
-  for (int j = 32; j < n; ++j) hi |= (id == __builtin_amdgcn_readlane(id, j) ? 1u : 0u) << (j - 32);
-  return static_cast<uint64_t>(hi) << 32 | lo;
+  uint64_t same = 0;
+  for (int j0 = 0; j0 < n; j0 += 8) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m |= (id == __builtin_amdgcn_readlane(id, j0 + j) ? 1u : 0u) << j;
+    same |= static_cast<uint64_t>(m) << j0;
+  }
+  return same;
 }
 // Lane `from`'s v, in every lane.
 __device__ __forceinline__ uint64_t lane_u64(uint64_t v, int from) {
@@ -62,6 +76,33 @@ __device__ __forceinline__ uint64_t lane_u64(uint64_t v, int from) {
 __device__ __forceinline__ int nth_bit(uint64_t m, int u) {
   const uint64_t hit = __ballot(((m >> lane_id()) & 1) && popc_below(m) == u);
   return __ffsll(static_cast<unsigned long long>(hit)) - 1;
+}
+
+// One wave: the units of a chunk's tokens, one for each adapter (tokens without
+// one are alike) and for every further 16 of its tokens.
+__device__ __forceinline__ void make_units(const StreamArgs& p, int chunk) {
+  const int lane = lane_id();
+  const int64_t t0 = static_cast<int64_t>(chunk) * kFewTokens;
+  const int n_tok = static_cast<int>(min(static_cast<int64_t>(kFewTokens), p.T - t0));
+  int id = lane < n_tok ? p.ids[t0 + lane] : -2;
+  if (lane < n_tok && (id < 0 || id >= p.A)) id = -1;
+  AdapterUnit* out = p.units + static_cast<int64_t>(chunk) * p.n_units;
+  const uint64_t same = same_id(id, n_tok);
+  const int rank = __popcll(same & ((1ull << lane) - 1));
+  uint64_t leads = __ballot(lane < n_tok && rank % 16 == 0);
+  int u = 0;
+  for (; leads; leads &= leads - 1, ++u) {
+    const int lead = __ffsll(static_cast<unsigned long long>(leads)) - 1;
+    const int first = __builtin_amdgcn_readlane(rank, lead);
+    const uint64_t tokens = lane_u64(same, lead);
+    const int at = popc_below(tokens) - first;
+    if (((tokens >> lane) & 1) && at >= 0 && at < 16) out[u].tok[at] = lane;
+    if (lane == lead) {
+      out[u].aid = id;
+      out[u].n = min(16, __popcll(tokens) - first);
+    }
+  }
+  for (u += lane; u < p.n_units; u += kWave) out[u].n = 0;
 }
 
 // Unit (chunk, tile, s): 16 weight rows against the chunk's tokens (64, the last
@@ -88,7 +129,7 @@ __device__ __forceinline__ void stream_unit(const StreamArgs& p, int chunk, int 
   } else {
     const int u = tile - p.tiles, slot = u / p.rank_tiles;
     rt = u % p.rank_tiles;
-    const int id = lane < n_tok ? p.ids[t0 + lane] : -1;
+    const int id = lane < n_tok ? p.ids[t0 + lane] : -2;
     // the first tokens of the different adapters
     const uint64_t same = same_id(id, n_tok);
     const int lead = nth_bit(__ballot(id >= 0 && id < p.A && (same & ((1ull << lane) - 1)) == 0), slot);
@@ -168,61 +209,37 @@ __device__ __forceinline__ void stream_unit(const StreamArgs& p, int chunk, int 
 struct ExpandArgs {
   const float* part;     // [S, T, Np]
   const float* vpart;    // [S, T, Rp]
-  const int32_t* ids;
+  const AdapterUnit* units;   // [chunks, n_units]
   const float* scales;   // [A] or NULL
   const void* b;         // [A, N, R]
   void* y;               // [T, N]
   int64_t T;
-  int S, N, Np, A, R, Rp;
+  int S, N, Np, A, R, Rp, n_units;
 };
 
 // y[t, n] = the sum of the parts + s[a] sum_j v[t, j] B[a][n, j]. One block:
-// 256 columns of up to 16 tokens of one adapter (unit blockIdx.y of the 64
-// tokens of chunk blockIdx.z), 64 columns a wave. Rows of B are one MFMA
-// operand, read whole and once for all of the adapter's tokens, the low-rank
-// sums the other: for bf16 as two bf16 numbers each (16 significant bits), so
-// that y is rounded once. Bound by latency: the loads of B and of the parts go
-// out before the low-rank sums are made.
+// 128 columns of one unit's tokens, 32 columns a wave. Rows of B are one MFMA
+// operand, read whole and once for all of the unit's tokens, the low-rank sums
+// the other: for bf16 as two bf16 numbers each (16 significant bits), so that y
+// is rounded once. Bound by latency: the loads of B, of the parts (eight at a
+// time) and of the low-rank sums go out together.
 template <bool kF32>
 __global__ __launch_bounds__(kThreads) void adapter_few(ExpandArgs p) {
   typedef typename Elem<kF32>::type E;
   constexpr int kC = Elem<kF32>::kChunk;
   constexpr int kV = kF32 ? 1 : 2;       // numbers that make up a low-rank sum
-  constexpr int kTok = 16, kNs = 4, kKb = 2;
+  constexpr int kTok = 16, kNs = 2, kKb = 4, kParts = 8;
   constexpr int kPitch = kMaxRank + kC;  // (a pad: rows in other banks)
   __shared__ E v_s[kV][kTok][kPitch];
-  __shared__ int unit_s[2 + kTok];   // adapter, tokens, which
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, r = lane & 15;
   const int64_t t0 = static_cast<int64_t>(blockIdx.z) * kFewTokens;
-  const int n_tok = static_cast<int>(min(static_cast<int64_t>(kFewTokens), p.T - t0));
-  if (wave == 0) {
-    // each adapter's tokens by sixteens (tokens without one are alike): every
-    // sixteenth of them leads a unit
-    int id = lane < n_tok ? p.ids[t0 + lane] : -1;
-    if (id < 0 || id >= p.A) id = -1;
-    const uint64_t same = same_id(id, n_tok);
-    const int rank = __popcll(same & ((1ull << lane) - 1));
-    const int found = nth_bit(__ballot(lane < n_tok && rank % kTok == 0), blockIdx.y);
-    const int lead = max(found, 0);
-    const uint64_t tokens = lane_u64(same, lead);
-    const int first = __builtin_amdgcn_readlane(rank, lead);
-    // lane t of the adapter's tokens: its place in the unit
-    const int at = popc_below(tokens) - first;
-    const int n = min(kTok, __popcll(tokens) - first);
-    if (lane == 0) {
-      unit_s[0] = __builtin_amdgcn_readlane(id, lead);
-      unit_s[1] = found < 0 ? 0 : n;
-    }
-    if (((tokens >> lane) & 1) && at >= 0 && at < n) unit_s[2 + at] = lane;
-  }
-  __syncthreads();
-  const int aid = __builtin_amdgcn_readfirstlane(unit_s[0]);
-  const int n = __builtin_amdgcn_readfirstlane(unit_s[1]);
+  const AdapterUnit* unit = p.units + static_cast<int64_t>(blockIdx.z) * p.n_units + blockIdx.y;
+  const int aid = unit->aid, n = unit->n;
   if (n == 0) return;   // fewer units
-  const int64_t t = t0 + unit_s[2 + min(r, n - 1)];   // this lane's token
+  const int64_t t = t0 + unit->tok[min(r, n - 1)];   // this lane's token
   const bool has = aid >= 0;   // the same for the whole block
-  const int col0 = blockIdx.x * kThreads + wave * 64;
+  const int col0 = (blockIdx.x * kWaves + wave) * 16 * kNs;
 
   // rows of B: lane r's column of each 16, chunk g of a k-block
   const E* row[kNs];
@@ -243,22 +260,22 @@ __global__ __launch_bounds__(kThreads) void adapter_few(ExpandArgs p) {
 #pragma unroll
       for (int j = 0; j < kNs; ++j) bv[kb][j] = b_chunk(j, kb);
   }
-  // The parts' sums, four parts' loads at a time (the last is read again), and
+  // The parts' sums, eight parts' loads at a time (the last is read again), and
   // this thread's first low-rank sum: all of these loads go out together.
   const int Rk = (p.R + 4 * kC - 1) / (4 * kC) * (4 * kC);   // v_s: zero from R to Rk
   const float sc = has && p.scales ? p.scales[aid] : 1.0f;
   const int n_v = has ? n * Rk : 0;
   auto v_at = [&](int i) {
     const int k = i / Rk, j = i - k * Rk;
-    return p.vpart + (t0 + unit_s[2 + min(k, n - 1)]) * p.Rp + min(j, p.R - 1);
+    return p.vpart + (t0 + unit->tok[min(k, n - 1)]) * p.Rp + min(j, p.R - 1);
   };
   floatx4 acc[kNs];
 #pragma unroll
   for (int j = 0; j < kNs; ++j) acc[j] = floatx4{0, 0, 0, 0};
-  floatx4 f[4][kNs];
+  floatx4 f[kParts][kNs];
   auto load_parts = [&](int s0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kParts; ++i)
 #pragma unroll
       for (int j = 0; j < kNs; ++j)
         f[i][j] = *reinterpret_cast<const floatx4*>(
@@ -266,16 +283,16 @@ __global__ __launch_bounds__(kThreads) void adapter_few(ExpandArgs p) {
   };
   auto add_parts = [&](int s0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kParts; ++i)
       if (s0 + i < p.S) {
 #pragma unroll
         for (int j = 0; j < kNs; ++j) acc[j] += f[i][j];
       }
   };
-  float fv[4];
+  float fv[kParts];
   auto load_v = [&](const float* v, int s0) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) fv[q] = v[min(s0 + q, p.S - 1) * p.T * p.Rp];
+    for (int q = 0; q < kParts; ++q) fv[q] = v[min(s0 + q, p.S - 1) * p.T * p.Rp];
   };
   const float* v0 = p.vpart;
   load_parts(0);
@@ -285,7 +302,7 @@ __global__ __launch_bounds__(kThreads) void adapter_few(ExpandArgs p) {
   }
   __builtin_amdgcn_sched_barrier(0);
   add_parts(0);
-  for (int s0 = 4; s0 < p.S; s0 += 4) {
+  for (int s0 = kParts; s0 < p.S; s0 += kParts) {
     load_parts(s0);
     add_parts(s0);
   }
@@ -296,10 +313,10 @@ __global__ __launch_bounds__(kThreads) void adapter_few(ExpandArgs p) {
         load_v(v0, 0);
       }
       float total = 0.0f;
-      for (int s0 = 0; s0 < p.S; s0 += 4) {
+      for (int s0 = 0; s0 < p.S; s0 += kParts) {
         if (s0 > 0) load_v(v0, s0);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < kParts; ++q)
           if (s0 + q < p.S) total += fv[q];
       }
       const int k = i / Rk, j = i - k * Rk;
@@ -790,6 +807,10 @@ __global__ __launch_bounds__(kThreads) void stream_partial(StreamArgs p) {
   const int64_t z = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
   if (z < p.n_zero) p.zero[z] = 0;
   __shared__ floatx4 red[kWaves * kWave];
+  if (p.units && blockIdx.x + 1 == gridDim.x) {   // the last blocks: the tokens' units
+    if (blockIdx.y == 0 && threadIdx.x < kWave) make_units(p, 0);
+    return;
+  }
   stream_unit<kF32, 1>(p, 0, blockIdx.x, blockIdx.y, gridDim.y, red);
 }
 
@@ -809,6 +830,8 @@ __global__ __launch_bounds__(kThreads) void few_linear(TileArgs p, StreamArgs q,
   static_assert(sizeof(u32x4) * FewShape::kN * kLine >= sizeof(floatx4) * kWaves * 4 * kWave, "");
   if (b < tiles) {
     tile_unit<kF32, FewShape, false>(p, b);
+  } else if (b + q.chunks >= static_cast<int>(gridDim.x)) {   // the last blocks: the tokens' units
+    if (threadIdx.x < kWave) make_units(q, static_cast<int>(gridDim.x) - 1 - b);
   } else {
     b -= tiles;
     const int u = b / p.parts;
@@ -842,10 +865,10 @@ int parts_for(int per_cu, int64_t n, int64_t ksteps, int64_t least, int64_t most
 }
 
 // For n 64 x 128 tiles: one block a CU, in four parts where that leaves seven
-// in eight CUs with one (adapter_few reads four parts in one go).
+// in eight CUs with one (adapter_few reads eight parts in one go).
 int few_parts(int64_t n, int64_t row_bytes) {
   const int64_t ktiles = cdiv(row_bytes, 128);
-  return parts_for(1, n, ktiles, 3, 4 * n >= kPlanCus * 7 / 8 ? 4 : 16);
+  return parts_for(1, n, ktiles, 3, 4 * n >= kPlanCus * 7 / 8 ? 4 : 8);
 }
 
 // At most 16 tokens: one batch of loads for each of a part's waves, or a few
@@ -938,8 +961,8 @@ bool adapter_in_parts(const tr_adapter_desc& d) {
   return cdiv(d.T, FewShape::kM) * cdiv(d.N, FewShape::kN) < kPlanCus;
 }
 struct AdapterLayout {
-  int parts, Np, Rp, Rq;
-  size_t part, vpart, v, total;
+  int parts, Np, Rp, Rq, n_units;
+  size_t vpart, units, total;
 };
 AdapterLayout adapter_layout(const tr_adapter_desc& d) {
   AdapterLayout L{};
@@ -952,7 +975,12 @@ AdapterLayout adapter_layout(const tr_adapter_desc& d) {
     L.parts = d.T <= 16 ? stream_parts(cdiv(d.N, 16), row_bytes)
                         : few_parts(cdiv(d.T, FewShape::kM) * cdiv(d.N, FewShape::kN), row_bytes);
     L.vpart = up256(sizeof(float) * static_cast<size_t>(L.parts) * d.T * L.Np);
-    L.total = L.vpart + up256(sizeof(float) * static_cast<size_t>(L.parts) * d.T * L.Rp);
+    L.units = L.vpart + up256(sizeof(float) * static_cast<size_t>(L.parts) * d.T * L.Rp);
+    // units of 64 tokens: one for each adapter (and for none), one more for every
+    // 16 tokens
+    const int64_t chunk = d.T < kFewTokens ? d.T : kFewTokens, most = d.A + 1 + chunk / 16;
+    L.n_units = static_cast<int>(most < chunk ? most : chunk);
+    L.total = L.units + up256(sizeof(AdapterUnit) * L.n_units * cdiv(d.T, kFewTokens));
   } else {
     L.total = up256(static_cast<size_t>(d.T) * L.Rq * (f32 ? 4 : 2));
   }
@@ -986,12 +1014,15 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
     s.R = d.R;
     s.Rp = L.Rp;
     s.rank_tiles = L.Rp / 16;
+    s.units = reinterpret_cast<AdapterUnit*>(static_cast<char*>(ws) + L.units);
+    s.n_units = L.n_units;
     const int64_t chunk = d.T < kFewTokens ? d.T : kFewTokens;
     const int slots = static_cast<int>(chunk < d.A ? chunk : d.A);   // adapters among 64 tokens
     const int chunks = static_cast<int>(cdiv(d.T, kFewTokens));
+    s.chunks = chunks;
     if (d.T <= 16) {
       s.tiles = static_cast<int>(cdiv(d.N, 16));
-      const dim3 grid(s.tiles + slots * s.rank_tiles, L.parts);
+      const dim3 grid(s.tiles + slots * s.rank_tiles + 1, L.parts);
       if (f32) hipLaunchKernelGGL(stream_partial<true>, grid, dim3(kThreads), 0, st, s);
       else hipLaunchKernelGGL(stream_partial<false>, grid, dim3(kThreads), 0, st, s);
     } else {
@@ -1008,7 +1039,7 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
       t.n_tiles = static_cast<int>(cdiv(d.N, FewShape::kN));
       const int tiles = t.m_tiles * t.n_tiles * t.parts;
       const int units = slots * s.rank_tiles;   // (s.tiles is 0: the adapters' only)
-      const dim3 grid(tiles + chunks * units * t.parts);
+      const dim3 grid(tiles + chunks * units * t.parts + chunks);
       if (f32) hipLaunchKernelGGL(few_linear<true>, grid, dim3(kThreads), 0, st, t, s, tiles, units);
       else hipLaunchKernelGGL(few_linear<false>, grid, dim3(kThreads), 0, st, t, s, tiles, units);
     }
@@ -1016,7 +1047,8 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
     ExpandArgs p{};
     p.part = s.part;
     p.vpart = s.vpart;
-    p.ids = ids;
+    p.units = s.units;
+    p.n_units = L.n_units;
     p.scales = scales;
     p.b = b;
     p.y = y;
@@ -1027,11 +1059,8 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
     p.A = d.A;
     p.R = d.R;
     p.Rp = L.Rp;
-    // units of 64 tokens: one for each adapter (and for none), one more for every
-    // 16 tokens
-    const int64_t units = d.A + 1 + chunk / 16;
-    const dim3 grid(static_cast<unsigned>(cdiv(d.N, kThreads)),
-                    static_cast<unsigned>(units < chunk ? units : chunk), static_cast<unsigned>(chunks));
+    const dim3 grid(static_cast<unsigned>(cdiv(d.N, 32 * kWaves)), static_cast<unsigned>(L.n_units),
+                    static_cast<unsigned>(chunks));
     if (f32) hipLaunchKernelGGL(adapter_few<true>, grid, dim3(kThreads), 0, st, p);
     else hipLaunchKernelGGL(adapter_few<false>, grid, dim3(kThreads), 0, st, p);
     return hipGetLastError();
