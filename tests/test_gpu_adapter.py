@@ -149,6 +149,30 @@ def test_outputs_past_four_gigabytes():
     S.check(y[rows.cuda()], ref, bound + S.U[BF] * mag * 2, "y")
 
 
+@pytest.mark.parametrize("N", [256, 250])
+def test_x_past_two_gigabytes(N):
+    """Rows too far apart for 32-bit offsets: taken in their own order."""
+    T, H, R, A = 300_007, 3584, 16, 3
+    g = torch.Generator(device="cuda").manual_seed(N)
+    x = torch.randn(T, H, generator=g, device="cuda", dtype=BF)      # 2.15 GB
+    _, w, a, b, _, scales = make(9, 1, H, N, R, A, BF)
+    ids = (torch.arange(T) // 37 % (A + 1)).to(torch.int32) - 1
+    y = tr.adapter_linear(x, w.cuda(), a.cuda(), b.cuda(), ids.cuda(), scales=scales.cuda())
+    rows = torch.cat([torch.arange(40), torch.arange(T - 80, T), torch.randint(0, T, (60,))])
+    ref, bound = S.adapter(x[rows.cuda()], w, a, b, ids[rows], scales)
+    S.check(y[rows.cuda()], ref, bound, "y")
+
+
+def test_rows_do_not_depend_on_their_order():
+    """A shuffled batch gives the shuffled rows: requests' tokens may be mixed."""
+    T, H, N, R, A = 5000, 256, 8192, 24, 7
+    x, w, a, b, ids, scales = (t.cuda() for t in make(12, T, H, N, R, A, BF, run=60))
+    y = tr.adapter_linear(x, w, a, b, ids, scales=scales)
+    at = torch.randperm(T, generator=torch.Generator().manual_seed(5)).cuda()
+    y2 = tr.adapter_linear(x[at].contiguous(), w, a, b, ids[at].contiguous(), scales=scales)
+    assert torch.equal(y[at], y2)
+
+
 def test_adapters_past_four_gigabytes():
     """The last adapter's rows of b lie past 2^32 bytes."""
     T, H, N, R, A = 3, 64, 4096, 256, 2100

@@ -74,8 +74,9 @@ struct GemmArgs {
   const int* n_take;
 };
 
-// The low-rank adapters of a shared projection (adapter_tiled): row t of the
-// output gets v[t] . B[ids[t]][n] on top.
+// The low-rank adapters of a shared projection (adapter_tiled): row p of the
+// tiles gets v[p] . B[ids[p]][n] on top. With gathering, row p is row gather[p] of
+// x and of the output.
 struct AdaptArgs {
   const int* ids;       // [rows]; outside [0, n): none
   const uint16_t* v;    // [rows, Rq] low-rank products, scaled; zero past R
@@ -688,13 +689,14 @@ __device__ __forceinline__ void gemm_tiles_impl(const GemmArgs& a, int I, const 
     // its product in the accumulators: the rows of B are loaded once for every
     // row block with that adapter (in prompts mostly all four). Row blocks with several adapters, or with rows that have none, are
     // marked in `mixed` and take theirs in the epilogue.
-    int aid[4];
+    int aid[4], to_row[4];
     uint32_t mixed = 0;
     if constexpr (kAdapt) {
       uint32_t todo = 0;   // row blocks of one adapter
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = wm * 128 + i * 32 + (lane & 31);
+        if constexpr (kGather) to_row[i] = row < t.rows_valid ? a.gather[t.row0 + row] : -1;
         aid[i] = row < t.rows_valid ? ad->ids[t.row0 + row] : -1;
         if (aid[i] < 0 || aid[i] >= ad->n) aid[i] = -1;
         const int lead = __builtin_amdgcn_readfirstlane(aid[i]);   // (row 0 of the block)
@@ -790,8 +792,9 @@ __device__ __forceinline__ void gemm_tiles_impl(const GemmArgs& a, int I, const 
         }
         if constexpr (kAdapt) {
           if ((mixed >> i) & 1) {
-            // one different adapter after another, added to its own rows only:
-            // its infinities reach no other
+            // one different adapter after another, in a copy of the accumulators
+            // that its own rows take over (its infinities reach no other; the sums
+            // are those of a row block with that adapter alone, bit for bit)
             uint32_t todo = static_cast<uint32_t>(__ballot(aid[i] >= 0));
             const int row = wm * 128 + i * 32 + (lane & 31);
             while (todo) {
@@ -803,7 +806,7 @@ __device__ __forceinline__ void gemm_tiles_impl(const GemmArgs& a, int I, const 
                   ad->b + (static_cast<int64_t>(which) * a.Nc + t.n0 + wn * 128 + j * 32 + (lane & 31)) * ad->R;
               const uint16_t* vrow =
                   ad->v + static_cast<int64_t>(t.row0 + (mine ? row : wm * 128 + i * 32 + lead)) * ad->Rq;
-              floatx16 d = {};
+              floatx16 d = xg;
 #pragma clang loop unroll(disable)
               for (int k0 = 0; k0 < ad->R; k0 += 16) {
                 const int k = k0 + (lane >> 5) * 8;
@@ -815,10 +818,7 @@ __device__ __forceinline__ void gemm_tiles_impl(const GemmArgs& a, int I, const 
                 d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, bf),
                                                             __builtin_bit_cast(bf16x8, vf), d, 0, 0, 0);
               }
-              if (mine) {
-#pragma unroll
-                for (int q = 0; q < 16; ++q) xg[q] += d[q];
-              }
+              if (mine) xg = d;
             }
           }
         }
@@ -847,7 +847,10 @@ __device__ __forceinline__ void gemm_tiles_impl(const GemmArgs& a, int I, const 
           const auto s1 = __builtin_amdgcn_permlane32_swap(d[qq][1], d[qq + 1][1], false, false);
           const u32x4 out = u32x4{s0[0], s1[0], s0[1], s1[1]};
           const uint32_t col = colj + 8 * (qq + hi);
-          if (!fused) {
+          if (kAdapt && kGather) {
+            if (to_row[i] >= 0)
+              *reinterpret_cast<u32x4*>(Cb + static_cast<int64_t>(to_row[i]) * a.Nc + col) = out;
+          } else if (!fused) {
             __builtin_amdgcn_raw_buffer_store_b128(out, rC, (row_off + col) * 2, 0, 0);
           } else {
             // a row of a received row with one local slot goes to y exactly
@@ -872,7 +875,7 @@ __device__ __forceinline__ void gemm_tiles_impl(const GemmArgs& a, int I, const 
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    stores_in_flight = !fused || t.rows_valid == BM;
+    stores_in_flight = !(fused || (kAdapt && kGather)) || t.rows_valid == BM;
     if (fused) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) slot_c[i] = slot_n[i];
@@ -933,7 +936,8 @@ __global__ __launch_bounds__(kThreads) void gemm_tiled(GemmArgs a, int I, int pa
 }
 
 // A projection that all rows share, with the rows' adapters: the tile loop over
-// one "expert" whose segment is every row.
+// one "expert" whose segment is every row. kGather: rows in the order of a.gather.
+template <bool kGather>
 __global__ __launch_bounds__(kThreads) void adapter_tiled(GemmArgs a, AdaptArgs ad) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ int pre[2], cnt_s[1], off_s[1];
@@ -945,7 +949,7 @@ __global__ __launch_bounds__(kThreads) void adapter_tiled(GemmArgs a, AdaptArgs 
     off_s[0] = 0;
   }
   __syncthreads();
-  gemm_tiles_impl<false, false, false, true>(a, 0, pre, cnt_s, off_s, total_m, 0,
+  gemm_tiles_impl<false, kGather, false, true>(a, 0, pre, cnt_s, off_s, total_m, 0,
                                              total_m * (a.Nc / BN), blockIdx.x, gridDim.x, &ad);
 #endif  // __HIP_DEVICE_COMPILE__
 }
@@ -1709,7 +1713,8 @@ bool adapter_can_tile(const tr_adapter_desc& d) {
 }
 
 hipError_t adapter_tiles(const tr_adapter_desc& d, const void* x, const void* w, const void* b,
-                         const int32_t* ids, const void* v, int Rq, void* y, hipStream_t st) {
+                         const int32_t* ids, const int32_t* perm, const void* v, int Rq, void* y,
+                         hipStream_t st) {
   GemmArgs a{};
   a.A = x;
   a.B = w;
@@ -1720,7 +1725,9 @@ hipError_t adapter_tiles(const tr_adapter_desc& d, const void* x, const void* w,
   a.a_rows = d.T;
   a.T = d.T;
   const AdaptArgs ad{ids, static_cast<const uint16_t*>(v), static_cast<const uint16_t*>(b), d.A, d.R, Rq};
-  hipLaunchKernelGGL(adapter_tiled, dim3(device_cu_count()), dim3(kThreads), 0, st, a, ad);
+  a.gather = perm;
+  if (perm) hipLaunchKernelGGL(adapter_tiled<true>, dim3(device_cu_count()), dim3(kThreads), 0, st, a, ad);
+  else hipLaunchKernelGGL(adapter_tiled<false>, dim3(device_cu_count()), dim3(kThreads), 0, st, a, ad);
   return hipGetLastError();
 }
 

@@ -361,12 +361,73 @@ __global__ __launch_bounds__(kThreads) void adapter_few(ExpandArgs p) {
 }
 
 // --------------------------------------------------------------------------
+// Many tokens: their order by adapter
+// --------------------------------------------------------------------------
+// Positions of each window of 2048 tokens sorted by adapter, tokens without one
+// last, equal ones in their order: perm[pos] is the token, sid[pos] its adapter
+// (or -1). The kernels that follow work on positions, so that a group of 16 or 32
+// has one adapter or two however the requests' tokens are mixed (8192 x 7168 x
+// 7168 with 32 adapters of rank 64 dealt at random took 808 + 1887 us in the
+// tokens' order, and takes 15 + 116 + 859 us so). A window whose tokens already
+// come in runs keeps its order (5 us). One bitonic sort in LDS of keys that hold
+// id and place; pairs at most 64 apart stay in a wave.
+constexpr int kWindow = 2048;
+constexpr int kOrderThreads = kWindow / 2;
+
+__global__ __launch_bounds__(kOrderThreads) void adapter_order(const int32_t* __restrict__ ids,
+                                                               int64_t T, int A, int32_t* perm,
+                                                               int32_t* sid) {
+  __shared__ uint32_t key[kWindow];
+  __shared__ int tmp[kOrderThreads / kWave];
+  const int tid = threadIdx.x;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kWindow;
+  const int n = static_cast<int>(min(static_cast<int64_t>(kWindow), T - t0));
+  int ends = 0, all = 0;   // tokens whose adapter differs from the one's before
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int i = tid + q * kOrderThreads;
+    uint32_t k = ~0u;   // past the last token: last (A is at most 2^20)
+    if (i < n) {
+      const int id = ids[t0 + i], before = ids[t0 + max(i - 1, 0)];
+      ends += id != before;
+      k = static_cast<uint32_t>(id < 0 || id >= A ? A : id) << 11 | static_cast<uint32_t>(i);
+    }
+    key[i] = k;
+  }
+  block_exclusive_scan<kOrderThreads>(ends, tmp, &all);
+  // runs of 32 tokens and more on average: the order is good as it is
+  const bool sort = all > kWindow / 32;
+  for (int size = sort ? 2 : kWindow + 1; size <= kWindow; size <<= 1)
+    for (int d = size >> 1; d > 0; d >>= 1) {
+      // thread tid: the pair (i, i + d); 64 threads take 128 neighbours when d <= 64
+      const int i = 2 * tid - (tid & (d - 1));
+      const uint32_t a = key[i], b = key[i + d];
+      const bool up = (i & size) == 0;
+      if ((a > b) == up) {
+        key[i] = b;
+        key[i + d] = a;
+      }
+      // the next step's pairs: another distance (d / 2, or size itself)
+      if (d > 64 || (d == 1 && size >= 128)) __syncthreads();
+      else __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    }
+  __syncthreads();
+  for (int i = tid; i < n; i += kOrderThreads) {
+    const uint32_t k = key[i];
+    perm[t0 + i] = static_cast<int32_t>(t0 + (k & (kWindow - 1)));
+    const int id = static_cast<int>(k >> 11);
+    sid[t0 + i] = id < A ? id : -1;
+  }
+}
+
+// --------------------------------------------------------------------------
 // Many tokens: the adapters' low-rank products
 // --------------------------------------------------------------------------
 struct ShrinkArgs {
   const char* x;
   const char* a;
-  const int32_t* ids;
+  const int32_t* ids;    // by position
+  const int32_t* perm;   // the positions' tokens, or NULL: the same
   const float* scales;
   void* v;               // [T, Rq] in the storage type, zero past R
   int64_t row_bytes;
@@ -398,9 +459,13 @@ __global__ __launch_bounds__(kShrinkThreads, 3) void adapter_shrink(ShrinkArgs p
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int g = lane >> 4, r = lane & 15;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * 16 * kNG;
-  const int id = lane < 16 * kNG && t0 + lane < p.T ? p.ids[t0 + lane] : -1;
+  const bool in = lane < 16 * kNG && t0 + lane < p.T;
+  const int id = in ? p.ids[t0 + lane] : -1;
   uint32_t todo = static_cast<uint32_t>(__ballot(id >= 0 && id < p.A));
-  const char* x0 = p.x + t0 * p.row_bytes;
+  // rows of x by 32-bit offsets: from the group's first token, or with perm from
+  // the first of all (x is below 2 GiB then)
+  const char* x0 = p.perm ? p.x : p.x + t0 * p.row_bytes;
+  const int row = p.perm ? (in ? p.perm[t0 + lane] : 0) : lane;
   const uint32_t row_bytes = static_cast<uint32_t>(p.row_bytes);
   const int nkb = static_cast<int>((row_bytes + 63) >> 6);
   const int nfull = static_cast<int>(row_bytes >> 6);
@@ -416,7 +481,7 @@ __global__ __launch_bounds__(kShrinkThreads, 3) void adapter_shrink(ShrinkArgs p
     uint32_t xo[kNG];
 #pragma unroll
     for (int q = 0; q < kNG; ++q)
-      xo[q] = ((mask >> (16 * q + r)) & 1 ? 16 * q + r : first) * row_bytes + g * 16;
+      xo[q] = __shfl(row, (mask >> (16 * q + r)) & 1 ? 16 * q + r : first, kWave) * row_bytes + g * 16;
     const float sc = p.scales ? p.scales[aid] : 1.0f;
     for (int j0 = 0; j0 < p.Rq; j0 += 16 * kRT) {
       // rows past R read the last one: zeros are stored for them
@@ -535,8 +600,9 @@ struct TileArgs {
   float* part;           // [parts, T, Np] fp32 sums, or NULL: y
   int Np;
   void* y;               // [T, N]
-  const int32_t* ids;    // adapters (NULL: none)
-  const void* v;         // [T, Rq]
+  const int32_t* ids;    // adapters by position (NULL: none)
+  const int32_t* perm;   // the positions' tokens, or NULL: the same
+  const void* v;         // [T, Rq], by position
   const void* b;         // [A, N, R]
   int A, R, Rq;
 };
@@ -681,8 +747,10 @@ __device__ __forceinline__ void tile_unit(const TileArgs& p, int block) {
   l.row_bytes = static_cast<uint32_t>(p.row_bytes);
   // at most 128 (256) rows of 2^24 (2^23) bytes: within the 2^31 that an offset
   // reaches
-  l.xr = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p.x + t0 * p.row_bytes), 0,
-                                           static_cast<int>(rows * l.row_bytes), kBufferFlags);
+  const bool moved = kAdapt && p.perm != nullptr;   // (x is below 2 GiB then)
+  l.xr = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<char*>(moved ? p.x : p.x + t0 * p.row_bytes), 0,
+      static_cast<int>((moved ? static_cast<uint32_t>(p.T) : rows) * l.row_bytes), kBufferFlags);
   l.wr = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<char*>(p.w + static_cast<int64_t>(n0) * p.row_bytes), 0,
       static_cast<int>(cols * l.row_bytes), kBufferFlags);
@@ -690,7 +758,8 @@ __device__ __forceinline__ void tile_unit(const TileArgs& p, int block) {
   for (int j = 0; j < C::kXp; ++j) {
     const int pc = wave * C::kXp + j, row = pc * 8 + (lane >> 3);
     l.xc[j] = ((lane & 7) ^ (lane >> 3) ^ (pc & 1)) * 16;
-    l.xo[j] = row < rows ? row * l.row_bytes + l.xc[j] : kPast;
+    l.xo[j] = kPast;
+    if (row < rows) l.xo[j] = (moved ? p.perm[t0 + row] : row) * l.row_bytes + l.xc[j];
   }
 #pragma unroll
   for (int j = 0; j < C::kWp; ++j) {
@@ -774,14 +843,15 @@ __device__ __forceinline__ void tile_unit(const TileArgs& p, int block) {
       }
     }
     if (lt0 + r >= rows) continue;
+    const int64_t out = moved ? p.perm[t] : t;
 #pragma unroll
     for (int j = 0; j < C::kNs; ++j) {
       const int n = n0 + (wn * C::kNs + j) * 16 + 4 * g;
       if (n >= p.N) continue;
       if constexpr (kAdapt)
-        store4<kF32>(static_cast<E*>(p.y) + t * p.N, n, p.N, (p.N & 3) == 0, acc[i][j]);
+        store4<kF32>(static_cast<E*>(p.y) + out * p.N, n, p.N, (p.N & 3) == 0, acc[i][j]);
       else
-        *reinterpret_cast<floatx4*>(p.part + (s * p.T + t) * p.Np + n) = acc[i][j];
+        *reinterpret_cast<floatx4*>(p.part + (s * p.T + out) * p.Np + n) = acc[i][j];
     }
   }
 }
@@ -962,7 +1032,7 @@ bool adapter_in_parts(const tr_adapter_desc& d) {
 }
 struct AdapterLayout {
   int parts, Np, Rp, Rq, n_units;
-  size_t vpart, units, total;
+  size_t vpart, units, perm, sid, total;
 };
 AdapterLayout adapter_layout(const tr_adapter_desc& d) {
   AdapterLayout L{};
@@ -982,7 +1052,9 @@ AdapterLayout adapter_layout(const tr_adapter_desc& d) {
     L.n_units = static_cast<int>(most < chunk ? most : chunk);
     L.total = L.units + up256(sizeof(AdapterUnit) * L.n_units * cdiv(d.T, kFewTokens));
   } else {
-    L.total = up256(static_cast<size_t>(d.T) * L.Rq * (f32 ? 4 : 2));
+    L.perm = up256(static_cast<size_t>(d.T) * L.Rq * (f32 ? 4 : 2));
+    L.sid = L.perm + up256(4 * static_cast<size_t>(d.T));
+    L.total = L.sid + up256(4 * static_cast<size_t>(d.T));
   }
   if (L.total == 0) L.total = 256;
   return L;
@@ -1065,10 +1137,22 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
     else hipLaunchKernelGGL(adapter_few<false>, grid, dim3(kThreads), 0, st, p);
     return hipGetLastError();
   }
+  // the positions' order: the tokens' own where x is past the 32-bit offsets that
+  // gather its rows
+  int32_t *perm = nullptr, *sid = nullptr;
+  if (d.T * row_bytes < (int64_t{1} << 31)) {
+    perm = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + L.perm);
+    sid = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + L.sid);
+    hipLaunchKernelGGL(adapter_order, dim3(static_cast<unsigned>(cdiv(d.T, kWindow))), dim3(kOrderThreads),
+                       0, st, ids, d.T, d.A, perm, sid);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    ids = sid;
+  }
   ShrinkArgs s{};
   s.x = static_cast<const char*>(x);
   s.a = static_cast<const char*>(a);
   s.ids = ids;
+  s.perm = perm;
   s.scales = scales;
   s.v = ws;
   s.row_bytes = row_bytes;
@@ -1080,7 +1164,7 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
   if (f32) hipLaunchKernelGGL(adapter_shrink<true>, groups, dim3(kShrinkThreads), 0, st, s);
   else hipLaunchKernelGGL(adapter_shrink<false>, groups, dim3(kShrinkThreads), 0, st, s);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  if (adapter_can_tile(d)) return adapter_tiles(d, x, w, b, ids, ws, L.Rq, y, st);
+  if (adapter_can_tile(d)) return adapter_tiles(d, x, w, b, ids, perm, ws, L.Rq, y, st);
   TileArgs t{};
   t.x = s.x;
   t.w = static_cast<const char*>(w);
@@ -1090,6 +1174,7 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
   t.parts = 1;
   t.y = y;
   t.ids = ids;
+  t.perm = perm;
   t.v = ws;
   t.b = b;
   t.A = d.A;

@@ -106,11 +106,13 @@ hipError_t few_layer(const tr_layer_desc& d, const void* x, const void* w_gate, 
                      void* ws, hipStream_t st);
 
 // The shared projection on the grouped GEMM's 256 x 256 tiles: whether its shape
-// allows that and gives at least two tiles a CU (bf16; v: low-rank products as
-// adapter_linear makes them, rows of Rq).
+// allows that and gives at least two tiles a CU (bf16; ids and v, low-rank
+// products as adapter_linear makes them, rows of Rq, by position; perm: the
+// positions' tokens, x being below 2 GiB, or NULL: the same).
 bool adapter_can_tile(const tr_adapter_desc& d);
 hipError_t adapter_tiles(const tr_adapter_desc& d, const void* x, const void* w, const void* b,
-                         const int32_t* ids, const void* v, int Rq, void* y, hipStream_t st);
+                         const int32_t* ids, const int32_t* perm, const void* v, int Rq, void* y,
+                         hipStream_t st);
 size_t adapter_workspace(const tr_adapter_desc& d);
 hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w, const void* a,
                           const void* b, const int32_t* ids, const float* scales, void* y, void* ws,
