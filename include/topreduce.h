@@ -319,7 +319,7 @@ typedef enum { TR_SCORE_SOFTMAX = 0, TR_SCORE_SIGMOID = 1 } tr_score;
 
 /* T rows of x against G experts. */
 typedef struct tr_route_desc {
-    int64_t T;             /* rows, >= 0; T * K < 2^31 */
+    int64_t T;             /* rows, >= 0, < 2^26; T * K < 2^31 */
     int64_t H;             /* hidden size, a multiple of 8, at most 2^22 */
     int32_t G;             /* experts, 1..4096 */
     int32_t K;             /* experts chosen per row, 1..32, at most G */
@@ -378,7 +378,7 @@ tr_status moe_layer(const tr_layer_desc* desc, const void* x, const void* w_gate
 /* A projection that all rows share, with a low-rank adapter of each row's
  * request beside it. */
 typedef struct tr_adapter_desc {
-    int64_t T;             /* rows, >= 0, < 2^31 */
+    int64_t T;             /* rows, >= 0, < 2^28; T * N below 2^44 */
     int64_t H;             /* input size, a multiple of 8, at most 2^22 */
     int64_t N;             /* output size, 1..2^22 */
     int32_t R;             /* rank, 1..256 (adapters of lower rank: zero rows) */
@@ -393,8 +393,9 @@ size_t moe_adapter_linear_workspace(const tr_adapter_desc* desc);
 
 /* y[t] = w x[t] + scales[i] * b[i] (a[i] x[t]) with i = ids[t]; rows whose id is
  * outside [0, A) (-1, say) have no adapter and read none. Accumulation is
- * fp32; with more than 64 bf16 rows the low-rank product a x is rounded to
- * bf16. x: device [T, H]; w: device [N, H]; a: device [A, R, H]; b: device
+ * fp32 and y is rounded once; in bf16 the low-rank product scales[i] a[i] x is
+ * held in 16 significant bits, or is rounded to bf16 where the rows and columns
+ * make 256 or more tiles of 64 x 128. x: device [T, H]; w: device [N, H]; a: device [A, R, H]; b: device
  * [A, N, R]; ids: device int32 [T]; scales: device fp32 [A] or NULL (1);
  * y: device [T, N], must not overlap x; ws: device, 256-byte aligned, its
  * contents before and after of no meaning. */

@@ -504,6 +504,8 @@ tr_status check_route_desc(const tr_route_desc* d) {
   if (d->H % 8 || d->H > (int64_t{1} << 22))
     return fail(TR_EUNSUPPORTED, "H must be a multiple of 8, at most 2^22 (got %lld)", (long long)d->H);
   if (d->T > ((int64_t{1} << 31) - 1) / d->K) return fail(TR_EUNSUPPORTED, "T*K must be < 2^31");
+  // the selection takes a wave a row, and a launch has fewer than 2^32 threads
+  if (d->T >= (int64_t{1} << 26)) return fail(TR_EUNSUPPORTED, "T must be < 2^26");
   return TR_OK;
 }
 
@@ -532,7 +534,9 @@ tr_status check_adapter_desc(const tr_adapter_desc* d) {
   if (d->reserved != 0) return fail(TR_EINVAL, "reserved must be 0");
   if (d->R > tr::kMaxRank) return fail(TR_EUNSUPPORTED, "R must be at most %d (got %d)", tr::kMaxRank, d->R);
   if (d->A > (1 << 20)) return fail(TR_EUNSUPPORTED, "A must be at most 2^20 (got %d)", d->A);
-  if (d->T >= (int64_t{1} << 31)) return fail(TR_EUNSUPPORTED, "T must be < 2^31");
+  // the low-rank products take 384 threads for 32 rows, and a launch has fewer
+  // than 2^32 threads
+  if (d->T >= (int64_t{1} << 28)) return fail(TR_EUNSUPPORTED, "T must be < 2^28");
   if (d->H % 8 || d->H > (int64_t{1} << 22))
     return fail(TR_EUNSUPPORTED, "H must be a multiple of 8, at most 2^22 (got %lld)", (long long)d->H);
   if (d->N > (int64_t{1} << 22)) return fail(TR_EUNSUPPORTED, "N must be at most 2^22");

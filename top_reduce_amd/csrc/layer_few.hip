@@ -15,9 +15,8 @@
 // other's products run, with a batch small enough that 16 waves fit a CU.
 //
 // The gate weight is folded into h. bf16: h is kept as two bf16 numbers whose
-// sum has 16 significant bits, and few_down multiplies both; the MFMA units
-// have time for it while the weights stream, and y is then rounded once, as
-// if h had never been rounded.
+// sum has 16 significant bits, and few_down multiplies both, as different columns
+// of one MFMA operand; y is then rounded once, as if h had never been rounded.
 #include "tr_chunk.h"
 #include "tr_internal.h"
 #include "tr_select.h"
@@ -30,9 +29,9 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kDownThreads = 256;
 constexpr int kDownWaves = kDownThreads / kWave;
 constexpr int kU = 4;   // 64-byte k-blocks of one batch of loads
-// groups of 16 tokens of an expert: one for each expert with a token, and one
-// more for every 16 routes at most
-constexpr int kMaxGroups = kMaxE + kFewTokens * kMaxK / 16;
+// groups of 8 or 16 tokens of an expert: one for each expert with a token, and
+// one more for every 8 routes at most
+constexpr int kMaxGroups = kMaxE + kFewTokens * kMaxK / 8;
 
 struct FewArgs {
   const char* x;                     // [T, H]
@@ -55,9 +54,9 @@ struct Groups {
   int rank[kMaxGroups];        // that token's rank among the expert's
 };
 
-// Fills `s` from masks (E of them); returns the number of groups. tmp: LDS of
-// kBlock / 64 ints.
-template <int kBlock>
+// Fills `s` from masks (E of them) with groups of up to kGroup tokens; returns
+// their number. tmp: LDS of kBlock / 64 ints.
+template <int kBlock, int kGroup>
 __device__ __forceinline__ int find_groups(const unsigned long long* masks, int E, Groups& s, int* tmp) {
   constexpr int kPer = (kMaxE + kBlock - 1) / kBlock;
   const int per = (E + kBlock - 1) / kBlock;
@@ -68,19 +67,19 @@ __device__ __forceinline__ int find_groups(const unsigned long long* masks, int 
     m[j] = j < per && e < E ? masks[e] : 0;
   }
   // routes and groups of the experts before: one scan of both (at most 2048
-  // routes and 1152 groups)
+  // routes and 1280 groups)
   int n = 0, total = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int c = __popcll(m[j]);
-    n += c | ((c + 15) / 16) << 16;
+    n += c | ((c + kGroup - 1) / kGroup) << 16;
   }
   int at = block_exclusive_scan<kBlock>(n, tmp, &total);
   int row = at & 0xffff, g = at >> 16;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int c = __popcll(m[j]);
-    for (int k = 0; k < c; k += 16) {
+    for (int k = 0; k < c; k += kGroup) {
       s.mask[g] = m[j];
       s.expert[g] = static_cast<int>(threadIdx.x) * per + j;
       s.row[g] = row + k;
@@ -93,15 +92,14 @@ __device__ __forceinline__ int find_groups(const unsigned long long* masks, int 
   return total >> 16;
 }
 
-// Lane l's token: the one of rank `rank` + l % 16 in `mask` (for ranks past the
-// last, the group's first token). mask and rank are the same in every lane.
-__device__ __forceinline__ int group_token(uint64_t mask, int rank, int n) {
+// The token of rank `rank` + r in `mask` (r the lane's; r >= n: the group's first
+// token). mask and rank are the same in every lane.
+__device__ __forceinline__ int group_token(uint64_t mask, int rank, int n, int r) {
   const int lane = lane_id();
   // lane t of the mask sends t to the lane of its rank
   const int to = (mask >> lane) & 1 ? popc_below(mask) : 63;
   int by_rank = __builtin_amdgcn_ds_permute(to * 4, lane);
   // (64 tokens: lane 63 is its own rank; fewer: what lane 63 gets is not used)
-  const int r = lane & 15;
   return __shfl(by_rank, rank + (r < n ? r : 0), kWave);
 }
 
@@ -140,7 +138,7 @@ __global__ __launch_bounds__(kThreads, 3) void few_up(FewArgs a, SelectArgs sel,
     if (blockIdx.x == 0)
       for (int e = threadIdx.x; e < a.E; e += kThreads) a.masks[e] = mask_s[e];
   }
-  const int n_groups = find_groups<kThreads>(NR ? mask_s : a.masks, a.E, s, tmp);
+  const int n_groups = find_groups<kThreads, 16>(NR ? mask_s : a.masks, a.E, s, tmp);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int g = lane >> 4, r = lane & 15;
@@ -156,7 +154,7 @@ __global__ __launch_bounds__(kThreads, 3) void few_up(FewArgs a, SelectArgs sel,
     const uint64_t mask = s.mask[q];
     const int rank = s.rank[q];
     const int n = min(16, __popcll(mask) - rank);   // tokens of the group
-    const int t = group_token(mask, rank, n);
+    const int t = group_token(mask, rank, n, r);
     // addresses: a start that is the same for the wave, 32-bit offsets in it.
     // Rows past I (the last units fill h up to Ip with zeros) read the last row.
     const int64_t c0 = min(static_cast<int64_t>(c * 16), a.I - 1);
@@ -280,19 +278,24 @@ struct Item {
 // reduction. A wave adds a group's sums to its tokens' totals, which it keeps
 // in LDS, experts ascending, so an expert's infinities reach its own tokens
 // only; then the waves' totals are added.
+// The second MFMA operand has 16 columns. bf16: a group is 8 tokens, whose h
+// fill columns 0 to 7 with their first numbers and 8 to 15 with their second, so
+// that a batch loads as much of h as of w2. (16 tokens and two operands load
+// twice as much of h: OLD)
 // kVec: rows of w2 start on 16 bytes.
 template <bool kF32, bool kVec>
 __global__ __launch_bounds__(kDownThreads, 3) void few_down(FewArgs a) {
   typedef typename Elem<kF32>::type E;
   constexpr int kC = Elem<kF32>::kChunk, kB = Elem<kF32>::kBytes;
-  constexpr int kParts = kF32 ? 1 : 2;
+  constexpr int kParts = kF32 ? 1 : 2, kGroup = 16 / kParts;
   __shared__ Groups s;
   __shared__ int tmp[kDownWaves];
   __shared__ floatx4 sum[kDownWaves][kFewTokens][4];
-  const int n_groups = find_groups<kDownThreads>(a.masks, a.E, s, tmp);
+  const int n_groups = find_groups<kDownThreads, kGroup>(a.masks, a.E, s, tmp);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int g = lane >> 4, r = lane & 15;
+  const int tr = r % kGroup, part = r / kGroup;   // the lane's token of a group and number
   const int I = static_cast<int>(a.I), Ip = static_cast<int>(a.Ip);
   // This wave's 64-byte blocks of every row of h and w2 (the same for every
   // expert, so that a token's sums do not depend on the other tokens), in
@@ -313,7 +316,7 @@ __global__ __launch_bounds__(kDownThreads, 3) void few_down(FewArgs a) {
     floatx4 acc = {0, 0, 0, 0};
 
     struct Batch {
-      u32x4 w[kU], h[kParts][kU];
+      u32x4 w[kU], h[kU];
     } b0, b1;
     auto start = [&](int b) { return min(kb0 + b * kU, max(kbf - kU, 0)); };
     auto w_at = [&](int q) {
@@ -327,7 +330,7 @@ __global__ __launch_bounds__(kDownThreads, 3) void few_down(FewArgs a) {
     // the lane's row of h; past the group's last token its first one's
     auto h_off = [&](int q) {
       const int n = __popcll(s.mask[q]) - s.rank[q];
-      return static_cast<uint32_t>(r < n ? r : 0) * kParts * Ip * kB + g * 16;
+      return static_cast<uint32_t>((tr < n ? tr * kParts : 0) + part) * Ip * kB + g * 16;
     };
     auto load = [&](Batch& v, const Item& it) {
       const char* w0 = w_at(it.q);
@@ -336,8 +339,7 @@ __global__ __launch_bounds__(kDownThreads, 3) void few_down(FewArgs a) {
 #pragma unroll
       for (int j = 0; j < kU; ++j) {
         v.w[j] = load16(w0 + (wo + k) + j * 64);
-#pragma unroll
-        for (int part = 0; part < kParts; ++part) v.h[part][j] = load16(h0 + part * Ip * kB + ho + j * 64);
+        v.h[j] = load16(h0 + ho + j * 64);
       }
       __builtin_amdgcn_sched_barrier(0);
     };
@@ -345,8 +347,14 @@ __global__ __launch_bounds__(kDownThreads, 3) void few_down(FewArgs a) {
     auto add = [&](int q) {
       const uint64_t mask = s.mask[q];
       const int rank = s.rank[q];
-      const int n = __popcll(mask) - rank;
-      const int t = group_token(mask, rank, n);
+      const int n = min(kGroup, __popcll(mask) - rank);
+      const int t = group_token(mask, rank, n, r);
+      if constexpr (kParts == 2) {
+        // lanes 0 to 7 of each 16: what the second numbers, 8 lanes on, gave
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[j] += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(acc[j]), 0x128, 15, 15, true));
+      }
       if (r < n) sum[wave][t][g] += acc;
       acc = floatx4{0, 0, 0, 0};
     };
@@ -355,10 +363,7 @@ __global__ __launch_bounds__(kDownThreads, 3) void few_down(FewArgs a) {
       const int k = start(it.b), kb = kb0 + it.b * kU;
 #pragma unroll
       for (int j = 0; j < kU; ++j)
-        if (k + j >= kb && k + j < kbf) {
-#pragma unroll
-          for (int part = 0; part < kParts; ++part) acc = mma16<kF32>(v.w[j], v.h[part][j], acc);
-        }
+        if (k + j >= kb && k + j < kbf) acc = mma16<kF32>(v.w[j], v.h[j], acc);
       __builtin_amdgcn_sched_barrier(0);
       if (it.b + 1 == nbf) add(it.q);
       it.next(nbf);
@@ -391,7 +396,7 @@ __global__ __launch_bounds__(kDownThreads, 3) void few_down(FewArgs a) {
         const E* wrow = reinterpret_cast<const E*>(w_at(q) + lr * static_cast<uint32_t>(I * kB));
         const char* hrow = h_at(q) + h_off(q);
         for (int kb = kbf; kb < kb1; kb += kU) {
-          u32x4 w[kU], h[kParts][kU];
+          u32x4 w[kU], h[kU];
 #pragma unroll
           for (int j = 0; j < kU; ++j) {
             const int k = (kb + j) * 4 * kC + g * kC;
@@ -401,15 +406,10 @@ __global__ __launch_bounds__(kDownThreads, 3) void few_down(FewArgs a) {
               if constexpr (kVec) w[j] = load16(reinterpret_cast<const char*>(wrow + k));
               else w[j] = load16_any<kF32>(wrow, k, I);
             }
-#pragma unroll
-            for (int part = 0; part < kParts; ++part)
-              h[part][j] = in && k < Ip ? load16(hrow + part * Ip * kB + (kb + j) * 64)
-                                        : u32x4{0, 0, 0, 0};
+            h[j] = in && k < Ip ? load16(hrow + (kb + j) * 64) : u32x4{0, 0, 0, 0};
           }
 #pragma unroll
-          for (int part = 0; part < kParts; ++part)
-#pragma unroll
-            for (int j = 0; j < kU; ++j) acc = mma16<kF32>(w[j], h[part][j], acc);
+          for (int j = 0; j < kU; ++j) acc = mma16<kF32>(w[j], h[j], acc);
         }
         add(q);
       }

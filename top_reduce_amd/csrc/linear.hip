@@ -4,17 +4,23 @@
 //   logits[t, g] = x[t] . Wg[g]
 //   y[t, n] = x[t] . W[n] + s[a] sum_j (x[t] . A[a][j]) B[a][n, j],  a = ids[t]
 //
-// Three forms, by the number of tokens T (the same code for bf16 and fp32, see
-// tr_chunk.h):
-//  - stream_partial (T <= 64): bound by reading W. Weight rows go from memory
+// The same code serves bf16 and fp32 (tr_chunk.h). Forms, by the number of
+// tokens T:
+//  - stream_partial (T <= 16): bound by reading W. Weight rows go from memory
 //    straight into MFMA operands, the tokens ride in the other operand, and
 //    the reduction dimension is split over the waves of a block and over
-//    blocks, so that a few hundred rows still occupy every compute unit. The
-//    sums of a block's part go to fp32 partials; the kernel that follows
-//    (router selection, adapter_few) adds them in a fixed order.
-//    The adapters' low-rank products x A^T are units of the same launch.
-//  - linear_tile (more tokens): 128 x 128 tiles staged through LDS.
-//  - adapter_shrink + linear_tile with the adapters in its epilogue.
+//    blocks, so that a few hundred rows still occupy every compute unit.
+//  - few_linear (more, as long as tiles of 64 x 128 leave CUs without one): the
+//    same split of the reduction over blocks, W and x staged through LDS, so that
+//    a weight row is read for 64 tokens.
+//    The sums of a block's part go to fp32 partials; the kernel that follows
+//    (router selection, adapter_few) adds them in a fixed order. The adapters'
+//    low-rank products x A^T are units of the same launch, and one wave of it
+//    writes the table of units (a unit: up to 16 tokens of one adapter) that
+//    adapter_few goes by.
+//  - adapter_order, adapter_shrink, then linear_tile or adapter_tiled
+//    (grouped_gemm.hip) with the adapters on top, for many tokens; the router's
+//    logits of many tokens are linear_tile alone.
 #include "tr_chunk.h"
 #include "tr_internal.h"
 
@@ -106,10 +112,10 @@ __device__ __forceinline__ void make_units(const StreamArgs& p, int chunk) {
 }
 
 // Unit (chunk, tile, s): 16 weight rows against the chunk's tokens (64, the last
-// chunk the rest) over part s of the reduction, which its waves share. Tiles past the weight's are adapter tiles:
-// unit (slot, rank tile) takes 16 rows of the slot-th different adapter among
-// the tokens' ids, and keeps the sums of that adapter's tokens. red: LDS of
-// kWaves * NQ * kWave floatx4.
+// chunk the rest) over part s of the reduction, which its waves share. Tiles past
+// the weight's are adapter tiles: unit (slot, rank tile) takes 16 rows of the
+// slot-th different adapter among the tokens' ids, and keeps the sums of that
+// adapter's tokens. red: LDS of kWaves * NQ * kWave floatx4.
 template <bool kF32, int NQ>
 __device__ __forceinline__ void stream_unit(const StreamArgs& p, int chunk, int tile, int s, int S,
                                             floatx4* red) {
@@ -437,13 +443,13 @@ struct ShrinkArgs {
 
 // v[t, j] = s[a] x[t] . A[a][j] for a group of 32 tokens: up to 32 rows of A at
 // a time, the waves sharing the reduction, two batches of loads in flight.
-// Bound by x from memory and A from L2 (16 tokens a group, which read A twice
-// as often, took 58 us for 8192 x 7168 and rank 32, of which 41 us were A's
-// loads alone; x alone takes 25 us). The different adapters among the tokens (one where tokens of a request are
-// neighbours) are dealt to kSlots blocks, so that a group at the border of two
-// requests takes no longer than the others. v is rounded to the storage type,
-// to be an MFMA operand of the tile's epilogue: its error is that of one
-// rounding of the adapter's part.
+// Bound by x from memory and A from L2: 39 us for 8192 x 7168 and rank 32 (16
+// tokens a group, which read A twice as often, took 58 us, of which 41 us were
+// A's loads alone; x alone takes 25 us). The different adapters among the tokens
+// (one where tokens of a request are neighbours) are dealt to kSlots blocks, so
+// that a group at the border of two requests takes no longer than the others. v
+// is rounded to the storage type, to be an MFMA operand of the tiles: its error
+// is that of one rounding of the adapter's part.
 constexpr int kSlots = 2;
 constexpr int kShrinkThreads = 384;   // two blocks a CU
 constexpr int kShrinkWaves = kShrinkThreads / kWave;
