@@ -26,11 +26,15 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kDownThreads = 256;
-constexpr int kDownWaves = kDownThreads / kWave;
-constexpr int kU = 4;   // 64-byte k-blocks of one batch of loads
-// groups of 8 or 16 tokens of an expert: one for each expert with a token, and
-// one more for every 8 routes at most
+// h is kept as few_down multiplies it. An expert's tokens, ascending, in blocks of
+// kGroup; of a block, for each 64 bytes of a row, the tokens' pieces with their
+// second numbers beside them: 16 pieces, the columns of an MFMA operand.
+template <bool kF32>
+struct HPlace {
+  static constexpr int kParts = kF32 ? 1 : 2, kGroup = 16 / kParts;
+};
+// groups of tokens of an expert, blocks of h: one for each expert with a token,
+// and one more for every 8 routes at most
 constexpr int kMaxGroups = kMaxE + kFewTokens * kMaxK / 8;
 
 struct FewArgs {
@@ -40,7 +44,7 @@ struct FewArgs {
   unsigned long long* masks;         // [E] tokens of each local expert
   const uint8_t* slots;              // [E, 64] slot of token t that names expert e
   const float* w;                    // [T, K] gate weights
-  char* h;                           // [routes][parts][Ip]
+  char* h;                           // [blocks][Ip * bytes / 64][16][64 bytes]
   void* y;                           // [T, H]
   int T, K, E;
   int64_t H, I, Ip;
@@ -48,15 +52,15 @@ struct FewArgs {
 
 // Groups in LDS, experts ascending.
 struct Groups {
-  uint64_t mask[kMaxGroups];   // the expert's tokens
-  int expert[kMaxGroups];
-  int row[kMaxGroups];         // row of h of the group's first token
-  int rank[kMaxGroups];        // that token's rank among the expert's
+  uint64_t mask[kMaxGroups];     // the expert's tokens
+  uint16_t expert[kMaxGroups];
+  uint16_t block[kMaxGroups];    // block of h of the group's first token
+  uint16_t rank[kMaxGroups];     // that token's rank among the expert's
 };
 
 // Fills `s` from masks (E of them) with groups of up to kGroup tokens; returns
 // their number. tmp: LDS of kBlock / 64 ints.
-template <int kBlock, int kGroup>
+template <bool kF32, int kBlock, int kGroup>
 __device__ __forceinline__ int find_groups(const unsigned long long* masks, int E, Groups& s, int* tmp) {
   constexpr int kPer = (kMaxE + kBlock - 1) / kBlock;
   const int per = (E + kBlock - 1) / kBlock;
@@ -66,41 +70,40 @@ __device__ __forceinline__ int find_groups(const unsigned long long* masks, int 
     const int e = static_cast<int>(threadIdx.x) * per + j;
     m[j] = j < per && e < E ? masks[e] : 0;
   }
-  // routes and groups of the experts before: one scan of both (at most 2048
-  // routes and 1280 groups)
+  constexpr int kH = HPlace<kF32>::kGroup;
+  static_assert(kGroup % kH == 0, "whole blocks of h");
+  // blocks and groups of the experts before: one scan of both (at most 1280)
   int n = 0, total = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int c = __popcll(m[j]);
-    n += c | ((c + kGroup - 1) / kGroup) << 16;
+    n += (c + kH - 1) / kH | ((c + kGroup - 1) / kGroup) << 16;
   }
   int at = block_exclusive_scan<kBlock>(n, tmp, &total);
-  int row = at & 0xffff, g = at >> 16;
+  int block = at & 0xffff, g = at >> 16;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int c = __popcll(m[j]);
     for (int k = 0; k < c; k += kGroup) {
       s.mask[g] = m[j];
-      s.expert[g] = static_cast<int>(threadIdx.x) * per + j;
-      s.row[g] = row + k;
-      s.rank[g] = k;
+      s.expert[g] = static_cast<uint16_t>(static_cast<int>(threadIdx.x) * per + j);
+      s.block[g] = static_cast<uint16_t>(block + k / kH);
+      s.rank[g] = static_cast<uint16_t>(k);
       ++g;
     }
-    row += c;
+    block += (c + kH - 1) / kH;
   }
   __syncthreads();
   return total >> 16;
 }
 
-// The token of rank `rank` + r in `mask` (r the lane's; r >= n: the group's first
-// token). mask and rank are the same in every lane.
-__device__ __forceinline__ int group_token(uint64_t mask, int rank, int n, int r) {
+// Lane i < the number of tokens in `mask` (the same in every lane): the token of
+// rank i.
+__device__ __forceinline__ int tokens_by_rank(uint64_t mask) {
   const int lane = lane_id();
-  // lane t of the mask sends t to the lane of its rank
-  const int to = (mask >> lane) & 1 ? popc_below(mask) : 63;
-  int by_rank = __builtin_amdgcn_ds_permute(to * 4, lane);
-  // (64 tokens: lane 63 is its own rank; fewer: what lane 63 gets is not used)
-  return __shfl(by_rank, rank + (r < n ? r : 0), kWave);
+  // lane t of the mask sends t to the lane of its rank, the others to lane 63,
+  // which counts with 64 tokens only
+  return __builtin_amdgcn_ds_permute(((mask >> lane) & 1 ? popc_below(mask) : 63) * 4, lane);
 }
 
 // Up to this many tokens (one a wave) and experts few_up makes the choice: every
@@ -113,11 +116,12 @@ constexpr int kChooseGates = 256;
 // A unit: 16 gate rows and the matching 16 up rows of one group's expert, the
 // reduction over the block's waves. NR > 0: every block makes the tokens'
 // choice from the logits' parts (NR registers a lane); block 0 stores it.
-template <bool kF32, int NR>
-__global__ __launch_bounds__(kThreads, 3) void few_up(FewArgs a, SelectArgs sel, int64_t begin) {
+template <bool kF32, int NR, int NQ>
+__global__ __launch_bounds__(kThreads, NQ == 4 ? 2 : 3) void few_up(FewArgs a, SelectArgs sel, int64_t begin) {
+  constexpr int kU = NQ == 1 ? 4 : 2;   // 64-byte k-blocks of one batch of loads
   __shared__ Groups s;
   __shared__ int tmp[kWaves];
-  __shared__ floatx4 red[kWaves][2][kWave];
+  __shared__ floatx4 red[kWaves][NQ][2][kWave];
   __shared__ unsigned long long mask_s[NR ? kChooseGates : 1];
   __shared__ float w_s[NR ? kChooseGates * kChooseTokens : 1];   // [local expert][token]
   __shared__ SelectScratch scratch[NR ? kWaves : 1];
@@ -138,7 +142,7 @@ __global__ __launch_bounds__(kThreads, 3) void few_up(FewArgs a, SelectArgs sel,
     if (blockIdx.x == 0)
       for (int e = threadIdx.x; e < a.E; e += kThreads) a.masks[e] = mask_s[e];
   }
-  const int n_groups = find_groups<kThreads, 16>(NR ? mask_s : a.masks, a.E, s, tmp);
+  const int n_groups = find_groups<kF32, kThreads, 16 * NQ>(NR ? mask_s : a.masks, a.E, s, tmp);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int g = lane >> 4, r = lane & 15;
@@ -153,8 +157,8 @@ __global__ __launch_bounds__(kThreads, 3) void few_up(FewArgs a, SelectArgs sel,
     const int e = __builtin_amdgcn_readfirstlane(s.expert[q]);
     const uint64_t mask = s.mask[q];
     const int rank = s.rank[q];
-    const int n = min(16, __popcll(mask) - rank);   // tokens of the group
-    const int t = group_token(mask, rank, n, r);
+    const int n = min(16 * NQ, __popcll(mask) - rank);   // tokens of the group
+    const int by_rank = tokens_by_rank(mask);
     // addresses: a start that is the same for the wave, 32-bit offsets in it.
     // Rows past I (the last units fill h up to Ip with zeros) read the last row.
     const int64_t c0 = min(static_cast<int64_t>(c * 16), a.I - 1);
@@ -162,12 +166,23 @@ __global__ __launch_bounds__(kThreads, 3) void few_up(FewArgs a, SelectArgs sel,
     const char* wu = wg + a.I * row_bytes;
     const uint32_t wo = static_cast<uint32_t>(min(static_cast<int64_t>(r), a.I - 1 - c0)) *
                             static_cast<uint32_t>(row_bytes) + g * 16;
-    const uint32_t xo = static_cast<uint32_t>(t) * static_cast<uint32_t>(row_bytes) + g * 16;
-    floatx4 ag = {0, 0, 0, 0}, au = {0, 0, 0, 0};
+    // (a lane past the group's last token reads its first one's row)
+    uint32_t xo[NQ];
+    floatx4 ag[NQ], au[NQ];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int t = __shfl(by_rank, rank + (16 * i + r < n ? 16 * i + r : 0), kWave);
+      xo[i] = static_cast<uint32_t>(t) * static_cast<uint32_t>(row_bytes) + g * 16;
+      ag[i] = au[i] = floatx4{0, 0, 0, 0};
+    }
 
     struct Batch {
-      u32x4 wg[kU], wu[kU], x[kU];
+      u32x4 wg[kU], wu[kU], x[NQ][kU];
     } b0, b1;
+    auto products = [&](const u32x4& vg, const u32x4& vu, int i, const u32x4& vx) {
+      ag[i] = mma16<kF32>(vg, vx, ag[i]);
+      au[i] = mma16<kF32>(vu, vx, au[i]);
+    };
     // a share's last batch starts early enough to end with it; the products of
     // blocks that it reads again are skipped
     auto start = [&](int kb) { return min(kb, max(kbf - kU, 0)); };
@@ -177,7 +192,8 @@ __global__ __launch_bounds__(kThreads, 3) void few_up(FewArgs a, SelectArgs sel,
       for (int j = 0; j < kU; ++j) {
         b.wg[j] = load16(wg + (wo + k) + j * 64);
         b.wu[j] = load16(wu + (wo + k) + j * 64);
-        b.x[j] = load16(a.x + (xo + k) + j * 64);
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) b.x[i][j] = load16(a.x + (xo[i] + k) + j * 64);
       }
       __builtin_amdgcn_sched_barrier(0);
     };
@@ -186,8 +202,8 @@ __global__ __launch_bounds__(kThreads, 3) void few_up(FewArgs a, SelectArgs sel,
 #pragma unroll
       for (int j = 0; j < kU; ++j)
         if (k + j >= kb && k + j < kbf) {
-          ag = mma16<kF32>(b.wg[j], b.x[j], ag);
-          au = mma16<kF32>(b.wu[j], b.x[j], au);
+#pragma unroll
+          for (int i = 0; i < NQ; ++i) products(b.wg[j], b.wu[j], i, b.x[i][j]);
         }
       __builtin_amdgcn_sched_barrier(0);
     };
@@ -214,9 +230,9 @@ __global__ __launch_bounds__(kThreads, 3) void few_up(FewArgs a, SelectArgs sel,
       }
     } else {   // rows of fewer blocks than a batch has
       for (int kb = kb0; kb < kbf; ++kb) {
-        const u32x4 vx = load16(a.x + xo + kb * 64);
-        ag = mma16<kF32>(load16(wg + wo + kb * 64), vx, ag);
-        au = mma16<kF32>(load16(wu + wo + kb * 64), vx, au);
+        const u32x4 vg = load16(wg + wo + kb * 64), vu = load16(wu + wo + kb * 64);
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) products(vg, vu, i, load16(a.x + xo[i] + kb * 64));
       }
     }
     if (kb1 > nfull) {   // the short block at the end of the rows
@@ -224,28 +240,37 @@ __global__ __launch_bounds__(kThreads, 3) void few_up(FewArgs a, SelectArgs sel,
       const u32x4 z = {0, 0, 0, 0};
       const u32x4 vg = in ? load16(wg + wo + nfull * 64) : z;
       const u32x4 vu = in ? load16(wu + wo + nfull * 64) : z;
-      const u32x4 vx = in ? load16(a.x + xo + nfull * 64) : z;
-      ag = mma16<kF32>(vg, vx, ag);
-      au = mma16<kF32>(vu, vx, au);
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) products(vg, vu, i, in ? load16(a.x + xo[i] + nfull * 64) : z);
     }
-    red[wave][0][lane] = ag;
-    red[wave][1][lane] = au;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      red[wave][i][0][lane] = ag[i];
+      red[wave][i][1][lane] = au[i];
+    }
     __syncthreads();
-    if (wave == 0 && r < n) {
-      floatx4 vg = red[0][0][lane], vu = red[0][1][lane];
+    static_assert(NQ <= kWaves, "a wave for every 16 tokens");
+    const int at = 16 * wave + r;   // of the group's tokens
+    const int t = __shfl(by_rank, min(rank + at, kWave - 1), kWave);
+    if (wave < NQ && at < n) {
+      const int i = min(wave, NQ - 1);
+      floatx4 vg = red[0][i][0][lane], vu = red[0][i][1][lane];
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) {
-        vg += red[w][0][lane];
-        vu += red[w][1][lane];
+        vg += red[w][i][0][lane];
+        vu += red[w][i][1][lane];
       }
       const float wt = NR ? w_s[e * a.T + t] : a.w[t * a.K + a.slots[e * 64 + t]];
       const int64_t col = c * 16 + 4 * g;
-      const int64_t row = s.row[q] + r;
+      typedef HPlace<kF32> P;
+      char* dst = a.h + ((s.block[q] + at / P::kGroup) * (a.Ip * Elem<kF32>::kBytes >> 6) +
+                         (col * Elem<kF32>::kBytes >> 6)) * 1024 +
+                  at % P::kGroup * P::kParts * 64 + (col * Elem<kF32>::kBytes & 63);
       floatx4 v;
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = col + j < a.I ? wt * swiglu<kF32>(vg[j], vu[j]) : 0.0f;
       if constexpr (kF32) {
-        *reinterpret_cast<floatx4*>(a.h + (row * a.Ip + col) * 4) = v;
+        *reinterpret_cast<floatx4*>(dst) = v;
       } else {
         const uint32_t h0 = cvt_bf16x2(v[0], v[1]), h1 = cvt_bf16x2(v[2], v[3]);
         // the rest of a number past bf16's range (or of a NaN) is 0, not NaN
@@ -254,9 +279,8 @@ __global__ __launch_bounds__(kThreads, 3) void few_up(FewArgs a, SelectArgs sel,
         float lo[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) lo[j] = fabsf(hf[j]) <= 3.3895314e38f ? v[j] - hf[j] : 0.0f;
-        char* dst = a.h + (row * 2 * a.Ip + col) * 2;
         *reinterpret_cast<uint2*>(dst) = uint2{h0, h1};
-        *reinterpret_cast<uint2*>(dst + a.Ip * 2) = uint2{cvt_bf16x2(lo[0], lo[1]), cvt_bf16x2(lo[2], lo[3])};
+        *reinterpret_cast<uint2*>(dst + 64) = uint2{cvt_bf16x2(lo[0], lo[1]), cvt_bf16x2(lo[2], lo[3])};
       }
     }
     __syncthreads();
@@ -283,27 +307,29 @@ struct Item {
 // that a batch loads as much of h as of w2. (16 tokens and two operands load
 // twice as much of h: OLD)
 // kVec: rows of w2 start on 16 bytes.
-template <bool kF32, bool kVec>
-__global__ __launch_bounds__(kDownThreads, 3) void few_down(FewArgs a) {
+template <bool kF32, bool kVec, int ND>
+__global__ __launch_bounds__(kThreads, 3) void few_down(FewArgs a) {
+  constexpr int kU = ND <= 2 ? 4 : 2;   // 64-byte k-blocks of one batch of loads
   typedef typename Elem<kF32>::type E;
   constexpr int kC = Elem<kF32>::kChunk, kB = Elem<kF32>::kBytes;
-  constexpr int kParts = kF32 ? 1 : 2, kGroup = 16 / kParts;
+  constexpr int kParts = HPlace<kF32>::kParts, kGroup = HPlace<kF32>::kGroup;
   __shared__ Groups s;
-  __shared__ int tmp[kDownWaves];
-  __shared__ floatx4 sum[kDownWaves][kFewTokens][4];
-  const int n_groups = find_groups<kDownThreads, kGroup>(a.masks, a.E, s, tmp);
+  __shared__ int tmp[kWaves];
+  __shared__ floatx4 sum[kWaves][kFewTokens][4];
+  const int n_groups = find_groups<kF32, kThreads, kGroup * ND>(a.masks, a.E, s, tmp);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int g = lane >> 4, r = lane & 15;
-  const int tr = r % kGroup, part = r / kGroup;   // the lane's token of a group and number
-  const int I = static_cast<int>(a.I), Ip = static_cast<int>(a.Ip);
+  const int tr = r / kParts, part = r % kParts;   // the lane's token of a block and number
+  const int I = static_cast<int>(a.I);
+  const uint32_t h_bytes = static_cast<uint32_t>(a.Ip * kB) * 16;   // of a block of h
   // This wave's 64-byte blocks of every row of h and w2 (the same for every
   // expert, so that a token's sums do not depend on the other tokens), in
   // batches of kU: whole blocks by wide loads, the last of which start early
   // enough to end with the share; then what is left of the row's end.
   const int nkb = (I * kB + 63) >> 6;
   const int nfull = kVec && (I * kB >> 6) >= kU ? I * kB >> 6 : 0;
-  const int kb0 = wave * nkb / kDownWaves, kb1 = (wave + 1) * nkb / kDownWaves;
+  const int kb0 = wave * nkb / kWaves, kb1 = (wave + 1) * nkb / kWaves;
   const int kbf = max(min(kb1, nfull), kb0);
   const int nbf = (kbf - kb0 + kU - 1) / kU;
   const int items = n_groups * nbf;
@@ -313,10 +339,12 @@ __global__ __launch_bounds__(kDownThreads, 3) void few_down(FewArgs a) {
     const uint32_t lr = static_cast<uint32_t>(min(static_cast<int64_t>(r), a.H - 1 - u * 16));
     const uint32_t wo = lr * static_cast<uint32_t>(I * kB) + g * 16;
     for (int t = lane; t < a.T * 4; t += kWave) sum[wave][t >> 2][t & 3] = floatx4{0, 0, 0, 0};
-    floatx4 acc = {0, 0, 0, 0};
+    floatx4 acc[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d) acc[d] = floatx4{0, 0, 0, 0};
 
     struct Batch {
-      u32x4 w[kU], h[kU];
+      u32x4 w[kU], h[ND][kU];
     } b0, b1;
     auto start = [&](int b) { return min(kb0 + b * kU, max(kbf - kU, 0)); };
     auto w_at = [&](int q) {
@@ -324,22 +352,26 @@ __global__ __launch_bounds__(kDownThreads, 3) void few_down(FewArgs a) {
       return static_cast<const char*>(a.w2) + (e * a.H + u * 16) * a.I * kB;
     };
     auto h_at = [&](int q) {
-      const int row = __builtin_amdgcn_readfirstlane(s.row[q]);
-      return a.h + static_cast<int64_t>(row) * kParts * Ip * kB;
+      const int block = __builtin_amdgcn_readfirstlane(s.block[q]);
+      return a.h + static_cast<int64_t>(block) * h_bytes;
     };
-    // the lane's row of h; past the group's last token its first one's
-    auto h_off = [&](int q) {
-      const int n = __popcll(s.mask[q]) - s.rank[q];
-      return static_cast<uint32_t>((tr < n ? tr * kParts : 0) + part) * Ip * kB + g * 16;
+    // the lane's column of h; past the group's last token its first one's
+    auto h_off = [&](int q, int d) {
+      const int n = __popcll(s.mask[q]) - s.rank[q], at = d * kGroup + tr;
+      return (at < n ? d * h_bytes + r * 64 : part * 64) + g * 16;
     };
     auto load = [&](Batch& v, const Item& it) {
       const char* w0 = w_at(it.q);
       const char* h0 = h_at(it.q);
-      const uint32_t k = static_cast<uint32_t>(start(it.b)) * 64, ho = h_off(it.q) + k;
+      const uint32_t k = static_cast<uint32_t>(start(it.b));
+      uint32_t ho[ND];
+#pragma unroll
+      for (int d = 0; d < ND; ++d) ho[d] = h_off(it.q, d) + k * 1024;
 #pragma unroll
       for (int j = 0; j < kU; ++j) {
-        v.w[j] = load16(w0 + (wo + k) + j * 64);
-        v.h[j] = load16(h0 + ho + j * 64);
+        v.w[j] = load16(w0 + (wo + k * 64) + j * 64);
+#pragma unroll
+        for (int d = 0; d < ND; ++d) v.h[d][j] = load16(h0 + ho[d] + j * 1024);
       }
       __builtin_amdgcn_sched_barrier(0);
     };
@@ -347,23 +379,30 @@ __global__ __launch_bounds__(kDownThreads, 3) void few_down(FewArgs a) {
     auto add = [&](int q) {
       const uint64_t mask = s.mask[q];
       const int rank = s.rank[q];
-      const int n = min(kGroup, __popcll(mask) - rank);
-      const int t = group_token(mask, rank, n, r);
-      if constexpr (kParts == 2) {
-        // lanes 0 to 7 of each 16: what the second numbers, 8 lanes on, gave
+      const int n = __popcll(mask) - rank, by_rank = tokens_by_rank(mask);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[j] += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(acc[j]), 0x128, 15, 15, true));
+      for (int d = 0; d < ND; ++d) {
+        const int at = d * kGroup + tr;
+        const int t = __shfl(by_rank, min(rank + at, kWave - 1), kWave);
+        if constexpr (kParts == 2) {
+          // even lanes: what the second numbers, a lane on, gave
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            acc[d][j] += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(acc[d][j]), 0xf5, 15, 15, true));
+        }
+        if (part == 0 && at < n) sum[wave][t][g] += acc[d];
+        acc[d] = floatx4{0, 0, 0, 0};
       }
-      if (r < n) sum[wave][t][g] += acc;
-      acc = floatx4{0, 0, 0, 0};
     };
     auto mma = [&](const Batch& v, Item& it) {
       // products of blocks that a batch reads again are skipped
       const int k = start(it.b), kb = kb0 + it.b * kU;
 #pragma unroll
       for (int j = 0; j < kU; ++j)
-        if (k + j >= kb && k + j < kbf) acc = mma16<kF32>(v.w[j], v.h[j], acc);
+        if (k + j >= kb && k + j < kbf) {
+#pragma unroll
+          for (int d = 0; d < ND; ++d) acc[d] = mma16<kF32>(v.w[j], v.h[d][j], acc[d]);
+        }
       __builtin_amdgcn_sched_barrier(0);
       if (it.b + 1 == nbf) add(it.q);
       it.next(nbf);
@@ -394,9 +433,9 @@ __global__ __launch_bounds__(kDownThreads, 3) void few_down(FewArgs a) {
       // I to Ip)
       for (int q = 0; q < n_groups; ++q) {
         const E* wrow = reinterpret_cast<const E*>(w_at(q) + lr * static_cast<uint32_t>(I * kB));
-        const char* hrow = h_at(q) + h_off(q);
+        const char* h0 = h_at(q);
         for (int kb = kbf; kb < kb1; kb += kU) {
-          u32x4 w[kU], h[kU];
+          u32x4 w[kU];
 #pragma unroll
           for (int j = 0; j < kU; ++j) {
             const int k = (kb + j) * 4 * kC + g * kC;
@@ -406,48 +445,72 @@ __global__ __launch_bounds__(kDownThreads, 3) void few_down(FewArgs a) {
               if constexpr (kVec) w[j] = load16(reinterpret_cast<const char*>(wrow + k));
               else w[j] = load16_any<kF32>(wrow, k, I);
             }
-            h[j] = in && k < Ip ? load16(hrow + (kb + j) * 64) : u32x4{0, 0, 0, 0};
           }
 #pragma unroll
-          for (int j = 0; j < kU; ++j) acc = mma16<kF32>(w[j], h[j], acc);
+          for (int d = 0; d < ND; ++d) {
+            u32x4 h[kU];
+#pragma unroll
+            for (int j = 0; j < kU; ++j)
+              h[j] = kb + j < kb1 ? load16(h0 + h_off(q, d) + (kb + j) * 1024) : u32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < kU; ++j) acc[d] = mma16<kF32>(w[j], h[j], acc[d]);
+          }
         }
         add(q);
       }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < a.T * 4; i += kDownThreads) {
+    for (int i = threadIdx.x; i < a.T * 4; i += kThreads) {
       const int t = i >> 2, gg = i & 3;
       floatx4 v = sum[0][t][gg];
 #pragma unroll
-      for (int w = 1; w < kDownWaves; ++w) v += sum[w][t][gg];
+      for (int w = 1; w < kWaves; ++w) v += sum[w][t][gg];
       store4<kF32>(static_cast<E*>(a.y) + t * a.H, u * 16 + 4 * gg, a.H, true, v);
     }
     __syncthreads();
   }
 }
 
+template <bool kF32, bool kVec, int ND>
+hipError_t launch_down(const FewArgs& a, unsigned grid, hipStream_t st) {
+  hipLaunchKernelGGL((few_down<kF32, kVec, ND>), dim3(grid), dim3(kThreads), 0, st, a);
+  return hipGetLastError();
+}
 template <bool kF32>
-hipError_t launch_few(const FewArgs& a, const SelectArgs* sel, int64_t begin, hipStream_t st) {
+hipError_t launch_down(const FewArgs& a, double per_expert, unsigned grid, hipStream_t st) {
+  constexpr int kGroup = kF32 ? 16 : 8;
+  const bool vec = a.I % Elem<kF32>::kChunk == 0;
+  if (per_expert <= kGroup)
+    return vec ? launch_down<kF32, true, 1>(a, grid, st) : launch_down<kF32, false, 1>(a, grid, st);
+  if (per_expert <= 2 * kGroup)
+    return vec ? launch_down<kF32, true, 2>(a, grid, st) : launch_down<kF32, false, 2>(a, grid, st);
+  return vec ? launch_down<kF32, true, 4>(a, grid, st) : launch_down<kF32, false, 4>(a, grid, st);
+}
+
+template <bool kF32>
+hipError_t launch_few(const FewArgs& a, const SelectArgs* sel, double per_expert, int64_t begin, hipStream_t st) {
   const int cus = device_cu_count();
   const int64_t most = static_cast<int64_t>(a.T) * a.K < a.E ? static_cast<int64_t>(a.T) * a.K
                                                              : a.E + static_cast<int64_t>(a.T) * a.K / 16;
   const int64_t u1 = most * (a.Ip / 16), u2 = cdiv(a.H, 16);
   // as many blocks as fit at once
-  const unsigned g1 = static_cast<unsigned>(u1 < 3 * cus ? u1 : 3 * cus);
+  const int nq = a.T <= 16 || per_expert <= 8 ? 1 : a.T <= 32 || per_expert <= 32 ? 2 : 4;
+  const int b1 = (nq == 4 ? 2 : 3) * cus;
+  const unsigned g1 = static_cast<unsigned>(u1 < b1 ? u1 : b1);
   const unsigned g2 = static_cast<unsigned>(u2 < 2 * cus ? u2 : 2 * cus);
-  if (!sel)
-    hipLaunchKernelGGL((few_up<kF32, 0>), dim3(g1), dim3(kThreads), 0, st, a, SelectArgs{}, begin);
-  else if (sel->G <= 64)
-    hipLaunchKernelGGL((few_up<kF32, 1>), dim3(g1), dim3(kThreads), 0, st, a, *sel, begin);
+  if (sel && sel->G <= 64)
+    hipLaunchKernelGGL((few_up<kF32, 1, 1>), dim3(g1), dim3(kThreads), 0, st, a, *sel, begin);
+  else if (sel)
+    hipLaunchKernelGGL((few_up<kF32, 4, 1>), dim3(g1), dim3(kThreads), 0, st, a, *sel, begin);
+  else if (nq == 1)
+    hipLaunchKernelGGL((few_up<kF32, 0, 1>), dim3(g1), dim3(kThreads), 0, st, a, SelectArgs{}, begin);
+  else if (nq == 2)
+    hipLaunchKernelGGL((few_up<kF32, 0, 2>), dim3(g1), dim3(kThreads), 0, st, a, SelectArgs{}, begin);
   else
-    hipLaunchKernelGGL((few_up<kF32, 4>), dim3(g1), dim3(kThreads), 0, st, a, *sel, begin);
+    hipLaunchKernelGGL((few_up<kF32, 0, 4>), dim3(g1), dim3(kThreads), 0, st, a, SelectArgs{}, begin);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (a.I % Elem<kF32>::kChunk == 0)
-    hipLaunchKernelGGL((few_down<kF32, true>), dim3(g2), dim3(kDownThreads), 0, st, a);
-  else
-    hipLaunchKernelGGL((few_down<kF32, false>), dim3(g2), dim3(kDownThreads), 0, st, a);
-  return hipGetLastError();
+  return launch_down<kF32>(a, per_expert, g2, st);
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -463,8 +526,10 @@ FewLayout few_layout(const tr_layer_desc& d) {
   auto take = [&](size_t n) { const size_t at = o; o = up256(o + n); return at; };
   L.masks = take(8 * static_cast<size_t>(d.E));
   L.slots = take(64 * static_cast<size_t>(d.E));
-  // two bf16 or one fp32 number: 4 bytes each
-  L.h = take(4 * static_cast<size_t>(d.route.T) * d.route.K * L.Ip);
+  const size_t routes = static_cast<size_t>(d.route.T) * d.route.K, E = d.E;
+  const bool f32 = d.route.dtype == TR_F32;
+  const size_t blocks = (routes < E ? routes : E) + routes / (f32 ? HPlace<true>::kGroup : HPlace<false>::kGroup);
+  L.h = take(blocks * 16 * L.Ip * (f32 ? 4 : 2));
   L.total = o;
   return L;
 }
@@ -502,8 +567,9 @@ hipError_t few_layer(const tr_layer_desc& d, const void* x, const void* w_gate, 
   a.I = d.I;
   a.Ip = L.Ip;
   const SelectArgs sel = select_args(r, bias, idx, w, route_ws);
-  return f32 ? launch_few<true>(a, fused ? &sel : nullptr, d.expert_begin, st)
-             : launch_few<false>(a, fused ? &sel : nullptr, d.expert_begin, st);
+  const double per_expert = static_cast<double>(r.T) * r.K / r.G;
+  return f32 ? launch_few<true>(a, fused ? &sel : nullptr, per_expert, d.expert_begin, st)
+             : launch_few<false>(a, fused ? &sel : nullptr, per_expert, d.expert_begin, st);
 }
 
 }  // namespace tr
