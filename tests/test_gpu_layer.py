@@ -48,6 +48,22 @@ def test_against_the_formula(T, H, I, E, G, K, begin, dtype):
     assert not y.cpu()[none].view(view).any()        # +0
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,H,I,E,G,K", [
+    (20, 512, 160, 4, 4, 2), (40, 256, 99, 6, 12, 4), (40, 264, 99, 6, 6, 4), (64, 136, 257, 3, 3, 3),
+    (64, 256, 70, 5, 10, 8), (33, 128, 64, 1, 1, 1),    # many tokens an expert
+    (8, 264, 2056, 16, 16, 4), (8, 512, 2051, 16, 16, 4), (9, 136, 1030, 40, 40, 5),
+    (64, 72, 1536, 24, 24, 6), (1, 96, 1800, 32, 32, 32),    # the reduction in parts
+    (3, 4096, 24, 4, 4, 2), (3, 4104, 24, 4, 4, 2), (3, 7168, 24, 4, 4, 2),
+])
+def test_shapes_that_divide_the_work_differently(T, H, I, E, G, K, dtype):
+    say(f"layer T={T} H={H} I={I} E={E} G={G} K={K} {dtype}")
+    x, gate, w1, w2 = make(T + H + I, T, H, I, E, G, dtype)
+    y, idx, w = run(x, gate, w1, w2, K, expert_begin=G - E)
+    ref, bound = S.layer(x, idx, w, w1, w2, G - E)
+    S.check(y, ref, bound, "y")
+
+
 @pytest.mark.parametrize("T", [65, 200])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_more_rows_are_the_router_plan_and_forward(T, dtype):

@@ -8,11 +8,16 @@
 //
 // Bound: reading the weights of the experts that some token chose, once. The
 // tokens of an expert are a 64-bit mask, so there is no route scan and no
-// expanded copy of x: 16 of an expert's tokens (in most decode batches all of
-// them) are the columns of one MFMA operand, weight rows go from memory into
-// the other, and a row of h has its place by the expert's tokens before it.
-// Both kernels keep two batches of loads per wave, one in flight while the
-// other's products run, with a batch small enough that 16 waves fit a CU.
+// expanded copy of x: an expert's tokens are the columns of one MFMA operand,
+// weight rows go from memory into the other, and h has its place by the expert's
+// tokens before. Both kernels keep two batches of loads per wave, one in flight
+// while the other's products run, with a batch small enough that 12 waves fit a
+// CU. What a CU reads of rows (16 rows of 64 bytes a load) is at most 34 KB/us,
+// from L2 too, so operands beside the weights count: h is stored in the order in
+// which few_down loads it (64 tokens of 8 experts, all chosen: 147 -> 98 us).
+//
+// One token, 8 of 32 experts of 7168 x 2048: 81 + 43 us, 5.8 and 5.4 TB/s; 64
+// tokens, 8 of 256 experts, 32 of them here: 227 + 124 us, 7.2 and 6.6 TB/s.
 //
 // The gate weight is folded into h. bf16: h is kept as two bf16 numbers whose
 // sum has 16 significant bits, and few_down multiplies both, as different columns
@@ -47,6 +52,8 @@ struct FewArgs {
   char* h;                           // [blocks][Ip * bytes / 64][16][64 bytes]
   void* y;                           // [T, H]
   int T, K, E;
+  int cols, parts;                   // few_down's units: output columns, parts of the reduction
+  float* sums;                       // [parts][T][H] with more than one part
   int64_t H, I, Ip;
 };
 
@@ -114,7 +121,8 @@ constexpr int kChooseTokens = kWaves;
 constexpr int kChooseGates = 256;
 
 // A unit: 16 gate rows and the matching 16 up rows of one group's expert, the
-// reduction over the block's waves. NR > 0: every block makes the tokens'
+// reduction over the block's waves. A group: up to 16 NQ tokens of an expert, for
+// which weights are loaded once. NR > 0: every block makes the tokens'
 // choice from the logits' parts (NR registers a lane); block 0 stores it.
 template <bool kF32, int NR, int NQ>
 __global__ __launch_bounds__(kThreads, NQ == 4 ? 2 : 3) void few_up(FewArgs a, SelectArgs sel, int64_t begin) {
@@ -298,14 +306,14 @@ struct Item {
   }
 };
 
-// A unit: 16 output columns of every token; the block's waves share the
-// reduction. A wave adds a group's sums to its tokens' totals, which it keeps
+// A unit: a.cols (at most 16) output columns of every token; the block's waves (and
+// a.parts blocks) share the reduction. A wave adds a group's sums to its tokens' totals, which it keeps
 // in LDS, experts ascending, so an expert's infinities reach its own tokens
 // only; then the waves' totals are added.
-// The second MFMA operand has 16 columns. bf16: a group is 8 tokens, whose h
-// fill columns 0 to 7 with their first numbers and 8 to 15 with their second, so
-// that a batch loads as much of h as of w2. (16 tokens and two operands load
-// twice as much of h: OLD)
+// A group: ND blocks of h, for which weights are loaded once. bf16: a block is 8
+// tokens with both numbers of each, so that a batch loads as much of h as of w2
+// (16 tokens in two operands, with half of their columns empty in most decode
+// batches, took 50 us for one token and not 43).
 // kVec: rows of w2 start on 16 bytes.
 template <bool kF32, bool kVec, int ND>
 __global__ __launch_bounds__(kThreads, 3) void few_down(FewArgs a) {
@@ -329,14 +337,17 @@ __global__ __launch_bounds__(kThreads, 3) void few_down(FewArgs a) {
   // enough to end with the share; then what is left of the row's end.
   const int nkb = (I * kB + 63) >> 6;
   const int nfull = kVec && (I * kB >> 6) >= kU ? I * kB >> 6 : 0;
-  const int kb0 = wave * nkb / kWaves, kb1 = (wave + 1) * nkb / kWaves;
+  const int share = blockIdx.y * kWaves + wave, shares = a.parts * kWaves;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(share) * nkb / shares);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(share + 1) * nkb / shares);
   const int kbf = max(min(kb1, nfull), kb0);
   const int nbf = (kbf - kb0 + kU - 1) / kU;
   const int items = n_groups * nbf;
-  const int units = static_cast<int>((a.H + 15) / 16);
+  const int units = static_cast<int>((a.H + a.cols - 1) / a.cols);
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    // (H is a multiple of 8: the last unit may have 8 columns)
-    const uint32_t lr = static_cast<uint32_t>(min(static_cast<int64_t>(r), a.H - 1 - u * 16));
+    // (a lane past the unit's last column reads that one's row)
+    const int64_t col0 = static_cast<int64_t>(u) * a.cols;
+    const uint32_t lr = static_cast<uint32_t>(min(static_cast<int64_t>(min(r, a.cols - 1)), a.H - 1 - col0));
     const uint32_t wo = lr * static_cast<uint32_t>(I * kB) + g * 16;
     for (int t = lane; t < a.T * 4; t += kWave) sum[wave][t >> 2][t & 3] = floatx4{0, 0, 0, 0};
     floatx4 acc[ND];
@@ -349,7 +360,7 @@ __global__ __launch_bounds__(kThreads, 3) void few_down(FewArgs a) {
     auto start = [&](int b) { return min(kb0 + b * kU, max(kbf - kU, 0)); };
     auto w_at = [&](int q) {
       const int e = __builtin_amdgcn_readfirstlane(s.expert[q]);
-      return static_cast<const char*>(a.w2) + (e * a.H + u * 16) * a.I * kB;
+      return static_cast<const char*>(a.w2) + (e * a.H + col0) * a.I * kB;
     };
     auto h_at = [&](int q) {
       const int block = __builtin_amdgcn_readfirstlane(s.block[q]);
@@ -462,18 +473,34 @@ __global__ __launch_bounds__(kThreads, 3) void few_down(FewArgs a) {
     __syncthreads();
     for (int i = threadIdx.x; i < a.T * 4; i += kThreads) {
       const int t = i >> 2, gg = i & 3;
+      if (4 * gg >= a.cols) continue;
       floatx4 v = sum[0][t][gg];
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) v += sum[w][t][gg];
-      store4<kF32>(static_cast<E*>(a.y) + t * a.H, u * 16 + 4 * gg, a.H, true, v);
+      const int64_t col = col0 + 4 * gg;
+      if (a.parts == 1) {
+        store4<kF32>(static_cast<E*>(a.y) + t * a.H, col, a.H, true, v);
+      } else if (col < a.H) {   // (H is a multiple of 8)
+        *reinterpret_cast<floatx4*>(a.sums + (static_cast<int64_t>(blockIdx.y) * a.T + t) * a.H + col) = v;
+      }
     }
     __syncthreads();
   }
 }
 
+// y = the sum of few_down's parts, four elements a thread.
+template <bool kF32>
+__global__ __launch_bounds__(kThreads) void few_join(FewArgs a) {
+  const int64_t n = a.T * a.H, i = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * 4;
+  if (i >= n) return;
+  floatx4 v = *reinterpret_cast<const floatx4*>(a.sums + i);
+  for (int s = 1; s < a.parts; ++s) v += *reinterpret_cast<const floatx4*>(a.sums + s * n + i);
+  store4<kF32>(static_cast<typename Elem<kF32>::type*>(a.y), i, n, true, v);
+}
+
 template <bool kF32, bool kVec, int ND>
 hipError_t launch_down(const FewArgs& a, unsigned grid, hipStream_t st) {
-  hipLaunchKernelGGL((few_down<kF32, kVec, ND>), dim3(grid), dim3(kThreads), 0, st, a);
+  hipLaunchKernelGGL((few_down<kF32, kVec, ND>), dim3(grid, a.parts), dim3(kThreads), 0, st, a);
   return hipGetLastError();
 }
 template <bool kF32>
@@ -492,8 +519,12 @@ hipError_t launch_few(const FewArgs& a, const SelectArgs* sel, double per_expert
   const int cus = device_cu_count();
   const int64_t most = static_cast<int64_t>(a.T) * a.K < a.E ? static_cast<int64_t>(a.T) * a.K
                                                              : a.E + static_cast<int64_t>(a.T) * a.K / 16;
-  const int64_t u1 = most * (a.Ip / 16), u2 = cdiv(a.H, 16);
-  // as many blocks as fit at once
+  const int64_t u1 = most * (a.Ip / 16), u2 = cdiv(a.H, a.cols);
+  // Tokens for which weights are loaded once, by those that an expert gets on
+  // average (4096 x 2048, 64 tokens; 8 of 8 experts: up 178, 121 and 97 us, down
+  // 229, 174 and 146 us with 16, 32 and 64; 2 of 8: up 71, 56 and 78; 2 of 16 by 48
+  // tokens: up 93, 98 and 122, down 63, 70 and 88)
+  // As many blocks as fit at once.
   const int nq = a.T <= 16 || per_expert <= 8 ? 1 : a.T <= 32 || per_expert <= 32 ? 2 : 4;
   const int b1 = (nq == 4 ? 2 : 3) * cus;
   const unsigned g1 = static_cast<unsigned>(u1 < b1 ? u1 : b1);
@@ -510,14 +541,47 @@ hipError_t launch_few(const FewArgs& a, const SelectArgs* sel, double per_expert
     hipLaunchKernelGGL((few_up<kF32, 0, 4>), dim3(g1), dim3(kThreads), 0, st, a, SelectArgs{}, begin);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return launch_down<kF32>(a, per_expert, g2, st);
+  if ((e = launch_down<kF32>(a, per_expert, g2, st)) != hipSuccess || a.parts == 1) return e;
+  hipLaunchKernelGGL(few_join<kF32>, dim3(static_cast<unsigned>(cdiv(a.T * a.H, 4 * kThreads))), dim3(kThreads), 0,
+                     st, a);
+  return hipGetLastError();
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
+// few_down's units. Columns: those that leave the fullest CU the fewest (2880
+// columns by 12 and not 16: 33 us instead of 35; 4160: 66 instead of 75). Parts:
+// where not even half of the CUs get a unit of 16 and the split takes 192 KiB of
+// weights and more from each, 8 us at what a CU reads, which pays for the launch
+// that adds the parts (1024 x 2048, 8 tokens that choose 4 of 16 experts: 31 us
+// whole, 13 + 4 in four parts; two experts, 128 KiB a unit: 6 whole, 5 + 2).
+struct DownShape {
+  int cols, parts;
+};
+DownShape down_shape(const tr_layer_desc& d) {
+  const int64_t H = d.route.H, row = d.I * (d.route.dtype == TR_F32 ? 4 : 2);
+  const int64_t units = cdiv(H, 16);
+  DownShape s{16, 1};
+  int64_t parts = kPlanCus / units;
+  if (parts > row / 1024) parts = row / 1024;   // a batch of loads for a wave
+  if (parts > 8) parts = 8;
+  // bytes of weights of a unit, for the experts that the rows choose at most
+  const double routes = static_cast<double>(d.route.T) * d.route.K * d.E / d.route.G;
+  const double bytes = 16.0 * row * (routes < 1 ? 1 : routes < d.E ? routes : d.E);
+  if (parts > 1 && bytes * (1.0 - 1.0 / parts) >= 3 << 16) {
+    s.parts = static_cast<int>(parts);
+    return s;
+  }
+  auto fullest = [&](int cols) { return cdiv(cdiv(H, cols), kPlanCus) * cols; };
+  for (int cols = 12; cols >= 8; cols -= 4)
+    if (fullest(cols) < fullest(s.cols)) s.cols = cols;
+  return s;
+}
+
 struct FewLayout {
-  size_t masks, slots, h, total;
+  size_t masks, slots, h, sums, total;
   int64_t Ip;
+  DownShape down;
 };
 FewLayout few_layout(const tr_layer_desc& d) {
   FewLayout L{};
@@ -529,6 +593,8 @@ FewLayout few_layout(const tr_layer_desc& d) {
   const size_t routes = static_cast<size_t>(d.route.T) * d.route.K, E = d.E;
   const bool f32 = d.route.dtype == TR_F32;
   const size_t blocks = (routes < E ? routes : E) + routes / (f32 ? HPlace<true>::kGroup : HPlace<false>::kGroup);
+  L.down = down_shape(d);
+  L.sums = take(L.down.parts > 1 ? 4 * static_cast<size_t>(L.down.parts) * d.route.T * d.route.H : 0);
   L.h = take(blocks * 16 * L.Ip * (f32 ? 4 : 2));
   L.total = o;
   return L;
@@ -559,6 +625,9 @@ hipError_t few_layer(const tr_layer_desc& d, const void* x, const void* w_gate, 
   a.slots = f.slots;
   a.w = w;
   a.h = b + L.h;
+  a.sums = reinterpret_cast<float*>(b + L.sums);
+  a.cols = L.down.cols;
+  a.parts = L.down.parts;
   a.y = y;
   a.T = static_cast<int>(r.T);
   a.K = r.K;
