@@ -84,6 +84,24 @@ def test_rows_of_infinities_and_nan():
     assert not (idx.cpu() == 0).any()
 
 
+@pytest.mark.parametrize("T,H,G,K", [(1, 8, 1, 1), (16, 264, 32, 9), (17, 520, 17, 4), (100, 1000, 32, 32),
+                                     (333, 2040, 16, 2), (4096, 40, 9, 3), (4097, 40, 9, 3)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_small_routers(T, H, G, K, dtype):
+    x, w = exact_inputs(T + H, T, H, G, dtype)
+    idx, wt = tr.route_topk(x.cuda(), w.cuda(), K, renorm=False)
+    ref, rw, tol, _ = S.route(x, w, K, renorm=False)
+    assert torch.equal(idx.cpu(), ref)
+    S.check(wt, rw, tol, "weights")
+    # a row that is not a number stays by itself
+    bad = x.clone()
+    bad[T // 2, H - 1] = float("nan")
+    i2, w2 = tr.route_topk(bad.cuda(), w.cuda(), K, renorm=False)
+    rest = torch.arange(T) != T // 2
+    assert torch.equal(i2.cpu()[rest], idx.cpu()[rest]) and torch.equal(w2.cpu()[rest], wt.cpu()[rest])
+    assert sorted(i2[T // 2].tolist()) == i2[T // 2].unique().tolist()
+
+
 def test_scores_that_vanish():
     """All sigmoids 0: weights 0 with renorm, not NaN."""
     x = torch.full((2, 8), 10.0, dtype=F32)
