@@ -314,8 +314,7 @@ struct Item {
 // tokens with both numbers of each, so that a batch loads as much of h as of w2
 // (16 tokens in two operands, with half of their columns empty in most decode
 // batches, took 50 us for one token and not 43).
-// kVec: rows of w2 start on 16 bytes.
-template <bool kF32, bool kVec, int ND>
+template <bool kF32, int ND>
 __global__ __launch_bounds__(kThreads, 3) void few_down(FewArgs a) {
   constexpr int kU = ND <= 2 ? 4 : 2;   // 64-byte k-blocks of one batch of loads
   typedef typename Elem<kF32>::type E;
@@ -336,7 +335,7 @@ __global__ __launch_bounds__(kThreads, 3) void few_down(FewArgs a) {
   // batches of kU: whole blocks by wide loads, the last of which start early
   // enough to end with the share; then what is left of the row's end.
   const int nkb = (I * kB + 63) >> 6;
-  const int nfull = kVec && (I * kB >> 6) >= kU ? I * kB >> 6 : 0;
+  const int nfull = (I * kB >> 6) >= kU ? I * kB >> 6 : 0;
   const int share = blockIdx.y * kWaves + wave, shares = a.parts * kWaves;
   const int kb0 = static_cast<int>(static_cast<int64_t>(share) * nkb / shares);
   const int kb1 = static_cast<int>(static_cast<int64_t>(share + 1) * nkb / shares);
@@ -380,7 +379,7 @@ __global__ __launch_bounds__(kThreads, 3) void few_down(FewArgs a) {
       for (int d = 0; d < ND; ++d) ho[d] = h_off(it.q, d) + k * 1024;
 #pragma unroll
       for (int j = 0; j < kU; ++j) {
-        v.w[j] = load16(w0 + (wo + k * 64) + j * 64);
+        v.w[j] = load16_odd(w0 + (wo + k * 64) + j * 64);
 #pragma unroll
         for (int d = 0; d < ND; ++d) v.h[d][j] = load16(h0 + ho[d] + j * 1024);
       }
@@ -452,10 +451,7 @@ __global__ __launch_bounds__(kThreads, 3) void few_down(FewArgs a) {
             const int k = (kb + j) * 4 * kC + g * kC;
             const bool in = kb + j < kb1;
             w[j] = u32x4{0, 0, 0, 0};
-            if (in && k < I) {
-              if constexpr (kVec) w[j] = load16(reinterpret_cast<const char*>(wrow + k));
-              else w[j] = load16_any<kF32>(wrow, k, I);
-            }
+            if (in && k < I) w[j] = load16_any<kF32>(wrow, k, I);
           }
 #pragma unroll
           for (int d = 0; d < ND; ++d) {
@@ -498,20 +494,19 @@ __global__ __launch_bounds__(kThreads) void few_join(FewArgs a) {
   store4<kF32>(static_cast<typename Elem<kF32>::type*>(a.y), i, n, true, v);
 }
 
-template <bool kF32, bool kVec, int ND>
+template <bool kF32, int ND>
 hipError_t launch_down(const FewArgs& a, unsigned grid, hipStream_t st) {
-  hipLaunchKernelGGL((few_down<kF32, kVec, ND>), dim3(grid, a.parts), dim3(kThreads), 0, st, a);
+  hipLaunchKernelGGL((few_down<kF32, ND>), dim3(grid, a.parts), dim3(kThreads), 0, st, a);
   return hipGetLastError();
 }
 template <bool kF32>
 hipError_t launch_down(const FewArgs& a, double per_expert, unsigned grid, hipStream_t st) {
   constexpr int kGroup = kF32 ? 16 : 8;
-  const bool vec = a.I % Elem<kF32>::kChunk == 0;
   if (per_expert <= kGroup)
-    return vec ? launch_down<kF32, true, 1>(a, grid, st) : launch_down<kF32, false, 1>(a, grid, st);
+    return launch_down<kF32, 1>(a, grid, st);
   if (per_expert <= 2 * kGroup)
-    return vec ? launch_down<kF32, true, 2>(a, grid, st) : launch_down<kF32, false, 2>(a, grid, st);
-  return vec ? launch_down<kF32, true, 4>(a, grid, st) : launch_down<kF32, false, 4>(a, grid, st);
+    return launch_down<kF32, 2>(a, grid, st);
+  return launch_down<kF32, 4>(a, grid, st);
 }
 
 template <bool kF32>

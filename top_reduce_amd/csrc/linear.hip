@@ -402,8 +402,10 @@ __global__ __launch_bounds__(kOrderThreads) void adapter_order(const int32_t* __
   }
   block_exclusive_scan<kOrderThreads>(ends, tmp, &all);
   // runs of 32 tokens and more on average: the order is good as it is
-  const bool sort = all > kWindow / 32;
-  for (int size = sort ? 2 : kWindow + 1; size <= kWindow; size <<= 1)
+  // (positions past the last token hold the largest keys: a window that is not full
+  // sorts as many as the next power of two)
+  const bool sort = all * 32 > n;
+  for (int size = sort ? 2 : 2 * n; size < 2 * n; size <<= 1)
     for (int d = size >> 1; d > 0; d >>= 1) {
       // thread tid: the pair (i, i + d); 64 threads take 128 neighbours when d <= 64
       const int i = 2 * tid - (tid & (d - 1));
@@ -441,7 +443,7 @@ struct ShrinkArgs {
   int A, R, Rq;
 };
 
-// v[t, j] = s[a] x[t] . A[a][j] for a group of 32 tokens: up to 32 rows of A at
+// v[t, j] = s[a] x[t] . A[a][j] for a group of 16 kNG tokens: 16 kRT rows of A at
 // a time, the waves sharing the reduction, two batches of loads in flight.
 // Bound by x from memory and A from L2: 39 us for 8192 x 7168 and rank 32 (16
 // tokens a group, which read A twice as often, took 58 us, of which 41 us were
@@ -454,12 +456,11 @@ constexpr int kSlots = 2;
 constexpr int kShrinkThreads = 384;   // two blocks a CU
 constexpr int kShrinkWaves = kShrinkThreads / kWave;
 
-template <bool kF32>
+template <bool kF32, int kRT, int kNG>
 __global__ __launch_bounds__(kShrinkThreads, 3) void adapter_shrink(ShrinkArgs p) {
   typedef typename Elem<kF32>::type E;
-  constexpr int kRT = 2;   // rank tiles of 16 at a time
-  constexpr int kNG = 2;   // groups of 16 tokens
-  constexpr int kB = 3;    // 64-byte blocks of a batch (4: registers spill, 42 us; 2: 50 us; 3: 39 us)
+  // 64-byte blocks of a batch (kRT = kNG = 2: 4 spill registers, 42 us; 2: 50 us; 3: 39 us)
+  constexpr int kB = kRT + kNG == 4 ? 3 : 4;
   __shared__ floatx4 red[kShrinkWaves][kRT][kNG][kWave];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
@@ -489,7 +490,7 @@ __global__ __launch_bounds__(kShrinkThreads, 3) void adapter_shrink(ShrinkArgs p
     for (int q = 0; q < kNG; ++q)
       xo[q] = __shfl(row, (mask >> (16 * q + r)) & 1 ? 16 * q + r : first, kWave) * row_bytes + g * 16;
     const float sc = p.scales ? p.scales[aid] : 1.0f;
-    for (int j0 = 0; j0 < p.Rq; j0 += 16 * kRT) {
+    for (int j0 = blockIdx.z * 16 * kRT; j0 < p.R; j0 += gridDim.z * 16 * kRT) {
       // rows past R read the last one: zeros are stored for them
       const int base = min(j0, p.R - 1);
       const char* a0 = p.a + (static_cast<int64_t>(aid) * p.R + base) * p.row_bytes;
@@ -582,11 +583,32 @@ __global__ __launch_bounds__(kShrinkThreads, 3) void adapter_shrink(ShrinkArgs p
         for (int w = 1; w < kShrinkWaves; ++w) v += red[w][c][q][lane];
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = col + i < p.R ? v[i] * sc : 0.0f;
-        store4<kF32>(static_cast<E*>(p.v) + (t0 + 16 * q + r) * p.Rq, col, p.Rq, true, v);
+        E* out = static_cast<E*>(p.v) + (t0 + 16 * q + r) * p.Rq;
+        store4<kF32>(out, col, p.Rq, true, v);
+        // (one tile of two that an MFMA takes: zeros in the other's place)
+        if (kRT == 1 && col + 16 < p.Rq) store4<kF32>(out, col + 16, p.Rq, true, floatx4{0, 0, 0, 0});
       }
       __syncthreads();
     }
   }
+}
+
+template <bool kF32, int kRT, int kNG>
+hipError_t launch_shrink(const ShrinkArgs& s, int64_t passes, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(cdiv(s.T, 16 * kNG)), kSlots, static_cast<unsigned>(passes));
+  hipLaunchKernelGGL((adapter_shrink<kF32, kRT, kNG>), grid, dim3(kShrinkThreads), 0, st, s);
+  return hipGetLastError();
+}
+// Groups of 16 tokens where their blocks, with some more for the borders of
+// requests, fit the CUs once (1000 x 4096, rank 16: 10 us and not 14; 3600 x 7168,
+// rank 32: 26 and not 32; but 4000 x 4096, rank 16: 19 and not 16). Ranks past 32:
+// a block for every 32 (2048 x 7168, rank 64: 32 us; one block for both 58).
+template <bool kF32>
+hipError_t launch_shrink(const ShrinkArgs& s, hipStream_t st) {
+  const int64_t passes = cdiv(s.R, 32);
+  const bool few = cdiv(s.T, 16) * passes * 8 <= kPlanCus * 7;
+  if (s.R <= 16) return few ? launch_shrink<kF32, 1, 1>(s, 1, st) : launch_shrink<kF32, 1, 2>(s, 1, st);
+  return few ? launch_shrink<kF32, 2, 1>(s, passes, st) : launch_shrink<kF32, 2, 2>(s, passes, st);
 }
 
 // --------------------------------------------------------------------------
@@ -1166,10 +1188,7 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
   s.A = d.A;
   s.R = d.R;
   s.Rq = L.Rq;
-  const dim3 groups(static_cast<unsigned>(cdiv(d.T, 32)), kSlots);
-  if (f32) hipLaunchKernelGGL(adapter_shrink<true>, groups, dim3(kShrinkThreads), 0, st, s);
-  else hipLaunchKernelGGL(adapter_shrink<false>, groups, dim3(kShrinkThreads), 0, st, s);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if ((e = f32 ? launch_shrink<true>(s, st) : launch_shrink<false>(s, st)) != hipSuccess) return e;
   if (adapter_can_tile(d)) return adapter_tiles(d, x, w, b, ids, perm, ws, L.Rq, y, st);
   TileArgs t{};
   t.x = s.x;

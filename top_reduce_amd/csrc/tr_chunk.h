@@ -45,10 +45,25 @@ __device__ __forceinline__ u32x4 load16(const char* p) {
   return *reinterpret_cast<const u32x4*>(p);
 }
 
+// 16 bytes that need not start on 16: one load, as global memory takes any
+// alignment.
+__device__ __forceinline__ u32x4 load16_odd(const void* p) {
+  typedef uint32_t Odd __attribute__((ext_vector_type(4), aligned(2)));
+  return *static_cast<const Odd*>(p);
+}
+
 // The 16 bytes at element k of a row of n elements that need not start on 16
-// bytes; zero past n.
+// bytes; zero past n. Near the end the row's last 16 bytes are read, and shifted.
 template <bool kF32>
 __device__ __forceinline__ u32x4 load16_any(const typename Elem<kF32>::type* row, int k, int n) {
+  constexpr int kC = Elem<kF32>::kChunk;
+  if (n >= kC) {
+    const int at = min(k, n - kC), over = k - at;
+    const u32x4 v = load16_odd(row + at);
+    if (over == 0) return v;
+    const unsigned __int128 all = __builtin_bit_cast(unsigned __int128, v);
+    return __builtin_bit_cast(u32x4, over < kC ? all >> (over * Elem<kF32>::kBytes * 8) : 0);
+  }
   u32x4 v = {0, 0, 0, 0};
   if constexpr (kF32) {
 #pragma unroll
