@@ -104,15 +104,6 @@ __device__ __forceinline__ int find_groups(const unsigned long long* masks, int 
   return total >> 16;
 }
 
-// Lane i < the number of tokens in `mask` (the same in every lane): the token of
-// rank i.
-__device__ __forceinline__ int tokens_by_rank(uint64_t mask) {
-  const int lane = lane_id();
-  // lane t of the mask sends t to the lane of its rank, the others to lane 63,
-  // which counts with 64 tokens only
-  return __builtin_amdgcn_ds_permute(((mask >> lane) & 1 ? popc_below(mask) : 63) * 4, lane);
-}
-
 // Up to this many tokens (one a wave) and experts few_up makes the choice: every
 // block repeats it, 2.5 us, which is less than the launch that it saves (about
 // 5 us on the GPU, 3 on the host). Two tokens a wave cost as much as the launch,

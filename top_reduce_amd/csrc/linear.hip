@@ -145,17 +145,14 @@ __device__ __forceinline__ void stream_unit(const StreamArgs& p, int chunk, int 
     wp = p.a + (static_cast<int64_t>(aid) * p.R + min(rt * 16 + r, p.R - 1)) * p.row_bytes;
   }
 
-  // A lane whose token is not of this tile reads the first one's row: its sums
-  // are never stored, and the columns of an MFMA do not mix.
-  const int first = __ffsll(static_cast<unsigned long long>(mask)) - 1;
+  // The tile's tokens are its first columns. A lane past the last one reads the
+  // first one's row: its sums are never stored, and the columns of an MFMA do not
+  // mix.
+  const int n = __popcll(mask), by_rank = tokens_by_rank(mask);
   const char* xp[NQ];
-  bool on[NQ];
 #pragma unroll
-  for (int q = 0; q < NQ; ++q) {
-    const int t = q * 16 + r;
-    on[q] = (mask >> (16 * q)) & 0xffff;
-    xp[q] = x0 + ((mask >> t) & 1 ? t : first) * p.row_bytes + g * 16;
-  }
+  for (int q = 0; q < NQ; ++q)
+    xp[q] = x0 + __shfl(by_rank, q * 16 + r < n ? q * 16 + r : 0, kWave) * p.row_bytes + g * 16;
   wp += g * 16;
 
   // this wave's 64-byte blocks; the last one of a row may be short
@@ -177,7 +174,7 @@ __device__ __forceinline__ void stream_unit(const StreamArgs& p, int chunk, int 
     for (int j = 0; j < kU; ++j) wa[j] = load16(wp + min(kb + j, kbf - 1) * 64);
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      if (!on[q]) continue;
+      if (q * 16 >= n) continue;
       u32x4 xb[kU];
 #pragma unroll
       for (int j = 0; j < kU; ++j) xb[j] = load16(xp[q] + min(kb + j, kbf - 1) * 64);
@@ -191,7 +188,7 @@ __device__ __forceinline__ void stream_unit(const StreamArgs& p, int chunk, int 
     const u32x4 wa = in ? load16(wp + nfull * 64) : u32x4{0, 0, 0, 0};
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      if (!on[q]) continue;
+      if (q * 16 >= n) continue;
       const u32x4 xb = in ? load16(xp[q] + nfull * 64) : u32x4{0, 0, 0, 0};
       acc[q] = mma16<kF32>(wa, xb, acc[q]);
     }
@@ -200,8 +197,8 @@ __device__ __forceinline__ void stream_unit(const StreamArgs& p, int chunk, int 
   for (int q = 0; q < NQ; ++q) red[(wave * NQ + q) * kWave + lane] = acc[q];
   __syncthreads();
   for (int q = wave; q < NQ; q += kWaves) {
-    const int t = q * 16 + r;
-    if (!((mask >> t) & 1)) continue;
+    const int t = __shfl(by_rank, q * 16 + r, kWave);
+    if (q * 16 + r >= n) continue;
     floatx4 v = red[q * kWave + lane];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) v += red[(w * NQ + q) * kWave + lane];
@@ -227,14 +224,14 @@ struct ExpandArgs {
 // 128 columns of one unit's tokens, 32 columns a wave. Rows of B are one MFMA
 // operand, read whole and once for all of the unit's tokens, the low-rank sums
 // the other: for bf16 as two bf16 numbers each (16 significant bits), so that y
-// is rounded once. Bound by latency: the loads of B, of the parts (eight at a
-// time) and of the low-rank sums go out together.
-template <bool kF32>
+// is rounded once. Bound by latency: the loads of B (kKb blocks of it at a time),
+// of the parts (kParts at a time) and of the low-rank sums go out together.
+template <bool kF32, int kKb, int kParts>
 __global__ __launch_bounds__(kThreads) void adapter_few(ExpandArgs p) {
   typedef typename Elem<kF32>::type E;
   constexpr int kC = Elem<kF32>::kChunk;
   constexpr int kV = kF32 ? 1 : 2;       // numbers that make up a low-rank sum
-  constexpr int kTok = 16, kNs = 2, kKb = 4, kParts = 8;
+  constexpr int kTok = 16, kNs = 2;
   constexpr int kPitch = kMaxRank + kC;  // (a pad: rows in other banks)
   __shared__ E v_s[kV][kTok][kPitch];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -962,11 +959,15 @@ int parts_for(int per_cu, int64_t n, int64_t ksteps, int64_t least, int64_t most
   return static_cast<int>(want < 1 ? 1 : want);
 }
 
-// For n 64 x 128 tiles: one block a CU, in four parts where that leaves seven
-// in eight CUs with one (adapter_few reads eight parts in one go).
-int few_parts(int64_t n, int64_t row_bytes) {
-  const int64_t ktiles = cdiv(row_bytes, 128);
-  return parts_for(1, n, ktiles, 3, 4 * n >= kPlanCus * 7 / 8 ? 4 : 8);
+// For n 64 x 128 tiles: at most one block a CU (64 x 4096 x 11008 in two parts 24
+// us, in three 29; 216 x 1088 x 2816 in two 12.5, in three 14.9). fp32, bound by
+// its products and not by reading, gets two parts in any case (211 x 1840 x 5392,
+// 172 tiles: 69 us, in one 79).
+int few_parts(int64_t n, int64_t row_bytes, bool f32) {
+  int64_t parts = kPlanCus / n, most = cdiv(row_bytes, 128) / 3;
+  if (f32 && parts < 2) parts = 2;
+  if (parts > most) parts = most;
+  return static_cast<int>(parts < 1 ? 1 : parts > 8 ? 8 : parts);
 }
 
 // At most 16 tokens: one batch of loads for each of a part's waves, or a few
@@ -1058,6 +1059,11 @@ namespace {
 bool adapter_in_parts(const tr_adapter_desc& d) {
   return cdiv(d.T, FewShape::kM) * cdiv(d.N, FewShape::kN) < kPlanCus;
 }
+template <bool kF32, int kKb, int kParts>
+hipError_t launch_expand(const ExpandArgs& p, dim3 grid, hipStream_t st) {
+  hipLaunchKernelGGL((adapter_few<kF32, kKb, kParts>), grid, dim3(kThreads), 0, st, p);
+  return hipGetLastError();
+}
 struct AdapterLayout {
   int parts, Np, Rp, Rq, n_units;
   size_t vpart, units, perm, sid, total;
@@ -1071,7 +1077,7 @@ AdapterLayout adapter_layout(const tr_adapter_desc& d) {
   L.Rq = static_cast<int>(f32 ? up16(d.R) : cdiv(d.R, 32) * 32);
   if (adapter_in_parts(d)) {
     L.parts = d.T <= 16 ? stream_parts(cdiv(d.N, 16), row_bytes)
-                        : few_parts(cdiv(d.T, FewShape::kM) * cdiv(d.N, FewShape::kN), row_bytes);
+                        : few_parts(cdiv(d.T, FewShape::kM) * cdiv(d.N, FewShape::kN), row_bytes, f32);
     L.vpart = up256(sizeof(float) * static_cast<size_t>(L.parts) * d.T * L.Np);
     L.units = L.vpart + up256(sizeof(float) * static_cast<size_t>(L.parts) * d.T * L.Rp);
     // units of 64 tokens: one for each adapter (and for none), one more for every
@@ -1161,9 +1167,12 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
     p.Rp = L.Rp;
     const dim3 grid(static_cast<unsigned>(cdiv(d.N, 32 * kWaves)), static_cast<unsigned>(L.n_units),
                     static_cast<unsigned>(chunks));
-    if (f32) hipLaunchKernelGGL(adapter_few<true>, grid, dim3(kThreads), 0, st, p);
-    else hipLaunchKernelGGL(adapter_few<false>, grid, dim3(kThreads), 0, st, p);
-    return hipGetLastError();
+    // few parts and ranks: 84 registers a lane, five waves a SIMD, and not 137 and
+    // three (64 x 7168 x 7168, 24 adapters of rank 64: 11 us and not 14.7); more
+    // parts in steps of four take longer (100 x 7168 x 1024: 7.3 us, by eight 6.5)
+    const bool small = L.parts <= 4 && d.R <= (f32 ? 32 : 64);
+    if (f32) return small ? launch_expand<true, 2, 4>(p, grid, st) : launch_expand<true, 4, 8>(p, grid, st);
+    return small ? launch_expand<false, 2, 4>(p, grid, st) : launch_expand<false, 4, 8>(p, grid, st);
   }
   // the positions' order: the tokens' own where x is past the 32-bit offsets that
   // gather its rows

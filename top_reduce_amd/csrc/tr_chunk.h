@@ -80,6 +80,15 @@ __device__ __forceinline__ u32x4 load16_any(const typename Elem<kF32>::type* row
   return v;
 }
 
+// Lane i < the number of tokens in `mask` (the same in every lane): the token of
+// rank i.
+__device__ __forceinline__ int tokens_by_rank(uint64_t mask) {
+  const int lane = lane_id();
+  // lane t of the mask sends t to the lane of its rank, the others to lane 63,
+  // which counts with 64 tokens only
+  return __builtin_amdgcn_ds_permute(((mask >> lane) & 1 ? popc_below(mask) : 63) * 4, lane);
+}
+
 // Two floats rounded to bf16 (nearest even) by one hardware conversion; lo in
 // bits 0..15.
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
