@@ -16,8 +16,8 @@
 // from L2 too, so operands beside the weights count: h is stored in the order in
 // which few_down loads it (64 tokens of 8 experts, all chosen: 147 -> 98 us).
 //
-// One token, 8 of 32 experts of 7168 x 2048: 81 + 43 us, 5.8 and 5.4 TB/s; 64
-// tokens, 8 of 256 experts, 32 of them here: 227 + 124 us, 7.2 and 6.6 TB/s.
+// One token, 8 of 32 experts of 7168 x 2048: 81 + 40 us, 5.8 TB/s; 64 tokens, 8 of
+// 256 experts, 32 of them here: 227 + 115 us, 7.2 TB/s.
 //
 // The gate weight is folded into h. bf16: h is kept as two bf16 numbers whose
 // sum has 16 significant bits, and few_down multiplies both, as different columns
@@ -304,7 +304,7 @@ struct Item {
 // A group: ND blocks of h, for which weights are loaded once. bf16: a block is 8
 // tokens with both numbers of each, so that a batch loads as much of h as of w2
 // (16 tokens in two operands, with half of their columns empty in most decode
-// batches, took 50 us for one token and not 43).
+// batches, took 50 us for one token where this took 43).
 template <bool kF32, int ND>
 __global__ __launch_bounds__(kThreads, 3) void few_down(FewArgs a) {
   constexpr int kU = ND <= 2 ? 4 : 2;   // 64-byte k-blocks of one batch of loads
@@ -466,7 +466,7 @@ __global__ __launch_bounds__(kThreads, 3) void few_down(FewArgs a) {
       for (int w = 1; w < kWaves; ++w) v += sum[w][t][gg];
       const int64_t col = col0 + 4 * gg;
       if (a.parts == 1) {
-        store4<kF32>(static_cast<E*>(a.y) + t * a.H, col, a.H, true, v);
+        store4<kF32>(static_cast<E*>(a.y) + t * a.H, col, min(a.H, col0 + a.cols), (a.cols & 3) == 0, v);
       } else if (col < a.H) {   // (H is a multiple of 8)
         *reinterpret_cast<floatx4*>(a.sums + (static_cast<int64_t>(blockIdx.y) * a.T + t) * a.H + col) = v;
       }
@@ -536,7 +536,7 @@ hipError_t launch_few(const FewArgs& a, const SelectArgs* sel, double per_expert
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // few_down's units. Columns: those that leave the fullest CU the fewest (2880
-// columns by 12 and not 16: 33 us instead of 35; 4160: 66 instead of 75). Parts:
+// columns by 12 and not 16: 33 us instead of 35; 7168 by 14: 40 instead of 44). Parts:
 // where not even half of the CUs get a unit of 16 and the split takes 192 KiB of
 // weights and more from each, 8 us at what a CU reads, which pays for the launch
 // that adds the parts (1024 x 2048, 8 tokens that choose 4 of 16 experts: 31 us
@@ -559,7 +559,7 @@ DownShape down_shape(const tr_layer_desc& d) {
     return s;
   }
   auto fullest = [&](int cols) { return cdiv(cdiv(H, cols), kPlanCus) * cols; };
-  for (int cols = 12; cols >= 8; cols -= 4)
+  for (int cols = 14; cols >= 8; cols -= 2)
     if (fullest(cols) < fullest(s.cols)) s.cols = cols;
   return s;
 }
