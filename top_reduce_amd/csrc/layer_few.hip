@@ -53,6 +53,7 @@ struct FewArgs {
   void* y;                           // [T, H]
   int T, K, E;
   int cols, parts;                   // few_down's units: output columns, parts of the reduction
+  bool by_expert;                    // its waves share the experts, not their reductions
   float* sums;                       // [parts][T][H] with more than one part
   int64_t H, I, Ip;
 };
@@ -312,6 +313,7 @@ __global__ __launch_bounds__(kThreads, 3) void few_down(FewArgs a) {
   constexpr int kC = Elem<kF32>::kChunk, kB = Elem<kF32>::kBytes;
   constexpr int kParts = HPlace<kF32>::kParts, kGroup = HPlace<kF32>::kGroup;
   __shared__ Groups s;
+  __shared__ uint16_t mine[kWaves][kMaxGroups];
   __shared__ int tmp[kWaves];
   __shared__ floatx4 sum[kWaves][kFewTokens][4];
   const int n_groups = find_groups<kF32, kThreads, kGroup * ND>(a.masks, a.E, s, tmp);
@@ -321,18 +323,29 @@ __global__ __launch_bounds__(kThreads, 3) void few_down(FewArgs a) {
   const int tr = r / kParts, part = r % kParts;   // the lane's token of a block and number
   const int I = static_cast<int>(a.I);
   const uint32_t h_bytes = static_cast<uint32_t>(a.Ip * kB) * 16;   // of a block of h
-  // This wave's 64-byte blocks of every row of h and w2 (the same for every
-  // expert, so that a token's sums do not depend on the other tokens), in
-  // batches of kU: whole blocks by wide loads, the last of which start early
-  // enough to end with the share; then what is left of the row's end.
+  // The waves share every expert's reduction, or the experts (either way a token's
+  // sums do not depend on the other tokens).
+  // This wave's 64-byte blocks of rows of h and w2, in batches of kU: whole blocks
+  // by wide loads, the last of which start early enough to end with the share;
+  // then what is left of the row's end.
   const int nkb = (I * kB + 63) >> 6;
   const int nfull = (I * kB >> 6) >= kU ? I * kB >> 6 : 0;
-  const int share = blockIdx.y * kWaves + wave, shares = a.parts * kWaves;
+  const bool by_expert = a.by_expert;
+  const int share = by_expert ? 0 : blockIdx.y * kWaves + wave, shares = by_expert ? 1 : a.parts * kWaves;
   const int kb0 = static_cast<int>(static_cast<int64_t>(share) * nkb / shares);
   const int kb1 = static_cast<int>(static_cast<int64_t>(share + 1) * nkb / shares);
   const int kbf = max(min(kb1, nfull), kb0);
   const int nbf = (kbf - kb0 + kU - 1) / kU;
-  const int items = n_groups * nbf;
+  // this wave's groups
+  int n_mine = 0;
+  for (int q0 = 0; q0 < n_groups; q0 += kWave) {
+    const int q = q0 + lane;
+    const bool in = q < n_groups && (!by_expert || s.expert[min(q, n_groups - 1)] % kWaves == wave);
+    const uint64_t all = __ballot(in);
+    if (in) mine[wave][n_mine + popc_below(all)] = static_cast<uint16_t>(q);
+    n_mine += __popcll(all);
+  }
+  const int items = n_mine * nbf;
   const int units = static_cast<int>((a.H + a.cols - 1) / a.cols);
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
     // (a lane past the unit's last column reads that one's row)
@@ -362,12 +375,13 @@ __global__ __launch_bounds__(kThreads, 3) void few_down(FewArgs a) {
       return (at < n ? d * h_bytes + r * 64 : part * 64) + g * 16;
     };
     auto load = [&](Batch& v, const Item& it) {
-      const char* w0 = w_at(it.q);
-      const char* h0 = h_at(it.q);
+      const int group = mine[wave][it.q];
+      const char* w0 = w_at(group);
+      const char* h0 = h_at(group);
       const uint32_t k = static_cast<uint32_t>(start(it.b));
       uint32_t ho[ND];
 #pragma unroll
-      for (int d = 0; d < ND; ++d) ho[d] = h_off(it.q, d) + k * 1024;
+      for (int d = 0; d < ND; ++d) ho[d] = h_off(group, d) + k * 1024;
 #pragma unroll
       for (int j = 0; j < kU; ++j) {
         v.w[j] = load16_odd(w0 + (wo + k * 64) + j * 64);
@@ -405,7 +419,7 @@ __global__ __launch_bounds__(kThreads, 3) void few_down(FewArgs a) {
           for (int d = 0; d < ND; ++d) acc[d] = mma16<kF32>(v.w[j], v.h[d][j], acc[d]);
         }
       __builtin_amdgcn_sched_barrier(0);
-      if (it.b + 1 == nbf) add(it.q);
+      if (it.b + 1 == nbf) add(mine[wave][it.q]);
       it.next(nbf);
     };
     if (items > 0) {   // as in few_up: no load under a condition
@@ -432,7 +446,8 @@ __global__ __launch_bounds__(kThreads, 3) void few_down(FewArgs a) {
     if (kbf < kb1) {
       // what is left of the rows: past I both operands are zero (h has zeros from
       // I to Ip)
-      for (int q = 0; q < n_groups; ++q) {
+      for (int i = 0; i < n_mine; ++i) {
+        const int q = mine[wave][i];
         const E* wrow = reinterpret_cast<const E*>(w_at(q) + lr * static_cast<uint32_t>(I * kB));
         const char* h0 = h_at(q);
         for (int kb = kbf; kb < kb1; kb += kU) {
@@ -541,23 +556,30 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // weights and more from each, 8 us at what a CU reads, which pays for the launch
 // that adds the parts (1024 x 2048, 8 tokens that choose 4 of 16 experts: 31 us
 // whole, 13 + 4 in four parts; two experts, 128 KiB a unit: 6 whole, 5 + 2).
+// Experts to the waves: rows of less than a batch of loads for each wave (64 tokens
+// that choose 4 of 32, I = 128: 10 us, by shares of rows 28), or of less than two
+// with experts enough to be even (8 tokens, 4 of 16, I = 800: 16 us, 19; but one
+// token, 8 of 64, I = 768: 12 us, by shares 11).
 struct DownShape {
   int cols, parts;
+  bool by_expert;
 };
 DownShape down_shape(const tr_layer_desc& d) {
   const int64_t H = d.route.H, row = d.I * (d.route.dtype == TR_F32 ? 4 : 2);
   const int64_t units = cdiv(H, 16);
-  DownShape s{16, 1};
+  DownShape s{16, 1, false};
   int64_t parts = kPlanCus / units;
   if (parts > row / 1024) parts = row / 1024;   // a batch of loads for a wave
   if (parts > 8) parts = 8;
   // bytes of weights of a unit, for the experts that the rows choose at most
   const double routes = static_cast<double>(d.route.T) * d.route.K * d.E / d.route.G;
-  const double bytes = 16.0 * row * (routes < 1 ? 1 : routes < d.E ? routes : d.E);
+  const double experts = routes < 1 ? 1 : routes < d.E ? routes : d.E;
+  const double bytes = 16.0 * row * experts;
   if (parts > 1 && bytes * (1.0 - 1.0 / parts) >= 3 << 16) {
     s.parts = static_cast<int>(parts);
     return s;
   }
+  s.by_expert = row <= 64 * 15 || (row <= 64 * 31 && experts >= 16);
   auto fullest = [&](int cols) { return cdiv(cdiv(H, cols), kPlanCus) * cols; };
   for (int cols = 14; cols >= 8; cols -= 2)
     if (fullest(cols) < fullest(s.cols)) s.cols = cols;
@@ -614,6 +636,7 @@ hipError_t few_layer(const tr_layer_desc& d, const void* x, const void* w_gate, 
   a.sums = reinterpret_cast<float*>(b + L.sums);
   a.cols = L.down.cols;
   a.parts = L.down.parts;
+  a.by_expert = L.down.by_expert;
   a.y = y;
   a.T = static_cast<int>(r.T);
   a.K = r.K;
