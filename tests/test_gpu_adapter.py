@@ -173,6 +173,17 @@ def test_rows_do_not_depend_on_their_order():
     assert torch.equal(y[at], y2)
 
 
+@pytest.mark.parametrize("A", [3, 1023, 1024, 5000])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_mixed_rows_of_few_and_of_many_adapters(A, dtype):
+    T, H, N, R = 2100, 64, 1030, 8
+    x, w, a, b, ids, scales = make(A, T, H, N, R, A, dtype, run=1)
+    ids[5], ids[2099], ids[2047], ids[2048] = A, A - 1, A - 1, -7
+    y = tr.adapter_linear(x.cuda(), w.cuda(), a.cuda(), b.cuda(), ids.cuda(), scales=scales.cuda())
+    ref, bound = S.adapter(x, w, a, b, ids, scales)
+    S.check(y, ref, bound, "y")
+
+
 def test_adapters_past_four_gigabytes():
     """The last adapter's rows of b lie past 2^32 bytes."""
     T, H, N, R, A = 3, 64, 4096, 256, 2100

@@ -366,62 +366,64 @@ __global__ __launch_bounds__(kThreads) void adapter_few(ExpandArgs p) {
 // --------------------------------------------------------------------------
 // Many tokens: their order by adapter
 // --------------------------------------------------------------------------
-// Positions of each window of 2048 tokens sorted by adapter, tokens without one
-// last, equal ones in their order: perm[pos] is the token, sid[pos] its adapter
-// (or -1). The kernels that follow work on positions, so that a group of 16 or 32
-// has one adapter or two however the requests' tokens are mixed (8192 x 7168 x
-// 7168 with 32 adapters of rank 64 dealt at random took 808 + 1887 us in the
-// tokens' order, and takes 15 + 116 + 859 us so). A window whose tokens already
-// come in runs keeps its order (5 us). One bitonic sort in LDS of keys that hold
-// id and place; pairs at most 64 apart stay in a wave.
+// Positions of each window of 2048 tokens in the order of their adapters, tokens
+// without one last: perm[pos] is the token, sid[pos] its adapter (or -1). The
+// kernels that follow work on positions, so that a group of 16 or 32 has one
+// adapter or two however the requests' tokens are mixed (8192 x 7168 x 7168 with
+// 32 adapters of rank 64 dealt at random took 808 + 1887 us in the tokens' order,
+// and takes 5 + 107 + 834 us so). A window whose tokens already come in runs keeps
+// its order.
+// Counting in LDS: a thread's token takes its place among its adapter's by an
+// atomic add, whose order varies and does not matter, as a row's sums do not
+// depend on its place. More than kBins adapters share bins with their neighbours.
+// (A bitonic sort of the same window took 15 us.)
 constexpr int kWindow = 2048;
 constexpr int kOrderThreads = kWindow / 2;
+constexpr int kBins = kOrderThreads - 1;   // and one for tokens without an adapter
 
 __global__ __launch_bounds__(kOrderThreads) void adapter_order(const int32_t* __restrict__ ids,
                                                                int64_t T, int A, int32_t* perm,
                                                                int32_t* sid) {
-  __shared__ uint32_t key[kWindow];
+  __shared__ int bins[kOrderThreads];
   __shared__ int tmp[kOrderThreads / kWave];
   const int tid = threadIdx.x;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kWindow;
   const int n = static_cast<int>(min(static_cast<int64_t>(kWindow), T - t0));
+  int id[2], bin[2], at[2];
   int ends = 0, all = 0;   // tokens whose adapter differs from the one's before
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const int i = tid + q * kOrderThreads;
-    uint32_t k = ~0u;   // past the last token: last (A is at most 2^20)
+    id[q] = -1;
+    bin[q] = kBins;
     if (i < n) {
-      const int id = ids[t0 + i], before = ids[t0 + max(i - 1, 0)];
-      ends += id != before;
-      k = static_cast<uint32_t>(id < 0 || id >= A ? A : id) << 11 | static_cast<uint32_t>(i);
+      id[q] = ids[t0 + i];
+      ends += id[q] != ids[t0 + max(i - 1, 0)];
+      if (id[q] < 0 || id[q] >= A) id[q] = -1;
+      else bin[q] = A <= kBins ? id[q] : static_cast<int>(static_cast<int64_t>(id[q]) * kBins / A);
     }
-    key[i] = k;
+    at[q] = i;
   }
-  block_exclusive_scan<kOrderThreads>(ends, tmp, &all);
-  // runs of 32 tokens and more on average: the order is good as it is
-  // (positions past the last token hold the largest keys: a window that is not full
-  // sorts as many as the next power of two)
-  const bool sort = all * 32 > n;
-  for (int size = sort ? 2 : 2 * n; size < 2 * n; size <<= 1)
-    for (int d = size >> 1; d > 0; d >>= 1) {
-      // thread tid: the pair (i, i + d); 64 threads take 128 neighbours when d <= 64
-      const int i = 2 * tid - (tid & (d - 1));
-      const uint32_t a = key[i], b = key[i + d];
-      const bool up = (i & size) == 0;
-      if ((a > b) == up) {
-        key[i] = b;
-        key[i + d] = a;
-      }
-      // the next step's pairs: another distance (d / 2, or size itself)
-      if (d > 64 || (d == 1 && size >= 128)) __syncthreads();
-      else __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-    }
-  __syncthreads();
-  for (int i = tid; i < n; i += kOrderThreads) {
-    const uint32_t k = key[i];
-    perm[t0 + i] = static_cast<int32_t>(t0 + (k & (kWindow - 1)));
-    const int id = static_cast<int>(k >> 11);
-    sid[t0 + i] = id < A ? id : -1;
+  bins[tid] = 0;
+  block_exclusive_scan<kOrderThreads>(ends, tmp, &all);   // (with a barrier)
+  // runs of fewer than 32 tokens on average (the same in every thread)
+  if (all * 32 > n) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      if (tid + q * kOrderThreads < n) at[q] = atomicAdd(&bins[bin[q]], 1);
+    __syncthreads();
+    const int count = bins[tid];
+    bins[tid] = block_exclusive_scan<kOrderThreads>(count, tmp, &all);
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 2; ++q) at[q] += bins[bin[q]];
+  }
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int i = tid + q * kOrderThreads;
+    if (i >= n) continue;
+    perm[t0 + at[q]] = static_cast<int32_t>(t0 + i);
+    sid[t0 + at[q]] = id[q];
   }
 }
 
