@@ -184,6 +184,16 @@ def test_mixed_rows_of_few_and_of_many_adapters(A, dtype):
     S.check(y, ref, bound, "y")
 
 
+@pytest.mark.parametrize("T", [1, 5, 16])
+@pytest.mark.parametrize("H,N,dtype", [(7168, 7160, BF), (7176, 6001, BF), (4104, 8200, F32)])
+def test_few_tokens_of_long_weights(T, H, N, dtype):
+    R, A = 20, 3
+    x, w, a, b, ids, scales = make(T, T, H, N, R, A, dtype, run=1)
+    y = tr.adapter_linear(x.cuda(), w.cuda(), a.cuda(), b.cuda(), ids.cuda(), scales=scales.cuda())
+    ref, bound = S.adapter(x, w, a, b, ids, scales)
+    S.check(y, ref, bound, "y")
+
+
 def test_adapters_past_four_gigabytes():
     """The last adapter's rows of b lie past 2^32 bytes."""
     T, H, N, R, A = 3, 64, 4096, 256, 2100

@@ -48,7 +48,7 @@ struct StreamArgs {
   int64_t row_bytes;     // bytes of a row of x and of w
   int64_t T;
   int N, Np;
-  int tiles;             // ceil(N / 16)
+  int tiles;             // ceil(N / 16), of stream_wide ceil(N / 32)
   // adapters (NULL ids: none)
   const int32_t* ids;    // [T]
   const char* a;         // [A, R, H]
@@ -206,6 +206,92 @@ __device__ __forceinline__ void stream_unit(const StreamArgs& p, int chunk, int 
     float* dst = is_w ? p.part + row * p.Np + tile * 16 + 4 * g
                       : p.vpart + row * p.Rp + rt * 16 + 4 * g;
     *reinterpret_cast<floatx4*>(dst) = v;
+  }
+}
+
+// Unit (tile, s) with 32 weight rows, for at most 16 tokens and long weights: x is
+// loaded once for both halves, and a batch of loads is in flight while the other's
+// products run. red: LDS of 2 * kWaves * kWave floatx4.
+template <bool kF32>
+__device__ __forceinline__ void stream_wide(const StreamArgs& p, int tile, int s, int S, floatx4* red) {
+  constexpr int kW = 4;   // 64-byte blocks of a batch
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  const int g = lane >> 4, r = lane & 15;
+  const int n = static_cast<int>(p.T);
+  // addresses: starts that are the same for the wave, 32-bit offsets. A lane past
+  // the last row or token reads the last one's.
+  const uint32_t row_bytes = static_cast<uint32_t>(p.row_bytes);
+  const int row0 = tile * 32;
+  const char* w0 = p.w + static_cast<int64_t>(row0) * p.row_bytes;
+  uint32_t wo[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) wo[c] = static_cast<uint32_t>(min(c * 16 + r, p.N - 1 - row0)) * row_bytes + g * 16;
+  const uint32_t xo = static_cast<uint32_t>(min(r, n - 1)) * row_bytes + g * 16;
+  const int nkb = static_cast<int>((row_bytes + 63) >> 6), nfull = static_cast<int>(row_bytes >> 6);
+  const int part = s * kWaves + wave, parts = S * kWaves;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(part) * nkb / parts);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(part + 1) * nkb / parts);
+  const int kbf = min(kb1, nfull);
+  floatx4 acc[2] = {floatx4{0, 0, 0, 0}, floatx4{0, 0, 0, 0}};
+  struct Batch {
+    u32x4 w[2][kW], x[kW];
+  } b0, b1;
+  // a share's last batch starts early enough to end with it; the products of
+  // blocks that it reads again are skipped
+  auto start = [&](int kb) { return min(kb, kbf - kW); };
+  auto load = [&](Batch& b, int kb) {
+    const uint32_t k = static_cast<uint32_t>(start(kb)) * 64;
+#pragma unroll
+    for (int j = 0; j < kW; ++j) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) b.w[c][j] = load16(w0 + (wo[c] + k) + j * 64);
+      b.x[j] = load16(p.x + (xo + k) + j * 64);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto mma = [&](const Batch& b, int kb) {
+    const int k = start(kb);
+#pragma unroll
+    for (int j = 0; j < kW; ++j)
+      if (k + j >= kb && k + j < kbf) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) acc[c] = mma16<kF32>(b.w[c][j], b.x[j], acc[c]);
+      }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // (a share has 16 whole blocks: stream_rows)
+  load(b0, kb0);
+  int kb = kb0;
+  for (; kb + 2 * kW < kbf; kb += 2 * kW) {
+    load(b1, kb + kW);
+    mma(b0, kb);
+    load(b0, kb + 2 * kW);
+    mma(b1, kb + kW);
+  }
+  if (kb + kW < kbf) {
+    load(b1, kb + kW);
+    mma(b0, kb);
+    mma(b1, kb + kW);
+  } else {
+    mma(b0, kb);
+  }
+  if (kb1 > nfull) {   // the short block at the end of the rows
+    const bool in = nfull * 64u + g * 16 < row_bytes;
+    const u32x4 z = {0, 0, 0, 0};
+    const u32x4 xv = in ? load16(p.x + xo + nfull * 64) : z;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) acc[c] = mma16<kF32>(in ? load16(w0 + wo[c] + nfull * 64) : z, xv, acc[c]);
+  }
+#pragma unroll
+  for (int c = 0; c < 2; ++c) red[(wave * 2 + c) * kWave + lane] = acc[c];
+  __syncthreads();
+  const int col = row0 + wave * 16 + 4 * g;   // wave c: half c
+  if (wave < 2 && r < n && col < p.Np) {
+    floatx4 v = red[wave * kWave + lane];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) v += red[(w * 2 + wave) * kWave + lane];
+    *reinterpret_cast<floatx4*>(p.part + (static_cast<int64_t>(s) * p.T + r) * p.Np + col) = v;
   }
 }
 
@@ -899,16 +985,19 @@ __global__ __launch_bounds__(C::kBlock) void linear_tile(TileArgs p) {
 
 // At most 16 tokens: block (tile, s) of the weight's and then the adapters'
 // tiles.
-template <bool kF32>
-__global__ __launch_bounds__(kThreads) void stream_partial(StreamArgs p) {
+template <bool kF32, bool kWide>
+__global__ __launch_bounds__(kThreads, 3) void stream_partial(StreamArgs p) {
   const int64_t z = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
   if (z < p.n_zero) p.zero[z] = 0;
-  __shared__ floatx4 red[kWaves * kWave];
+  __shared__ floatx4 red[(kWide ? 2 : 1) * kWaves * kWave];
   if (p.units && blockIdx.x + 1 == gridDim.x) {   // the last blocks: the tokens' units
     if (blockIdx.y == 0 && threadIdx.x < kWave) make_units(p, 0);
     return;
   }
-  stream_unit<kF32, 1>(p, 0, blockIdx.x, blockIdx.y, gridDim.y, red);
+  if (kWide && static_cast<int>(blockIdx.x) < p.tiles)
+    stream_wide<kF32>(p, blockIdx.x, blockIdx.y, gridDim.y, red);
+  else
+    stream_unit<kF32, 1>(p, 0, blockIdx.x, blockIdx.y, gridDim.y, red);
 }
 
 // More tokens: the first `tiles` blocks are weight tiles of 64 tokens x 128 rows
@@ -972,13 +1061,36 @@ int few_parts(int64_t n, int64_t row_bytes, bool f32) {
   return static_cast<int>(parts < 1 ? 1 : parts > 8 ? 8 : parts);
 }
 
-// At most 16 tokens: one batch of loads for each of a part's waves, or a few
+// At most 16 tokens. Parts of units of 32 rows (stream_wide): three blocks a CU at
+// most.
+int wide_parts(int64_t N) {
+  const int64_t parts = 3 * kPlanCus / cdiv(N, 32);
+  return static_cast<int>(parts < 1 ? 1 : parts);
+}
+// Rows of a unit: 32 where that leaves a wave four batches of loads, else 16 (one
+// and eight tokens of 7168 x 7168: 21 and 25 us, by 16 28 and 33; 16 of 4096 x
+// 4096, with two batches: 15.7 us, by 16 14.1).
+int stream_rows(int64_t N, int64_t row_bytes) {
+  return row_bytes / 64 >= 16 * kWaves * wide_parts(N) ? 32 : 16;
+}
+// Parts of units of 16: one batch of loads for each of a part's waves, or a few
 // where that already gives four blocks a CU.
-int stream_parts(int64_t tiles, int64_t row_bytes) {
-  const int64_t batches = cdiv(cdiv(row_bytes, 64), kU * kWaves);
+int stream_parts(int64_t N, int64_t row_bytes) {
+  if (stream_rows(N, row_bytes) == 32) return wide_parts(N);
+  const int64_t tiles = cdiv(N, 16), batches = cdiv(cdiv(row_bytes, 64), kU * kWaves);
   int64_t each = 1;
   while (each < batches && tiles * cdiv(batches, each + 1) >= 4 * kPlanCus) ++each;
   return static_cast<int>(cdiv(batches, each));
+}
+template <bool kF32, bool kWide>
+hipError_t launch_stream(const StreamArgs& a, int x, int parts, hipStream_t st) {
+  hipLaunchKernelGGL((stream_partial<kF32, kWide>), dim3(x, parts), dim3(kThreads), 0, st, a);
+  return hipGetLastError();
+}
+hipError_t launch_stream(const StreamArgs& a, bool f32, int x, int parts, hipStream_t st) {
+  if (stream_rows(a.N, a.row_bytes) == 32)
+    return f32 ? launch_stream<true, true>(a, x, parts, st) : launch_stream<false, true>(a, x, parts, st);
+  return f32 ? launch_stream<true, false>(a, x, parts, st) : launch_stream<false, false>(a, x, parts, st);
 }
 
 int64_t up16(int64_t v) { return cdiv(v, 16) * 16; }
@@ -1001,7 +1113,7 @@ LogitsLayout logits_layout(int64_t T, int64_t H, int N, bool f32) {
   const int64_t row_bytes = H * (f32 ? 4 : 2), ktiles = cdiv(row_bytes, 128);
   L.pitch = static_cast<int>(up16(N));
   if (T <= 16)
-    L.parts = stream_parts(cdiv(N, 16), row_bytes);
+    L.parts = stream_parts(N, row_bytes);
   else if (T <= kFewTokens)
     L.parts = parts_for(1, cdiv(N, FewShape::kN), ktiles, 3, 16);
   else if (wide_logits(T, row_bytes, N))
@@ -1024,13 +1136,11 @@ hipError_t logits(int64_t T, int64_t H, int N, bool f32, const void* x, const vo
   a.T = T;
   a.N = N;
   a.Np = L.pitch;
-  a.tiles = static_cast<int>(cdiv(N, 16));
+  a.tiles = static_cast<int>(cdiv(N, stream_rows(N, row_bytes)));
   a.zero = zero;
   a.n_zero = n_zero;
   if (T <= 16) {
-    if (f32) hipLaunchKernelGGL(stream_partial<true>, dim3(a.tiles, L.parts), dim3(kThreads), 0, st, a);
-    else hipLaunchKernelGGL(stream_partial<false>, dim3(a.tiles, L.parts), dim3(kThreads), 0, st, a);
-    return hipGetLastError();
+    return launch_stream(a, f32, a.tiles, L.parts, st);
   }
   TileArgs t{};
   t.x = a.x;
@@ -1078,7 +1188,7 @@ AdapterLayout adapter_layout(const tr_adapter_desc& d) {
   L.Rp = static_cast<int>(up16(d.R));
   L.Rq = static_cast<int>(f32 ? up16(d.R) : cdiv(d.R, 32) * 32);
   if (adapter_in_parts(d)) {
-    L.parts = d.T <= 16 ? stream_parts(cdiv(d.N, 16), row_bytes)
+    L.parts = d.T <= 16 ? stream_parts(d.N, row_bytes)
                         : few_parts(cdiv(d.T, FewShape::kM) * cdiv(d.N, FewShape::kN), row_bytes, f32);
     L.vpart = up256(sizeof(float) * static_cast<size_t>(L.parts) * d.T * L.Np);
     L.units = L.vpart + up256(sizeof(float) * static_cast<size_t>(L.parts) * d.T * L.Rp);
@@ -1129,10 +1239,8 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
     const int chunks = static_cast<int>(cdiv(d.T, kFewTokens));
     s.chunks = chunks;
     if (d.T <= 16) {
-      s.tiles = static_cast<int>(cdiv(d.N, 16));
-      const dim3 grid(s.tiles + slots * s.rank_tiles + 1, L.parts);
-      if (f32) hipLaunchKernelGGL(stream_partial<true>, grid, dim3(kThreads), 0, st, s);
-      else hipLaunchKernelGGL(stream_partial<false>, grid, dim3(kThreads), 0, st, s);
+      s.tiles = static_cast<int>(cdiv(d.N, stream_rows(d.N, row_bytes)));
+      if ((e = launch_stream(s, f32, s.tiles + slots * s.rank_tiles + 1, L.parts, st)) != hipSuccess) return e;
     } else {
       TileArgs t{};
       t.x = s.x;
