@@ -160,6 +160,15 @@ def test_same_bits_in_place_in_a_dirty_workspace_and_on_another_stream(T):
     assert torch.equal(x2, y)
 
 
+@pytest.mark.parametrize("T,I,E,dtype", [(3, 96, 8, BF), (40, 96, 8, BF), (64, 1030, 2, BF), (29, 200, 5, F32)])
+def test_rows_do_not_depend_on_their_order(T, I, E, dtype):
+    x, gate, w1, w2 = (t.cuda() for t in make(T, T, 256, I, E, E, dtype))
+    y, idx, w = tr.layer(x, gate, w1, w2, 2)
+    at = torch.randperm(T, generator=torch.Generator().manual_seed(T)).cuda()
+    y2, i2, w2_ = tr.layer(x[at].contiguous(), gate, w1, w2, 2)
+    assert torch.equal(idx[at], i2) and torch.equal(w[at], w2_) and torch.equal(y[at], y2)
+
+
 def test_graph_replays_follow_their_inputs():
     T, H, I, E, G, K = 8, 512, 128, 16, 32, 4
     x, gate, w1, w2 = (t.cuda() for t in make(2, T, H, I, E, G, BF))
