@@ -345,6 +345,7 @@ __global__ __launch_bounds__(kThreads, 3) void few_down(FewArgs a) {
     if (in) mine[wave][n_mine + popc_below(all)] = static_cast<uint16_t>(q);
     n_mine += __popcll(all);
   }
+  __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
   const int items = n_mine * nbf;
   const int units = static_cast<int>((a.H + a.cols - 1) / a.cols);
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
@@ -571,7 +572,8 @@ DownShape down_shape(const tr_layer_desc& d) {
   int64_t parts = kPlanCus / units;
   if (parts > row / 1024) parts = row / 1024;   // a batch of loads for a wave
   if (parts > 8) parts = 8;
-  // bytes of weights of a unit, for the experts that the rows choose at most
+  // bytes of weights of a unit, for the experts that the rows would choose at most,
+  // were the routes uniform
   const double routes = static_cast<double>(d.route.T) * d.route.K * d.E / d.route.G;
   const double experts = routes < 1 ? 1 : routes < d.E ? routes : d.E;
   const double bytes = 16.0 * row * experts;
