@@ -595,9 +595,9 @@ def route_topk(x: torch.Tensor, w_gate: torch.Tensor, K: int, bias: Optional[tor
     gp = _arg(w_gate, "w_gate", dt, (G, H), dev)
     bp = None if bias is None else _arg(bias, "bias", torch.float32, (G,), dev)
     if idx is None:
-        idx = torch.empty((T, K), dtype=idx_dtype, device=dev)
+        idx = torch.empty(T, K, dtype=idx_dtype, device=dev)
     if weights is None:
-        weights = torch.empty((T, K), dtype=torch.float32, device=dev)
+        weights = torch.empty(T, K, dtype=torch.float32, device=dev)
     ip = _arg(idx, "idx", idx_dtype, (T, K), dev)
     wp = _arg(weights, "weights", torch.float32, (T, K), dev)
     ws = _ws_arg(ws, need, dev)
@@ -639,9 +639,9 @@ def layer(x: torch.Tensor, w_gate: torch.Tensor, w1: torch.Tensor, w2: torch.Ten
     w1p = _arg(w1, "w1", dt, (E, 2 * I, H), dev)
     w2p = _arg(w2, "w2", dt, (E, H, I), dev)
     if idx is None:
-        idx = torch.empty((T, K), dtype=idx_dtype, device=dev)
+        idx = torch.empty(T, K, dtype=idx_dtype, device=dev)
     if weights is None:
-        weights = torch.empty((T, K), dtype=torch.float32, device=dev)
+        weights = torch.empty(T, K, dtype=torch.float32, device=dev)
     if y is None:
         y = torch.empty_like(x)
     ip = _arg(idx, "idx", idx_dtype, (T, K), dev)
@@ -682,7 +682,7 @@ def adapter_linear(x: torch.Tensor, w: torch.Tensor, a: torch.Tensor, b: torch.T
     ip = _arg(ids, "ids", torch.int32, (T,), dev)
     sp = None if scales is None else _arg(scales, "scales", torch.float32, (A,), dev)
     if y is None:
-        y = torch.empty((T, N), dtype=dt, device=dev)
+        y = torch.empty(T, N, dtype=dt, device=dev)
     yp = _arg(y, "y", dt, (T, N), dev)
     ws = _ws_arg(ws, need, dev)
     status = _lib.moe_adapter_linear(desc, x.data_ptr(), wp, ap, bp, ip, sp, yp, ws.data_ptr(),
