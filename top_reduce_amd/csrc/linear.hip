@@ -1050,15 +1050,23 @@ int parts_for(int per_cu, int64_t n, int64_t ksteps, int64_t least, int64_t most
   return static_cast<int>(want < 1 ? 1 : want);
 }
 
-// For n 64 x 128 tiles: at most one block a CU (64 x 4096 x 11008 in two parts 24
-// us, in three 29; 216 x 1088 x 2816 in two 12.5, in three 14.9). fp32, bound by
-// its products and not by reading, gets two parts in any case (211 x 1840 x 5392,
-// 172 tiles: 69 us, in one 79).
+// For n 64 x 128 tiles. bf16: at most one block a CU (64 x 4096 x 11008 in two
+// parts 24 us, in three 29; 216 x 1088 x 2816 in two 12.5, in three 14.9, in five
+// 16.6). fp32, bound by its products and not by reading: the least work for the
+// fullest CU (200 x 3000 x 4500, 144 tiles: in five parts 78 us, in two 108; 211 x
+// 1840 x 5392, 172 tiles: in four 61, in two 70, in one 79).
 int few_parts(int64_t n, int64_t row_bytes, bool f32) {
-  int64_t parts = kPlanCus / n, most = cdiv(row_bytes, 128) / 3;
-  if (f32 && parts < 2) parts = 2;
+  int64_t most = cdiv(row_bytes, 128) / 3;
+  if (most < 1) most = 1;
+  if (most > 8) most = 8;
+  int64_t parts = kPlanCus / n;
+  if (f32) {
+    parts = 1;
+    for (int64_t p = 2; p <= most; ++p)   // a block more must be worth 3% of its work
+      if (cdiv(n * p, kPlanCus) * (100 + 3 * p) * parts < cdiv(n * parts, kPlanCus) * (100 + 3 * parts) * p) parts = p;
+  }
   if (parts > most) parts = most;
-  return static_cast<int>(parts < 1 ? 1 : parts > 8 ? 8 : parts);
+  return static_cast<int>(parts < 1 ? 1 : parts);
 }
 
 // At most 16 tokens. Parts of units of 32 rows (stream_wide): three blocks a CU at
