@@ -757,10 +757,12 @@ struct TileLoad {
   uint32_t row_bytes;
 };
 
-// k-tile kt into stage S. Row i of a stage keeps its chunk c at c ^ (i & 7) ^
-// ((i >> 3) & 1): the 16 rows of a fragment read lie in different banks. Rows
-// past T or N, bytes past the row and k-tiles from k1 on are given an offset
-// past the buffer, whose DMA writes zeros.
+// k-tile kt into stage S. Row i of a stage keeps its chunk c at c ^ ((i >> 1) & 7):
+// the 16 lanes that LDS serves at a time, rows 0-3 and 12-15 of one chunk and 4-11
+// of the next, lie in different banks (no conflict counted; c ^ (i & 7) ^ ((i >> 3)
+// & 1) had two lanes in each, and twice the LDS cycles). Rows past T or N, bytes
+// past the row and k-tiles from k1 on are given an offset past the buffer, whose
+// DMA writes zeros.
 template <typename C, int S>
 __device__ __forceinline__ void tile_dma(const TileLoad<C>& l, int wave, int kt, int k1) {
   const uint32_t k = kt < k1 ? static_cast<uint32_t>(kt) * 128 : l.row_bytes;
@@ -870,19 +872,19 @@ __device__ __forceinline__ void tile_unit(const TileArgs& p, int block) {
 #pragma unroll
   for (int j = 0; j < C::kXp; ++j) {
     const int pc = wave * C::kXp + j, row = pc * 8 + (lane >> 3);
-    l.xc[j] = ((lane & 7) ^ (lane >> 3) ^ (pc & 1)) * 16;
+    l.xc[j] = ((lane & 7) ^ ((pc & 1) * 4 + (lane >> 4))) * 16;
     l.xo[j] = kPast;
     if (row < rows) l.xo[j] = (moved ? p.perm[t0 + row] : row) * l.row_bytes + l.xc[j];
   }
 #pragma unroll
   for (int j = 0; j < C::kWp; ++j) {
     const int pc = wave * C::kWp + j, row = pc * 8 + (lane >> 3);
-    l.wc[j] = ((lane & 7) ^ (lane >> 3) ^ (pc & 1)) * 16;
+    l.wc[j] = ((lane & 7) ^ ((pc & 1) * 4 + (lane >> 4))) * 16;
     l.wo[j] = row < cols ? row * l.row_bytes + l.wc[j] : kPast;
   }
   int frag[2];
 #pragma unroll
-  for (int q = 0; q < 2; ++q) frag[q] = r * kLine + ((4 * q + g) ^ (r & 7) ^ ((r >> 3) & 1));
+  for (int q = 0; q < 2; ++q) frag[q] = r * kLine + ((4 * q + g) ^ (r >> 1));
 
   floatx4 acc[C::kMs][C::kNs];
 #pragma unroll
