@@ -972,6 +972,11 @@ __device__ __forceinline__ void tile_unit(const TileArgs& p, int block) {
 }
 #endif  // __HIP_DEVICE_COMPILE__
 
+// Bound by the loop's loads, LDS reads and products together, and with one tile a
+// CU by what nothing covers, its first loads and its stores. bf16: 16384 x 7168 x
+// 256 in two parts 69 us, 0.87 PFLOP/s; 8192 x 7160 x 7000 with adapters 1020 us,
+// 0.80; 1000 x 4096 x 4096 60 us, 0.56. fp32: 1000 x 4096 x 4096 315 us, 107
+// TFLOP/s of the 155 that a large product reaches.
 // kAdapt: the epilogue adds each token's adapter, v B^T, one different adapter
 // of a 16-token group after another, and writes y; otherwise fp32 parts.
 template <bool kF32, typename C, bool kAdapt>
@@ -986,7 +991,8 @@ __global__ __launch_bounds__(C::kBlock) void linear_tile(TileArgs p) {
 }
 
 // At most 16 tokens: block (tile, s) of the weight's and then the adapters'
-// tiles.
+// tiles. Bound by latency for small weights (3584 x 3584: 10 us, a burst of loads),
+// by reading W for large ones (7168 x 7168: 21 us, 4.9 TB/s).
 template <bool kF32, bool kWide>
 __global__ __launch_bounds__(kThreads, 3) void stream_partial(StreamArgs p) {
   const int64_t z = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
@@ -1005,8 +1011,8 @@ __global__ __launch_bounds__(kThreads, 3) void stream_partial(StreamArgs p) {
 // More tokens: the first `tiles` blocks are weight tiles of 64 tokens x 128 rows
 // (every token beside each weight byte, so that x is read once a tile and not
 // once for 16 rows), the others units of the adapters' low-rank products,
-// `units` for each 64 tokens (first they would fill the CUs' LDS: 43 us against
-// 32 us for 64 tokens and a 7168 x 7168 weight).
+// `units` for each 64 tokens (first they would fill the CUs' LDS: 44 us and not 26
+// for 64 tokens, a 7168 x 7168 weight and 24 adapters of rank 64).
 typedef Shape<1, 4, 4, 2, 3> FewShape;
 template <bool kF32>
 __global__ __launch_bounds__(kThreads) void few_linear(TileArgs p, StreamArgs q, int tiles, int units) {
@@ -1111,7 +1117,9 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // ---- the router's logits --------------------------------------------------
 namespace {
 // Shapes of the logits' tiles: 128 x 256 where that leaves a tile for every
-// fourth CU or more, so that four parts fill them all; else 64 x 64.
+// fourth CU or more, so that four parts fill them all; else 64 x 64 (7168 x 256:
+// 16384 tokens 69 us, by 64 x 64 126; 8192 tokens 39 and 64; 4096 tokens 31 and 27;
+// 2048 tokens 28 and 17.5).
 bool wide_logits(int64_t T, int64_t row_bytes, int N) {
   return N > 128 && row_bytes <= (int64_t{1} << 23) &&
          cdiv(T, WideShape::kM) * cdiv(N, WideShape::kN) >= kPlanCus / 4;
@@ -1335,8 +1343,8 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
   t.R = d.R;
   t.Rq = L.Rq;
   // the largest tiles of which there is one for each CU: 8192 x 7160 x 7000 takes
-  // 1035 us on the wide ones and 1189 us on the middle ones, 1000 x 5000 x 6001
-  // (376 middle tiles) 140 us on the middle and 181 us on the small ones
+  // 1020 us on the wide ones and 1076 us on the middle ones, 1000 x 5000 x 6001
+  // (376 middle tiles) 122 us on the middle and 168 us on the small ones
   if (cdiv(d.T, WideShape::kM) * cdiv(d.N, WideShape::kN) >= kPlanCus && row_bytes <= (int64_t{1} << 23))
     return f32 ? launch_tile<true, WideShape, true>(t, st) : launch_tile<false, WideShape, true>(t, st);
   if (cdiv(d.T, MidShape::kM) * cdiv(d.N, MidShape::kN) >= kPlanCus)

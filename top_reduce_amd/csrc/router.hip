@@ -180,8 +180,12 @@ hipError_t route_topk(const tr_route_desc& d, const void* x, const void* w_gate,
                         few ? reinterpret_cast<uint32_t*>(few->masks) : nullptr,
                         few ? 2 * few->E : 0, st);
   if (e != hipSuccess) return e;
+  // registers of logits for the experts there are (16384 tokens of 128 experts by 2
+  // 10.7 us, by 4 12.7; 4096 of 512 by 8 10.4 us, by 16 14.2)
   if (d.G <= 64) return launch_select<1>(a, f, st);
+  if (d.G <= 128) return launch_select<2>(a, f, st);
   if (d.G <= 256) return launch_select<4>(a, f, st);
+  if (d.G <= 512) return launch_select<8>(a, f, st);
   if (d.G <= 1024) return launch_select<16>(a, f, st);
   return launch_select<64>(a, f, st);
 }
