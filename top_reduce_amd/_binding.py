@@ -496,7 +496,8 @@ def compact_rows(src: torch.Tensor, block_rows: int, block_counts: torch.Tensor,
 # These calls run in a few microseconds on the GPU, so their own checks are kept
 # cheap: descriptors and workspace sizes are made once for each set of sizes, and
 # a tensor is compared with what its argument must be in one expression before
-# the error is worked out.
+# the error is worked out. With `stream`, tensors that the caller gives must be
+# ready on that stream; what the call allocates belongs to it (_run_on).
 _SCORES = {"softmax": 0, "sigmoid": 1}
 
 
@@ -535,10 +536,32 @@ def _ws_arg(ws: Optional[torch.Tensor], need: int, device) -> torch.Tensor:
     return ws
 
 
-def _raw_stream(stream, device) -> int:
-    if stream is not None:
-        return stream.cuda_stream
+def _raw_stream(device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _elsewhere(stream, device) -> bool:
+    """Whether `stream` is another one than the device's current stream."""
+    if stream is None:
+        return False
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, x on {device}")
+    return stream.cuda_stream != _raw_stream(device)
+
+
+def _run_on(stream, given, call, *args):
+    """call(*args) with `stream` as the current one, so that what it allocates
+    belongs to that stream: its memory may have been another tensor's, whose work
+    the kernels then come after, and the workspace, freed on return, is not handed
+    out again before they are done. Outputs the caller did not give are the
+    caller's to use on its own current stream: they are kept until that is done."""
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = call(*args)
+    for t in out if isinstance(out, tuple) else (out,):
+        if not any(t is g for g in given):
+            t.record_stream(caller)
+    return out
 
 
 def _route_sizes(T, H, G, K, dtype, score, renorm, scale, idx_dtype) -> RouteDesc:
@@ -587,6 +610,9 @@ def route_topk(x: torch.Tensor, w_gate: torch.Tensor, K: int, bias: Optional[tor
     bias (fp32 [G]) by score + bias. The weights are the scores, divided by
     their sum with renorm, times scale. idx is what plan() takes."""
     dev = _x_arg(x)
+    if _elsewhere(stream, dev):
+        return _run_on(stream, (idx, weights), route_topk, x, w_gate, K, bias, score, renorm, scale,
+                       idx_dtype, idx, weights, ws)
     if not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 2:
         raise ValueError("w_gate must be a [G, H] tensor")
     T, H = x.shape
@@ -602,7 +628,7 @@ def route_topk(x: torch.Tensor, w_gate: torch.Tensor, K: int, bias: Optional[tor
     wp = _arg(weights, "weights", torch.float32, (T, K), dev)
     ws = _ws_arg(ws, need, dev)
     status = _lib.moe_route_topk(desc, x.data_ptr(), gp, bp, ip, wp, ws.data_ptr(), ws.numel(),
-                                 _raw_stream(stream, dev))
+                                 _raw_stream(dev))
     if status:
         _check(status)
     return idx, weights
@@ -626,6 +652,9 @@ def layer(x: torch.Tensor, w_gate: torch.Tensor, w1: torch.Tensor, w2: torch.Ten
     (w1 [E, 2I, H] gate | up, w2 [E, H, I]) and their weighted sum. Rows
     without a local expert are +0. y may be x."""
     dev = _x_arg(x)
+    if _elsewhere(stream, dev):
+        return _run_on(stream, (y, idx, weights), layer, x, w_gate, w1, w2, K, bias, score, renorm,
+                       scale, expert_begin, idx_dtype, y, idx, weights, ws)
     if not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 2:
         raise ValueError("w_gate must be a [G, H] tensor")
     if not isinstance(w1, torch.Tensor) or w1.dim() != 3 or w1.shape[1] % 2:
@@ -649,7 +678,7 @@ def layer(x: torch.Tensor, w_gate: torch.Tensor, w1: torch.Tensor, w2: torch.Ten
     yp = _arg(y, "y", dt, (T, H), dev)
     ws = _ws_arg(ws, need, dev)
     status = _lib.moe_layer(desc, x.data_ptr(), gp, bp, w1p, w2p, yp, ip, wp, ws.data_ptr(),
-                            ws.numel(), _raw_stream(stream, dev))
+                            ws.numel(), _raw_stream(dev))
     if status:
         _check(status)
     return y, idx, weights
@@ -668,6 +697,8 @@ def adapter_linear(x: torch.Tensor, w: torch.Tensor, a: torch.Tensor, b: torch.T
     i = ids[t] (int32 [T]; outside [0, A): no adapter). x [T, H], w [N, H],
     a [A, R, H], b [A, N, R], scales fp32 [A] or None for 1."""
     dev = _x_arg(x)
+    if _elsewhere(stream, dev):
+        return _run_on(stream, (y,), adapter_linear, x, w, a, b, ids, scales, y, ws)
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("w must be an [N, H] tensor")
     if not isinstance(a, torch.Tensor) or a.dim() != 3:
@@ -686,7 +717,7 @@ def adapter_linear(x: torch.Tensor, w: torch.Tensor, a: torch.Tensor, b: torch.T
     yp = _arg(y, "y", dt, (T, N), dev)
     ws = _ws_arg(ws, need, dev)
     status = _lib.moe_adapter_linear(desc, x.data_ptr(), wp, ap, bp, ip, sp, yp, ws.data_ptr(),
-                                     ws.numel(), _raw_stream(stream, dev))
+                                     ws.numel(), _raw_stream(dev))
     if status:
         _check(status)
     return y
