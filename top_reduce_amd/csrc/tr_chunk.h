@@ -99,11 +99,12 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
 
 // silu(g) * u in fp32. bf16 results take the hardware exponential and
 // reciprocal (about 1 ulp of fp32 each, far below their own rounding); fp32
-// results the exact division.
+// results the exact division. silu first: g u alone may be past fp32 where the
+// result is not (g = -64, u = 2e38), and times a reciprocal of 0 would be NaN.
 template <bool kF32>
 __device__ __forceinline__ float swiglu(float g, float u) {
   if constexpr (kF32) return g / (1.0f + expf(-g)) * u;
-  return g * u * __builtin_amdgcn_rcpf(1.0f + __expf(-g));
+  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
 
 // Stores the four neighbouring outputs v of a row at column col, those below
