@@ -31,3 +31,43 @@ def test_gate_far_below_zero_beside_a_huge_up_value(T, dtype):
     want = 0.5 * I * g / (1 + torch.tensor(-g).double().exp()) * u * w2[0, 0, 0].double()
     # e^64 in fp32: its argument's last bit is 64 2^-24 of the result; then one rounding
     assert ((S.f64(y) - want).abs() <= (2.0 ** -16 + S.U[dtype]) * want.abs()).all()
+
+
+def alike(got, want, what):
+    """Infinities of the same signs, NaN in the same places, the rest finite."""
+    got = S.f64(got)
+    assert torch.equal(got.isposinf(), want.isposinf()), what
+    assert torch.equal(got.isneginf(), want.isneginf()), what
+    assert torch.equal(got.isnan(), want.isnan()), what
+
+
+@pytest.mark.parametrize("T,I,dtype", [(1, 96, BF), (9, 70, BF), (33, 257, BF), (64, 2048, BF), (9, 70, F32)])
+def test_infinite_down_weights_give_infinities_of_the_right_sign(T, I, dtype):
+    """h is two numbers in bf16: the second one times an infinite weight is NaN
+    where it is 0, and of either sign where it is not."""
+    say(f"infinite w2 T={T} I={I} {dtype}")
+    H, E = 264, 2
+    g = torch.Generator().manual_seed(T + I)
+    x = S.inputs(g, T, H, dtype=dtype)
+    gate = torch.zeros(E, H, dtype=dtype)
+    w1 = S.inputs(g, E, 2 * I, H, dtype=dtype, std=H ** -0.5)
+    # one row of each expert whose h are bf16 numbers (0 as the second one): u is a
+    # power of two times x's column of ones, g is large
+    x[:, 0] = 1.0
+    w1[:, 3], w1[:, I + 3] = 0.0, 0.0
+    w1[:, 3, 0], w1[:, I + 3, 0] = 32.0, -4.0
+    w2 = S.inputs(g, E, H, I, dtype=dtype, std=I ** -0.5)
+    inf = float("inf")
+    w2[0, 5, 7], w2[1, 40, 2], w2[0, 41, 3], w2[1, 100, 3] = inf, -inf, inf, -inf
+    w2[0, 200, 8], w2[0, 200, 9], w2[1, 201, 4] = inf, -inf, float("nan")
+    y, idx, w = tr.layer(x.cuda(), gate.cuda(), w1.cuda(), w2.cuda(), 2)
+    assert idx.tolist() == [[0, 1]] * T
+    x6 = S.f64(x)
+    want = 0.0
+    for e in range(E):
+        gu = x6 @ S.f64(w1[e]).t()
+        h = 0.5 * gu[:, :I] * torch.sigmoid(gu[:, :I]) * gu[:, I:]
+        assert (h.abs() > 1e-30).all()
+        want = want + h @ S.f64(w2[e]).t()
+    alike(y, want, "y")
+    assert (~torch.isfinite(want)).sum() >= 6 * T

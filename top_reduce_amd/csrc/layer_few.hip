@@ -401,10 +401,14 @@ __global__ __launch_bounds__(kThreads, 3) void few_down(FewArgs a) {
         const int at = d * kGroup + tr;
         const int t = __shfl(by_rank, min(rank + at, kWave - 1), kWave);
         if constexpr (kParts == 2) {
-          // even lanes: what the second numbers, a lane on, gave
+          // even lanes: what the second numbers, a lane on, gave. With a weight that
+          // is not a number or infinite that says nothing (0 or another sign times
+          // infinity), and the first numbers have given the result.
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            acc[d][j] += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(acc[d][j]), 0xf5, 15, 15, true));
+          for (int j = 0; j < 4; ++j) {
+            const float lo = __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(acc[d][j]), 0xf5, 15, 15, true));
+            acc[d][j] += fabsf(lo) <= kMaxFloat ? lo : 0.0f;
+          }
         }
         if (part == 0 && at < n) sum[wave][t][g] += acc[d];
         acc[d] = floatx4{0, 0, 0, 0};

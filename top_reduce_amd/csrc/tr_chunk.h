@@ -14,6 +14,8 @@
 
 namespace tr {
 
+constexpr float kMaxFloat = 3.4028234664e38f;   // the largest finite fp32
+
 template <bool kF32>
 struct Elem;
 template <>
