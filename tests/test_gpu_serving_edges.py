@@ -71,3 +71,36 @@ def test_infinite_down_weights_give_infinities_of_the_right_sign(T, I, dtype):
         want = want + h @ S.f64(w2[e]).t()
     alike(y, want, "y")
     assert (~torch.isfinite(want)).sum() >= 6 * T
+
+
+@pytest.mark.parametrize("T,H,N,R,A,dtype", [
+    (1, 256, 130, 12, 2, BF), (40, 264, 257, 33, 3, BF), (90, 256, 300, 64, 2, BF), (9, 256, 130, 12, 2, F32),
+])
+def test_infinite_adapter_weights_give_infinities_of_the_right_sign(T, H, N, R, A, dtype):
+    check_infinite_adapters(T, H, N, R, A, 1, dtype)
+
+
+def check_infinite_adapters(T, H, N, R, A, run, dtype):
+    say(f"infinite b T={T} H={H} N={N} R={R} {dtype}")
+    g = torch.Generator().manual_seed(T + N)
+    x = S.inputs(g, T, H, dtype=dtype)
+    w = S.inputs(g, N, H, dtype=dtype, std=H ** -0.5)
+    a = S.inputs(g, A, R, H, dtype=dtype, std=H ** -0.5)
+    b = S.inputs(g, A, N, R, dtype=dtype, std=R ** -0.5)
+    ids = (torch.arange(-(-T // run)) % (A + 1)).to(torch.int32).repeat_interleave(run)[:T].contiguous()
+    # a low-rank product that is a bf16 number: its second number is 0
+    x[:, 0] = 1.0
+    a[:, 3] = 0.0
+    a[:, 3, 0] = -4.0
+    inf = float("inf")
+    b[:, 5, 7], b[:, 40, 2], b[:, 41, 3], b[:, 100, 3] = inf, -inf, inf, -inf
+    b[:, 120, 8], b[:, 120, 9], b[:, 121, 4] = inf, -inf, float("nan")
+    y = tr.adapter_linear(x.cuda(), w.cuda(), a.cuda(), b.cuda(), ids.cuda())
+    want = S.f64(x) @ S.f64(w).t()
+    for i in range(A):
+        mine = ids == i
+        v = S.f64(x[mine]) @ S.f64(a[i]).t()
+        assert (v.abs() > 1e-30).all()
+        want[mine] += v @ S.f64(b[i]).t()
+    alike(y, want, "y")
+    assert (~torch.isfinite(want)).sum() >= 6 * int((ids < A).sum())

@@ -312,6 +312,9 @@ struct ExpandArgs {
 // the other: for bf16 as two bf16 numbers each (16 significant bits), so that y
 // is rounded once. Bound by latency: the loads of B (kKb blocks of it at a time),
 // of the parts (kParts at a time) and of the low-rank sums go out together.
+// (Sums with the second numbers in accumulators of their own, dropped where they
+// are not finite, took 1.7 us more than finite_bf16's 0.3 us for 64 x 7168 x 7168
+// with 24 adapters of rank 64.)
 template <bool kF32, int kKb, int kParts>
 __global__ __launch_bounds__(kThreads) void adapter_few(ExpandArgs p) {
   typedef typename Elem<kF32>::type E;
@@ -430,7 +433,8 @@ __global__ __launch_bounds__(kThreads) void adapter_few(ExpandArgs p) {
         for (int q = 0; q < kV; ++q) {
           const u32x4 vv = *reinterpret_cast<const u32x4*>(&v_s[q][r][(kb0 + kb) * 4 * kC + g * kC]);
 #pragma unroll
-          for (int j = 0; j < kNs; ++j) acc[j] = mma16<kF32>(bv[kb][j], vv, acc[j]);
+          for (int j = 0; j < kNs; ++j)
+            acc[j] = mma16<kF32>(q == 0 ? bv[kb][j] : finite_bf16(bv[kb][j]), vv, acc[j]);
         }
       }
       if ((kb0 + kKb) * 4 * kC < Rk) {
