@@ -394,11 +394,10 @@ size_t moe_adapter_linear_workspace(const tr_adapter_desc* desc);
 /* y[t] = w x[t] + scales[i] * b[i] (a[i] x[t]) with i = ids[t]; rows whose id is
  * outside [0, A) (-1, say) have no adapter and read none. Accumulation is
  * fp32 and y is rounded once; in bf16 the low-rank product scales[i] a[i] x is
- * held in 16 significant bits, or is rounded to bf16 where the rows and columns
- * make 256 or more tiles of 64 x 128. x: device [T, H]; w: device [N, H]; a: device [A, R, H]; b: device
- * [A, N, R]; ids: device int32 [T]; scales: device fp32 [A] or NULL (1);
- * y: device [T, N], must not overlap x; ws: device, 256-byte aligned, its
- * contents before and after of no meaning. */
+ * held in 16 significant bits. x: device [T, H]; w: device [N, H]; a: device
+ * [A, R, H]; b: device [A, N, R]; ids: device int32 [T]; scales: device fp32 [A]
+ * or NULL (1); y: device [T, N], must not overlap x; ws: device, 256-byte
+ * aligned, its contents before and after of no meaning. */
 tr_status moe_adapter_linear(const tr_adapter_desc* desc, const void* x, const void* w,
                              const void* a, const void* b, const int32_t* ids,
                              const float* scales, void* y, void* ws, size_t ws_bytes,

@@ -104,3 +104,12 @@ def check_infinite_adapters(T, H, N, R, A, run, dtype):
         want[mine] += v @ S.f64(b[i]).t()
     alike(y, want, "y")
     assert (~torch.isfinite(want)).sum() >= 6 * int((ids < A).sum())
+
+
+@pytest.mark.parametrize("T,H,N,R,A,run,dtype", [
+    (700, 264, 4096, 20, 3, 9, BF), (2048, 256, 4100, 16, 2, 300, BF),       # 64 x 64, 128 x 256
+    (4100, 128, 8192, 24, 4, 1, BF), (4100, 256, 8192, 16, 4, 300, BF),      # 256 x 256
+    (700, 264, 4096, 20, 3, 9, F32),
+])
+def test_infinite_adapter_weights_on_tiles(T, H, N, R, A, run, dtype):
+    check_infinite_adapters(T, H, N, R, A, run, dtype)

@@ -79,7 +79,8 @@ struct GemmArgs {
 // x and of the output.
 struct AdaptArgs {
   const int* ids;       // [rows]; outside [0, n): none
-  const uint16_t* v;    // [rows, Rq] low-rank products, scaled; zero past R
+  const uint16_t* v;    // [rows, 2, Rq] low-rank products, scaled, as two bf16 numbers
+                        // whose sum has 16 significant bits; zero past R
   const uint16_t* b;    // [n, Nc, R]
   int n, R, Rq;         // R a multiple of 8
 };
@@ -715,30 +716,39 @@ __device__ __forceinline__ void gemm_tiles_impl(const GemmArgs& a, int I, const 
           if (((todo >> i) & 1) && __builtin_amdgcn_readfirstlane(aid[i]) == which) now |= 1u << i;
         todo &= ~now;
         const uint16_t* brow = ad->b + (static_cast<int64_t>(which) * a.Nc + t.n0 + wn * 128 + (lane & 31)) * ad->R;
-        const uint16_t* vrow = ad->v + static_cast<int64_t>(t.row0 + wm * 128 + (lane & 31)) * ad->Rq;
+        const uint16_t* vrow = ad->v + static_cast<int64_t>(t.row0 + wm * 128 + (lane & 31)) * (2 * ad->Rq);
 #pragma clang loop unroll(disable)
         for (int k0 = 0; k0 < ad->R; k0 += 16) {
           const int k = k0 + (lane >> 5) * 8;
           u32x4 vf[4], bf[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            bf[j] = vf[j] = u32x4{0, 0, 0, 0};
-            if (k < ad->R) {
-              bf[j] = *reinterpret_cast<const u32x4*>(brow + j * 32 * ad->R + k);
-              // (rows past the last are not read)
-              if (wm * 128 + j * 32 + (lane & 31) < t.rows_valid)
-                vf[j] = *reinterpret_cast<const u32x4*>(vrow + j * 32 * ad->Rq + k);
-            }
+            bf[j] = u32x4{0, 0, 0, 0};
+            if (k < ad->R) bf[j] = *reinterpret_cast<const u32x4*>(brow + j * 32 * ad->R + k);
           }
+          // the first numbers' products, then the second ones', one set of
+          // registers for both (all loads at once spill 35 registers)
+#pragma clang loop unroll(disable)
+          for (int q = 0; q < 2; ++q) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if ((now >> i) & 1) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                f.acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                    __builtin_bit_cast(bf16x8, bf[j]), __builtin_bit_cast(bf16x8, vf[i]),
-                    f.acc[i][j], 0, 0, 0);
+            for (int j = 0; j < 4; ++j) {
+              vf[j] = u32x4{0, 0, 0, 0};
+              // (rows past the last are not read)
+              if (k < ad->R && wm * 128 + j * 32 + (lane & 31) < t.rows_valid)
+                vf[j] = *reinterpret_cast<const u32x4*>(vrow + (2 * j * 32 + q) * ad->Rq + k);
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if ((now >> i) & 1) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  f.acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                      __builtin_bit_cast(bf16x8, bf[j]), __builtin_bit_cast(bf16x8, vf[i]),
+                      f.acc[i][j], 0, 0, 0);
+              }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) bf[j] = finite_bf16(bf[j]);
+          }
         }
       }
     }
@@ -805,18 +815,21 @@ __device__ __forceinline__ void gemm_tiles_impl(const GemmArgs& a, int I, const 
               const uint16_t* brow =
                   ad->b + (static_cast<int64_t>(which) * a.Nc + t.n0 + wn * 128 + j * 32 + (lane & 31)) * ad->R;
               const uint16_t* vrow =
-                  ad->v + static_cast<int64_t>(t.row0 + (mine ? row : wm * 128 + i * 32 + lead)) * ad->Rq;
+                  ad->v + static_cast<int64_t>(t.row0 + (mine ? row : wm * 128 + i * 32 + lead)) * (2 * ad->Rq);
               floatx16 d = xg;
 #pragma clang loop unroll(disable)
               for (int k0 = 0; k0 < ad->R; k0 += 16) {
                 const int k = k0 + (lane >> 5) * 8;
-                u32x4 bf = {0, 0, 0, 0}, vf = {0, 0, 0, 0};
+                u32x4 bf = {0, 0, 0, 0}, vf[2] = {bf, bf};
                 if (k < ad->R) {
                   bf = *reinterpret_cast<const u32x4*>(brow + k);
-                  vf = *reinterpret_cast<const u32x4*>(vrow + k);
+                  vf[0] = *reinterpret_cast<const u32x4*>(vrow + k);
+                  vf[1] = *reinterpret_cast<const u32x4*>(vrow + ad->Rq + k);
                 }
                 d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, bf),
-                                                            __builtin_bit_cast(bf16x8, vf), d, 0, 0, 0);
+                                                            __builtin_bit_cast(bf16x8, vf[0]), d, 0, 0, 0);
+                d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, finite_bf16(bf)),
+                                                            __builtin_bit_cast(bf16x8, vf[1]), d, 0, 0, 0);
               }
               if (mine) xg = d;
             }

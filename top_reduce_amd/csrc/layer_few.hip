@@ -272,15 +272,10 @@ __global__ __launch_bounds__(kThreads, NQ == 4 ? 2 : 3) void few_up(FewArgs a, S
       if constexpr (kF32) {
         *reinterpret_cast<floatx4*>(dst) = v;
       } else {
-        const uint32_t h0 = cvt_bf16x2(v[0], v[1]), h1 = cvt_bf16x2(v[2], v[3]);
-        // the rest of a number past bf16's range (or of a NaN) is 0, not NaN
-        const float hf[4] = {__uint_as_float(h0 << 16), __uint_as_float(h0 & 0xffff0000u),
-                             __uint_as_float(h1 << 16), __uint_as_float(h1 & 0xffff0000u)};
-        float lo[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) lo[j] = fabsf(hf[j]) <= 3.3895314e38f ? v[j] - hf[j] : 0.0f;
-        *reinterpret_cast<uint2*>(dst) = uint2{h0, h1};
-        *reinterpret_cast<uint2*>(dst + 64) = uint2{cvt_bf16x2(lo[0], lo[1]), cvt_bf16x2(lo[2], lo[3])};
+        uint2 hi, lo;
+        split_bf16(v, hi, lo);
+        *reinterpret_cast<uint2*>(dst) = hi;
+        *reinterpret_cast<uint2*>(dst + 64) = lo;
       }
     }
     __syncthreads();

@@ -526,7 +526,7 @@ struct ShrinkArgs {
   const int32_t* ids;    // by position
   const int32_t* perm;   // the positions' tokens, or NULL: the same
   const float* scales;
-  void* v;               // [T, Rq] in the storage type, zero past R
+  void* v;               // [T, parts, Rq], zero past R: fp32, or two bf16 numbers
   int64_t row_bytes;
   int64_t T;
   int A, R, Rq;
@@ -539,8 +539,10 @@ struct ShrinkArgs {
 // A's loads alone; x alone takes 25 us). The different adapters among the tokens
 // (one where tokens of a request are neighbours) are dealt to kSlots blocks, so
 // that a group at the border of two requests takes no longer than the others. v
-// is rounded to the storage type, to be an MFMA operand of the tiles: its error
-// is that of one rounding of the adapter's part.
+// is kept as the tiles multiply it: fp32, or two bf16 numbers with 16 significant
+// bits, so that a row is the same however many rows share its call.
+template <bool kF32>
+constexpr int kVParts = kF32 ? 1 : 2;   // numbers that make up an element of v
 constexpr int kSlots = 2;
 constexpr int kShrinkThreads = 384;   // two blocks a CU
 constexpr int kShrinkWaves = kShrinkThreads / kWave;
@@ -672,10 +674,18 @@ __global__ __launch_bounds__(kShrinkThreads, 3) void adapter_shrink(ShrinkArgs p
         for (int w = 1; w < kShrinkWaves; ++w) v += red[w][c][q][lane];
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = col + i < p.R ? v[i] * sc : 0.0f;
-        E* out = static_cast<E*>(p.v) + (t0 + 16 * q + r) * p.Rq;
-        store4<kF32>(out, col, p.Rq, true, v);
-        // (one tile of two that an MFMA takes: zeros in the other's place)
-        if (kRT == 1 && col + 16 < p.Rq) store4<kF32>(out, col + 16, p.Rq, true, floatx4{0, 0, 0, 0});
+        E* out = static_cast<E*>(p.v) + (t0 + 16 * q + r) * kVParts<kF32> * p.Rq + col;
+        if constexpr (kF32) {
+          *reinterpret_cast<floatx4*>(out) = v;
+        } else {
+          uint2 hi, lo;
+          split_bf16(v, hi, lo);
+          *reinterpret_cast<uint2*>(out) = hi;
+          *reinterpret_cast<uint2*>(out + p.Rq) = lo;
+          // (one tile of two that an MFMA takes: zeros in the other's place)
+          if (kRT == 1 && col + 16 < p.Rq)
+            *reinterpret_cast<uint2*>(out + 16) = *reinterpret_cast<uint2*>(out + p.Rq + 16) = uint2{0, 0};
+        }
       }
       __syncthreads();
     }
@@ -719,7 +729,7 @@ struct TileArgs {
   void* y;               // [T, N]
   const int32_t* ids;    // adapters by position (NULL: none)
   const int32_t* perm;   // the positions' tokens, or NULL: the same
-  const void* v;         // [T, Rq], by position
+  const void* v;         // [T, parts, Rq], by position (ShrinkArgs)
   const void* b;         // [A, N, R]
   int A, R, Rq;
 };
@@ -937,13 +947,15 @@ __device__ __forceinline__ void tile_unit(const TileArgs& p, int block) {
         const int aid = __builtin_amdgcn_readlane(id, lead);
         const bool mine = id == aid;
         todo &= ~static_cast<uint32_t>(__ballot(mine));
-        const E* vrow = static_cast<const E*>(p.v) + (mine ? t : t0 + lt0 + lead) * p.Rq;
+        const E* vrow = static_cast<const E*>(p.v) + (mine ? t : t0 + lt0 + lead) * kVParts<kF32> * p.Rq;
         floatx4 d[C::kNs];
 #pragma unroll
         for (int j = 0; j < C::kNs; ++j) d[j] = floatx4{0, 0, 0, 0};
         for (int j0 = 0; j0 < p.R; j0 += 4 * kC) {
           const int k = j0 + g * kC;
           const u32x4 fv = load16(reinterpret_cast<const char*>(vrow + k));
+          u32x4 fl = {0, 0, 0, 0};
+          if constexpr (!kF32) fl = load16(reinterpret_cast<const char*>(vrow + p.Rq + k));
 #pragma unroll
           for (int j = 0; j < C::kNs; ++j) {
             const int n = min(n0 + (wn * C::kNs + j) * 16 + r, p.N - 1);
@@ -952,6 +964,7 @@ __device__ __forceinline__ void tile_unit(const TileArgs& p, int block) {
             if (k < p.R)
               fb = vec ? load16(reinterpret_cast<const char*>(row + k)) : load16_any<kF32>(row, k, p.R);
             d[j] = mma16<kF32>(fb, fv, d[j]);
+            if constexpr (!kF32) d[j] = mma16<kF32>(finite_bf16(fb), fl, d[j]);
           }
         }
         // added to its own tokens only: an adapter's infinities reach no other
@@ -1220,7 +1233,7 @@ AdapterLayout adapter_layout(const tr_adapter_desc& d) {
     L.n_units = static_cast<int>(most < chunk ? most : chunk);
     L.total = L.units + up256(sizeof(AdapterUnit) * L.n_units * cdiv(d.T, kFewTokens));
   } else {
-    L.perm = up256(static_cast<size_t>(d.T) * L.Rq * (f32 ? 4 : 2));
+    L.perm = up256(static_cast<size_t>(d.T) * L.Rq * 4);   // fp32, or two bf16 numbers
     L.sid = L.perm + up256(4 * static_cast<size_t>(d.T));
     L.total = L.sid + up256(4 * static_cast<size_t>(d.T));
   }

@@ -43,21 +43,6 @@ __device__ __forceinline__ floatx4 mma16(const u32x4& a, const u32x4& b, floatx4
   }
 }
 
-// Eight bf16 numbers, zeros in place of infinities and NaN. A factor that is held
-// as two bf16 numbers, hi + lo, takes the other operand as it is with hi and so
-// with lo: lo (0, or of either sign) times infinity says nothing, and hi has given
-// the result.
-__device__ __forceinline__ u32x4 finite_bf16(u32x4 v) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // bit 15 of each half: its exponent is all ones (the addition carries into
-    // that bit only, 0x7f80 + 0x80 at most)
-    const uint32_t top = ((v[i] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-    v[i] &= ~(top | (top - (top >> 15)));
-  }
-  return v;
-}
-
 __device__ __forceinline__ u32x4 load16(const char* p) {
   return *reinterpret_cast<const u32x4*>(p);
 }
@@ -112,6 +97,19 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
   const bf16x2 v = {static_cast<__bf16>(lo), static_cast<__bf16>(hi)};
   return __builtin_bit_cast(uint32_t, v);
+}
+
+// Four floats as two bf16 numbers each, v = hi + lo with 16 significant bits,
+// packed like cvt_bf16x2. The rest of an infinity, of a number past bf16's range or
+// of a NaN is 0, not NaN.
+__device__ __forceinline__ void split_bf16(const floatx4& v, uint2& hi, uint2& lo) {
+  hi = uint2{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
+  const float h[4] = {__uint_as_float(hi.x << 16), __uint_as_float(hi.x & 0xffff0000u),
+                      __uint_as_float(hi.y << 16), __uint_as_float(hi.y & 0xffff0000u)};
+  float r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = fabsf(h[i]) <= 3.3895314e38f ? v[i] - h[i] : 0.0f;
+  lo = uint2{cvt_bf16x2(r[0], r[1]), cvt_bf16x2(r[2], r[3])};
 }
 
 // silu(g) * u in fp32. bf16 results take the hardware exponential and

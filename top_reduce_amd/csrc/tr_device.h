@@ -29,6 +29,21 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return f32_to_bf16_bits(lo) | (f32_to_bf16_bits(hi) << 16);
 }
 
+// Eight bf16 numbers, zeros in place of infinities and NaN. A factor that is held
+// as two bf16 numbers, hi + lo, takes the other operand as it is with hi and so
+// with lo: lo (0, or of either sign) times infinity says nothing, and hi has given
+// the result.
+__device__ __forceinline__ u32x4 finite_bf16(u32x4 v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // bit 15 of each half: its exponent is all ones (the addition carries into
+    // that bit only, 0x7f80 + 0x80 at most)
+    const uint32_t top = ((v[i] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+    v[i] &= ~(top | (top - (top >> 15)));
+  }
+  return v;
+}
+
 __device__ __forceinline__ int lane_id() { return __lane_id(); }
 
 // Count of set bits of `mask` in lanes below the calling lane.

@@ -107,7 +107,7 @@ hipError_t few_layer(const tr_layer_desc& d, const void* x, const void* w_gate, 
 
 // The shared projection on the grouped GEMM's 256 x 256 tiles: whether its shape
 // allows that and gives at least two tiles a CU (bf16; ids and v, low-rank
-// products as adapter_linear makes them, rows of Rq, by position; perm: the
+// products as adapter_linear makes them, [T, 2, Rq], by position; perm: the
 // positions' tokens, x being below 2 GiB, or NULL: the same).
 bool adapter_can_tile(const tr_adapter_desc& d);
 hipError_t adapter_tiles(const tr_adapter_desc& d, const void* x, const void* w, const void* b,
