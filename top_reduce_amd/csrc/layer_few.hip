@@ -340,7 +340,7 @@ __global__ __launch_bounds__(kThreads, 3) void few_down(FewArgs a) {
     if (in) mine[wave][n_mine + popc_below(all)] = static_cast<uint16_t>(q);
     n_mine += __popcll(all);
   }
-  __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+  wave_lds_fence();
   const int items = n_mine * nbf;
   const int units = static_cast<int>((a.H + a.cols - 1) / a.cols);
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
@@ -405,6 +405,8 @@ __global__ __launch_bounds__(kThreads, 3) void few_down(FewArgs a) {
             acc[d][j] += fabsf(lo) <= kMaxFloat ? lo : 0.0f;
           }
         }
+        // (the token's sum so far is another lane's, of another group or the zero)
+        wave_lds_fence();
         if (part == 0 && at < n) sum[wave][t][g] += acc[d];
         acc[d] = floatx4{0, 0, 0, 0};
       }

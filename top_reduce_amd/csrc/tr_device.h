@@ -46,6 +46,13 @@ __device__ __forceinline__ u32x4 finite_bf16(u32x4 v) {
 
 __device__ __forceinline__ int lane_id() { return __lane_id(); }
 
+// Between lanes of a wave that hand each other values through LDS: the wave's LDS
+// accesses before it come before those after it. No instruction (a wave's LDS
+// accesses go in order); it keeps the compiler from moving them.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront", "local");
+}
+
 // Count of set bits of `mask` in lanes below the calling lane.
 __device__ __forceinline__ int popc_below(uint64_t mask) {
   return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),

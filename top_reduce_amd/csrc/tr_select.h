@@ -202,6 +202,7 @@ __device__ __forceinline__ Chosen choose(const SelectArgs& a, int64_t t, SelectS
       }
       c_n += __popcll(in);
     }
+    wave_lds_fence();
     if (c_n <= kWave) {
       c_key = s.key[lane];
       c_id = s.id[lane];
