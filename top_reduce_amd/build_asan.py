@@ -8,7 +8,8 @@ only (-Xarch_host before each sanitizer flag); the device code is the
 ordinary gfx950 code. The result is _build_asan/libtopreduce_asan.so. A
 Python process loads it with the sanitizer runtime preloaded
 (LD_PRELOAD=asan_runtime()) and TOP_REDUCE_LIB pointing at it; the ABI tests
-run that way in tests/test_abi_asan.py. Not for GPU runs.
+run that way in tests/test_abi_asan.py and tests/test_abi_serving_asan.py. Not for
+GPU runs.
 """
 
 from __future__ import annotations
