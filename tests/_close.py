@@ -13,6 +13,9 @@ they are an ulp apart. With an error of e |y| before the rounding the chance is
 squares is at most 2^-6 e |y|^2. e is eps, and 2^-17 for a factor that is held in 16
 significant bits (8 bits: 2^-9, sixteen times the difference). A few elements may by
 chance all be at a midpoint: FLIPS of them.
+
+The sizes are those of rows and blocks of a few dozen elements and more: a row of one
+or two may come out near zero, far below what its sums went through.
 """
 
 import torch

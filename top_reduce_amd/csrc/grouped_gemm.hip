@@ -688,8 +688,9 @@ __device__ __forceinline__ void gemm_tiles_impl(const GemmArgs& a, int I, const 
 
     // Adapters. A wave's row block of 32 rows that all have one adapter takes
     // its product in the accumulators: the rows of B are loaded once for every
-    // row block with that adapter (in prompts mostly all four). Row blocks with several adapters, or with rows that have none, are
-    // marked in `mixed` and take theirs in the epilogue.
+    // row block with that adapter (in prompts mostly all four). Row blocks with
+    // several adapters, or with rows that have none, are marked in `mixed` and take
+    // theirs in the epilogue.
     int aid[4], to_row[4];
     uint32_t mixed = 0;
     if constexpr (kAdapt) {
@@ -951,7 +952,8 @@ __global__ __launch_bounds__(kThreads) void gemm_tiled(GemmArgs a, int I, int pa
 // A projection that all rows share, with the rows' adapters: the tile loop over
 // one "expert" whose segment is every row. kGather: rows in the order of a.gather.
 // Bound by MFMA at the clock that the power allows: 8192 x 7168 x 7168 with 16
-// adapters of rank 32 takes 748 us, 1.13 PFLOP/s (a library's plain 8192^3 1.29).
+// adapters of rank 32 takes 798 us, 1.06 PFLOP/s (787 us with v in one bf16 number; a
+// library's plain 8192^3 1.29 PFLOP/s).
 template <bool kGather>
 __global__ __launch_bounds__(kThreads) void adapter_tiled(GemmArgs a, AdaptArgs ad) {
 #if defined(__HIP_DEVICE_COMPILE__)

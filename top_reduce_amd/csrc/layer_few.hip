@@ -14,10 +14,11 @@
 // while the other's products run, with a batch small enough that 12 waves fit a
 // CU. What a CU reads of rows (16 rows of 64 bytes a load) is at most 34 KB/us,
 // from L2 too, so operands beside the weights count: h is stored in the order in
-// which few_down loads it (64 tokens of 8 experts, all chosen: 147 -> 98 us).
+// which few_down loads it (64 tokens of 8 experts, all chosen: 147 -> 100 us).
 //
-// One token, 8 of 32 experts of 7168 x 2048: 81 + 40 us, 5.8 TB/s; 64 tokens, 8 of
-// 256 experts, 32 of them here: 227 + 115 us, 7.2 TB/s.
+// One token, 8 of 32 experts of 7168 x 2048: 83 + 42 us for 708 MB, 5.7 TB/s; 64
+// tokens, 8 of 256 experts, 32 of them here: 237 + 127 us for the 2091 MB of the
+// experts chosen, 5.7 TB/s (a kernel that only reads reaches 6.3).
 //
 // The gate weight is folded into h. bf16: h is kept as two bf16 numbers whose
 // sum has 16 significant bits, and few_down multiplies both, as different columns
@@ -524,9 +525,9 @@ hipError_t launch_few(const FewArgs& a, const SelectArgs* sel, double per_expert
                                                              : a.E + static_cast<int64_t>(a.T) * a.K / 16;
   const int64_t u1 = most * (a.Ip / 16), u2 = cdiv(a.H, a.cols);
   // Tokens for which weights are loaded once, by those that an expert gets on
-  // average (4096 x 2048, 64 tokens; 8 of 8 experts: up 178, 121 and 97 us, down
-  // 229, 174 and 146 us with 16, 32 and 64; 2 of 8: up 71, 56 and 78; 2 of 16 by 48
-  // tokens: up 93, 98 and 122, down 63, 70 and 88)
+  // average (4096 x 2048; up by 16, 32 and 64, down by 8, 16 and 32 tokens: 64
+  // tokens, 8 of 8 experts 178, 122 and 98 us, 176, 124 and 100 us; 2 of 8 71, 58 and
+  // 70, 61, 47 and 48; 48 tokens, 2 of 16 92, 97 and 122, 55, 60 and 81)
   // As many blocks as fit at once.
   const int nq = a.T <= 16 || per_expert <= 8 ? 1 : a.T <= 32 || per_expert <= 32 ? 2 : 4;
   const int b1 = (nq == 4 ? 2 : 3) * cus;

@@ -460,8 +460,8 @@ __global__ __launch_bounds__(kThreads) void adapter_few(ExpandArgs p) {
 // without one last: perm[pos] is the token, sid[pos] its adapter (or -1). The
 // kernels that follow work on positions, so that a group of 16 or 32 has one
 // adapter or two however the requests' tokens are mixed (8192 x 7168 x 7168 with
-// 32 adapters of rank 64 dealt at random took 808 + 1887 us in the tokens' order,
-// and takes 5 + 107 + 834 us so). A window whose tokens already come in runs keeps
+// 32 adapters of rank 64 dealt at random take 826 + 2277 us in the tokens' order,
+// and 5 + 106 + 870 to 910 us so). A window whose tokens already come in runs keeps
 // its order.
 // Counting in LDS: a thread's token takes its place among its adapter's by an
 // atomic add, whose order varies and does not matter, as a row's sums do not
@@ -534,9 +534,10 @@ struct ShrinkArgs {
 
 // v[t, j] = s[a] x[t] . A[a][j] for a group of 16 kNG tokens: 16 kRT rows of A at
 // a time, the waves sharing the reduction, two batches of loads in flight.
-// Bound by x from memory and A from L2: 39 us for 8192 x 7168 and rank 32 (16
-// tokens a group, which read A twice as often, took 58 us, of which 41 us were
-// A's loads alone; x alone takes 25 us). The different adapters among the tokens
+// Bound by x from memory and A from L2: 39 us for 8192 x 7168 and rank 32 with x
+// in the last-level cache, 63 us with x from memory (16 tokens a group, which read A
+// twice as often, took 58 us where this takes 39, of which 41 us were A's loads
+// alone; x alone takes 25 us). The different adapters among the tokens
 // (one where tokens of a request are neighbours) are dealt to kSlots blocks, so
 // that a group at the border of two requests takes no longer than the others. v
 // is kept as the tiles multiply it: fp32, or two bf16 numbers with 16 significant
@@ -550,7 +551,8 @@ constexpr int kShrinkWaves = kShrinkThreads / kWave;
 template <bool kF32, int kRT, int kNG>
 __global__ __launch_bounds__(kShrinkThreads, 3) void adapter_shrink(ShrinkArgs p) {
   typedef typename Elem<kF32>::type E;
-  // 64-byte blocks of a batch (kRT = kNG = 2: 4 spill registers, 42 us; 2: 50 us; 3: 39 us)
+  // 64-byte blocks of a batch (kRT = kNG = 2: by 4, which spill, 42 us; by 2 50 us;
+  // by 3 39 us, in fp32 with three registers spilled)
   constexpr int kB = kRT + kNG == 4 ? 3 : 4;
   __shared__ floatx4 red[kShrinkWaves][kRT][kNG][kWave];
   const int lane = threadIdx.x & 63;
@@ -698,10 +700,11 @@ hipError_t launch_shrink(const ShrinkArgs& s, int64_t passes, hipStream_t st) {
   hipLaunchKernelGGL((adapter_shrink<kF32, kRT, kNG>), grid, dim3(kShrinkThreads), 0, st, s);
   return hipGetLastError();
 }
-// Groups of 16 tokens where their blocks, with some more for the borders of
-// requests, fit the CUs once (1000 x 4096, rank 16: 10 us and not 14; 3600 x 7168,
-// rank 32: 26 and not 32; but 4000 x 4096, rank 16: 19 and not 16). Ranks past 32:
-// a block for every 32 (2048 x 7168, rank 64: 32 us; one block for both 58).
+// Groups of 16 tokens where their blocks fit the CUs once (1000 x 4096, rank 16: 10 us
+// and not 14; 3500 x 7168, rank 32, one request: 25 and not 33, but with eleven borders
+// of requests, whose second blocks share CUs, 41 and not 33; 4000 x 4096, rank 16: 20
+// and not 17). Ranks past 32: a block for every 32 (2048 x 7168, rank 64: 33 us; one
+// block for both 58).
 template <bool kF32>
 hipError_t launch_shrink(const ShrinkArgs& s, hipStream_t st) {
   const int64_t passes = cdiv(s.R, 32);
@@ -991,9 +994,9 @@ __device__ __forceinline__ void tile_unit(const TileArgs& p, int block) {
 
 // Bound by the loop's loads, LDS reads and products together, and with one tile a
 // CU by what nothing covers, its first loads and its stores. bf16: 16384 x 7168 x
-// 256 in two parts 69 us, 0.87 PFLOP/s; 8192 x 7160 x 7000 with adapters 1020 us,
-// 0.80; 1000 x 4096 x 4096 60 us, 0.56. fp32: 1000 x 4096 x 4096 315 us, 107
-// TFLOP/s of the 155 that a large product reaches.
+// 256 in two parts 69 us, 0.87 PFLOP/s; 8192 x 7160 x 7000 with adapters 1040 us,
+// 0.79; 1000 x 4096 x 4096 60 us, 0.56. fp32: 1000 x 4096 x 4096 305 us, 110
+// TFLOP/s of the 155 that a large product reaches; 16384 x 7168 x 256 480 us, 125.
 // kAdapt: the epilogue adds each token's adapter, v B^T, one different adapter
 // of a 16-token group after another, and writes y; otherwise fp32 parts.
 template <bool kF32, typename C, bool kAdapt>
@@ -1312,9 +1315,9 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
     p.Rp = L.Rp;
     const dim3 grid(static_cast<unsigned>(cdiv(d.N, 32 * kWaves)), static_cast<unsigned>(L.n_units),
                     static_cast<unsigned>(chunks));
-    // few parts and ranks: 84 registers a lane, five waves a SIMD, and not 137 and
-    // three (64 x 7168 x 7168, 24 adapters of rank 64: 11 us and not 14.7); more
-    // parts in steps of four take longer (100 x 7168 x 1024: 7.3 us, by eight 6.5)
+    // few parts and ranks: 86 registers a lane, five waves a SIMD, and not 139 and
+    // three (64 x 7168 x 7168, 24 adapters of rank 64: 12.8 us and not 15.6); more
+    // parts in steps of four take longer (100 x 7168 x 1024: 6.8 us, by eight 6.0)
     const bool small = L.parts <= 4 && d.R <= (f32 ? 32 : 64);
     if (f32) return small ? launch_expand<true, 2, 4>(p, grid, st) : launch_expand<true, 4, 8>(p, grid, st);
     return small ? launch_expand<false, 2, 4>(p, grid, st) : launch_expand<false, 4, 8>(p, grid, st);
@@ -1360,8 +1363,8 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
   t.R = d.R;
   t.Rq = L.Rq;
   // the largest tiles of which there is one for each CU: 8192 x 7160 x 7000 takes
-  // 1020 us on the wide ones and 1076 us on the middle ones, 1000 x 5000 x 6001
-  // (376 middle tiles) 122 us on the middle and 168 us on the small ones
+  // 1040 us on the wide ones and 1090 us on the middle ones, 1000 x 5000 x 6001
+  // (376 middle tiles) 111 us on the middle and 165 us on the small ones
   if (cdiv(d.T, WideShape::kM) * cdiv(d.N, WideShape::kN) >= kPlanCus && row_bytes <= (int64_t{1} << 23))
     return f32 ? launch_tile<true, WideShape, true>(t, st) : launch_tile<false, WideShape, true>(t, st);
   if (cdiv(d.T, MidShape::kM) * cdiv(d.N, MidShape::kN) >= kPlanCus)

@@ -181,7 +181,8 @@ hipError_t route_topk(const tr_route_desc& d, const void* x, const void* w_gate,
                         few ? 2 * few->E : 0, st);
   if (e != hipSuccess) return e;
   // registers of logits for the experts there are (16384 tokens of 128 experts by 2
-  // 10.7 us, by 4 12.7; 4096 of 512 by 8 10.4 us, by 16 14.2)
+  // 10.7 us, by 4 12.7; 4096 of 512 by 8 10.4 us, by 16 14.2). Past 1024 experts 64 of
+  // them leave one wave a SIMD: 4096 tokens, 8 of 1025 experts 63 us, 16 of 4096 55 us.
   if (d.G <= 64) return launch_select<1>(a, f, st);
   if (d.G <= 128) return launch_select<2>(a, f, st);
   if (d.G <= 256) return launch_select<4>(a, f, st);
