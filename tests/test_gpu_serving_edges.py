@@ -113,3 +113,39 @@ def check_infinite_adapters(T, H, N, R, A, run, dtype):
 ])
 def test_infinite_adapter_weights_on_tiles(T, H, N, R, A, run, dtype):
     check_infinite_adapters(T, H, N, R, A, run, dtype)
+
+
+# 2^128 - 2^118: a number of fp32 (the largest is 2^128 - 2^104), but 2^128, infinity,
+# once it is rounded to bf16 (the largest is 2^128 - 2^120)
+TOP = 2.0 ** 128 - 2.0 ** 118
+
+
+@pytest.mark.parametrize("T,dtype", [(1, BF), (20, BF), (64, BF), (20, F32)])
+def test_h_between_the_ranges_of_bf16_and_fp32(T, dtype):
+    say(f"h past bf16 T={T} {dtype}")
+    H, I = 64, 40
+    x = torch.ones(T, H, dtype=dtype)
+    w1 = torch.zeros(1, 2 * I, H, dtype=dtype)
+    w1[0, :I, 0], w1[0, :I, 1], w1[0, I:, 2] = 2.0 ** 60, -2.0 ** 50, 2.0 ** 68     # h = TOP
+    w1[0, I // 2:I] *= -1.0       # silu is 0 there
+    w2 = torch.zeros(1, H, I, dtype=dtype)
+    w2[0, :, 3], w2[0, 1::2, 3] = 2.0 ** -120, -2.0 ** -121
+    y, _, w = tr.layer(x.cuda(), torch.zeros(1, H, dtype=dtype).cuda(), w1.cuda(), w2.cuda(), 1)
+    assert w.tolist() == [[1.0]] * T
+    want = (TOP * w2[0, :, 3].double()).to(dtype).expand(T, H)
+    assert torch.equal(y.cpu(), want)
+
+
+@pytest.mark.parametrize("T,N,dtype", [(1, 64, BF), (40, 130, BF), (700, 4096, BF), (4100, 8192, BF), (40, 130, F32)])
+def test_low_rank_products_between_the_ranges_of_bf16_and_fp32(T, N, dtype):
+    say(f"low-rank product past bf16 T={T} N={N} {dtype}")
+    H, R = 128, 8
+    x = torch.zeros(T, H, dtype=dtype)
+    x[:, :3] = 1.0
+    a, b = torch.zeros(1, R, H, dtype=dtype), torch.zeros(1, N, R, dtype=dtype)
+    a[0, 5, 0], a[0, 5, 1], a[0, 5, 2] = 2.0 ** 127, 2.0 ** 126, 2.0 ** 126 - 2.0 ** 118     # their sum: TOP
+    b[0, :, 5], b[0, 1::2, 5] = 2.0 ** -120, -2.0 ** -121
+    y = tr.adapter_linear(x.cuda(), torch.zeros(N, H, dtype=dtype).cuda(), a.cuda(), b.cuda(),
+                          torch.zeros(T, dtype=torch.int32).cuda())
+    want = (TOP * b[0, :, 5].double()).to(dtype).expand(T, N)
+    assert torch.equal(y.cpu(), want)

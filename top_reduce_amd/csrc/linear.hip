@@ -416,12 +416,10 @@ __global__ __launch_bounds__(kThreads) void adapter_few(ExpandArgs p) {
       if constexpr (kF32) {
         v_s[0][k][j] = total;
       } else {
-        const uint32_t hi = cvt_bf16x2(total, 0.0f) & 0xffffu;
-        const float hf = bf16_bits_to_f32(hi);
-        // (the rest of an infinity is 0, not NaN)
+        const uint32_t hi = cvt_bf16x2(first_bf16(total), 0.0f) & 0xffffu;
         v_s[0][k][j] = static_cast<uint16_t>(hi);
-        v_s[1][k][j] = static_cast<uint16_t>(
-            cvt_bf16x2(fabsf(hf) <= 3.3895314e38f ? total - hf : 0.0f, 0.0f) & 0xffffu);
+        v_s[1][k][j] =
+            static_cast<uint16_t>(cvt_bf16x2(second_bf16(total, bf16_bits_to_f32(hi)), 0.0f) & 0xffffu);
       }
     }
     __syncthreads();
@@ -552,7 +550,7 @@ template <bool kF32, int kRT, int kNG>
 __global__ __launch_bounds__(kShrinkThreads, 3) void adapter_shrink(ShrinkArgs p) {
   typedef typename Elem<kF32>::type E;
   // 64-byte blocks of a batch (kRT = kNG = 2: by 4, which spill, 42 us; by 2 50 us;
-  // by 3 39 us, in fp32 with three registers spilled)
+  // by 3 39 us, with one register spilled, three in fp32)
   constexpr int kB = kRT + kNG == 4 ? 3 : 4;
   __shared__ floatx4 red[kShrinkWaves][kRT][kNG][kWave];
   const int lane = threadIdx.x & 63;

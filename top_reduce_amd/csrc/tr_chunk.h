@@ -99,17 +99,23 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-// Four floats as two bf16 numbers each, v = hi + lo with 16 significant bits,
-// packed like cvt_bf16x2. The rest of an infinity, of a number past bf16's range or
-// of a NaN is 0, not NaN.
+// v as two bf16 numbers, hi + lo with 16 significant bits: what is to be rounded to
+// the first one. A number past bf16's range (not past fp32's) has the largest of bf16
+// as its first one, and its rest in the second.
+__device__ __forceinline__ float first_bf16(float v) {
+  constexpr float kMaxBf16 = 3.38953139e38f;
+  return fabsf(v) <= kMaxFloat ? fminf(fmaxf(v, -kMaxBf16), kMaxBf16) : v;
+}
+// The second one, given the first. Of an infinity or a NaN it is 0, not NaN.
+__device__ __forceinline__ float second_bf16(float v, float hi) { return fabsf(hi) <= kMaxFloat ? v - hi : 0.0f; }
+
+// Four floats as two bf16 numbers each, packed like cvt_bf16x2.
 __device__ __forceinline__ void split_bf16(const floatx4& v, uint2& hi, uint2& lo) {
-  hi = uint2{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
-  const float h[4] = {__uint_as_float(hi.x << 16), __uint_as_float(hi.x & 0xffff0000u),
-                      __uint_as_float(hi.y << 16), __uint_as_float(hi.y & 0xffff0000u)};
-  float r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = fabsf(h[i]) <= 3.3895314e38f ? v[i] - h[i] : 0.0f;
-  lo = uint2{cvt_bf16x2(r[0], r[1]), cvt_bf16x2(r[2], r[3])};
+  hi = uint2{cvt_bf16x2(first_bf16(v[0]), first_bf16(v[1])), cvt_bf16x2(first_bf16(v[2]), first_bf16(v[3]))};
+  lo = uint2{cvt_bf16x2(second_bf16(v[0], __uint_as_float(hi.x << 16)),
+                        second_bf16(v[1], __uint_as_float(hi.x & 0xffff0000u))),
+             cvt_bf16x2(second_bf16(v[2], __uint_as_float(hi.y << 16)),
+                        second_bf16(v[3], __uint_as_float(hi.y & 0xffff0000u)))};
 }
 
 // silu(g) * u in fp32. bf16 results take the hardware exponential and
