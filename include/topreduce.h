@@ -403,6 +403,97 @@ tr_status moe_adapter_linear(const tr_adapter_desc* desc, const void* x, const v
                              const float* scales, void* y, void* ws, size_t ws_bytes,
                              hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Rows and weights in 8 and 4 bits: norm, experts' products, projections (serving).
+ *
+ * A row of K numbers (K a multiple of 32) in blocks of 32: K elements of 8 bits
+ * (e4m3, no infinities) or 4 bits (e2m1, the number at an even k in the low half of
+ * its byte), and K / 32 scale bytes (e8m0: b stands for 2^(b - 127), 255 for NaN). A
+ * number is element times scale. Elements and scales are two dense arrays.
+ * Quantization: the scale is the smallest power of two, 2^-127 at least, that brings
+ * the block's largest magnitude to 448 (4 bits: 6) or below; elements are rounded to
+ * nearest, ties to even. A number that is not finite becomes a NaN element and has no
+ * part in the scale; in 4 bits, which have no NaN, it makes its block's scale NaN.
+ * ------------------------------------------------------------------------ */
+
+/* x, a [rows, K] matrix of dtype, as q [rows, K * bits / 8] and s [rows, K / 32]; bits 8
+ * or 4, rows * K < 2^40. */
+tr_status moe_quantize_mx(int64_t rows, int64_t K, tr_dtype dtype, int32_t bits, const void* x, void* q,
+                          void* s, hipStream_t stream);
+
+typedef struct tr_norm_desc {
+    int64_t T;             /* rows, >= 0, < 2^31 */
+    int64_t H;             /* hidden size, a multiple of 8 (with q: of 32), at most 2^22 */
+    int32_t dtype;         /* tr_dtype of x, residual, weight and y */
+    float eps;             /* finite, >= 0 */
+} tr_norm_desc;
+
+/* Root-mean-square norm with the residual's addition:
+ *   z = x + residual, y = z / sqrt(mean(z^2) + eps) * weight, residual_out = z
+ * in fp32; y and residual_out are rounded once to dtype, q and s are y (as it is in
+ * fp32) in 8 bits. z is normalized as it is before its own rounding. residual may be
+ * NULL (z = x, and residual_out may then be NULL or receive x); y may be NULL where q
+ * is not, q and s together NULL where y is not. residual_out may be NULL. x, residual,
+ * y, residual_out: device [T, H]; weight: device [H]; q: device [T, H] bytes; s: device
+ * [T, H / 32] bytes. y and residual_out may be x or residual themselves; no other
+ * overlap. */
+tr_status moe_rms_norm(const tr_norm_desc* desc, const void* x, const void* residual, const void* weight,
+                       void* y, void* residual_out, void* q, void* s, hipStream_t stream);
+
+typedef struct tr_expert_desc {
+    int64_t T;             /* rows of x, >= 0, < 2^31 (>= 1 where R > 0) */
+    int64_t R;             /* rows of the result, >= 0, < 2^31 */
+    int64_t K;             /* reduction length, a multiple of 32, at most 2^22 */
+    int64_t N;             /* rows of an expert's weights; N * K < 2^31 */
+    int32_t E;             /* experts, 1..1024 */
+    int32_t bits;          /* of the weights: 8 or 4 */
+    int32_t swiglu;        /* 1: rows [0, N/2) of w gate, the others up; result silu(g) u */
+    int32_t out;           /* 0: y is bf16; 1: y is in 8 bits with scales (outputs a row a
+                              multiple of 32) */
+} tr_expert_desc;
+
+/* Products grouped by expert: for rows r of segment e, offsets[e] <= r < offsets[e + 1],
+ *   y[r][n] = sum over k of x[rows[r]][k] w[e][n][k]
+ * or, with swiglu, silu of that times the same of n + N/2 (N/2 outputs). Sums are fp32;
+ * y is rounded once. Rows of an expert with more than 64 are multiplied by the matrix
+ * instructions for such blocks, which add products in groups of eight and drop what is
+ * 2^-13 below a group's largest (about 2e-5 of the result, a hundredth of its rounding to
+ * bf16); with fewer rows every product counts in full. x: device [T, K] in 8 bits, xs its
+ * scales; w: device [E, N, K], ws its scales; offsets: device int32 [E + 1], ascending,
+ * those below 0 or past R taken as 0 and R (the plan's offsets); rows: device int32 [R],
+ * or NULL for r itself, which needs T >= R (the plan's row_src); entries outside [0, T)
+ * are taken as the nearest row; y: device [R, N or N/2]; ys: its scales where out is 1,
+ * else NULL. Rows outside every segment are left as they are. y and ys must not overlap
+ * x or xs. */
+tr_status moe_expert_linear(const tr_expert_desc* desc, const void* x, const void* xs, const void* w,
+                            const void* ws, const int32_t* offsets, const int32_t* rows, void* y, void* ys,
+                            hipStream_t stream);
+
+typedef struct tr_linear4_desc {
+    int64_t T;             /* rows, >= 0, < 2^31 */
+    int64_t K;             /* reduction length, a multiple of 32, at most 2^22 */
+    int64_t N;             /* outputs, 1..2^22 */
+    int32_t dtype;         /* tr_dtype of x and y */
+    int32_t reserved;      /* 0 */
+} tr_linear4_desc;
+
+/* y[t][n] = sum over k of x[t][k] w[n][k], weights in 4 bits. x: device [T, K] of dtype;
+ * w: device [N, K / 2] bytes; ws: device [N, K / 32] bytes; y: device [T, N], must not
+ * overlap x. Sums are fp32, y is rounded once. For few rows (the weights are read once
+ * for every 64). */
+tr_status moe_linear_mx4(const tr_linear4_desc* desc, const void* x, const void* w, const void* ws, void* y,
+                         hipStream_t stream);
+
+/* The whole layer of a plan, as moe_forward, with rows and weights in 8 bits (or weights
+ * in 4): moe_expert_linear with swiglu over the plan's segments, its result in 8 bits in
+ * the plan's h; moe_expert_linear into the plan's O; moe_combine_reduce. plan: of dtype
+ * TR_BF16, H and I multiples of 32. x: device [T, H] in 8 bits, xs its scales; w1: device
+ * [E, 2I, H], w2: device [E, H, I], of bits, and their scales; topk_weights, y: as
+ * moe_forward (y may not overlap x). */
+tr_status moe_forward_mx(const tr_moe_plan* plan, const void* x, const void* xs, const float* topk_weights,
+                         int32_t bits, const void* w1, const void* w1s, const void* w2, const void* w2s,
+                         void* y, hipStream_t stream);
+
 /* Copies stats to host_out[4] = {R, rows with a local route, ignored slots,
  * empty experts} and synchronises `stream` (opt-in host sync, the counterpart
  * of dispatch's do_cpu_sync in DeepEP issue #760's repro). */

@@ -1,0 +1,60 @@
+"""linear_mx4 against its formula in 64 bits."""
+
+import pytest
+import torch
+
+import top_reduce_amd as tr
+from tests import _close as C
+from tests import _mx as M
+from tests import _serving as S
+from tests._gpu import say
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def case(T, K, N, dtype):
+    g = torch.Generator().manual_seed(T + K + N)
+    x = S.inputs(g, T, K, dtype=dtype)
+    w = M.quantize(torch.randn(N, K, generator=g, dtype=torch.float64) * K ** -0.5, 4)
+    return x, w
+
+
+@pytest.mark.parametrize("T,K,N", [
+    (1, 32, 1), (1, 7168, 256), (2, 96, 33), (3, 1440, 1001), (15, 160, 64), (16, 512, 500), (17, 2880, 66),
+    (33, 1056, 129), (64, 1024, 256), (65, 256, 48), (130, 4096, 40), (1, 4128, 300), (7, 128, 4), (5, 640, 2),
+    (500, 352, 70),
+])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_linear(T, K, N, dtype):
+    say(f"linear4 T={T} K={K} N={N} {dtype}")
+    x, w = case(T, K, N, dtype)
+    y = tr.linear_mx4(x.cuda(), (w[0].cuda(), w[1].cuda()))
+    xv, wv = S.f64(x), M.value(*w)
+    want = xv @ wv.t()
+    S.check(y, want, S.U[dtype] * want.abs() + (K + 64) * S.EPS * (xv.abs() @ wv.abs().t()), "y")
+    if N >= 32:
+        C.check(y, want, K, dtype, "y", bits16=False)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [1, 9, 70])
+def test_rows_stand_alone(T, dtype):
+    x, w = case(T, 256, 96, dtype)
+    w = (w[0].cuda(), w[1].cuda())
+    clean = tr.linear_mx4(x.cuda(), w)
+    bad = x.clone()
+    bad[T // 2, 200] = float("nan")
+    got = tr.linear_mx4(bad.cuda(), w)
+    keep = torch.arange(T) != T // 2
+    assert torch.isnan(got[T // 2]).all() and torch.equal(got[keep.cuda()], clean[keep.cuda()])
+    s = w[1].view(torch.uint8).clone()
+    s[50, 2] = 255
+    got = tr.linear_mx4(x.cuda(), (w[0], s.view(M.E8M0)))
+    keep = torch.arange(96, device="cuda") != 50
+    assert torch.isnan(got[:, 50]).all() and torch.equal(got[:, keep], clean[:, keep])
+
+
+def test_no_rows():
+    _, w = case(1, 64, 32, BF)
+    assert tr.linear_mx4(torch.empty(0, 64, dtype=BF, device="cuda"), (w[0].cuda(), w[1].cuda())).shape == (0, 32)

@@ -22,6 +22,11 @@ Before and beside the expert path: ``route_topk`` (the router: logits, top-k,
 gate weights), ``layer`` (the whole layer from hidden rows, router included)
 and ``adapter_linear`` (a projection all rows share, with a low-rank adapter
 of each row's request), each with its ``*_workspace_size``.
+
+In 8 and 4 bits (blocks of 32 numbers with a power of two as scale): ``rms_norm`` (the
+residual's addition and the norm, its result in the rows' type, in 8 bits, or both),
+``quantize_mx``, ``expert_linear`` (products grouped by expert over ragged segments),
+``forward_mx`` (the plan's whole layer) and ``linear_mx4`` (few rows, weights in 4 bits).
 """
 
 from ._binding import (  # noqa: F401
@@ -58,4 +63,13 @@ from ._binding import (  # noqa: F401
     route_topk,
     route_workspace_size,
     workspace_size,
+)
+
+from ._mx import (  # noqa: F401
+    Normed,
+    expert_linear,
+    forward_mx,
+    linear_mx4,
+    quantize_mx,
+    rms_norm,
 )

@@ -70,6 +70,20 @@ class AdapterDesc(C.Structure):
                 ("A", C.c_int32), ("dtype", C.c_int32), ("reserved", C.c_int32)]
 
 
+class NormDesc(C.Structure):
+    _fields_ = [("T", C.c_int64), ("H", C.c_int64), ("dtype", C.c_int32), ("eps", C.c_float)]
+
+
+class ExpertDesc(C.Structure):
+    _fields_ = [("T", C.c_int64), ("R", C.c_int64), ("K", C.c_int64), ("N", C.c_int64),
+                ("E", C.c_int32), ("bits", C.c_int32), ("swiglu", C.c_int32), ("out", C.c_int32)]
+
+
+class Linear4Desc(C.Structure):
+    _fields_ = [("T", C.c_int64), ("K", C.c_int64), ("N", C.c_int64), ("dtype", C.c_int32),
+                ("reserved", C.c_int32)]
+
+
 _lib = None
 
 
@@ -137,6 +151,17 @@ def load_library():
     lib.moe_adapter_linear.restype = st
     lib.moe_adapter_linear.argtypes = [C.POINTER(AdapterDesc), vp, vp, vp, vp, vp, vp, vp, vp,
                                        C.c_size_t, vp]
+    i64, i32 = C.c_int64, C.c_int32
+    lib.moe_quantize_mx.restype = st
+    lib.moe_quantize_mx.argtypes = [i64, i64, i32, i32, vp, vp, vp, vp]
+    lib.moe_rms_norm.restype = st
+    lib.moe_rms_norm.argtypes = [C.POINTER(NormDesc), vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.moe_expert_linear.restype = st
+    lib.moe_expert_linear.argtypes = [C.POINTER(ExpertDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.moe_linear_mx4.restype = st
+    lib.moe_linear_mx4.argtypes = [C.POINTER(Linear4Desc), vp, vp, vp, vp, vp]
+    lib.moe_forward_mx.restype = st
+    lib.moe_forward_mx.argtypes = [C.POINTER(PlanStruct), vp, vp, vp, i32, vp, vp, vp, vp, vp, vp]
     lib.moe_plan_stats.restype = st
     lib.moe_plan_stats.argtypes = [C.POINTER(PlanStruct), C.POINTER(C.c_int32), vp]
     lib.moe_last_error.restype = C.c_char_p

@@ -684,6 +684,179 @@ tr_status moe_adapter_linear(const tr_adapter_desc* desc, const void* x, const v
                     "moe_adapter_linear launch");
 }
 
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Rows and weights in 8 and 4 bits: norm, experts' products, projections
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int64_t kMostRows = (int64_t{1} << 31) - 1;
+
+// Whether [a, a + na) and [b, b + nb) have a byte in common (neither NULL).
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return a && b && p < q + static_cast<uintptr_t>(nb) && q < p + static_cast<uintptr_t>(na);
+}
+
+tr_status check_k(int64_t K, const char* name) {
+  if (K < 1) return fail(TR_EINVAL, "%s must be >= 1 (got %lld)", name, (long long)K);
+  if (K % 32 || K > (int64_t{1} << 22))
+    return fail(TR_EUNSUPPORTED, "%s must be a multiple of 32, at most 2^22 (got %lld)", name, (long long)K);
+  return TR_OK;
+}
+
+tr_status check_expert_desc(const tr_expert_desc* d) {
+  if (!d) return fail(TR_EINVAL, "desc is NULL");
+  if (d->T < 0 || d->R < 0) return fail(TR_EINVAL, "T and R must be >= 0");
+  if (d->N < 1) return fail(TR_EINVAL, "N must be >= 1 (got %lld)", (long long)d->N);
+  if (d->E < 1 || d->E > tr::kMaxE) return fail(TR_EINVAL, "E must be in [1, %d] (got %d)", tr::kMaxE, d->E);
+  if (d->bits != 8 && d->bits != 4) return fail(TR_EINVAL, "bits must be 8 or 4 (got %d)", d->bits);
+  if (d->swiglu != 0 && d->swiglu != 1) return fail(TR_EINVAL, "swiglu must be 0 or 1");
+  if (d->out != 0 && d->out != 1) return fail(TR_EINVAL, "out must be 0 or 1");
+  if (d->swiglu && d->N % 2) return fail(TR_EINVAL, "swiglu needs an even N (got %lld)", (long long)d->N);
+  const tr_status s = check_k(d->K, "K");
+  if (s != TR_OK) return s;
+  const int64_t No = d->swiglu ? d->N / 2 : d->N;
+  if (d->out == 1 && No % 32)
+    return fail(TR_EUNSUPPORTED, "rows of %lld outputs have no whole blocks of 32", (long long)No);
+  if (d->N > kMostRows / d->K) return fail(TR_EUNSUPPORTED, "N * K must be < 2^31");
+  if (d->T > kMostRows || d->R > kMostRows) return fail(TR_EUNSUPPORTED, "T and R must be < 2^31");
+  if (d->R > 0 && d->T < 1) return fail(TR_EINVAL, "R rows need a row of x");
+  return TR_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+tr_status moe_quantize_mx(int64_t rows, int64_t K, tr_dtype dtype, int32_t bits, const void* x, void* q,
+                          void* s, hipStream_t stream) {
+  if (rows < 0) return fail(TR_EINVAL, "rows must be >= 0 (got %lld)", (long long)rows);
+  if (dtype != TR_BF16 && dtype != TR_F32) return fail(TR_EINVAL, "unknown dtype %d", (int)dtype);
+  if (bits != 8 && bits != 4) return fail(TR_EINVAL, "bits must be 8 or 4 (got %d)", bits);
+  tr_status e = check_k(K, "K");
+  if (e != TR_OK) return e;
+  if (rows >= (int64_t{1} << 40) / K) return fail(TR_EUNSUPPORTED, "rows * K must be < 2^40");
+  if (rows == 0) return ok();
+  if ((e = check_buf(x, "x", true)) != TR_OK) return e;
+  if ((e = check_buf(q, "q", true)) != TR_OK) return e;
+  if (!s) return fail(TR_EINVAL, "s is NULL");
+  const int64_t n = rows * K, xb = n * (dtype == TR_BF16 ? 2 : 4);
+  if (overlap(x, xb, q, n * bits / 8) || overlap(x, xb, s, n / 32))
+    return fail(TR_EINVAL, "q and s must not overlap x");
+  return hip_status(tr::quantize_mx(rows, K, dtype == TR_F32, bits, x, q, s, stream), "moe_quantize_mx launch");
+}
+
+tr_status moe_rms_norm(const tr_norm_desc* desc, const void* x, const void* residual, const void* weight,
+                       void* y, void* residual_out, void* q, void* s, hipStream_t stream) {
+  if (!desc) return fail(TR_EINVAL, "desc is NULL");
+  const tr_norm_desc& d = *desc;
+  if (d.T < 0) return fail(TR_EINVAL, "T must be >= 0 (got %lld)", (long long)d.T);
+  if (d.H < 1) return fail(TR_EINVAL, "H must be >= 1 (got %lld)", (long long)d.H);
+  if (d.dtype != TR_BF16 && d.dtype != TR_F32) return fail(TR_EINVAL, "unknown dtype %d", d.dtype);
+  if (!(d.eps >= 0.0f && d.eps <= 3.4e38f)) return fail(TR_EINVAL, "eps must be finite and >= 0");
+  if (d.T > kMostRows) return fail(TR_EUNSUPPORTED, "T must be < 2^31");
+  if (d.H % 8 || d.H > (int64_t{1} << 22))
+    return fail(TR_EUNSUPPORTED, "H must be a multiple of 8, at most 2^22 (got %lld)", (long long)d.H);
+  if ((q != nullptr) != (s != nullptr)) return fail(TR_EINVAL, "q and s go together");
+  if (q && d.H % 32) return fail(TR_EUNSUPPORTED, "H must be a multiple of 32 for 8 bits (got %lld)", (long long)d.H);
+  if (d.T == 0) return ok();
+  if (!y && !q) return fail(TR_EINVAL, "y and q are both NULL");
+  tr_status e;
+  if ((e = check_buf(x, "x", true)) != TR_OK) return e;
+  if ((e = check_buf(weight, "weight", true)) != TR_OK) return e;
+  if ((e = check_buf(residual, "residual", residual != nullptr)) != TR_OK) return e;
+  if ((e = check_buf(y, "y", y != nullptr)) != TR_OK) return e;
+  if ((e = check_buf(residual_out, "residual_out", residual_out != nullptr)) != TR_OK) return e;
+  if ((e = check_buf(q, "q", q != nullptr)) != TR_OK) return e;
+  const int64_t n = d.T * d.H, b = n * (d.dtype == TR_BF16 ? 2 : 4);
+  const void* in[2] = {x, residual};
+  for (const void* p : in) {
+    if ((y != p && overlap(y, b, p, b)) || (residual_out != p && overlap(residual_out, b, p, b)) ||
+        overlap(q, n, p, b) || overlap(s, n / 32, p, b))
+      return fail(TR_EINVAL, "an output overlaps x or residual without being it");
+  }
+  if (overlap(y, b, residual_out, b)) return fail(TR_EINVAL, "y and residual_out overlap");
+  return hip_status(tr::rms_norm(d, x, residual, weight, y, residual_out, q, s, stream), "moe_rms_norm launch");
+}
+
+tr_status moe_expert_linear(const tr_expert_desc* desc, const void* x, const void* xs, const void* w,
+                            const void* ws, const int32_t* offsets, const int32_t* rows, void* y, void* ys,
+                            hipStream_t stream) {
+  tr_status e = check_expert_desc(desc);
+  if (e != TR_OK) return e;
+  const tr_expert_desc& d = *desc;
+  if (!rows && d.T < d.R) return fail(TR_EINVAL, "without rows T must be at least R");
+  if (d.R == 0) return ok();
+  if ((e = check_buf(x, "x", true)) != TR_OK) return e;
+  if ((e = check_buf(w, "w", true)) != TR_OK) return e;
+  if ((e = check_buf(y, "y", true)) != TR_OK) return e;
+  if (!xs || !ws) return fail(TR_EINVAL, "xs and ws must be non-NULL");
+  if (!offsets || !aligned(offsets, 4)) return fail(TR_EINVAL, "offsets must be non-NULL and 4-byte aligned");
+  if (rows && !aligned(rows, 4)) return fail(TR_EINVAL, "rows misaligned");
+  if ((d.out == 1) != (ys != nullptr)) return fail(TR_EINVAL, "ys goes with out 1");
+  const int64_t No = d.swiglu ? d.N / 2 : d.N;
+  const int64_t yb = d.R * No * (d.out ? 1 : 2);
+  if (overlap(y, yb, x, d.T * d.K) || overlap(y, yb, xs, d.T * d.K / 32) ||
+      overlap(ys, d.R * No / 32, x, d.T * d.K) || overlap(ys, d.R * No / 32, xs, d.T * d.K / 32))
+    return fail(TR_EINVAL, "y and ys must not overlap x or xs");
+  return hip_status(tr::expert_few(d, x, xs, w, ws, offsets, rows, y, ys, 0x7fffffff, stream),
+                    "moe_expert_linear launch");
+}
+
+tr_status moe_linear_mx4(const tr_linear4_desc* desc, const void* x, const void* w, const void* ws, void* y,
+                         hipStream_t stream) {
+  if (!desc) return fail(TR_EINVAL, "desc is NULL");
+  const tr_linear4_desc& d = *desc;
+  if (d.T < 0) return fail(TR_EINVAL, "T must be >= 0 (got %lld)", (long long)d.T);
+  if (d.N < 1) return fail(TR_EINVAL, "N must be >= 1 (got %lld)", (long long)d.N);
+  if (d.dtype != TR_BF16 && d.dtype != TR_F32) return fail(TR_EINVAL, "unknown dtype %d", d.dtype);
+  if (d.reserved != 0) return fail(TR_EINVAL, "reserved must be 0");
+  tr_status e = check_k(d.K, "K");
+  if (e != TR_OK) return e;
+  if (d.N > (int64_t{1} << 22)) return fail(TR_EUNSUPPORTED, "N must be at most 2^22");
+  if (d.T > kMostRows) return fail(TR_EUNSUPPORTED, "T must be < 2^31");
+  if (d.T == 0) return ok();
+  if ((e = check_buf(x, "x", true)) != TR_OK) return e;
+  if ((e = check_buf(w, "w", true)) != TR_OK) return e;
+  if ((e = check_buf(y, "y", true)) != TR_OK) return e;
+  if (!ws) return fail(TR_EINVAL, "ws is NULL");
+  const int64_t es = d.dtype == TR_BF16 ? 2 : 4;
+  if (overlap(y, es * d.T * d.N, x, es * d.T * d.K)) return fail(TR_EINVAL, "y must not overlap x");
+  return hip_status(tr::linear_mx4(d, x, w, ws, y, stream), "moe_linear_mx4 launch");
+}
+
+tr_status moe_forward_mx(const tr_moe_plan* plan, const void* x, const void* xs, const float* topk_weights,
+                         int32_t bits, const void* w1, const void* w1s, const void* w2, const void* w2s,
+                         void* y, hipStream_t stream) {
+  tr_status e = check_plan(plan);
+  if (e != TR_OK) return e;
+  const tr_moe_desc& d = plan->d;
+  if (d.dtype != TR_BF16) return fail(TR_EUNSUPPORTED, "moe_forward_mx needs a plan of TR_BF16");
+  if (d.I % 32) return fail(TR_EUNSUPPORTED, "I must be a multiple of 32 (got %lld)", (long long)d.I);
+  const tr_expert_desc gate_up{d.T, plan->R_cap, d.H, 2 * d.I, d.E, bits, 1, 1};
+  const tr_expert_desc down{plan->R_cap, plan->R_cap, d.I, d.H, d.E, bits, 0, 0};
+  if ((e = check_expert_desc(&gate_up)) != TR_OK) return e;
+  if ((e = check_expert_desc(&down)) != TR_OK) return e;
+  if (d.T == 0) return ok();
+  if ((e = check_buf(y, "y", true)) != TR_OK) return e;
+  if (topk_weights && !aligned(topk_weights, 4)) return fail(TR_EINVAL, "topk_weights misaligned");
+  if (overlap(y, d.T * d.H * 2, x, d.T * d.H) || overlap(y, d.T * d.H * 2, xs, d.T * d.H / 32))
+    return fail(TR_EINVAL, "y must not overlap x or xs");
+  // h: R_cap rows of I bytes, then their scales (the plan holds two bytes a number)
+  char* h = static_cast<char*>(plan->h);
+  char* hs = h + up(static_cast<size_t>(plan->R_cap) * d.I);
+  if ((e = moe_expert_linear(&gate_up, x, xs, w1, w1s, plan->offsets, plan->row_src, h, hs, stream)) != TR_OK) return e;
+  if ((e = moe_expert_linear(&down, h, hs, w2, w2s, plan->offsets, nullptr, plan->O, nullptr, stream)) != TR_OK)
+    return e;
+  return moe_combine_reduce(plan, nullptr, topk_weights, y, stream);
+}
+
+}  // extern "C"
+
+extern "C" {
+
 tr_status moe_plan_stats(const tr_moe_plan* plan, int32_t* host_out, hipStream_t stream) {
   tr_status s = check_plan(plan);
   if (s != TR_OK) return s;

@@ -118,4 +118,16 @@ hipError_t adapter_linear(const tr_adapter_desc& d, const void* x, const void* w
                           const void* b, const int32_t* ids, const float* scales, void* y, void* ws,
                           hipStream_t st);
 
+// --- rows and weights in 8 and 4 bits (tr_mx.h) ------------------------------
+// residual and residual_out, y, q and s: NULL where there is none.
+hipError_t rms_norm(const tr_norm_desc& d, const void* x, const void* residual, const void* weight, void* y,
+                    void* residual_out, void* q, void* s, hipStream_t st);
+hipError_t quantize_mx(int64_t rows, int64_t K, bool f32, int bits, const void* x, void* q, void* s,
+                       hipStream_t st);
+// Experts with 1 to `most` rows.
+hipError_t expert_few(const tr_expert_desc& d, const void* x, const void* xs, const void* w, const void* ws,
+                      const int* offsets, const int* rows, void* y, void* ys, int most, hipStream_t st);
+hipError_t linear_mx4(const tr_linear4_desc& d, const void* x, const void* w, const void* ws, void* y,
+                      hipStream_t st);
+
 }  // namespace tr

@@ -1,0 +1,69 @@
+// Numbers in blocks of 32 with a scale each (gfx950, wave64).
+//
+// A row of K numbers (K a multiple of 32) is K elements of 8 bits (e4m3: 4 bits of
+// exponent, 3 of mantissa, no infinities) or 4 (e2m1: 0, 1/2, 1, 3/2, 2, 3, 4, 6 and a
+// sign; the number at an even k in the low half of its byte), and K / 32 scale bytes
+// (e8m0: byte b is 2^(b - 127), 255 is NaN). The scale of a block is the smallest power
+// of two, 2^-127 at least, that brings its largest magnitude to 448 (6) or below, so no
+// element saturates; elements are rounded to nearest, ties to even. In 8 bits an element
+// that is not finite is NaN and has no part in the scale; in 4 bits, which have no NaN,
+// it makes its block's scale NaN.
+#pragma once
+
+#include "tr_chunk.h"
+
+namespace tr {
+
+constexpr int kMxBlock = 32;
+
+// The scale byte of a block whose largest finite magnitude is `top`: the exponent of
+// top, less that of 448 = 1.75 2^8 (6 = 1.5 2^2), and one more where top's mantissa is
+// past 1.75 (1.5), by a carry out of the mantissa.
+template <int kBits>
+__device__ __forceinline__ int mx_scale_byte(float top) {
+  const int u = static_cast<int>(__float_as_uint(top));
+  const int b = kBits == 8 ? ((u + 0x1fffff) >> 23) - 8 : ((u + 0x3fffff) >> 23) - 2;
+  return max(b, 0);
+}
+
+// 2^-(b - 127) of a scale byte that mx_scale_byte gives (at most 253).
+__device__ __forceinline__ float mx_inverse(int b) { return __uint_as_float(static_cast<uint32_t>(254 - b) << 23); }
+
+// |v|, 0 where v is not finite.
+__device__ __forceinline__ float mx_magnitude(float v) {
+  const float a = fabsf(v);
+  return a <= kMaxFloat ? a : 0.0f;
+}
+
+// Four floats, already scaled, as four bytes of e4m3.
+__device__ __forceinline__ uint32_t mx_pack8(float a, float b, float c, float d) {
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true));
+}
+
+// The float that scales a block's elements, for the conversions: their scale operand
+// is an fp32 number of which the exponent counts, 2^-127 being a subnormal one.
+__device__ __forceinline__ float mx_scale(uint32_t byte) {
+  return __uint_as_float(max(byte << 23, 0x00400000u));
+}
+
+typedef float floatx2 __attribute__((ext_vector_type(2)));
+
+// Elements 2 i, 2 i + 1 of a dword of e2m1 (i < 4) or e4m3 (i < 2), scaled, as two bf16
+// (exact: at most 4 significant bits) or two floats.
+template <int kBits, int kI>
+__device__ __forceinline__ uint32_t mx_pair_bf16(uint32_t v, float scale) {
+  if constexpr (kBits == 4)
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, scale, kI));
+  else
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, scale, kI != 0));
+}
+template <int kBits, int kI>
+__device__ __forceinline__ floatx2 mx_pair_f32(uint32_t v, float scale) {
+  if constexpr (kBits == 4)
+    return __builtin_bit_cast(floatx2, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(v, scale, kI));
+  else
+    return __builtin_bit_cast(floatx2, __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(v, scale, kI != 0));
+}
+
+}  // namespace tr
