@@ -801,8 +801,11 @@ tr_status moe_expert_linear(const tr_expert_desc* desc, const void* x, const voi
   if (overlap(y, yb, x, d.T * d.K) || overlap(y, yb, xs, d.T * d.K / 32) ||
       overlap(ys, d.R * No / 32, x, d.T * d.K) || overlap(ys, d.R * No / 32, xs, d.T * d.K / 32))
     return fail(TR_EINVAL, "y and ys must not overlap x or xs");
-  return hip_status(tr::expert_few(d, x, xs, w, ws, offsets, rows, y, ys, 0x7fffffff, stream),
-                    "moe_expert_linear launch");
+  const bool tiles = tr::expert_can_tile(d, rows != nullptr);
+  hipError_t h = tr::expert_few(d, x, xs, w, ws, offsets, rows, y, ys, tiles ? tr::kMxFewRows : 0x7fffffff, stream);
+  if (h == hipSuccess && tiles && d.R > tr::kMxFewRows)
+    h = tr::expert_tiles(d, x, xs, w, ws, offsets, rows, y, ys, tr::kMxFewRows + 1, stream);
+  return hip_status(h, "moe_expert_linear launch");
 }
 
 tr_status moe_linear_mx4(const tr_linear4_desc* desc, const void* x, const void* w, const void* ws, void* y,
