@@ -440,6 +440,13 @@ typedef struct tr_norm_desc {
 tr_status moe_rms_norm(const tr_norm_desc* desc, const void* x, const void* residual, const void* weight,
                        void* y, void* residual_out, void* q, void* s, hipStream_t stream);
 
+/* Kernel of moe_expert_linear. AUTO goes by the sizes; the others are for testing, and
+ * TR_EUNSUPPORTED where the sizes do not fit: ROWS multiplies in bf16 and takes any size,
+ * the TILEs (32, 64 and 256 rows) take K of 256 and more. */
+typedef enum {
+    TR_EXPERT_AUTO = 0, TR_EXPERT_ROWS = 1, TR_EXPERT_TILE32 = 2, TR_EXPERT_TILE64 = 3, TR_EXPERT_TILE256 = 4
+} tr_expert_kernel;
+
 typedef struct tr_expert_desc {
     int64_t T;             /* rows of x, >= 0, < 2^31 (>= 1 where R > 0) */
     int64_t R;             /* rows of the result, >= 0, < 2^31 */
@@ -450,21 +457,23 @@ typedef struct tr_expert_desc {
     int32_t swiglu;        /* 1: rows [0, N/2) of w gate, the others up; result silu(g) u */
     int32_t out;           /* 0: y is bf16; 1: y is in 8 bits with scales (outputs a row a
                               multiple of 32) */
+    int32_t kernel;        /* tr_expert_kernel */
+    int32_t reserved;      /* 0 */
 } tr_expert_desc;
 
 /* Products grouped by expert: for rows r of segment e, offsets[e] <= r < offsets[e + 1],
  *   y[r][n] = sum over k of x[rows[r]][k] w[e][n][k]
  * or, with swiglu, silu of that times the same of n + N/2 (N/2 outputs). Sums are fp32;
- * y is rounded once. Rows of an expert with more than 64 are multiplied by the matrix
- * instructions for such blocks, which add products in groups of eight and drop what is
- * 2^-13 below a group's largest (about 2e-5 of the result, a hundredth of its rounding to
- * bf16); with fewer rows every product counts in full. x: device [T, K] in 8 bits, xs its
- * scales; w: device [E, N, K], ws its scales; offsets: device int32 [E + 1], ascending,
- * those below 0 or past R taken as 0 and R (the plan's offsets); rows: device int32 [R],
- * or NULL for r itself, which needs T >= R (the plan's row_src); entries outside [0, T)
- * are taken as the nearest row; y: device [R, N or N/2]; ys: its scales where out is 1,
- * else NULL. Rows outside every segment are left as they are. y and ys must not overlap
- * x or xs. */
+ * y is rounded once. The tiles multiply by the matrix instructions for such blocks, which
+ * add products in groups of eight and drop what is 2^-13 below a group's largest (about
+ * 2e-5 of the result, a hundredth of its rounding to bf16); the kernel for few rows (ROWS)
+ * counts every product in full. A row's result does not hang on the other rows, but for
+ * that choice. x: device [T, K] in 8 bits, xs its scales; w: device [E, N, K], ws its
+ * scales; offsets: device int32 [E + 1], ascending, those below 0 or past R taken as 0 and
+ * R (the plan's offsets); rows: device int32 [R], or NULL for r itself, which needs T >= R
+ * (the plan's row_src); entries outside [0, T) are taken as the nearest row; y: device
+ * [R, N or N/2]; ys: its scales where out is 1, else NULL. Rows outside every segment are
+ * left as they are. y and ys must not overlap x or xs. */
 tr_status moe_expert_linear(const tr_expert_desc* desc, const void* x, const void* xs, const void* w,
                             const void* ws, const int32_t* offsets, const int32_t* rows, void* y, void* ys,
                             hipStream_t stream);

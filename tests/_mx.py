@@ -85,7 +85,7 @@ def rms_norm(x, weight, eps, residual=None):
 def products(x, w, offsets, rows=None, swiglu=False, tiled=0.0):
     """(y, bound before rounding) in 64 bits of the rows in the segments; x [T, K] and
     w [E, N, K] in 64 bits. tiled: what a matrix instruction drops, relative to the sum of
-    the products' magnitudes, for segments of more than 64 rows."""
+    the products' magnitudes."""
     offsets = offsets.tolist()
     R = x.shape[0] if rows is None else rows.shape[0]
     K, N = x.shape[1], w.shape[1]
@@ -101,8 +101,7 @@ def products(x, w, offsets, rows=None, swiglu=False, tiled=0.0):
             continue
         inside[a:b] = True
         p = x[a:b] @ w[e].t()
-        d = (K + 64) * EPS + (tiled if b - a > 64 else 0.0)
-        d = d * (x[a:b].abs() @ w[e].abs().t())
+        d = ((K + 64) * EPS + tiled) * (x[a:b].abs() @ w[e].abs().t())
         if swiglu:
             g, u, dg, du = p[:, :outs], p[:, outs:], d[:, :outs], d[:, outs:]
             s = g * torch.sigmoid(g)

@@ -86,7 +86,8 @@ def test_expert_refusals():
                       (dict(T=0), -1), (dict(K=0), -1), (dict(K=40), -2), (dict(K=(1 << 22) + 32), -2),
                       (dict(N=0), -1), (dict(N=127), -1), (dict(N=96), -2), (dict(N=100, swiglu=0), -2),
                       (dict(N=1 << 26), -2), (dict(E=0), -1), (dict(E=1025), -1), (dict(bits=6), -1),
-                      (dict(swiglu=2), -1), (dict(out=2), -1)):
+                      (dict(swiglu=2), -1), (dict(out=2), -1), (dict(kernel=5), -1), (dict(kernel=-1), -1),
+                      (dict(reserved=1), -1), (dict(kernel=2), -2), (dict(kernel=4), -2)):
         assert call(d, {}) == status, d
         assert lib.moe_last_error()
     for a in (dict(x=None), dict(xs=None), dict(w=None), dict(ws=None), dict(offsets=None), dict(y=None),

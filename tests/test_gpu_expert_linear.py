@@ -30,7 +30,10 @@ def cuda(t):
     return tuple(v.cuda() for v in t) if isinstance(t, tuple) else None if t is None else t.cuda()
 
 
-def check(x, w, offsets, rows, swiglu, out, what):
+TILES = ["tile32", "tile64", "tile256"]
+
+
+def check(x, w, offsets, rows, swiglu, out, what, kernel="auto"):
     R = x[0].shape[0] if rows is None else rows.shape[0]
     outs = w[0].shape[1] // (2 if swiglu else 1)
     if out == "bf16":
@@ -39,8 +42,10 @@ def check(x, w, offsets, rows, swiglu, out, what):
     else:
         y = torch.full((R, outs), 7, dtype=torch.uint8, device="cuda").view(M.E4M3)
         ys = torch.full((R, outs // 32), 7, dtype=torch.uint8, device="cuda").view(M.E8M0)
-    got = tr.expert_linear(cuda(x), cuda(w), cuda(offsets), rows=cuda(rows), swiglu=swiglu, out=out, y=y, ys=ys)
-    want, err, inside = M.products(M.value(*x), M.value(*w), offsets, rows, swiglu, TILED)
+    got = tr.expert_linear(cuda(x), cuda(w), cuda(offsets), rows=cuda(rows), swiglu=swiglu, out=out, y=y, ys=ys,
+                           kernel=kernel)
+    want, err, inside = M.products(M.value(*x), M.value(*w), offsets, rows, swiglu,
+                                   0.0 if kernel == "rows" else TILED)
     if out == "bf16":
         assert got is y
         M.check_rows(y, want, err, inside, what)
@@ -59,15 +64,40 @@ FORMS = [(False, "bf16"), (True, "bf16"), (False, "mx8"), (True, "mx8")]
     ([1], 1, 32, 64), ([0, 1, 0], 3, 96, 128), ([1, 1, 1, 1], 2, 512, 192), ([16, 15, 17, 1], 9, 160, 64),
     ([33, 0, 64, 5], 20, 256, 448), ([63, 65], 128, 1024, 64), ([2, 31, 32], 40, 2880, 192),
     ([100, 3, 260, 0, 1], 90, 384, 320), ([300], 300, 640, 512), ([129, 128, 127], 200, 224, 576),
-    ([513, 0, 0, 70], 600, 128, 64),
+    ([513, 0, 0, 70], 600, 288, 64), ([5, 0, 9], 14, 1024, 128), ([16], 7, 2880, 192), ([1], 1, 8480, 64),
+    ([3, 4], 9, 544, 320), ([40, 24], 64, 768, 192),
 ])
 @pytest.mark.parametrize("bits", [8, 4])
 @pytest.mark.parametrize("swiglu,out", FORMS)
 def test_products(counts, T, K, N, bits, swiglu, out):
+    """By every kernel that takes the sizes."""
     say(f"experts {counts} T={T} K={K} N={N} bits={bits} swiglu={swiglu} {out}")
     for gather in (False, True):
         x, w, offsets, rows = case(K + N, counts, T, K, N, bits, gather)
-        check(x, w, offsets, rows, swiglu, out, f"gather={gather}")
+        for kernel in ["auto", "rows"] + (TILES if K >= 256 else []):
+            check(x, w, offsets, rows, swiglu, out, f"gather={gather} {kernel}", kernel)
+
+
+@pytest.mark.parametrize("counts,K,N,swiglu,out", [
+    ([700], 256, 16384, False, "bf16"), ([300, 257, 0, 100], 320, 8192, True, "mx8"),
+    ([90, 33, 200, 64], 512, 1024, True, "bf16"),
+])
+@pytest.mark.parametrize("bits", [8, 4])
+def test_many_tiles(counts, K, N, swiglu, out, bits):
+    """More than one tile a CU; what the rule chooses."""
+    say(f"experts many {counts} K={K} N={N} bits={bits}")
+    x, w, offsets, rows = case(K + N, counts, 90, K, N, bits, True)
+    for kernel in ["auto"] + TILES:
+        check(x, w, offsets, rows, swiglu, out, kernel, kernel)
+
+
+def test_a_kernel_that_does_not_take_the_sizes():
+    x, w, offsets, rows = case(1, [3], 3, 224, 64, 8, False)
+    for kernel in TILES:
+        with pytest.raises(tr.TopReduceError, match="does not take"):
+            tr.expert_linear(cuda(x), cuda(w), cuda(offsets), kernel=kernel)
+    with pytest.raises(ValueError):
+        tr.expert_linear(cuda(x), cuda(w), cuda(offsets), kernel="other")
 
 
 @pytest.mark.parametrize("N", [1, 2, 7, 30, 66, 250, 1001])
@@ -76,58 +106,65 @@ def test_odd_outputs(N, counts):
     for swiglu in (False, True):
         if N % 2 and swiglu:
             continue
-        x, w, offsets, rows = case(N, counts, 30, 96, N, 8, True)
-        check(x, w, offsets, rows, swiglu, "bf16", f"N={N}")
+        for K in (96, 320):
+            x, w, offsets, rows = case(N, counts, 30, K, N, 8, True)
+            for kernel in ["rows"] + (TILES if K >= 256 else []):
+                check(x, w, offsets, rows, swiglu, "bf16", f"N={N} {kernel}", kernel)
 
 
 @pytest.mark.parametrize("counts", [[4, 0, 9], [2, 200, 80]])
 @pytest.mark.parametrize("out", ["bf16", "mx8"])
 def test_rows_outside_the_segments_stay(counts, out):
     for gather in (False, True):
-        x, w, offsets, rows = case(5, counts, 50, 128, 96, 8, gather, gap=(3, 40))
-        check(x, w, offsets, rows, False, out, f"gather={gather}")
+        x, w, offsets, rows = case(5, counts, 50, 256, 96, 8, gather, gap=(3, 40))
+        for kernel in ["rows"] + TILES:
+            check(x, w, offsets, rows, False, out, f"gather={gather} {kernel}", kernel)
 
 
-@pytest.mark.parametrize("n", [20, 300])
+@pytest.mark.parametrize("n", [6, 20, 300])
 def test_offsets_and_rows_out_of_range_are_held_inside(n):
-    x, w, _, rows = case(6, [n, n], 40, 64, 64, 8, True)
+    x, w, _, rows = case(6, [n, n], 40, 256, 64, 8, True)
     rows[3], rows[7], rows[n] = -5, 1 << 30, 40
     for offsets in ([-9, n, 1 << 30], [0, n, n - 4], [2 * n, 2 * n, 2 * n], [5, 5, 9]):
-        check(x, w, torch.tensor(offsets, dtype=torch.int32), rows, False, "bf16", str(offsets))
+        for kernel in ["rows"] + TILES:
+            check(x, w, torch.tensor(offsets, dtype=torch.int32), rows, False, "bf16", f"{offsets} {kernel}", kernel)
 
 
 @pytest.mark.parametrize("n", [5, 200])
 @pytest.mark.parametrize("bits", [8, 4])
-def test_what_is_not_a_number_stays_in_its_row(n, bits):
-    x, w, offsets, rows = case(7, [n, n], n, 128, 96, bits, True)
+@pytest.mark.parametrize("kernel", ["rows"] + TILES)
+def test_what_is_not_a_number_stays_in_its_row(n, bits, kernel):
+    x, w, offsets, rows = case(7, [n, n], n, 288, 96, bits, True)
     args = cuda(w), cuda(offsets)
-    clean = tr.expert_linear(cuda(x), *args, rows=cuda(rows)).cpu()
+    clean = tr.expert_linear(cuda(x), *args, rows=cuda(rows), kernel=kernel).cpu()
     q = x[0].clone()
     q[2, 100] = float("nan")
     s = x[1].clone().view(torch.uint8)
     s[3, 1] = 255
-    got = tr.expert_linear((q.cuda(), s.view(M.E8M0).cuda()), *args, rows=cuda(rows)).cpu()
+    got = tr.expert_linear((q.cuda(), s.view(M.E8M0).cuda()), *args, rows=cuda(rows), kernel=kernel).cpu()
     bad = (rows == 2) | (rows == 3)
     assert bad.any() and torch.isnan(got[bad]).all() and torch.equal(got[~bad], clean[~bad])
     # a weight row: its output column, of its expert only
     ws = w[1].clone().view(torch.uint8)
     ws[1, 40, 3] = 255
-    got = tr.expert_linear(cuda(x), (cuda(w)[0], ws.view(M.E8M0).cuda()), cuda(offsets), rows=cuda(rows)).cpu()
+    got = tr.expert_linear(cuda(x), (cuda(w)[0], ws.view(M.E8M0).cuda()), cuda(offsets), rows=cuda(rows),
+                           kernel=kernel).cpu()
     hit = torch.zeros(2 * n, 96, dtype=torch.bool)
     hit[n:, 40] = True
     assert torch.isnan(got[hit]).all() and torch.equal(got[~hit], clean[~hit])
 
 
 @pytest.mark.parametrize("counts", [[1, 7], [90, 300]])
-def test_scales_of_any_size(counts):
+@pytest.mark.parametrize("kernel", ["rows"] + TILES)
+def test_scales_of_any_size(counts, kernel):
     """Blocks whose scales lie 2^60 apart, and the same product scaled."""
-    x, w, offsets, rows = case(8, counts, 60, 160, 64, 8, True)
+    x, w, offsets, rows = case(8, counts, 60, 416, 64, 8, True)
     s = x[1].view(torch.uint8).clone()
     s[:, 1] -= 60
     x = (x[0], s.view(M.E8M0))
-    y = check(x, w, offsets, rows, False, "bf16", "wide scales")
+    y = check(x, w, offsets, rows, False, "bf16", "wide scales", kernel)
     up = ((x[1].view(torch.uint8) + 100).view(M.E8M0), (w[1].view(torch.uint8) - 90).view(M.E8M0))
-    far = tr.expert_linear(cuda((x[0], up[0])), cuda((w[0], up[1])), cuda(offsets), rows=cuda(rows))
+    far = tr.expert_linear(cuda((x[0], up[0])), cuda((w[0], up[1])), cuda(offsets), rows=cuda(rows), kernel=kernel)
     assert torch.equal(far.double(), y.double() * 2.0 ** 10)
 
 
@@ -141,9 +178,10 @@ def test_nothing_to_do():
 
 
 @pytest.mark.parametrize("counts", [[3, 1, 8], [200, 20, 70]])
-def test_order_of_rows_keeps_their_bits(counts):
+@pytest.mark.parametrize("kernel", ["rows"] + TILES)
+def test_order_of_rows_keeps_their_bits(counts, kernel):
     x, w, offsets, rows = case(10, counts, 64, 256, 128, 4, True)
-    y = tr.expert_linear(cuda(x), cuda(w), cuda(offsets), rows=cuda(rows))
+    y = tr.expert_linear(cuda(x), cuda(w), cuda(offsets), rows=cuda(rows), kernel=kernel)
     perm = torch.cat([o + torch.randperm(n) for o, n in zip(offsets.tolist(), counts)])
-    z = tr.expert_linear(cuda(x), cuda(w), cuda(offsets), rows=cuda(rows[perm]))
+    z = tr.expert_linear(cuda(x), cuda(w), cuda(offsets), rows=cuda(rows[perm]), kernel=kernel)
     assert torch.equal(z, y[perm.cuda()])

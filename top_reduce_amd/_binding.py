@@ -76,7 +76,8 @@ class NormDesc(C.Structure):
 
 class ExpertDesc(C.Structure):
     _fields_ = [("T", C.c_int64), ("R", C.c_int64), ("K", C.c_int64), ("N", C.c_int64),
-                ("E", C.c_int32), ("bits", C.c_int32), ("swiglu", C.c_int32), ("out", C.c_int32)]
+                ("E", C.c_int32), ("bits", C.c_int32), ("swiglu", C.c_int32), ("out", C.c_int32),
+                ("kernel", C.c_int32), ("reserved", C.c_int32)]
 
 
 class Linear4Desc(C.Structure):

@@ -21,6 +21,7 @@ from ._binding import (_arg, _check, _dev_tensor, _dtype_code, _elsewhere, _raw_
 
 E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 BLOCK = 32
+KERNELS = {"auto": 0, "rows": 1, "tile32": 2, "tile64": 3, "tile256": 4}
 
 Mx = Tuple[torch.Tensor, torch.Tensor]
 
@@ -149,13 +150,16 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
 
 
 @functools.lru_cache(maxsize=512)
-def _expert_desc(T, R, K, N, E, bits, swiglu, out):
-    return C.byref(B.ExpertDesc(T=T, R=R, K=K, N=N, E=E, bits=bits, swiglu=swiglu, out=out))
+def _expert_desc(T, R, K, N, E, bits, swiglu, out, kernel):
+    if kernel not in KERNELS:
+        raise ValueError(f"kernel must be one of {', '.join(KERNELS)} (got {kernel!r})")
+    return C.byref(B.ExpertDesc(T=T, R=R, K=K, N=N, E=E, bits=bits, swiglu=swiglu, out=out,
+                                kernel=KERNELS[kernel], reserved=0))
 
 
 def expert_linear(x: Mx, w: Mx, offsets: torch.Tensor, rows: Optional[torch.Tensor] = None,
                   swiglu: bool = False, out: str = "bf16", y: Optional[torch.Tensor] = None,
-                  ys: Optional[torch.Tensor] = None,
+                  ys: Optional[torch.Tensor] = None, kernel: str = "auto",
                   stream: Optional[torch.cuda.Stream] = None) -> Union[torch.Tensor, Mx]:
     """moe_expert_linear: y[r] = w[e] x[rows[r]] for the rows r of each expert's segment,
     offsets[e] <= r < offsets[e + 1].
@@ -170,7 +174,8 @@ def expert_linear(x: Mx, w: Mx, offsets: torch.Tensor, rows: Optional[torch.Tens
     wq, ws = _pair(w, "w")
     dev = _x_arg(xq)
     if _elsewhere(stream, dev):
-        return _run_on(stream, (y, ys), expert_linear, x, w, offsets, rows, swiglu, out, y, ys)
+        return _run_on(stream, (y, ys), expert_linear, x, w, offsets, rows, swiglu, out, y, ys,
+                       kernel)
     if out not in ("bf16", "mx8"):
         raise ValueError(f"out must be 'bf16' or 'mx8' (got {out!r})")
     if wq.dim() != 3:
@@ -189,7 +194,7 @@ def expert_linear(x: Mx, w: Mx, offsets: torch.Tensor, rows: Optional[torch.Tens
     if rows is not None:
         R = rows.shape[0] if isinstance(rows, torch.Tensor) and rows.dim() == 1 else -1
         rp = _arg(rows, "rows", torch.int32, (R,), dev)
-    desc = _expert_desc(T, R, K, N, E, bits, 1 if swiglu else 0, 1 if out == "mx8" else 0)
+    desc = _expert_desc(T, R, K, N, E, bits, 1 if swiglu else 0, 1 if out == "mx8" else 0, kernel)
     outs = N // 2 if swiglu else N
     ysp = None
     if out == "bf16":

@@ -714,6 +714,8 @@ tr_status check_expert_desc(const tr_expert_desc* d) {
   if (d->bits != 8 && d->bits != 4) return fail(TR_EINVAL, "bits must be 8 or 4 (got %d)", d->bits);
   if (d->swiglu != 0 && d->swiglu != 1) return fail(TR_EINVAL, "swiglu must be 0 or 1");
   if (d->out != 0 && d->out != 1) return fail(TR_EINVAL, "out must be 0 or 1");
+  if (d->kernel < TR_EXPERT_AUTO || d->kernel > TR_EXPERT_TILE256) return fail(TR_EINVAL, "unknown kernel %d", d->kernel);
+  if (d->reserved != 0) return fail(TR_EINVAL, "reserved must be 0");
   if (d->swiglu && d->N % 2) return fail(TR_EINVAL, "swiglu needs an even N (got %lld)", (long long)d->N);
   const tr_status s = check_k(d->K, "K");
   if (s != TR_OK) return s;
@@ -801,10 +803,10 @@ tr_status moe_expert_linear(const tr_expert_desc* desc, const void* x, const voi
   if (overlap(y, yb, x, d.T * d.K) || overlap(y, yb, xs, d.T * d.K / 32) ||
       overlap(ys, d.R * No / 32, x, d.T * d.K) || overlap(ys, d.R * No / 32, xs, d.T * d.K / 32))
     return fail(TR_EINVAL, "y and ys must not overlap x or xs");
-  const bool tiles = tr::expert_can_tile(d, rows != nullptr);
-  hipError_t h = tr::expert_few(d, x, xs, w, ws, offsets, rows, y, ys, tiles ? tr::kMxFewRows : 0x7fffffff, stream);
-  if (h == hipSuccess && tiles && d.R > tr::kMxFewRows)
-    h = tr::expert_tiles(d, x, xs, w, ws, offsets, rows, y, ys, tr::kMxFewRows + 1, stream);
+  const tr_expert_kernel k = tr::expert_kernel(d, rows != nullptr);
+  if (k == TR_EXPERT_AUTO) return fail(TR_EUNSUPPORTED, "kernel %d does not take these sizes", d.kernel);
+  const hipError_t h = k == TR_EXPERT_ROWS ? tr::expert_few(d, x, xs, w, ws, offsets, rows, y, ys, stream)
+                                           : tr::expert_tiles(d, k, x, xs, w, ws, offsets, rows, y, ys, stream);
   return hip_status(h, "moe_expert_linear launch");
 }
 
@@ -838,8 +840,8 @@ tr_status moe_forward_mx(const tr_moe_plan* plan, const void* x, const void* xs,
   const tr_moe_desc& d = plan->d;
   if (d.dtype != TR_BF16) return fail(TR_EUNSUPPORTED, "moe_forward_mx needs a plan of TR_BF16");
   if (d.I % 32) return fail(TR_EUNSUPPORTED, "I must be a multiple of 32 (got %lld)", (long long)d.I);
-  const tr_expert_desc gate_up{d.T, plan->R_cap, d.H, 2 * d.I, d.E, bits, 1, 1};
-  const tr_expert_desc down{plan->R_cap, plan->R_cap, d.I, d.H, d.E, bits, 0, 0};
+  const tr_expert_desc gate_up{d.T, plan->R_cap, d.H, 2 * d.I, d.E, bits, 1, 1, TR_EXPERT_AUTO, 0};
+  const tr_expert_desc down{plan->R_cap, plan->R_cap, d.I, d.H, d.E, bits, 0, 0, TR_EXPERT_AUTO, 0};
   if ((e = check_expert_desc(&gate_up)) != TR_OK) return e;
   if ((e = check_expert_desc(&down)) != TR_OK) return e;
   if (d.T == 0) return ok();

@@ -13,12 +13,14 @@
 //
 // Both operands go from memory to LDS without registers, into the stage of two that the
 // step before has finished reading. A step (k-tile) is 32 matrix instructions a wave, 64
-// cycles each:
-//   0..7    the second half's fragments come from LDS; then the stage is free (a barrier)
-//   8..23   one load to LDS each, of the k-tile after next
-//   24..31  the next k-tile has landed (a barrier); its first half's fragments come
-// so a load has 1 to 1.5 steps, 2048 to 3072 cycles, to land. Scales go through registers
-// to LDS, eight bytes of every row for two k-tiles.
+// cycles each, and everything else lies between them, spread so that no unit gets a burst:
+//   0..7    the second half's fragments come from LDS, two reads each
+//   10      the stage is free (a barrier)
+//   10..25  one load to LDS each, of the k-tile after next
+//   20      the next k-tile has landed (a barrier)
+//   20..27  its first half's fragments come, and its scales
+// so a load has 27 to 42 instructions, 1700 to 2700 cycles, to land. Scales go through
+// registers to LDS, eight bytes of every row for two k-tiles.
 //
 // Scheduling is on the device from the offsets: groups of kGroupM m-tiles by all n-tiles,
 // in contiguous runs for each of the 8 XCDs, whose L2s then hold a group's rows and
@@ -45,7 +47,6 @@ struct MxArgs {
   uint8_t* ys;             // [R, No / 32]
   int64_t T;
   int R, K, N, E;
-  int least;               // experts with fewer rows are another kernel's
 };
 
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -99,8 +100,17 @@ struct Lane {
   uint32_t b_step;        // bytes from a piece of w to the next
 };
 
+// The row of x of row wave * 64 + lane of a tile.
+__device__ __forceinline__ int x_row(const MxArgs& a, const Tile& t, int wave, int lane) {
+  const int lr = min(wave * 64 + lane, t.valid - 1);
+  return a.rows ? a.rows[t.row0 + lr] : lr;     // (within the tile where rows are not gathered)
+}
+
+// `row`: x_row of the tile.
 template <int kBits, bool kSwiglu>
-__device__ __forceinline__ Source<kBits> source(const MxArgs& a, const Tile& t, int wave, int lane) {
+__device__ __forceinline__ Source<kBits> source(const MxArgs& a, const Tile& t, int row, int wave, int lane) {
+  asm volatile("" : "+v"(row));   // (waited for here, not where it is loaded)
+  if (a.rows) row = max(0, min(row, static_cast<int>(a.T) - 1));
   Source<kBits> s;
   const int blocks = a.K / kMxBlock;
   const int64_t kb = static_cast<int64_t>(a.K) * kBits / 8;   // bytes of a row of w
@@ -114,16 +124,11 @@ __device__ __forceinline__ Source<kBits> source(const MxArgs& a, const Tile& t, 
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int lr = wave * 64 + j * 8 + (lane >> 3);
-    uint32_t row = lr;
-    if (a.rows) row = max(0, min(a.rows[min(t.row0 + lr, a.R - 1)], static_cast<int>(a.T) - 1));
-    s.a_off[j] = lr < t.valid ? row * static_cast<uint32_t>(a.K) + (chunk ^ (j & 1)) * 16 : kPast;
+    const uint32_t r = __shfl(row, j * 8 + (lane >> 3), kWave);
+    s.a_off[j] = lr < t.valid ? r * static_cast<uint32_t>(a.K) + (chunk ^ (j & 1)) * 16 : kPast;
   }
-  {
-    const int lr = min(wave * 64 + lane, t.valid - 1);
-    int64_t row = t.row0 + lr;
-    if (a.rows) row = max(0, min(a.rows[row], static_cast<int>(a.T) - 1));
-    s.sa = a.xs + row * blocks;
-  }
+  const int64_t srow = a.rows ? row : t.row0 + row;
+  s.sa = a.xs + srow * blocks;
   // w: gate rows first, then up
   const uint8_t* wbase = a.w + static_cast<int64_t>(t.e) * a.N * kb;
   const int64_t w_bytes = a.N * kb;
@@ -157,24 +162,23 @@ __device__ __forceinline__ void load_b(const Source<kBits>& s, int kt, uint32_t 
                                            off | past, kt * (BK * kBits / 8), 0, 0);
 }
 
-// Eight scale bytes of a row from block `at` on, those past the last as 0.
-__device__ __forceinline__ uint2 load_scales(const uint8_t* p, int at, int blocks) {
+// Eight scale bytes of a row, blocks at .. at + 7, as they lie in memory (at least 8
+// blocks: the row's last eight at most), and with 0 for those past the last.
+__device__ __forceinline__ uint2 load_scale8(const uint8_t* p, int at, int blocks) {
   typedef uint32_t Odd __attribute__((ext_vector_type(2), aligned(1)));
-  if (at + 8 <= blocks) {
-    const Odd v = *reinterpret_cast<const Odd*>(p + at);
-    return uint2{v[0], v[1]};
-  }
-  uint32_t v[2] = {0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (at + i < blocks) v[i >> 2] |= static_cast<uint32_t>(p[at + i]) << (8 * (i & 3));
+  const Odd v = *reinterpret_cast<const Odd*>(p + min(at, blocks - 8));
   return uint2{v[0], v[1]};
+}
+__device__ __forceinline__ uint2 scale8(uint2 v, int at, int blocks) {
+  const int over = at - min(at, blocks - 8);
+  const uint64_t all = (static_cast<uint64_t>(v.y) << 32 | v.x) >> (8 * over & 63);
+  return over < 8 ? uint2{static_cast<uint32_t>(all), static_cast<uint32_t>(all >> 32)} : uint2{0, 0};
 }
 
 template <int kBits>
 struct Frags {
   intx8 a[2][4], b[2][4];   // of a step's two halves: rows of x, rows of w
-  uint32_t sa[2][4], sb[2][4];   // of this k-tile and the next: scales, from block h on
+  uint32_t sa[2][4], sb[2][4];   // of this k-tile and the next: scales (shift_scales: from block h on)
   floatx16 acc[4][4];       // acc[i][j]: row block i, block j of rows of w
 };
 
@@ -184,44 +188,41 @@ struct Geo {
   int b_unit[2][2];
 };
 
+typedef __attribute__((ext_vector_type(4))) int intx4;
+
+// Fragment n of half P of stage S: rows of w first, whose four the first instructions need.
 template <int S, int P, int kBits>
-__device__ __forceinline__ void read_frags(Frags<kBits>& f, const Geo& g) {
-  const u32x4* sa = stage_a<S>();
-  const u32x4* sb = stage_b<S>();
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const u32x4 lo = sa[(g.a_row + i * 32) * 8 + g.a_unit[P][0]], hi = sa[(g.a_row + i * 32) * 8 + g.a_unit[P][1]];
-    f.a[P][i] = __builtin_shufflevector(__builtin_bit_cast(__attribute__((ext_vector_type(4))) int, lo),
-                                        __builtin_bit_cast(__attribute__((ext_vector_type(4))) int, hi), 0, 1, 2, 3,
-                                        4, 5, 6, 7);
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if constexpr (kBits == 8) {
-      const u32x4 lo = sb[g.b_row[j] * 8 + g.b_unit[P][0]], hi = sb[g.b_row[j] * 8 + g.b_unit[P][1]];
-      f.b[P][j] = __builtin_shufflevector(__builtin_bit_cast(__attribute__((ext_vector_type(4))) int, lo),
-                                          __builtin_bit_cast(__attribute__((ext_vector_type(4))) int, hi), 0, 1, 2,
-                                          3, 4, 5, 6, 7);
-    } else {
-      const u32x4 v = sb[g.b_row[j] * 4 + g.b_unit[P][0]];
-      f.b[P][j] = intx8{static_cast<int>(v[0]), static_cast<int>(v[1]), static_cast<int>(v[2]),
-                        static_cast<int>(v[3]), 0, 0, 0, 0};
-    }
+__device__ __forceinline__ void read_frag(Frags<kBits>& f, const Geo& g, int n) {
+  if (n >= 4) {
+    const u32x4* s = stage_a<S>() + (g.a_row + (n - 4) * 32) * 8;
+    f.a[P][n - 4] = __builtin_shufflevector(__builtin_bit_cast(intx4, s[g.a_unit[P][0]]),
+                                            __builtin_bit_cast(intx4, s[g.a_unit[P][1]]), 0, 1, 2, 3, 4, 5, 6, 7);
+  } else if constexpr (kBits == 8) {
+    const u32x4* s = stage_b<S>() + g.b_row[n] * 8;
+    f.b[P][n] = __builtin_shufflevector(__builtin_bit_cast(intx4, s[g.b_unit[P][0]]),
+                                        __builtin_bit_cast(intx4, s[g.b_unit[P][1]]), 0, 1, 2, 3, 4, 5, 6, 7);
+  } else {
+    const u32x4 v = stage_b<S>()[g.b_row[n] * 4 + g.b_unit[P][0]];
+    f.b[P][n] = intx8{static_cast<int>(v[0]), static_cast<int>(v[1]), static_cast<int>(v[2]),
+                      static_cast<int>(v[3]), 0, 0, 0, 0};
   }
 }
 
-// Scales of the k-tile in half S of LDS buffer `buf`.
+// Scales of row block n of the k-tile in half S of LDS buffer `buf`.
 template <int S, int kBits>
-__device__ __forceinline__ void read_scales(Frags<kBits>& f, const Geo& g, int buf, int lane) {
+__device__ __forceinline__ void read_scale(Frags<kBits>& f, const Geo& g, int buf, int lane, int n) {
+  const uint2* p = &g_sa[buf][g.a_row + n * 32 + (lane & 31)];
+  f.sa[S][n] = S == 0 ? p->x : p->y;
+  const uint2* q = &g_sb[buf][g.b_row[n] + (lane & 31)];
+  f.sb[S][n] = S == 0 ? q->x : q->y;
+}
+
+template <int S, int kBits>
+__device__ __forceinline__ void shift_scales(Frags<kBits>& f, int lane) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint2* p = &g_sa[buf][g.a_row + i * 32 + (lane & 31)];
-    f.sa[S][i] = (S == 0 ? p->x : p->y) >> (8 * (lane >> 5));
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint2* p = &g_sb[buf][g.b_row[j] + (lane & 31)];
-    f.sb[S][j] = (S == 0 ? p->x : p->y) >> (8 * (lane >> 5));
+  for (int n = 0; n < 4; ++n) {
+    f.sa[S][n] >>= 8 * (lane >> 5);
+    f.sb[S][n] >>= 8 * (lane >> 5);
   }
 }
 
@@ -242,43 +243,46 @@ template <int S, bool kScales, int kBits>
 __device__ __forceinline__ void step(Frags<kBits>& f, const Geo& g, const Source<kBits>& src, int kt, int K,
                                      int a_chunk, int b_chunk, uint32_t b_step, int buf, int into, int wave,
                                      int lane) {
-  read_frags<S, 1>(f, g);
+  constexpr int kFree = 10, kLanded = 20, kLoads = 8 + Source<kBits>::kBPieces;
+  const int blocks = K / kMxBlock;
   uint2 na{}, nb{};
   if constexpr (kScales) {
-    na = load_scales(src.sa, kt * 4, K / kMxBlock);
-    nb = load_scales(src.sb, kt * 4, K / kMxBlock);
+    na = load_scale8(src.sa, kt * 4, blocks);
+    nb = load_scale8(src.sb, kt * 4, blocks);
   }
-  __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-  for (int m = 0; m < 8; ++m) mma<S, 0>(f, m);
-  __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt(waitcnt_vm(63, true));   // this wave's reads of the stage are done
-  barrier();
+  shift_scales<S>(f, lane);
   // chunks past K (pairs of them: K is a multiple of 32)
   const uint32_t past_a = kt * 8 + a_chunk < K / 16 ? 0 : kPast;
-  const uint32_t past_b = kBits == 8 ? (kt * 8 + b_chunk < K / 16 ? 0 : kPast) : (kt * 4 + b_chunk < K / 32 ? 0 : kPast);
+  const uint32_t past_b = kBits == 8 ? past_a : (kt * 4 + b_chunk < K / 32 ? 0 : kPast);
+  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int m = 8; m < 24; ++m) {
+  for (int m = 0; m < 32; ++m) {
+    if (m == kFree) {
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm(63, true));   // this wave's reads of the stage are done
+      barrier();
+    }
+    if (m == kLanded) {
+      // what the step before sent has landed
+      constexpr int kSent = kLoads < kLanded - kFree ? kLoads : kLanded - kFree;
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm(kSent, false));
+      barrier();
+      if constexpr (kScales) {
+        // (not shifted, and so not waited for, before this)
+        asm volatile("" : "+v"(na.x), "+v"(na.y), "+v"(nb.x), "+v"(nb.y));
+        g_sa[into][wave * 64 + lane] = scale8(na, kt * 4, blocks);
+        g_sb[into][wave * 64 + lane] = scale8(nb, kt * 4, blocks);
+      }
+    }
+    if (m < 8) read_frag<S, 1>(f, g, m);
+    if (m >= kLanded && m < kLanded + 8) read_frag<1 - S, 0>(f, g, m - kLanded);
+    if (m >= kLanded && m < kLanded + 4) read_scale<1 - S>(f, g, buf, lane, m - kLanded);
     if (m < 16) mma<S, 0>(f, m);
     else mma<S, 1>(f, m - 16);
-    const int n = m - 8;
-    if (n < 8) load_a<S>(src, kt, past_a, wave, n);
-    else if (n - 8 < Source<kBits>::kBPieces) load_b<S>(src, kt, past_b, b_step, wave, n - 8);
+    const int n = m - kFree;
+    if (n >= 0 && n < 8) load_a<S>(src, kt, past_a, wave, n);
+    else if (n >= 8 && n < kLoads) load_b<S>(src, kt, past_b, b_step, wave, n - 8);
     __builtin_amdgcn_sched_barrier(0);
   }
-  // what was sent before this step's loads has landed
-  __builtin_amdgcn_s_waitcnt(waitcnt_vm(8 + Source<kBits>::kBPieces, false));
-  barrier();
-  if constexpr (kScales) {
-    g_sa[into][wave * 64 + lane] = na;
-    g_sb[into][wave * 64 + lane] = nb;
-  }
-  read_frags<1 - S, 0>(f, g);
-  read_scales<1 - S>(f, g, buf, lane);
-  __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-  for (int m = 8; m < 16; ++m) mma<S, 1>(f, m);
-  __builtin_amdgcn_sched_barrier(0);
 }
 
 // Tile L of the order.
@@ -315,6 +319,48 @@ __device__ __forceinline__ void store_bf16(uint16_t* row, int col, int No, const
   }
 }
 
+// A 32 x 32 block of results: v[4 q + c] is column col + 8 q + 4 h + c of `row` (the
+// lane's; h = lane / 32), stored where the row is `in` its segment.
+template <bool kMxOut>
+__device__ __forceinline__ void store_block(const MxArgs& a, int64_t row, bool in, int col, int No, int h,
+                                            const floatx16& v) {
+  if constexpr (kMxOut) {
+    float top = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 16; ++c) top = fmaxf(top, mx_magnitude(v[c]));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    const int b = mx_scale_byte<8>(top);
+    const float inv = mx_inverse(b);
+    uint32_t d[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      d[q] = mx_pack8(v[4 * q] * inv, v[4 * q + 1] * inv, v[4 * q + 2] * inv, v[4 * q + 3] * inv);
+    // lanes below 32: columns 0..15, the others 16..31
+    const auto p0 = __builtin_amdgcn_permlane32_swap(d[0], d[2], false, false);
+    const auto p1 = __builtin_amdgcn_permlane32_swap(d[1], d[3], false, false);
+    if (in && col < No) {
+      *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(a.y) + row * No + col + 16 * h) =
+          u32x4{p0[0], p0[1], p1[0], p1[1]};
+      if (h == 0) a.ys[row * (No / kMxBlock) + col / kMxBlock] = static_cast<uint8_t>(b);
+    }
+  } else {
+    uint32_t d[4][2];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      d[q][0] = cvt_bf16x2(v[4 * q], v[4 * q + 1]);
+      d[q][1] = cvt_bf16x2(v[4 * q + 2], v[4 * q + 3]);
+    }
+    uint16_t* out = static_cast<uint16_t*>(a.y) + row * No;
+#pragma unroll
+    for (int q = 0; q < 4; q += 2) {
+      // lanes below 32: columns 8 q + [0, 8), the others 8 (q + 1) + [0, 8)
+      const auto p0 = __builtin_amdgcn_permlane32_swap(d[q][0], d[q + 1][0], false, false);
+      const auto p1 = __builtin_amdgcn_permlane32_swap(d[q][1], d[q + 1][1], false, false);
+      if (in) store_bf16(out, col + 8 * (q + h), No, u32x4{p0[0], p1[0], p0[1], p1[1]});
+    }
+  }
+}
+
 #endif  // __HIP_DEVICE_COMPILE__
 
 template <int kBits, bool kSwiglu, bool kMxOut>
@@ -334,7 +380,7 @@ __global__ __launch_bounds__(kThreads) void mx_tiles(MxArgs a) {
       const int begin = max(0, min(a.offsets[e], a.R)), end = max(begin, min(a.offsets[e + 1], a.R));
       off[e] = begin;
       cnt[e] = end - begin;
-      mine[i] = end - begin < a.least ? 0 : (end - begin + BM - 1) / BM;
+      mine[i] = (end - begin + BM - 1) / BM;
     }
     sum += mine[i];
   }
@@ -382,7 +428,7 @@ __global__ __launch_bounds__(kThreads) void mx_tiles(MxArgs a) {
   const int pairs = (a.K + 2 * BK - 1) / (2 * BK);
 
   Tile t = tile_of(pre, cnt, off, a.E, total_m, NT, kOuts, pos);
-  Source<kBits> s0 = source<kBits, kSwiglu>(a, t, wave, lane);
+  Source<kBits> s0 = source<kBits, kSwiglu>(a, t, x_row(a, t, wave, lane), wave, lane);
   Frags<kBits> f;
   int buf = 0;     // of the current pair's scales
   {
@@ -402,47 +448,50 @@ __global__ __launch_bounds__(kThreads) void mx_tiles(MxArgs a) {
         else load_b<1>(s0, q, past_b, b_step, wave, j);
       }
     }
-    g_sa[0][wave * 64 + lane] = load_scales(s0.sa, 0, a.K / kMxBlock);
-    g_sb[0][wave * 64 + lane] = load_scales(s0.sb, 0, a.K / kMxBlock);
+    g_sa[0][wave * 64 + lane] = load_scale8(s0.sa, 0, a.K / kMxBlock);
+    g_sb[0][wave * 64 + lane] = load_scale8(s0.sb, 0, a.K / kMxBlock);
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0, true));
     barrier();
-    read_frags<0, 0>(f, g);
-    read_scales<0>(f, g, 0, lane);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) read_frag<0, 0>(f, g, n);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) read_scale<0>(f, g, 0, lane, n);
   }
 
 #pragma clang loop unroll(disable)
   for (int L = pos; L < total; L += G) {
     {
-      // accumulators start as a product of zeros, in their own registers
-      bf16x8 zf;
-      int zero = 0;
-      asm volatile("" : "+v"(zero));
+      // accumulators start as products of zeros, in their own registers (zeros that
+      // differ to the compiler: it would make one product, and 15 copies of it)
 #pragma unroll
-      for (int q = 0; q < 8; ++q) zf[q] = __builtin_bit_cast(__bf16, static_cast<uint16_t>(zero));
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          f.acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(zf, zf, floatx16{}, 0, 0, 0);
+      for (int m = 0; m < 16; ++m) {
+        int zero = 0;
+        asm volatile("" : "+v"(zero));
+        const bf16x8 zf = __builtin_bit_cast(bf16x8, (intx4){zero, zero, zero, zero});
+        f.acc[m >> 2][m & 3] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(zf, zf, floatx16{}, 0, 0, 0);
+      }
     }
     // past the last tile: this one again, in bounds and not used
     const Tile tn = L + G < total ? tile_of(pre, cnt, off, a.E, total_m, NT, kOuts, L + G) : t;
-    const Source<kBits> s1 = source<kBits, kSwiglu>(a, tn, wave, lane);
+    const int rn = x_row(a, tn, wave, lane);   // (used in the last pair)
+    // (one loop that runs at least once: no copy of the accumulators, one of the steps)
+    int p = 1;
 #pragma clang loop unroll(disable)
-    for (int p = 1; p < pairs; ++p) {
-      step<0, true>(f, g, s0, 2 * p, a.K, a_chunk, b_chunk, b_step, buf, buf ^ 1, wave, lane);
-      step<1, false>(f, g, s0, 2 * p + 1, a.K, a_chunk, b_chunk, b_step, buf ^ 1, 0, wave, lane);
+    do {
+      int kt = 2 * p;
+      if (p == pairs) {     // what comes next is the next tile's
+        s0 = source<kBits, kSwiglu>(a, tn, rn, wave, lane);
+        kt = 0;
+      }
+      step<0, true>(f, g, s0, kt, a.K, a_chunk, b_chunk, b_step, buf, buf ^ 1, wave, lane);
+      step<1, false>(f, g, s0, kt + 1, a.K, a_chunk, b_chunk, b_step, buf ^ 1, 0, wave, lane);
       buf ^= 1;
-    }
-    step<0, true>(f, g, s1, 0, a.K, a_chunk, b_chunk, b_step, buf, buf ^ 1, wave, lane);
-    step<1, false>(f, g, s1, 1, a.K, a_chunk, b_chunk, b_step, buf ^ 1, 0, wave, lane);
-    buf ^= 1;
+    } while (p++ < pairs);
 
     // the accumulators stay where they are up to their block's turn
+    settle(f.acc[0][0]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) asm volatile("" : "+a"(f.acc[i][j]));
+    for (int m = 1; m < 16; ++m) settled(f.acc[m >> 2][m & 3]);
     // acc[i][j][4 q + c]: row lane & 31 of row block i, column 8 q + 4 h + c of block j
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -459,51 +508,358 @@ __global__ __launch_bounds__(kThreads) void mx_tiles(MxArgs a) {
           for (int c = 0; c < 16; ++c) v[c] = swiglu<false>(v[c], u[c]);
         }
         const int col = t.n0 + g.b_row[j];
-        if constexpr (kMxOut) {
-          float top = 0.0f;
-#pragma unroll
-          for (int c = 0; c < 16; ++c) top = fmaxf(top, mx_magnitude(v[c]));
-          top = fmaxf(top, __shfl_xor(top, 32, 64));
-          const int b = mx_scale_byte<8>(top);
-          const float inv = mx_inverse(b);
-          uint32_t d[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            d[q] = mx_pack8(v[4 * q] * inv, v[4 * q + 1] * inv, v[4 * q + 2] * inv, v[4 * q + 3] * inv);
-          // lanes below 32: columns 0..15, the others 16..31
-          const auto p0 = __builtin_amdgcn_permlane32_swap(d[0], d[2], false, false);
-          const auto p1 = __builtin_amdgcn_permlane32_swap(d[1], d[3], false, false);
-          if (lr < t.valid && col < No) {
-            *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(a.y) + row * No + col + 16 * h) =
-                u32x4{p0[0], p0[1], p1[0], p1[1]};
-            if (h == 0) a.ys[row * (No / kMxBlock) + col / kMxBlock] = static_cast<uint8_t>(b);
-          }
-        } else {
-          uint32_t d[4][2];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            d[q][0] = cvt_bf16x2(v[4 * q], v[4 * q + 1]);
-            d[q][1] = cvt_bf16x2(v[4 * q + 2], v[4 * q + 3]);
-          }
-          if (lr < t.valid) {
-            uint16_t* out = static_cast<uint16_t*>(a.y) + row * No;
-#pragma unroll
-            for (int q = 0; q < 4; q += 2) {
-              // lanes below 32: columns 8 q + [0, 8), the others 8 (q + 1) + [0, 8)
-              const auto p0 = __builtin_amdgcn_permlane32_swap(d[q][0], d[q + 1][0], false, false);
-              const auto p1 = __builtin_amdgcn_permlane32_swap(d[q][1], d[q + 1][1], false, false);
-              store_bf16(out, col + 8 * (q + h), No, u32x4{p0[0], p1[0], p0[1], p1[1]});
-            }
-          }
-        }
+        store_block<kMxOut>(a, row, lr < t.valid, col, No, h, v);
         __builtin_amdgcn_sched_barrier(0);   // one block at a time
       }
     }
     t = tn;
-    s0 = s1;
   }
   __builtin_amdgcn_s_waitcnt(waitcnt_vm(0, true));   // loads past the last tile
 #endif  // __HIP_DEVICE_COMPILE__
+}
+
+// --------------------------------------------------------------------------
+// Smaller tiles, a block each: where the experts have too few rows, or the call too few
+// tiles, for the loop above.
+// --------------------------------------------------------------------------
+// kBM x 128 (SwiGLU: 64 gate and 64 up rows of w); a k-tile is 128 bytes of every row of
+// w, 128 numbers or, in 4 bits, 256 (with 64 bytes of a row at a time, 434 MB of weights
+// in 4 bits came at 3.8 TB/s). kStages stages, one being multiplied and the others in
+// flight. Wave (m, n) of 2 x 2 has kBM / 2 rows by 64, for SwiGLU 32 gate and the matching
+// 32 up; with 32 rows wave (p, n) has them all and half p of every k-tile, and the halves'
+// sums are added in LDS.
+#if defined(__HIP_DEVICE_COMPILE__)
+constexpr int kMidN = 128;
+
+template <int k>
+struct Index {
+  static constexpr int value = k;
+};
+
+// The scales of a row's k-tile, kSub dwords, as they lie in memory (K >= 256: the row's last
+// dwords at most), and with 0 for the blocks past the last.
+template <int kSub>
+struct Scales {
+  uint32_t v[kSub];
+  __device__ __forceinline__ void load(const uint8_t* p, int kt, int blocks) {
+    typedef uint32_t Odd __attribute__((ext_vector_type(kSub), aligned(1)));
+    const Odd d = *reinterpret_cast<const Odd*>(p + min(kt * 4 * kSub, blocks - 4 * kSub));
+#pragma unroll
+    for (int u = 0; u < kSub; ++u) v[u] = d[u];
+  }
+  __device__ __forceinline__ void store(uint32_t* p, int kt, int blocks) const {
+    const int over = kt * 4 * kSub - min(kt * 4 * kSub, blocks - 4 * kSub);
+    uint64_t all = v[0];
+    if constexpr (kSub == 2) all |= static_cast<uint64_t>(v[1]) << 32;
+    all = over < 4 * kSub ? all >> (8 * over & 63) : 0;
+    p[0] = static_cast<uint32_t>(all);
+    if constexpr (kSub == 2) p[1] = static_cast<uint32_t>(all >> 32);
+  }
+};
+#endif
+
+template <int kBits, int kBM, int kStages, bool kSwiglu, bool kMxOut>
+__global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int kOuts = kSwiglu ? kMidN / 2 : kMidN;
+  constexpr bool kHalves = kBM == 32;        // waves share a k-tile's halves
+  constexpr int kI = kHalves ? 1 : kBM / 64; // row blocks of a wave
+  constexpr int kSub = kBits == 8 ? 1 : 2;   // 128 numbers of a k-tile
+  constexpr int kAPieces = kBM / 32;         // of a wave, of 128 numbers: 8 rows each
+  constexpr int kBPieces = 4;
+  constexpr int kLoads = kAPieces * kSub + kBPieces;
+  // (distinct objects, as above)
+  constexpr int kA = kBM * 8 * kSub, kB = kMidN * 8;
+  static_assert(kStages == 2 || kStages == 3, "stages");
+  __shared__ u32x4 a0[kA], a1[kA], a2[kStages > 2 ? kA : 1];
+  __shared__ u32x4 b0[kB], b1[kB], b2[kStages > 2 ? kB : 1];
+  auto sa_of = [&](auto i) -> u32x4* {
+    constexpr int k = decltype(i)::value;
+    if constexpr (k == 0) return a0;
+    else if constexpr (k == 1) return a1;
+    else return a2;
+  };
+  auto sb_of = [&](auto i) -> u32x4* {
+    constexpr int k = decltype(i)::value;
+    if constexpr (k == 0) return b0;
+    else if constexpr (k == 1) return b1;
+    else return b2;
+  };
+  __shared__ uint32_t sc[kStages][(kBM + kMidN) * kSub];
+  __shared__ int pre[kMaxE + 1], tmp[kThreads / kWave];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int No = kSwiglu ? a.N / 2 : a.N;
+  const int NT = (No + kOuts - 1) / kOuts;
+  // the experts' m-tiles
+  int total_m;
+  {
+    const int per = (a.E + kThreads - 1) / kThreads;
+    int sum = 0, mine[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = tid * per + i;
+      mine[i] = 0;
+      if (i < per && e < a.E) {
+        const int begin = max(0, min(a.offsets[e], a.R)), end = max(begin, min(a.offsets[e + 1], a.R));
+        mine[i] = (end - begin + kBM - 1) / kBM;
+      }
+      sum += mine[i];
+    }
+    int at = block_exclusive_scan<kThreads>(sum, tmp, &total_m);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = tid * per + i;
+      if (i < per && e < a.E) pre[e] = at;
+      at += mine[i];
+    }
+    if (tid == 0) pre[a.E] = total_m;
+    __syncthreads();
+  }
+  // contiguous tiles for each XCD; an expert's m-tiles of one n-tile one after another
+  const int total = total_m * NT;
+  const int share = (total + 7) / 8;
+  const int idx = blockIdx.x >> 3;
+  const int L = static_cast<int>(blockIdx.x & 7) * share + idx;
+  if (idx >= share || L >= total) return;
+  Tile t;
+  {
+    int lo = 0, hi = a.E;
+    const int gm = L / NT;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] <= gm) lo = mid; else hi = mid;
+    }
+    t.e = __builtin_amdgcn_readfirstlane(lo);
+    const int first = __builtin_amdgcn_readfirstlane(pre[t.e]);
+    const int mts = __builtin_amdgcn_readfirstlane(pre[t.e + 1]) - first;
+    const int within = L - first * NT;
+    const int begin = max(0, min(a.offsets[t.e], a.R)), end = max(begin, min(a.offsets[t.e + 1], a.R));
+    t.n0 = within / mts * kOuts;
+    t.row0 = begin + within % mts * kBM;
+    t.valid = min(kBM, end - t.row0);
+  }
+  const int blocks = a.K / kMxBlock;
+  const int64_t kb = static_cast<int64_t>(a.K) * kBits / 8;
+  const int chunk = (lane & 7) ^ (lane >> 3);
+  const uint8_t* abase = a.rows ? a.x : a.x + static_cast<int64_t>(t.row0) * a.K;
+  const uint64_t a_bytes = a.rows ? static_cast<uint64_t>(a.T) * a.K : static_cast<uint64_t>(t.valid) * a.K;
+  const __amdgpu_buffer_rsrc_t ra =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(abase), 0, static_cast<int>(a_bytes), kBufferFlags);
+  const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(a.w + static_cast<int64_t>(t.e) * a.N * kb), 0, static_cast<int>(a.N * kb), kBufferFlags);
+  uint32_t a_off[kAPieces], b_off[kBPieces];
+#pragma unroll
+  for (int j = 0; j < kAPieces; ++j) {
+    const int lr = wave * (kBM / 4) + j * 8 + (lane >> 3);
+    uint32_t row = lr;
+    if (a.rows) row = max(0, min(a.rows[min(t.row0 + lr, a.R - 1)], static_cast<int>(a.T) - 1));
+    a_off[j] = lr < t.valid ? row * static_cast<uint32_t>(a.K) + (chunk ^ ((lr >> 3) & 1)) * 16 : kPast;
+  }
+  // a row of the tile of w: outputs, for SwiGLU gate and then up
+  auto w_row = [&](int lr, bool* in) {
+    const int n = t.n0 + (kSwiglu ? lr & 63 : lr);
+    *in = n < No;
+    return min(n, No - 1) + (kSwiglu && lr >= 64 ? No : 0);
+  };
+#pragma unroll
+  for (int j = 0; j < kBPieces; ++j) {
+    const int lr = wave * 32 + j * 8 + (lane >> 3);
+    bool in;
+    const uint32_t row = w_row(lr, &in);
+    b_off[j] = in ? row * static_cast<uint32_t>(kb) + (chunk ^ (j & 1)) * 16 : kPast;
+  }
+  // this thread's row of scales: of x, then of w
+  const uint8_t* sp;
+  {
+    if (tid < kBM) {
+      int64_t row = t.row0 + min(tid, t.valid - 1);
+      if (a.rows) row = max(0, min(a.rows[row], static_cast<int>(a.T) - 1));
+      sp = a.xs + row * blocks;
+    } else {
+      bool in;
+      sp = a.ws + (static_cast<int64_t>(t.e) * a.N + w_row(min(tid - kBM, kMidN - 1), &in)) * blocks;
+    }
+  }
+  const int steps = (a.K + BK * kSub - 1) / (BK * kSub);
+  auto load = [&](u32x4* sa, u32x4* sb, int kt) {
+    // (the scalar offsets stay scalar)
+    const int a_at = __builtin_amdgcn_readfirstlane(kt * (BK * kSub)), b_at = __builtin_amdgcn_readfirstlane(kt * 128);
+#pragma unroll
+    for (int u = 0; u < kSub; ++u) {
+      // (chunks c and c ^ 1 are past K together: K is a multiple of 32)
+      const uint32_t past = (kt * kSub + u) * 8 + chunk < a.K / 16 ? 0 : kPast;
+#pragma unroll
+      for (int j = 0; j < kAPieces; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(sa + u * (kBM * 8) + wave * (kBM * 2) + j * 64), 16,
+                                                 a_off[j] | past, a_at + u * BK, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < kBPieces; ++j) {
+      const uint32_t past = kt * 8 + (chunk ^ (j & 1)) < a.K / (kBits == 8 ? 16 : 32) ? 0 : kPast;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(sb + wave * 256 + j * 64), 16, b_off[j] | past, b_at, 0,
+                                               0);
+    }
+  };
+  const int h = lane >> 5, l31 = lane & 31;
+  const int a_row = kHalves ? 0 : (wave >> 1) * (kBM / 2), wn = wave & 1;
+  const int half = kHalves ? wave >> 1 : 0;
+  const int b_row[2] = {kSwiglu ? wn * 32 : wn * 64, kSwiglu ? 64 + wn * 32 : wn * 64 + 32};
+  const int swz = (lane & 7) ^ ((lane >> 3) & 1);
+  floatx16 acc[kI][2];
+#pragma unroll
+  for (int i = 0; i < kI; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int c = 0; c < 16; ++c) acc[i][j][c] = 0.0f;
+  // 64 numbers at a time: q = 0 .. 2 kSub - 1, of which a wave has all, or its half
+  constexpr int kQ = kHalves ? kSub : 2 * kSub;
+  auto multiply = [&](const u32x4* sa, const u32x4* sb, const uint32_t* s) {
+    intx8 fa[kQ][kI], fb[kQ][2];
+    uint32_t fs[kQ][kI], gs[kQ][2];
+#pragma unroll
+    for (int i = 0; i < kQ; ++i) {
+      const int q = kHalves ? half * kSub + i : i;
+      const int u = q >> 1, p = q & 1;
+      // (in 8 bits half p is known to the wave only: its scales are shifted by 16 p)
+      const int shift = 8 * h + (kHalves && kSub == 1 ? 16 * p : 0);
+#pragma unroll
+      for (int m = 0; m < kI; ++m) {
+        const int row = a_row + m * 32 + l31;
+        const u32x4* r = sa + u * (kBM * 8) + row * 8;
+        fa[i][m] = __builtin_shufflevector(__builtin_bit_cast(intx4, r[(4 * p + h) ^ swz]),
+                                           __builtin_bit_cast(intx4, r[(4 * p + 2 + h) ^ swz]), 0, 1, 2, 3, 4, 5, 6, 7);
+        fs[i][m] = s[row * kSub + u] >> shift;
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const u32x4* r = sb + (b_row[j] + l31) * 8;
+        if constexpr (kBits == 8) {
+          fb[i][j] = __builtin_shufflevector(__builtin_bit_cast(intx4, r[(4 * p + h) ^ swz]),
+                                             __builtin_bit_cast(intx4, r[(4 * p + 2 + h) ^ swz]), 0, 1, 2, 3, 4, 5, 6,
+                                             7);
+        } else {
+          const u32x4 v = r[(2 * q + h) ^ swz];
+          fb[i][j] = intx8{static_cast<int>(v[0]), static_cast<int>(v[1]), static_cast<int>(v[2]),
+                           static_cast<int>(v[3]), 0, 0, 0, 0};
+        }
+        gs[i][j] = s[(kBM + b_row[j] + l31) * kSub + u] >> shift;
+      }
+    }
+    constexpr int kFormat = kBits == 4 ? 4 : 0;
+#pragma unroll
+    for (int i = 0; i < kQ; ++i)
+#pragma unroll
+      for (int m = 0; m < kI; ++m)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (i % 2 == 0 || kQ == 1)
+            acc[m][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[i][j], fa[i][m], acc[m][j], kFormat, 0, 0,
+                                                                        gs[i][j], 0, fs[i][m]);
+          else
+            acc[m][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[i][j], fa[i][m], acc[m][j], kFormat, 0, 2,
+                                                                        gs[i][j], 2, fs[i][m]);
+        }
+  };
+  // Step kt, in stage kt % kStages: its scales (loaded kStages steps before) go to LDS, its
+  // operands have landed; then the loads of step kt + kStages - 1, into the stage that the
+  // step before has read.
+  Scales<kSub> v[kStages];
+  v[0].load(sp, 0, blocks);
+  auto fill = [&](auto i) {
+    constexpr int k = decltype(i)::value;
+    if constexpr (k + 1 < kStages) {
+      v[k + 1].load(sp, k + 1, blocks);
+      load(sa_of(i), sb_of(i), k);
+      asm volatile("" ::: "memory");
+    }
+  };
+  fill(Index<0>{}), fill(Index<1>{});
+  auto stage = [&](auto i, int kt) {
+    constexpr int k = decltype(i)::value;
+    if constexpr (k < kStages) {
+      if (tid < kBM + kMidN) v[k].store(sc[k] + tid * kSub, kt, blocks);
+      // sent since this step's operands: scales and operands of kStages - 2 steps
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm((kLoads + 1) * (kStages - 2), true));
+      barrier();
+      v[k].load(sp, kt + kStages, blocks);
+      constexpr int next = (k + kStages - 1) % kStages;
+      load(sa_of(Index<next>{}), sb_of(Index<next>{}), kt + kStages - 1);
+      multiply(sa_of(i), sb_of(i), sc[k]);
+    }
+  };
+  int kt = 0;
+#pragma clang loop unroll(disable)
+  for (; kt + kStages <= steps; kt += kStages)
+    stage(Index<0>{}, kt), stage(Index<1>{}, kt + 1), stage(Index<2>{}, kt + 2);
+  // The last steps, fewer than kStages: everything they need has been sent.
+  auto put = [&](auto i) {
+    constexpr int k = decltype(i)::value;
+    if constexpr (k + 1 < kStages) {
+      if (kt + k < steps && tid < kBM + kMidN) v[k].store(sc[k] + tid * kSub, kt + k, blocks);
+    }
+  };
+  put(Index<0>{}), put(Index<1>{});
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0, true));   // (loads past the last k-tile, too)
+  barrier();
+  auto rest = [&](auto i) {
+    constexpr int k = decltype(i)::value;
+    if constexpr (k + 1 < kStages) {
+      if (kt + k < steps) multiply(sa_of(i), sb_of(i), sc[k]);
+    }
+  };
+  rest(Index<0>{}), rest(Index<1>{});
+  settle(acc[0][0]);
+#pragma unroll
+  for (int m = 1; m < 2 * kI; ++m) settled(acc[m >> 1][m & 1]);
+  if constexpr (kHalves) {
+    float* sum = reinterpret_cast<float*>(b0);    // a block of 32 x 32 for each of two waves
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      __syncthreads();
+      floatx4* mine = reinterpret_cast<floatx4*>(sum) + wn * 256 + lane;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (half == 1)
+          mine[c * 64] = floatx4{acc[0][j][4 * c], acc[0][j][4 * c + 1], acc[0][j][4 * c + 2], acc[0][j][4 * c + 3]};
+      __syncthreads();
+      if (half == 0) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const floatx4 o = mine[c * 64];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) acc[0][j][4 * c + b] += o[b];
+        }
+      }
+    }
+    if (half == 1) return;
+  }
+#pragma unroll
+  for (int i = 0; i < kI; ++i) {
+    const int lr = a_row + i * 32 + l31;
+    if constexpr (kSwiglu) {
+      floatx16 v;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) v[c] = swiglu<false>(acc[i][0][c], acc[i][1][c]);
+      store_block<kMxOut>(a, t.row0 + lr, lr < t.valid, t.n0 + b_row[0], No, h, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        store_block<kMxOut>(a, t.row0 + lr, lr < t.valid, t.n0 + b_row[j], No, h, acc[i][j]);
+    }
+  }
+#endif  // __HIP_DEVICE_COMPILE__
+}
+
+template <int kBits, int kBM, int kStages>
+void launch_mid(const tr_expert_desc& d, const MxArgs& a, hipStream_t st) {
+  const int64_t outs = d.swiglu ? d.N / 2 : d.N;
+  const int64_t tiles = (d.R / kBM + d.E) * cdiv(outs, d.swiglu ? 64 : 128);   // at most
+  const uint32_t blocks = static_cast<uint32_t>(cdiv(tiles, 8) * 8);
+  if (d.swiglu && d.out) mx_mid<kBits, kBM, kStages, true, true><<<blocks, kThreads, 0, st>>>(a);
+  else if (d.swiglu) mx_mid<kBits, kBM, kStages, true, false><<<blocks, kThreads, 0, st>>>(a);
+  else if (d.out) mx_mid<kBits, kBM, kStages, false, true><<<blocks, kThreads, 0, st>>>(a);
+  else mx_mid<kBits, kBM, kStages, false, false><<<blocks, kThreads, 0, st>>>(a);
 }
 
 template <int kBits>
@@ -517,21 +873,50 @@ void launch(const tr_expert_desc& d, const MxArgs& a, hipStream_t st) {
 
 }  // namespace
 
-// Whether the tiles take experts of this call: gathered rows are addressed with 31 bits,
-// tiles are numbered with 31.
-bool expert_can_tile(const tr_expert_desc& d, bool gather) {
-  const int64_t tiles = (cdiv(d.R, BM) + d.E) * cdiv(d.swiglu ? d.N / 2 : d.N, d.swiglu ? BN / 2 : BN);
-  return (!gather || d.T * d.K < (int64_t{1} << 31)) && tiles < (int64_t{1} << 30);
+// Which kernel, by what is known on the host: the experts with a row are at most
+// min(E, R), and have some R / min(E, R) rows each (tiles: half an m-tile of each expert is
+// empty; an n-tile is 128 or 256 rows of w). Measured, us a pass:
+//  - ROWS (a CU's weights in one burst, K shared by its waves) where one block a CU has all:
+//    1 expert of 8 rows, 7168 x 7168: 12.5 (8 bits), 10.0 (4), against 23.8 and 15.7 with 32-row
+//    tiles; 8 experts of a row, 7168 x 4096: 55, against 50.
+//  - 256-row tiles from 48 rows an expert, with tiles for half the CUs: 32 experts, 7168 x
+//    4096, 1024 / 2048 / 4096 rows: 200 / 205 / 226, against 200 / 278 / 380 with 64-row tiles;
+//    2 experts, 4096 x 4096, 1000 / 2000 / 4000 rows (80, 144, 272 tiles): 59 / 60 / 82, against
+//    34 / 62 / 129.
+//  - of the others 32-row tiles for up to 20 rows an expert, or where 64-row tiles are for
+//    less than half the CUs: 32 experts, 7168 x 4096, 256 / 1024 rows: 181 / 250, against
+//    184 / 200 with 64-row tiles; 1 expert of 64 rows, 7168 x 7168: 26, against 31.
+tr_expert_kernel expert_kernel(const tr_expert_desc& d, bool gather) {
+  const int64_t outs = d.swiglu ? d.N / 2 : d.N;
+  // (gathered rows are addressed with 31 bits, tiles are numbered with 31)
+  const int64_t most = (cdiv(d.R, 32) + d.E) * cdiv(outs, d.swiglu ? 64 : 128);
+  const bool tiles = d.K >= 256 && (!gather || d.T * d.K < (int64_t{1} << 31)) && most < (int64_t{1} << 30);
+  if (d.kernel == TR_EXPERT_ROWS || (d.kernel == TR_EXPERT_AUTO && !tiles)) return TR_EXPERT_ROWS;
+  if (!tiles) return TR_EXPERT_AUTO;
+  if (d.kernel != TR_EXPERT_AUTO) return static_cast<tr_expert_kernel>(d.kernel);
+  const int64_t cus = device_cu_count(), experts = d.R < d.E ? d.R : d.E;
+  if (d.R <= 16 && experts * cdiv(outs, d.swiglu && !d.out ? 16 : 32) <= cus) return TR_EXPERT_ROWS;
+  auto m_tiles = [&](int64_t rows) {
+    const int64_t m = d.R / rows + (experts + 1) / 2;
+    return m > experts ? m : experts;
+  };
+  if (d.R >= 48 * experts && m_tiles(256) * cdiv(outs, d.swiglu ? 128 : 256) * 2 >= cus) return TR_EXPERT_TILE256;
+  if (d.R <= 20 * experts || m_tiles(64) * cdiv(outs, d.swiglu ? 64 : 128) * 2 <= cus) return TR_EXPERT_TILE32;
+  return TR_EXPERT_TILE64;
 }
 
-hipError_t expert_tiles(const tr_expert_desc& d, const void* x, const void* xs, const void* w, const void* ws,
-                        const int* offsets, const int* rows, void* y, void* ys, int least, hipStream_t st) {
+hipError_t expert_tiles(const tr_expert_desc& d, tr_expert_kernel kernel, const void* x, const void* xs,
+                        const void* w, const void* ws, const int* offsets, const int* rows, void* y, void* ys,
+                        hipStream_t st) {
   const MxArgs a{static_cast<const uint8_t*>(x), static_cast<const uint8_t*>(xs),
                  static_cast<const uint8_t*>(w), static_cast<const uint8_t*>(ws), offsets, rows, y,
                  static_cast<uint8_t*>(ys), d.T, static_cast<int>(d.R), static_cast<int>(d.K),
-                 static_cast<int>(d.N), d.E, least};
-  if (d.bits == 4) launch<4>(d, a, st);
-  else launch<8>(d, a, st);
+                 static_cast<int>(d.N), d.E};
+  // (stages: as many as leave room for two blocks on a CU)
+  const bool four = d.bits == 4;
+  if (kernel == TR_EXPERT_TILE32) four ? launch_mid<4, 32, 3>(d, a, st) : launch_mid<8, 32, 3>(d, a, st);
+  else if (kernel == TR_EXPERT_TILE64) four ? launch_mid<4, 64, 2>(d, a, st) : launch_mid<8, 64, 3>(d, a, st);
+  else four ? launch<4>(d, a, st) : launch<8>(d, a, st);
   return hipGetLastError();
 }
 

@@ -124,15 +124,15 @@ hipError_t rms_norm(const tr_norm_desc& d, const void* x, const void* residual, 
                     void* residual_out, void* q, void* s, hipStream_t st);
 hipError_t quantize_mx(int64_t rows, int64_t K, bool f32, int bits, const void* x, void* q, void* s,
                        hipStream_t st);
-// Experts with at most this many rows have their weights streamed, the others are tiled.
-constexpr int kMxFewRows = 64;
-// Experts with 1 to `most` rows.
+// The kernel for a call's sizes (its tr_expert_kernel, or by rule), TR_EXPERT_AUTO where the
+// one that it names does not take them.
+tr_expert_kernel expert_kernel(const tr_expert_desc& d, bool gather);
+// TR_EXPERT_ROWS, and the others.
 hipError_t expert_few(const tr_expert_desc& d, const void* x, const void* xs, const void* w, const void* ws,
-                      const int* offsets, const int* rows, void* y, void* ys, int most, hipStream_t st);
-// Experts with `least` rows and more.
-bool expert_can_tile(const tr_expert_desc& d, bool gather);
-hipError_t expert_tiles(const tr_expert_desc& d, const void* x, const void* xs, const void* w, const void* ws,
-                        const int* offsets, const int* rows, void* y, void* ys, int least, hipStream_t st);
+                      const int* offsets, const int* rows, void* y, void* ys, hipStream_t st);
+hipError_t expert_tiles(const tr_expert_desc& d, tr_expert_kernel kernel, const void* x, const void* xs,
+                        const void* w, const void* ws, const int* offsets, const int* rows, void* y, void* ys,
+                        hipStream_t st);
 hipError_t linear_mx4(const tr_linear4_desc& d, const void* x, const void* w, const void* ws, void* y,
                       hipStream_t st);
 

@@ -66,4 +66,13 @@ __device__ __forceinline__ floatx2 mx_pair_f32(uint32_t v, float scale) {
     return __builtin_bit_cast(floatx2, __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(v, scale, kI != 0));
 }
 
+// Between matrix instructions and the first read of what they wrote: with 19 wait states
+// after a v_mfma_scale_f32_32x32x64_f8f6f4, which is what the compiler leaves, the last of
+// its 16 registers has been read before it was written. `acc`, and what later calls name,
+// is read after 48.
+__device__ __forceinline__ void settle(floatx16& acc) {
+  asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15" : "+a"(acc));
+}
+__device__ __forceinline__ void settled(floatx16& acc) { asm volatile("" : "+a"(acc)); }
+
 }  // namespace tr
