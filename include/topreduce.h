@@ -486,12 +486,17 @@ typedef struct tr_linear4_desc {
     int32_t reserved;      /* 0 */
 } tr_linear4_desc;
 
+/* Bytes of device workspace of moe_linear_mx4, 256 where it needs none (ws may then be
+ * NULL). 0 and the last error if desc is invalid. */
+size_t moe_linear_mx4_workspace(const tr_linear4_desc* desc);
+
 /* y[t][n] = sum over k of x[t][k] w[n][k], weights in 4 bits. x: device [T, K] of dtype;
- * w: device [N, K / 2] bytes; ws: device [N, K / 32] bytes; y: device [T, N], must not
- * overlap x. Sums are fp32, y is rounded once. For few rows (the weights are read once
- * for every 64). */
-tr_status moe_linear_mx4(const tr_linear4_desc* desc, const void* x, const void* w, const void* ws, void* y,
-                         hipStream_t stream);
+ * wq: device [N, K / 2] bytes; wscale: device [N, K / 32] bytes; y: device [T, N], must not
+ * overlap x. Sums are fp32, y is rounded once. Every product counts in full. ws: device,
+ * 256-byte aligned, its contents before and after of no meaning. For few rows: up to 16
+ * the time is that of reading the weights. */
+tr_status moe_linear_mx4(const tr_linear4_desc* desc, const void* x, const void* wq, const void* wscale, void* y,
+                         void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* The whole layer of a plan, as moe_forward, with rows and weights in 8 bits (or weights
  * in 4): moe_expert_linear with swiglu over the plan's segments, its result in 8 bits in

@@ -103,21 +103,29 @@ def test_expert_refusals():
 def test_linear4_refusals():
     lib = tr.load_library()
     d0 = dict(T=4, K=64, N=48, dtype=B.BF16, reserved=0)
-    a0 = dict(x=FAKE, w=FAKE + (1 << 20), ws=FAKE + (2 << 20), y=FAR)
+    a0 = dict(x=FAKE, w=FAKE + (1 << 20), wscale=FAKE + (2 << 20), y=FAR, ws=FAKE + (4 << 20), n=1 << 40)
 
     def call(d, a):
         return lib.moe_linear_mx4(C.byref(B.Linear4Desc(**{**d0, **d})), *{**a0, **a}.values(), None)
 
     for d, status in ((dict(T=-1), -1), (dict(T=1 << 31), -2), (dict(K=0), -1), (dict(K=16), -2),
                       (dict(K=(1 << 22) + 32), -2), (dict(N=0), -1), (dict(N=(1 << 22) + 1), -2),
-                      (dict(dtype=2), -1), (dict(reserved=1), -1)):
+                      (dict(T=1 << 30, N=1 << 11), -2), (dict(dtype=2), -1), (dict(reserved=1), -1)):
         assert call(d, {}) == status, d
         assert lib.moe_last_error()
-    for a in (dict(x=None), dict(w=None), dict(ws=None), dict(y=None), dict(x=FAKE + 8), dict(w=FAKE + 4),
+        assert lib.moe_linear_mx4_workspace(C.byref(B.Linear4Desc(**{**d0, **d}))) == 0
+    for a in (dict(x=None), dict(w=None), dict(wscale=None), dict(y=None), dict(x=FAKE + 8), dict(w=FAKE + 4),
               dict(y=FAR + 2), dict(y=FAKE + 496)):
         assert call({}, a) == -1, a
     assert lib.moe_linear_mx4(None, *a0.values(), None) == -1
-    assert call(dict(T=0), {k: None for k in a0}) == 0
+    assert call(dict(T=0), {k: v if k == "n" else None for k, v in a0.items()}) == 0
+    # some rows, few tiles: a workspace for the parts' sums
+    big = dict(T=40, K=1024, N=256)
+    need = lib.moe_linear_mx4_workspace(C.byref(B.Linear4Desc(**{**d0, **big})))
+    assert need >= 2 * 40 * 256 * 4 and need == tr.linear_mx4_workspace_size(40, 1024, 256)
+    for a, status in ((dict(ws=None), -1), (dict(ws=FAKE + 128), -1), (dict(n=need - 1), -3)):
+        assert call(big, a) == status, a
+    assert tr.linear_mx4_workspace_size(4, 64, 48) == 256
 
 
 def test_forward_refusals():

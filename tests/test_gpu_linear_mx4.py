@@ -23,7 +23,9 @@ def case(T, K, N, dtype):
 @pytest.mark.parametrize("T,K,N", [
     (1, 32, 1), (1, 7168, 256), (2, 96, 33), (3, 1440, 1001), (15, 160, 64), (16, 512, 500), (17, 2880, 66),
     (33, 1056, 129), (64, 1024, 256), (65, 256, 48), (130, 4096, 40), (1, 4128, 300), (7, 128, 4), (5, 640, 2),
-    (500, 352, 70),
+    (500, 352, 70), (17, 256, 128), (20, 7168, 300), (32, 768, 129), (33, 512, 1000), (64, 7168, 130),
+    (100, 1600, 384), (64, 2880, 2050), (200, 288, 520), (70, 8192, 17), (600, 1024, 4100), (8, 8480, 40),
+    (16, 16416, 33), (4, 16384, 50),
 ])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_linear(T, K, N, dtype):
@@ -38,9 +40,9 @@ def test_linear(T, K, N, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("T", [1, 9, 70])
-def test_rows_stand_alone(T, dtype):
-    x, w = case(T, 256, 96, dtype)
+@pytest.mark.parametrize("T,K", [(1, 256), (9, 256), (30, 544), (70, 256), (70, 800), (2, 224)])
+def test_rows_stand_alone(T, K, dtype):
+    x, w = case(T, K, 96, dtype)
     w = (w[0].cuda(), w[1].cuda())
     clean = tr.linear_mx4(x.cuda(), w)
     bad = x.clone()
@@ -58,3 +60,17 @@ def test_rows_stand_alone(T, dtype):
 def test_no_rows():
     _, w = case(1, 64, 32, BF)
     assert tr.linear_mx4(torch.empty(0, 64, dtype=BF, device="cuda"), (w[0].cuda(), w[1].cuda())).shape == (0, 32)
+
+
+def test_a_workspace_of_the_callers():
+    x, w = case(40, 1024, 256, BF)
+    x, w = x.cuda(), (w[0].cuda(), w[1].cuda())
+    want = tr.linear_mx4(x, w)
+    n = tr.linear_mx4_workspace_size(40, 1024, 256)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    y = torch.empty_like(want)
+    assert tr.linear_mx4(x, w, y=y, ws=ws) is y and torch.equal(y, want)
+    with pytest.raises(tr.TopReduceError):
+        tr.linear_mx4(x, w, ws=ws[:256])
+    # one that is not needed may be there all the same
+    assert torch.equal(tr.linear_mx4(x[:3].contiguous(), w, ws=ws), tr.linear_mx4(x[:3].contiguous(), w))

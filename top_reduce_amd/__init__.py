@@ -70,6 +70,7 @@ from ._mx import (  # noqa: F401
     expert_linear,
     forward_mx,
     linear_mx4,
+    linear_mx4_workspace_size,
     quantize_mx,
     rms_norm,
 )

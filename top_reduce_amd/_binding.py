@@ -160,7 +160,9 @@ def load_library():
     lib.moe_expert_linear.restype = st
     lib.moe_expert_linear.argtypes = [C.POINTER(ExpertDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.moe_linear_mx4.restype = st
-    lib.moe_linear_mx4.argtypes = [C.POINTER(Linear4Desc), vp, vp, vp, vp, vp]
+    lib.moe_linear_mx4.argtypes = [C.POINTER(Linear4Desc), vp, vp, vp, vp, vp, C.c_size_t, vp]
+    lib.moe_linear_mx4_workspace.restype = C.c_size_t
+    lib.moe_linear_mx4_workspace.argtypes = [C.POINTER(Linear4Desc)]
     lib.moe_forward_mx.restype = st
     lib.moe_forward_mx.argtypes = [C.POINTER(PlanStruct), vp, vp, vp, i32, vp, vp, vp, vp, vp, vp]
     lib.moe_plan_stats.restype = st

@@ -16,11 +16,12 @@ from typing import NamedTuple, Optional, Tuple, Union
 import torch
 
 from . import _binding as B
-from ._binding import (_arg, _check, _dev_tensor, _dtype_code, _elsewhere, _raw_stream, _run_on,
-                       _x_arg)
+from ._binding import (_arg, _check, _dev_tensor, _dtype_code, _elsewhere, _need, _raw_stream, _run_on,
+                       _ws_arg, _x_arg)
 
 E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 BLOCK = 32
+NO_WS = 256     # the size of a workspace that is not needed
 KERNELS = {"auto": 0, "rows": 1, "tile32": 2, "tile64": 3, "tile256": 4}
 
 Mx = Tuple[torch.Tensor, torch.Tensor]
@@ -44,6 +45,14 @@ def _launch(dev, call, *args) -> None:
             status = getattr(lib, call)(*args, _raw_stream(dev))
     if status:
         _check(status)
+
+
+def _out(t: Optional[torch.Tensor], name: str, dtype, shape, dev) -> Tuple[torch.Tensor, int]:
+    """An output that the caller gives, checked, or a new one; and its address."""
+    if t is None:
+        t = torch.empty(*shape, dtype=dtype, device=dev)
+        return t, t.data_ptr()
+    return t, _arg(t, name, dtype, shape, dev)
 
 
 def _pair(t, name: str) -> Mx:
@@ -80,12 +89,8 @@ def quantize_mx(x: torch.Tensor, bits: int = 8, q: Optional[torch.Tensor] = None
     if K % BLOCK:
         raise ValueError(f"rows of {K} have no whole blocks of {BLOCK}")
     qt, qs = (E4M3, (*lead, K)) if bits == 8 else (torch.uint8, (*lead, K // 2))
-    if q is None:
-        q = torch.empty(qs, dtype=qt, device=dev)
-    if s is None:
-        s = torch.empty((*lead, K // BLOCK), dtype=E8M0, device=dev)
-    qp = _arg(q, "q", qt, qs, dev)
-    sp = _arg(s, "s", E8M0, (*lead, K // BLOCK), dev)
+    q, qp = _out(q, "q", qt, qs, dev)
+    s, sp = _out(s, "s", E8M0, (*lead, K // BLOCK), dev)
     rows = x.numel() // K if K else 0
     if rows:
         _launch(dev, "moe_quantize_mx", rows, K, code, bits, x.data_ptr(), qp, sp)
@@ -121,27 +126,19 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     wp = _arg(weight, "weight", dt, (H,), dev)
     yp = qp = sp = rp = op = None
     if out != "mx8":
-        if y is None:
-            y = torch.empty_like(x)
-        yp = _arg(y, "y", dt, (T, H), dev)
+        y, yp = _out(y, "y", dt, (T, H), dev)
     elif y is not None:
         raise ValueError("y is given, and out is 'mx8'")
     if out != "same":
         if H % BLOCK:
             raise ValueError(f"rows of {H} have no whole blocks of {BLOCK}")
-        if q is None:
-            q = torch.empty(T, H, dtype=E4M3, device=dev)
-        if s is None:
-            s = torch.empty(T, H // BLOCK, dtype=E8M0, device=dev)
-        qp = _arg(q, "q", E4M3, (T, H), dev)
-        sp = _arg(s, "s", E8M0, (T, H // BLOCK), dev)
+        q, qp = _out(q, "q", E4M3, (T, H), dev)
+        s, sp = _out(s, "s", E8M0, (T, H // BLOCK), dev)
     elif q is not None or s is not None:
         raise ValueError("q or s is given, and out is 'same'")
     if residual is not None:
         rp = _arg(residual, "residual", dt, (T, H), dev)
-        if residual_out is None:
-            residual_out = torch.empty_like(x)
-        op = _arg(residual_out, "residual_out", dt, (T, H), dev)
+        residual_out, op = _out(residual_out, "residual_out", dt, (T, H), dev)
     elif residual_out is not None:
         raise ValueError("residual_out is given without a residual")
     if T:
@@ -200,48 +197,52 @@ def expert_linear(x: Mx, w: Mx, offsets: torch.Tensor, rows: Optional[torch.Tens
     if out == "bf16":
         if ys is not None:
             raise ValueError("ys is given, and out is 'bf16'")
-        if y is None:
-            y = torch.empty(R, outs, dtype=torch.bfloat16, device=dev)
-        yp = _arg(y, "y", torch.bfloat16, (R, outs), dev)
+        y, yp = _out(y, "y", torch.bfloat16, (R, outs), dev)
     else:
         if outs % BLOCK:
             raise ValueError(f"rows of {outs} outputs have no whole blocks of {BLOCK}")
-        if y is None:
-            y = torch.empty(R, outs, dtype=E4M3, device=dev)
-        if ys is None:
-            ys = torch.empty(R, outs // BLOCK, dtype=E8M0, device=dev)
-        yp = _arg(y, "y", E4M3, (R, outs), dev)
-        ysp = _arg(ys, "ys", E8M0, (R, outs // BLOCK), dev)
+        y, yp = _out(y, "y", E4M3, (R, outs), dev)
+        ys, ysp = _out(ys, "ys", E8M0, (R, outs // BLOCK), dev)
     _launch(dev, "moe_expert_linear", desc, xp, xsp, wp, wsp, op, rp, yp, ysp)
     return y if out == "bf16" else (y, ys)
 
 
 @functools.lru_cache(maxsize=512)
-def _linear4_desc(T, K, N, dtype):
-    return C.byref(B.Linear4Desc(T=T, K=K, N=N, dtype=_dtype_code(dtype), reserved=0))
+def _linear4_plan(T, K, N, dtype):
+    d = B.Linear4Desc(T=T, K=K, N=N, dtype=_dtype_code(dtype), reserved=0)
+    return C.byref(d), _need(B.load_library().moe_linear_mx4_workspace, d)
 
 
-def linear_mx4(x: torch.Tensor, w: Mx, y: Optional[torch.Tensor] = None,
+def linear_mx4_workspace_size(T: int, K: int, N: int, dtype=torch.bfloat16) -> int:
+    """Bytes of ws for linear_mx4 of these sizes."""
+    return _linear4_plan(T, K, N, dtype)[1]
+
+
+def linear_mx4(x: torch.Tensor, w: Mx, y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """moe_linear_mx4: y [T, N] = x w^T for a few rows x [T, K] (bfloat16 or float32) and
     weights in 4 bits, w = (q [N, K/2] uint8, s [N, K/32])."""
     dev = _x_arg(x)
-    wq, ws = _pair(w, "w")
+    wq, wscale = _pair(w, "w")
     if _elsewhere(stream, dev):
-        return _run_on(stream, (y,), linear_mx4, x, w, y)
+        return _run_on(stream, (y,), linear_mx4, x, w, y, ws)
     if wq.dim() != 2:
         raise ValueError("w must hold an [N, K/2] tensor")
     T, K = x.shape
     N, dt = wq.shape[0], x.dtype
     if K % BLOCK:
         raise ValueError(f"rows of {K} have no whole blocks of {BLOCK}")
-    desc = _linear4_desc(T, K, N, dt)
+    desc, need = _linear4_plan(T, K, N, dt)
     wp = _arg(wq, "w", torch.uint8, (N, K // 2), dev)
-    wsp = _arg(ws, "w's scales", E8M0, (N, K // BLOCK), dev)
-    if y is None:
-        y = torch.empty(T, N, dtype=dt, device=dev)
-    yp = _arg(y, "y", dt, (T, N), dev)
-    _launch(dev, "moe_linear_mx4", desc, x.data_ptr(), wp, wsp, yp)
+    sp = _arg(wscale, "w's scales", E8M0, (N, K // BLOCK), dev)
+    y, yp = _out(y, "y", dt, (T, N), dev)
+    if not T:
+        return y
+    if ws is None and need == NO_WS:
+        _launch(dev, "moe_linear_mx4", desc, x.data_ptr(), wp, sp, yp, None, 0)
+    else:
+        ws = _ws_arg(ws, need, dev)
+        _launch(dev, "moe_linear_mx4", desc, x.data_ptr(), wp, sp, yp, ws.data_ptr(), ws.numel())
     return y
 
 
@@ -268,8 +269,6 @@ def forward_mx(p: B.MoePlan, x: Mx, topk_weights: Optional[torch.Tensor], w1: Mx
     s2p = _arg(s2, "w2's scales", E8M0, (d.E, d.H, d.I // BLOCK), dev)
     wp = None if topk_weights is None else _arg(topk_weights, "topk_weights", torch.float32,
                                                 (d.T, d.K), dev)
-    if y is None:
-        y = torch.empty(d.T, d.H, dtype=torch.bfloat16, device=dev)
-    yp = _arg(y, "y", torch.bfloat16, (d.T, d.H), dev)
+    y, yp = _out(y, "y", torch.bfloat16, (d.T, d.H), dev)
     _launch(dev, "moe_forward_mx", C.byref(p.struct), xp, xsp, wp, bits, w1p, s1p, w2p, s2p, yp)
     return y

@@ -22,7 +22,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libtopreduce.so")
 
 SOURCES = ["api.hip", "route_scan.hip", "expand.hip", "grouped_gemm.hip", "combine_reduce.hip",
-           "compact.hip", "linear.hip", "router.hip", "layer_few.hip", "norm.hip", "mx_few.hip", "mx_gemm.hip"]
+           "compact.hip", "linear.hip", "router.hip", "layer_few.hip", "norm.hip", "mx_few.hip", "mx_gemm.hip",
+           "mx_linear.hip"]
 ARCH = os.environ.get("TOP_REDUCE_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall",

@@ -728,6 +728,21 @@ tr_status check_expert_desc(const tr_expert_desc* d) {
   return TR_OK;
 }
 
+tr_status check_linear4_desc(const tr_linear4_desc* d) {
+  if (!d) return fail(TR_EINVAL, "desc is NULL");
+  if (d->T < 0) return fail(TR_EINVAL, "T must be >= 0 (got %lld)", (long long)d->T);
+  if (d->N < 1) return fail(TR_EINVAL, "N must be >= 1 (got %lld)", (long long)d->N);
+  if (d->dtype != TR_BF16 && d->dtype != TR_F32) return fail(TR_EINVAL, "unknown dtype %d", d->dtype);
+  if (d->reserved != 0) return fail(TR_EINVAL, "reserved must be 0");
+  const tr_status s = check_k(d->K, "K");
+  if (s != TR_OK) return s;
+  if (d->N > (int64_t{1} << 22)) return fail(TR_EUNSUPPORTED, "N must be at most 2^22");
+  if (d->T > kMostRows) return fail(TR_EUNSUPPORTED, "T must be < 2^31");
+  // sums of parts are a launch of a thread a number
+  if (d->T > (int64_t{1} << 40) / d->N) return fail(TR_EUNSUPPORTED, "T * N must be at most 2^40");
+  return TR_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -810,26 +825,28 @@ tr_status moe_expert_linear(const tr_expert_desc* desc, const void* x, const voi
   return hip_status(h, "moe_expert_linear launch");
 }
 
-tr_status moe_linear_mx4(const tr_linear4_desc* desc, const void* x, const void* w, const void* ws, void* y,
-                         hipStream_t stream) {
-  if (!desc) return fail(TR_EINVAL, "desc is NULL");
-  const tr_linear4_desc& d = *desc;
-  if (d.T < 0) return fail(TR_EINVAL, "T must be >= 0 (got %lld)", (long long)d.T);
-  if (d.N < 1) return fail(TR_EINVAL, "N must be >= 1 (got %lld)", (long long)d.N);
-  if (d.dtype != TR_BF16 && d.dtype != TR_F32) return fail(TR_EINVAL, "unknown dtype %d", d.dtype);
-  if (d.reserved != 0) return fail(TR_EINVAL, "reserved must be 0");
-  tr_status e = check_k(d.K, "K");
+size_t moe_linear_mx4_workspace(const tr_linear4_desc* desc) {
+  if (check_linear4_desc(desc) != TR_OK) return 0;
+  ok();
+  const size_t n = tr::linear4_workspace(*desc);
+  return n ? n : kAlign;
+}
+
+tr_status moe_linear_mx4(const tr_linear4_desc* desc, const void* x, const void* wq, const void* wscale, void* y,
+                         void* ws, size_t ws_bytes, hipStream_t stream) {
+  tr_status e = check_linear4_desc(desc);
   if (e != TR_OK) return e;
-  if (d.N > (int64_t{1} << 22)) return fail(TR_EUNSUPPORTED, "N must be at most 2^22");
-  if (d.T > kMostRows) return fail(TR_EUNSUPPORTED, "T must be < 2^31");
+  const tr_linear4_desc& d = *desc;
+  const size_t need = tr::linear4_workspace(d);
+  if (need && (e = check_ws(ws, ws_bytes, need)) != TR_OK) return e;
   if (d.T == 0) return ok();
   if ((e = check_buf(x, "x", true)) != TR_OK) return e;
-  if ((e = check_buf(w, "w", true)) != TR_OK) return e;
+  if ((e = check_buf(wq, "wq", true)) != TR_OK) return e;
   if ((e = check_buf(y, "y", true)) != TR_OK) return e;
-  if (!ws) return fail(TR_EINVAL, "ws is NULL");
+  if (!wscale) return fail(TR_EINVAL, "wscale is NULL");
   const int64_t es = d.dtype == TR_BF16 ? 2 : 4;
   if (overlap(y, es * d.T * d.N, x, es * d.T * d.K)) return fail(TR_EINVAL, "y must not overlap x");
-  return hip_status(tr::linear_mx4(d, x, w, ws, y, stream), "moe_linear_mx4 launch");
+  return hip_status(tr::linear_mx4(d, x, wq, wscale, y, ws, stream), "moe_linear_mx4 launch");
 }
 
 tr_status moe_forward_mx(const tr_moe_plan* plan, const void* x, const void* xs, const float* topk_weights,

@@ -296,8 +296,9 @@ __global__ __launch_bounds__(kFewWaves* kWave) void few_products(FewArgs a) {
     begin = max(0, min(a.offsets[e], a.R));
     end = max(begin, min(a.offsets[e + 1], a.R));
   }
-  for (int first = begin; first < end; first += 16 * kNT)
-    few_strip<kBits, kRows, kGroups, kNT, kSwiglu, kMxOut>(a, e, first, end, blockIdx.x, part);
+  const int64_t step = static_cast<int64_t>(gridDim.z) * (16 * kNT);
+  for (int64_t first = begin + static_cast<int64_t>(blockIdx.z) * (16 * kNT); first < end; first += step)
+    few_strip<kBits, kRows, kGroups, kNT, kSwiglu, kMxOut>(a, e, static_cast<int>(first), end, blockIdx.x, part);
 }
 
 // --------------------------------------------------------------------------
@@ -312,16 +313,6 @@ constexpr int kPhase = 8192, kScalePitch = kPhase / kMxBlock + 16;   // (16 rows
 __device__ u32x4 few_zeros[1];     // what is loaded in place of numbers past K (never written)
 
 #if defined(__HIP_DEVICE_COMPILE__)
-constexpr int kBufferFlags = 0x00020000;      // raw buffer, 32-bit data format
-constexpr uint32_t kPast = 0x80000000u;       // an offset past every buffer here
-typedef __attribute__((address_space(3))) void lds_void;
-typedef const __attribute__((address_space(1))) void global_void;
-
-template <int k>
-struct Index {
-  static constexpr int value = k;
-};
-
 // 16 scale bytes of a row from block `at` on, 0 past the last.
 __device__ __forceinline__ u32x4 load_scales16(const uint8_t* row, int at, int blocks) {
   if (blocks >= 16) {
@@ -385,7 +376,7 @@ __global__ __launch_bounds__(kWaves* kWave) void stream_products(FewArgs a) {
   const uint64_t left = static_cast<uint64_t>(a.N - n0) * wbytes;
   const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(a.w + (static_cast<int64_t>(e) * a.N + n0) * wbytes), 0,
-      static_cast<int>(left < 0x7fffffff ? left : 0x7fffffff), kBufferFlags);
+      static_cast<int>(left < 0x7fffffff ? left : 0x7fffffff), kRawBuffer);
   uint32_t w_off[kWLoads];
 #pragma unroll
   for (int j = 0; j < kWLoads; ++j)
@@ -509,7 +500,7 @@ __global__ __launch_bounds__(kWaves* kWave) void stream_products(FewArgs a) {
     // A k-tile: it has landed (sent since: kStages - 2 others); the next one not yet sent
     // goes where the one before lay, which this wave has read.
     auto one = [&](u32x4* st, u32x4* next, int kt) {
-      __builtin_amdgcn_s_waitcnt(((kLoads * (kStages - 2)) & 15) | (((kLoads * (kStages - 2)) >> 4) << 14) | (7 << 4) | (15 << 8));
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLoads * (kStages - 2), false));
       asm volatile("" ::: "memory");
       load(next, kt + kStages - 1);
       multiply(st, kt);
@@ -547,7 +538,11 @@ struct Launch {
   }
   template <int kNT>
   static void few(const FewArgs& a, int E, hipStream_t st) {
-    few_products<kBits, kRows, kGroups, kNT, kSwiglu, kMxOut><<<grid(a, E), kFewWaves * kWave, 0, st>>>(a);
+    // rows beside each other, too, up to some thousand blocks
+    dim3 g = grid(a, E);
+    const int64_t chunks = cdiv(a.R, 16 * kNT), room = cdiv(4096, static_cast<int64_t>(g.x) * g.y);
+    g.z = static_cast<uint32_t>(chunks < room ? chunks : room);
+    few_products<kBits, kRows, kGroups, kNT, kSwiglu, kMxOut><<<g, kFewWaves * kWave, 0, st>>>(a);
   }
   template <int kXRows, int kWaves, int kStages>
   static void stream(const FewArgs& a, int E, hipStream_t st) {
@@ -601,8 +596,8 @@ hipError_t expert_few(const tr_expert_desc& d, const void* x, const void* xs, co
   return hipGetLastError();
 }
 
-hipError_t linear_mx4(const tr_linear4_desc& d, const void* x, const void* w, const void* ws, void* y,
-                      hipStream_t st) {
+hipError_t linear4_few(const tr_linear4_desc& d, const void* x, const void* w, const void* ws, void* y,
+                       hipStream_t st) {
   const FewArgs a{static_cast<const uint8_t*>(x), nullptr, static_cast<const uint8_t*>(w),
                   static_cast<const uint8_t*>(ws), nullptr, nullptr, y, nullptr, d.T,
                   static_cast<int>(d.T), static_cast<int>(d.K), static_cast<int>(d.N)};

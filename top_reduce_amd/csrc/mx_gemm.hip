@@ -51,10 +51,7 @@ struct MxArgs {
 
 #if defined(__HIP_DEVICE_COMPILE__)
 
-constexpr int kBufferFlags = 0x00020000;      // raw buffer, 32-bit data format
-constexpr uint32_t kPast = 0x80000000u;       // an offset past every buffer here
 typedef int intx8 __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(3))) void lds_void;
 
 // Distinct objects, so that an access to one stage does not wait for loads into the
 // other.
@@ -66,16 +63,6 @@ template <int S>
 __device__ __forceinline__ u32x4* stage_a() { return S == 0 ? g_a0 : g_a1; }
 template <int S>
 __device__ __forceinline__ u32x4* stage_b() { return S == 0 ? g_b0 : g_b1; }
-
-__host__ __device__ constexpr int waitcnt_vm(int n, bool lgkm0) {
-  return (n & 15) | ((n >> 4) << 14) | (7 << 4) | ((lgkm0 ? 0 : 15) << 8);
-}
-
-__device__ __forceinline__ void barrier() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
 
 struct Tile {
   int e, row0, valid, n0;
@@ -119,7 +106,7 @@ __device__ __forceinline__ Source<kBits> source(const MxArgs& a, const Tile& t, 
   // f(r) = (r & 7) ^ (r >> 3 & 1), which keeps 16 rows' reads on different banks
   const uint8_t* base = a.rows ? a.x : a.x + static_cast<int64_t>(t.row0) * a.K;
   const uint64_t a_bytes = a.rows ? static_cast<uint64_t>(a.T) * a.K : static_cast<uint64_t>(t.valid) * a.K;
-  s.a = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, static_cast<int>(a_bytes), kBufferFlags);
+  s.a = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, static_cast<int>(a_bytes), kRawBuffer);
   const int chunk = (lane & 7) ^ (lane >> 3);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -132,7 +119,7 @@ __device__ __forceinline__ Source<kBits> source(const MxArgs& a, const Tile& t, 
   // w: gate rows first, then up
   const uint8_t* wbase = a.w + static_cast<int64_t>(t.e) * a.N * kb;
   const int64_t w_bytes = a.N * kb;
-  s.b = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(wbase), 0, static_cast<int>(w_bytes), kBufferFlags);
+  s.b = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(wbase), 0, static_cast<int>(w_bytes), kRawBuffer);
   const int first = kSwiglu ? t.n0 + (wave & 1) * 64 : t.n0 + wave * 64;   // output of this wave's row 0
   const int up = kSwiglu && wave >= 2 ? No : 0;
   constexpr int kRows = kBits == 8 ? 8 : 16;    // of a piece
@@ -259,13 +246,13 @@ __device__ __forceinline__ void step(Frags<kBits>& f, const Geo& g, const Source
   for (int m = 0; m < 32; ++m) {
     if (m == kFree) {
       __builtin_amdgcn_s_waitcnt(waitcnt_vm(63, true));   // this wave's reads of the stage are done
-      barrier();
+      lds_barrier();
     }
     if (m == kLanded) {
       // what the step before sent has landed
       constexpr int kSent = kLoads < kLanded - kFree ? kLoads : kLanded - kFree;
       __builtin_amdgcn_s_waitcnt(waitcnt_vm(kSent, false));
-      barrier();
+      lds_barrier();
       if constexpr (kScales) {
         // (not shifted, and so not waited for, before this)
         asm volatile("" : "+v"(na.x), "+v"(na.y), "+v"(nb.x), "+v"(nb.y));
@@ -451,7 +438,7 @@ __global__ __launch_bounds__(kThreads) void mx_tiles(MxArgs a) {
     g_sa[0][wave * 64 + lane] = load_scale8(s0.sa, 0, a.K / kMxBlock);
     g_sb[0][wave * 64 + lane] = load_scale8(s0.sb, 0, a.K / kMxBlock);
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0, true));
-    barrier();
+    lds_barrier();
 #pragma unroll
     for (int n = 0; n < 8; ++n) read_frag<0, 0>(f, g, n);
 #pragma unroll
@@ -531,31 +518,6 @@ __global__ __launch_bounds__(kThreads) void mx_tiles(MxArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
 constexpr int kMidN = 128;
 
-template <int k>
-struct Index {
-  static constexpr int value = k;
-};
-
-// The scales of a row's k-tile, kSub dwords, as they lie in memory (K >= 256: the row's last
-// dwords at most), and with 0 for the blocks past the last.
-template <int kSub>
-struct Scales {
-  uint32_t v[kSub];
-  __device__ __forceinline__ void load(const uint8_t* p, int kt, int blocks) {
-    typedef uint32_t Odd __attribute__((ext_vector_type(kSub), aligned(1)));
-    const Odd d = *reinterpret_cast<const Odd*>(p + min(kt * 4 * kSub, blocks - 4 * kSub));
-#pragma unroll
-    for (int u = 0; u < kSub; ++u) v[u] = d[u];
-  }
-  __device__ __forceinline__ void store(uint32_t* p, int kt, int blocks) const {
-    const int over = kt * 4 * kSub - min(kt * 4 * kSub, blocks - 4 * kSub);
-    uint64_t all = v[0];
-    if constexpr (kSub == 2) all |= static_cast<uint64_t>(v[1]) << 32;
-    all = over < 4 * kSub ? all >> (8 * over & 63) : 0;
-    p[0] = static_cast<uint32_t>(all);
-    if constexpr (kSub == 2) p[1] = static_cast<uint32_t>(all >> 32);
-  }
-};
 #endif
 
 template <int kBits, int kBM, int kStages, bool kSwiglu, bool kMxOut>
@@ -644,9 +606,9 @@ __global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
   const uint8_t* abase = a.rows ? a.x : a.x + static_cast<int64_t>(t.row0) * a.K;
   const uint64_t a_bytes = a.rows ? static_cast<uint64_t>(a.T) * a.K : static_cast<uint64_t>(t.valid) * a.K;
   const __amdgpu_buffer_rsrc_t ra =
-      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(abase), 0, static_cast<int>(a_bytes), kBufferFlags);
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(abase), 0, static_cast<int>(a_bytes), kRawBuffer);
   const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t*>(a.w + static_cast<int64_t>(t.e) * a.N * kb), 0, static_cast<int>(a.N * kb), kBufferFlags);
+      const_cast<uint8_t*>(a.w + static_cast<int64_t>(t.e) * a.N * kb), 0, static_cast<int>(a.N * kb), kRawBuffer);
   uint32_t a_off[kAPieces], b_off[kBPieces];
 #pragma unroll
   for (int j = 0; j < kAPieces; ++j) {
@@ -781,7 +743,7 @@ __global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
       if (tid < kBM + kMidN) v[k].store(sc[k] + tid * kSub, kt, blocks);
       // sent since this step's operands: scales and operands of kStages - 2 steps
       __builtin_amdgcn_s_waitcnt(waitcnt_vm((kLoads + 1) * (kStages - 2), true));
-      barrier();
+      lds_barrier();
       v[k].load(sp, kt + kStages, blocks);
       constexpr int next = (k + kStages - 1) % kStages;
       load(sa_of(Index<next>{}), sb_of(Index<next>{}), kt + kStages - 1);
@@ -801,7 +763,7 @@ __global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
   };
   put(Index<0>{}), put(Index<1>{});
   __builtin_amdgcn_s_waitcnt(waitcnt_vm(0, true));   // (loads past the last k-tile, too)
-  barrier();
+  lds_barrier();
   auto rest = [&](auto i) {
     constexpr int k = decltype(i)::value;
     if constexpr (k + 1 < kStages) {

@@ -133,7 +133,10 @@ hipError_t expert_few(const tr_expert_desc& d, const void* x, const void* xs, co
 hipError_t expert_tiles(const tr_expert_desc& d, tr_expert_kernel kernel, const void* x, const void* xs,
                         const void* w, const void* ws, const int* offsets, const int* rows, void* y, void* ys,
                         hipStream_t st);
-hipError_t linear_mx4(const tr_linear4_desc& d, const void* x, const void* w, const void* ws, void* y,
+size_t linear4_workspace(const tr_linear4_desc& d);
+hipError_t linear_mx4(const tr_linear4_desc& d, const void* x, const void* w, const void* ws, void* y, void* scratch,
                       hipStream_t st);
+hipError_t linear4_few(const tr_linear4_desc& d, const void* x, const void* w, const void* ws, void* y,
+                       hipStream_t st);
 
 }  // namespace tr

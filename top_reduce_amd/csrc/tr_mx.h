@@ -66,6 +66,52 @@ __device__ __forceinline__ floatx2 mx_pair_f32(uint32_t v, float scale) {
     return __builtin_bit_cast(floatx2, __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(v, scale, kI != 0));
 }
 
+#if defined(__HIP_DEVICE_COMPILE__)
+constexpr int kRawBuffer = 0x00020000;        // word 3 of a buffer resource: raw, 32-bit data
+constexpr uint32_t kPast = 0x80000000u;       // an offset past every buffer here: reads 0
+typedef __attribute__((address_space(3))) void lds_void;
+typedef const __attribute__((address_space(1))) void global_void;
+
+// s_waitcnt immediate: at most n vector loads in flight, with lgkm no LDS access.
+__host__ __device__ constexpr int waitcnt_vm(int n, bool lgkm) {
+  return (n & 15) | ((n >> 4) << 14) | (7 << 4) | ((lgkm ? 0 : 15) << 8);
+}
+
+// A barrier for LDS that leaves loads to LDS in flight (the caller has waited for those
+// that it needs).
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// The scales of a row's k-tile, kWords times four, as they lie in memory (the row has as
+// many: its last ones at most), and with 0 for the blocks past the last.
+template <int kWords>
+struct Scales {
+  uint32_t v[kWords];
+  __device__ __forceinline__ void load(const uint8_t* row, int kt, int blocks) {
+    typedef uint32_t Odd __attribute__((ext_vector_type(kWords), aligned(1)));
+    const Odd d = *reinterpret_cast<const Odd*>(row + min(kt * 4 * kWords, blocks - 4 * kWords));
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) v[i] = d[i];
+  }
+  __device__ __forceinline__ void store(uint32_t* to, int kt, int blocks) const {
+    const int over = kt * 4 * kWords - min(kt * 4 * kWords, blocks - 4 * kWords);
+    uint64_t all = v[0];
+    if constexpr (kWords == 2) all |= static_cast<uint64_t>(v[1]) << 32;
+    all = over < 4 * kWords ? all >> (8 * over & 63) : 0;
+    to[0] = static_cast<uint32_t>(all);
+    if constexpr (kWords == 2) to[1] = static_cast<uint32_t>(all >> 32);
+  }
+};
+#endif
+
+template <int k>
+struct Index {
+  static constexpr int value = k;
+};
+
 // Between matrix instructions and the first read of what they wrote: with 19 wait states
 // after a v_mfma_scale_f32_32x32x64_f8f6f4, which is what the compiler leaves, the last of
 // its 16 registers has been read before it was written. `acc`, and what later calls name,
