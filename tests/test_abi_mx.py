@@ -120,9 +120,9 @@ def test_linear4_refusals():
     assert lib.moe_linear_mx4(None, *a0.values(), None) == -1
     assert call(dict(T=0), {k: v if k == "n" else None for k, v in a0.items()}) == 0
     # some rows, few tiles: a workspace for the parts' sums
-    big = dict(T=40, K=1024, N=256)
+    big = dict(T=40, K=4096, N=256)
     need = lib.moe_linear_mx4_workspace(C.byref(B.Linear4Desc(**{**d0, **big})))
-    assert need >= 2 * 40 * 256 * 4 and need == tr.linear_mx4_workspace_size(40, 1024, 256)
+    assert need >= 2 * 40 * 256 * 4 and need == tr.linear_mx4_workspace_size(40, 4096, 256)
     for a, status in ((dict(ws=None), -1), (dict(ws=FAKE + 128), -1), (dict(n=need - 1), -3)):
         assert call(big, a) == status, a
     assert tr.linear_mx4_workspace_size(4, 64, 48) == 256

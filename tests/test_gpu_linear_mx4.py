@@ -63,10 +63,10 @@ def test_no_rows():
 
 
 def test_a_workspace_of_the_callers():
-    x, w = case(40, 1024, 256, BF)
+    x, w = case(40, 4096, 256, BF)
     x, w = x.cuda(), (w[0].cuda(), w[1].cuda())
     want = tr.linear_mx4(x, w)
-    n = tr.linear_mx4_workspace_size(40, 1024, 256)
+    n = tr.linear_mx4_workspace_size(40, 4096, 256)
     ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
     y = torch.empty_like(want)
     assert tr.linear_mx4(x, w, y=y, ws=ws) is y and torch.equal(y, want)

@@ -59,6 +59,21 @@ def test_outputs_over_the_inputs(T, H):
     assert torch.equal(a, want.y) and torch.equal(b, want.residual)
 
 
+@pytest.mark.parametrize("T,H,dtype,residual", [(1100, 8192, BF, True), (12000, 8192, BF, True), (9000, 8192, F32, False)])
+def test_large_batches_are_their_rows(T, H, dtype, residual):
+    """Outputs, and inputs, that the caches do not hold."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn(T, H, generator=g, device="cuda").to(dtype)
+    r = torch.randn(T, H, generator=g, device="cuda").to(dtype) if residual else None
+    w = torch.randn(H, generator=g, device="cuda").to(dtype)
+    got = tr.rms_norm(x, w, residual=r, out="both")
+    for a in (0, T // 2, T - 64):
+        some = tr.rms_norm(x[a:a + 64], w, residual=None if r is None else r[a:a + 64], out="both")
+        for u, v in zip(got, some):
+            assert (u is None and v is None) or torch.equal(u[a:a + 64].view(torch.uint8), v.view(torch.uint8))
+    assert torch.isfinite(got.y).all()
+
+
 def test_rows_stand_alone():
     x, r, w = inputs(6, 96, BF, True)
     clean = tr.rms_norm(x.cuda(), w.cuda(), residual=r.cuda(), out="both")

@@ -6,7 +6,7 @@
 //
 // kBM x 128 tiles, k-tiles of 256 numbers (128 bytes of a row of w, 512 of x) in three
 // stages of LDS, filled without registers by whole lines, two in flight while one is
-// multiplied. A wave has 32 rows of w, which it widens once, and all rows of x. Where the
+// multiplied. A wave has 32 rows of w, which it widens, and 32 rows of x. Where the
 // tiles are fewer than the CUs, K is shared among `parts` blocks, whose fp32 sums a second
 // launch adds in order.
 //
@@ -19,7 +19,6 @@
 namespace tr {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kBN = 128, kBK = 256;
 
 struct LinearArgs {
@@ -32,11 +31,12 @@ struct LinearArgs {
   int K, N;
 };
 
+// Four waves for 32 rows of x.
 template <int kBM>
-__global__ __launch_bounds__(kThreads) void linear_tiles(LinearArgs a) {
+__global__ __launch_bounds__(8 * kBM) void linear_tiles(LinearArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int kI = kBM / 32;
-  constexpr int kXLoads = kBM / 8, kWLoads = 4, kLoads = kXLoads + kWLoads;     // of a wave: 1 KiB each
+  constexpr int kWaves = kBM / 8;
+  constexpr int kXLoads = kBM / 2 / kWaves, kWLoads = 16 / kWaves, kLoads = kXLoads + kWLoads;  // of a wave, 1 KiB each
   constexpr int kA = kBM * 32, kB = kBN * 8;                                    // chunks of 16 bytes
   // distinct objects: an access to one stage does not wait for loads into another
   __shared__ u32x4 a0[kA], a1[kA], a2[kA], b0[kB], b1[kB], b2[kB];
@@ -62,14 +62,14 @@ __global__ __launch_bounds__(kThreads) void linear_tiles(LinearArgs a) {
   uint32_t x_off[kXLoads], w_off[kWLoads];
 #pragma unroll
   for (int j = 0; j < kXLoads; ++j) {
-    const int r = wave * (kBM / 4) + j * 2 + h;
+    const int r = (wave * kXLoads + j) * 2 + h;
     x_off[j] = r < valid ? static_cast<uint32_t>(r) * static_cast<uint32_t>(a.K) * 2 + (l31 ^ (r & 15)) * 16 : kPast;
   }
   const int wc = (lane & 7) ^ (lane >> 3);
 #pragma unroll
   for (int j = 0; j < kWLoads; ++j) {
-    const int r = wave * 32 + j * 8 + (lane >> 3);
-    w_off[j] = r < rows ? static_cast<uint32_t>(r) * static_cast<uint32_t>(a.K / 2) + (wc ^ (j & 1)) * 16 : kPast;
+    const int r = (wave * kWLoads + j) * 8 + (lane >> 3);
+    w_off[j] = r < rows ? static_cast<uint32_t>(r) * static_cast<uint32_t>(a.K / 2) + (wc ^ (r >> 3 & 1)) * 16 : kPast;
   }
   const uint8_t* sp = a.ws + (n0 + static_cast<int64_t>(min(tid, rows - 1))) * blocks;
   auto load = [&](u32x4* sx, u32x4* sw, int kt) {
@@ -77,25 +77,23 @@ __global__ __launch_bounds__(kThreads) void linear_tiles(LinearArgs a) {
     const bool mine = at < k1;      // (past the part's last: nothing is read)
 #pragma unroll
     for (int j = 0; j < kXLoads; ++j) {
-      const int r = wave * (kBM / 4) + j * 2 + h;
+      const int r = (wave * kXLoads + j) * 2 + h;
       const uint32_t past = mine && at * 32 + (l31 ^ (r & 15)) < a.K / 8 ? 0 : kPast;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(sx + (wave * (kBM / 4) + j * 2) * 32), 16,
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(sx + (wave * kXLoads + j) * 64), 16,
                                                x_off[j] | past, at * 512, 0, 0);
     }
 #pragma unroll
     for (int j = 0; j < kWLoads; ++j) {
-      const uint32_t past = mine && at * 8 + (wc ^ (j & 1)) < blocks ? 0 : kPast;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(sw + (wave * 32 + j * 8) * 8), 16, w_off[j] | past,
+      const uint32_t past = mine && at * 8 + (wc ^ ((wave * kWLoads + j) & 1)) < blocks ? 0 : kPast;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(sw + (wave * kWLoads + j) * 64), 16, w_off[j] | past,
                                                at * 128, 0, 0);
     }
   };
-  floatx16 acc[kI];
+  floatx16 acc;
 #pragma unroll
-  for (int i = 0; i < kI; ++i)
-#pragma unroll
-    for (int c = 0; c < 16; ++c) acc[i][c] = 0.0f;
+  for (int c = 0; c < 16; ++c) acc[c] = 0.0f;
+  const int wr = (wave & 3) * 32 + l31, xr = (wave >> 2) * 32 + l31;     // this lane's rows
   auto multiply = [&](const u32x4* sx, const u32x4* sw, const uint32_t* s) {
-    const int wr = wave * 32 + l31;
     const int swz = (l31 & 7) ^ ((l31 >> 3) & 1);
     const uint32_t s0 = s[wr * 2], s1 = s[wr * 2 + 1];
 #pragma unroll
@@ -107,12 +105,9 @@ __global__ __launch_bounds__(kThreads) void linear_tiles(LinearArgs a) {
       for (int o = 0; o < 4; ++o) {
         const u32x4 v = {mx_pair_bf16<4, 0>(w[o], f), mx_pair_bf16<4, 1>(w[o], f), mx_pair_bf16<4, 2>(w[o], f),
                          mx_pair_bf16<4, 3>(w[o], f)};
-#pragma unroll
-        for (int i = 0; i < kI; ++i) {
-          const u32x4 x = sx[(i * 32 + l31) * 32 + ((4 * (2 * q + h) + o) ^ (l31 & 15))];
-          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v),
-                                                           __builtin_bit_cast(bf16x8, x), acc[i], 0, 0, 0);
-        }
+        const u32x4 x = sx[xr * 32 + ((4 * (2 * q + h) + o) ^ (l31 & 15))];
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v), __builtin_bit_cast(bf16x8, x),
+                                                      acc, 0, 0, 0);
       }
     }
   };
@@ -150,29 +145,18 @@ __global__ __launch_bounds__(kThreads) void linear_tiles(LinearArgs a) {
   lds_barrier();
   if (kt < k1) multiply(a0, b0, sc[0]);
   if (kt + 1 < k1) multiply(a1, b1, sc[1]);
-  settle(acc[0]);
-#pragma unroll
-  for (int i = 1; i < kI; ++i) settled(acc[i]);
+  settle(acc);
 
-  // acc[i][4 q + c]: row 32 i + lane % 32 of x, output 8 q + 4 h + c of this wave's 32
-  const int col0 = n0 + wave * 32;
+  // acc[4 q + c]: row xr of x, output 8 q + 4 h + c of this wave's 32
+  if (xr >= valid) return;
+  const int col0 = n0 + (wave & 3) * 32;
+  float* sums = a.part + (static_cast<int64_t>(blockIdx.z) * a.T + t0 + xr) * a.N;
+  uint16_t* out = a.y + (t0 + xr) * a.N;
 #pragma unroll
-  for (int i = 0; i < kI; ++i) {
-    const int r = i * 32 + l31;
-    if (r >= valid) continue;
-    if (parts > 1) {
-      float* row = a.part + (static_cast<int64_t>(blockIdx.z) * a.T + t0 + r) * a.N;
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        store4<true>(row, col0 + 8 * q + 4 * h, a.N, a.N % 4 == 0,
-                     floatx4{acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]});
-    } else {
-      uint16_t* row = a.y + (t0 + r) * a.N;
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        store4<false>(row, col0 + 8 * q + 4 * h, a.N, a.N % 4 == 0,
-                      floatx4{acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]});
-    }
+  for (int q = 0; q < 4; ++q) {
+    const floatx4 v = {acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
+    if (parts > 1) store4<true>(sums, col0 + 8 * q + 4 * h, a.N, a.N % 4 == 0, v);
+    else store4<false>(out, col0 + 8 * q + 4 * h, a.N, a.N % 4 == 0, v);
   }
 #endif  // __HIP_DEVICE_COMPILE__
 }
@@ -198,11 +182,13 @@ bool by_rows(const tr_linear4_desc& d) { return d.dtype == TR_F32 || d.T <= 16 |
 
 int tile_rows(const tr_linear4_desc& d) { return d.T <= 32 ? 32 : 64; }
 
-// Blocks that share K: as many as keep the blocks within the CUs, two k-tiles each at least.
+// Blocks that share K: as many as keep the blocks within the CUs, with four k-tiles each at
+// least (a k-tile is 0.7 us or so, and a second launch some 4 of the host's and the GPU's:
+// fewer than twelve are not shared).
 int parts_of(const tr_linear4_desc& d) {
-  const int64_t tiles = cdiv(d.N, kBN) * cdiv(d.T, tile_rows(d)), most = cdiv(d.K, kBK) / 2;
+  const int64_t tiles = cdiv(d.N, kBN) * cdiv(d.T, tile_rows(d)), all = cdiv(d.K, kBK), most = all / 4;
   const int64_t p = kPlanCus / tiles;
-  return static_cast<int>(p < 1 || most < 1 ? 1 : p < most ? p : most);
+  return static_cast<int>(p < 1 || all < 12 ? 1 : p < most ? p : most);
 }
 
 }  // namespace
@@ -226,8 +212,8 @@ hipError_t linear_mx4(const tr_linear4_desc& d, const void* x, const void* w, co
                        static_cast<float*>(scratch), here, static_cast<int>(d.K), static_cast<int>(d.N)};
     const dim3 grid(static_cast<uint32_t>(n_tiles), static_cast<uint32_t>(cdiv(here, rows)),
                     static_cast<uint32_t>(parts));
-    if (rows == 32) linear_tiles<32><<<grid, kThreads, 0, st>>>(a);
-    else linear_tiles<64><<<grid, kThreads, 0, st>>>(a);
+    if (rows == 32) linear_tiles<32><<<grid, 256, 0, st>>>(a);
+    else linear_tiles<64><<<grid, 512, 0, st>>>(a);
   }
   if (parts > 1) {
     const int64_t n = d.T * d.N;
