@@ -4,8 +4,8 @@
 //   y[r][n] = sum over k of x[rows[r]][k] w[e][n][k]; with SwiGLU silu(gate) * up
 //
 // 256 x 256 block tiles with k-tiles of 128 on the matrix instructions that take such
-// blocks (v_mfma_scale_f32_32x32x64_f8f6f4, twice the bf16 rate): four waves, each a 128 x
-// 128 quadrant in 256 accumulation registers. A row of a k-tile is 128 bytes (64 for
+// blocks (v_mfma_scale_f32_32x32x64_f8f6f4, twice the bf16 rate): four waves, each 128 x
+// 128 in 256 accumulation registers, every other 32 rows by 128 neighbouring rows of w. A row of a k-tile is 128 bytes (64 for
 // weights in 4 bits), so bytes, LDS reads and instruction times are those of bf16 tiles
 // with k-tiles of 64, and twice the numbers. The instruction's operands: lane 32 h + r
 // holds of row r the 16-byte chunks h and 2 + h of a step's four (in 4 bits the one chunk
@@ -21,6 +21,14 @@
 //   20..27  its first half's fragments come, and its scales
 // so a load has 27 to 42 instructions, 1700 to 2700 cycles, to land. Scales go through
 // registers to LDS, eight bytes of every row for two k-tiles.
+//
+// An expert's rows go over its m-tiles as evenly as units of 64 allow, and a wave leaves out
+// the instructions of row blocks past its tile's rows (of 64 rows 8 of 32 a step are left).
+// Against full tiles and a last one in full: 32 experts, 7168 x 2048, 2048 / 4096 / 8192
+// rows 126 / 136 / 179 -> 121 / 132 / 174 us, 4 bits 7168 x 4096, 4096 rows 174 -> 163; one
+// expert of 8192 rows pays 1% for the branches (425 -> 432). The rests of all experts after
+// all whole tiles would even out the blocks' work more, but brings their weights in twice:
+// 8192 rows 196 us.
 //
 // Scheduling is on the device from the offsets: groups of kGroupM m-tiles by all n-tiles,
 // in contiguous runs for each of the 8 XCDs, whose L2s then hold a group's rows and
@@ -170,7 +178,7 @@ struct Frags {
 };
 
 struct Geo {
-  int a_row, b_row[4];      // first row of this wave's blocks
+  int a_row, b_row[4];      // first row of this wave's blocks (of rows of x: every other, 64 apart)
   int a_unit[2][2];         // per half: unit in a row block of its two chunks
   int b_unit[2][2];
 };
@@ -181,7 +189,7 @@ typedef __attribute__((ext_vector_type(4))) int intx4;
 template <int S, int P, int kBits>
 __device__ __forceinline__ void read_frag(Frags<kBits>& f, const Geo& g, int n) {
   if (n >= 4) {
-    const u32x4* s = stage_a<S>() + (g.a_row + (n - 4) * 32) * 8;
+    const u32x4* s = stage_a<S>() + (g.a_row + (n - 4) * 64) * 8;
     f.a[P][n - 4] = __builtin_shufflevector(__builtin_bit_cast(intx4, s[g.a_unit[P][0]]),
                                             __builtin_bit_cast(intx4, s[g.a_unit[P][1]]), 0, 1, 2, 3, 4, 5, 6, 7);
   } else if constexpr (kBits == 8) {
@@ -198,7 +206,7 @@ __device__ __forceinline__ void read_frag(Frags<kBits>& f, const Geo& g, int n) 
 // Scales of row block n of the k-tile in half S of LDS buffer `buf`.
 template <int S, int kBits>
 __device__ __forceinline__ void read_scale(Frags<kBits>& f, const Geo& g, int buf, int lane, int n) {
-  const uint2* p = &g_sa[buf][g.a_row + n * 32 + (lane & 31)];
+  const uint2* p = &g_sa[buf][g.a_row + n * 64 + (lane & 31)];
   f.sa[S][n] = S == 0 ? p->x : p->y;
   const uint2* q = &g_sb[buf][g.b_row[n] + (lane & 31)];
   f.sb[S][n] = S == 0 ? q->x : q->y;
@@ -225,11 +233,11 @@ __device__ __forceinline__ void mma(Frags<kBits>& f, int m) {
 // Step of the k-tile in stage S, whose first half's fragments and scales are in
 // registers. `src`, `kt`: what comes into this stage next; `buf`: the scale buffer of the
 // next k-tile. kScales (the first step of a pair): the next pair's scales are loaded, and
-// written to buffer `into`.
+// written to buffer `into`. `active`: row blocks with rows.
 template <int S, bool kScales, int kBits>
 __device__ __forceinline__ void step(Frags<kBits>& f, const Geo& g, const Source<kBits>& src, int kt, int K,
-                                     int a_chunk, int b_chunk, uint32_t b_step, int buf, int into, int wave,
-                                     int lane) {
+                                     int a_chunk, int b_chunk, uint32_t b_step, int buf, int into, int active,
+                                     int wave, int lane) {
   constexpr int kFree = 10, kLanded = 20, kLoads = 8 + Source<kBits>::kBPieces;
   const int blocks = K / kMxBlock;
   uint2 na{}, nb{};
@@ -263,8 +271,10 @@ __device__ __forceinline__ void step(Frags<kBits>& f, const Geo& g, const Source
     if (m < 8) read_frag<S, 1>(f, g, m);
     if (m >= kLanded && m < kLanded + 8) read_frag<1 - S, 0>(f, g, m - kLanded);
     if (m >= kLanded && m < kLanded + 4) read_scale<1 - S>(f, g, buf, lane, m - kLanded);
-    if (m < 16) mma<S, 0>(f, m);
-    else mma<S, 1>(f, m - 16);
+    if (((m >> 2) & 3) < active) {
+      if (m < 16) mma<S, 0>(f, m);
+      else mma<S, 1>(f, m - 16);
+    }
     const int n = m - kFree;
     if (n >= 0 && n < 8) load_a<S>(src, kt, past_a, wave, n);
     else if (n >= 8 && n < kLoads) load_b<S>(src, kt, past_b, b_step, wave, n - 8);
@@ -287,9 +297,14 @@ __device__ __forceinline__ Tile tile_of(const int* pre, const int* cnt, const in
   }
   Tile t;
   t.e = __builtin_amdgcn_readfirstlane(lo);
+  // an expert's rows, in units of 64, as evenly over its m-tiles as they go
   const int mt = __builtin_amdgcn_readfirstlane(gm - pre[t.e]);
-  t.row0 = __builtin_amdgcn_readfirstlane(off[t.e]) + mt * BM;
-  t.valid = min(BM, __builtin_amdgcn_readfirstlane(cnt[t.e]) - mt * BM);
+  const int count = __builtin_amdgcn_readfirstlane(cnt[t.e]);
+  const int units = (count + 63) / 64, mts = (units + 3) / 4;
+  const int per = units / mts, more = units - per * mts;
+  const int at = 64 * (mt * per + min(mt, more));
+  t.row0 = __builtin_amdgcn_readfirstlane(off[t.e]) + at;
+  t.valid = min(64 * (per + (mt < more ? 1 : 0)), count - at);
   t.n0 = within / size * outs;
   return t;
 }
@@ -392,7 +407,7 @@ __global__ __launch_bounds__(kThreads) void mx_tiles(MxArgs a) {
 
   const int h = lane >> 5;
   Geo g;
-  g.a_row = (wave >> 1) * 128;
+  g.a_row = (wave >> 1) * 32;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     g.b_row[j] = kSwiglu ? (j < 2 ? (wave & 1) * 64 + j * 32 : 128 + (wave & 1) * 64 + (j - 2) * 32)
@@ -461,6 +476,7 @@ __global__ __launch_bounds__(kThreads) void mx_tiles(MxArgs a) {
     // past the last tile: this one again, in bounds and not used
     const Tile tn = L + G < total ? tile_of(pre, cnt, off, a.E, total_m, NT, kOuts, L + G) : t;
     const int rn = x_row(a, tn, wave, lane);   // (used in the last pair)
+    const int active = (t.valid - g.a_row + 63) >> 6;
     // (one loop that runs at least once: no copy of the accumulators, one of the steps)
     int p = 1;
 #pragma clang loop unroll(disable)
@@ -470,8 +486,8 @@ __global__ __launch_bounds__(kThreads) void mx_tiles(MxArgs a) {
         s0 = source<kBits, kSwiglu>(a, tn, rn, wave, lane);
         kt = 0;
       }
-      step<0, true>(f, g, s0, kt, a.K, a_chunk, b_chunk, b_step, buf, buf ^ 1, wave, lane);
-      step<1, false>(f, g, s0, kt + 1, a.K, a_chunk, b_chunk, b_step, buf ^ 1, 0, wave, lane);
+      step<0, true>(f, g, s0, kt, a.K, a_chunk, b_chunk, b_step, buf, buf ^ 1, active, wave, lane);
+      step<1, false>(f, g, s0, kt + 1, a.K, a_chunk, b_chunk, b_step, buf ^ 1, 0, active, wave, lane);
       buf ^= 1;
     } while (p++ < pairs);
 
@@ -482,7 +498,7 @@ __global__ __launch_bounds__(kThreads) void mx_tiles(MxArgs a) {
     // acc[i][j][4 q + c]: row lane & 31 of row block i, column 8 q + 4 h + c of block j
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int lr = g.a_row + i * 32 + (lane & 31);
+      const int lr = g.a_row + i * 64 + (lane & 31);
       const int64_t row = t.row0 + lr;
 #pragma unroll
       for (int j = 0; j < (kSwiglu ? 2 : 4); ++j) {
