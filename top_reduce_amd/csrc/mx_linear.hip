@@ -178,7 +178,13 @@ __global__ __launch_bounds__(256) void linear_join(const float* part, uint16_t* 
 }
 
 // Few rows, or none of the sizes above.
-bool by_rows(const tr_linear4_desc& d) { return d.dtype == TR_F32 || d.T <= 16 || d.K < kBK; }
+// Whether rows of w go over the blocks 32 at a time: always with x in fp32, else up to 16
+// rows of x while the tiles are for less than half the CUs. 7168 x 7168, 1 / 16 rows: 8.9 / 11.8
+// us against 11.9 / 13.1 in tiles; x 16384: 17.1 / 23.1 against 17.2 / 18.4; x 131072: 125 / 188
+// against 100 / 121.
+bool by_rows(const tr_linear4_desc& d) {
+  return d.dtype == TR_F32 || d.K < kBK || (d.T <= 16 && cdiv(d.N, kBN) * 2 < kPlanCus);
+}
 
 int tile_rows(const tr_linear4_desc& d) { return d.T <= 32 ? 32 : 64; }
 
