@@ -146,7 +146,7 @@ __device__ __forceinline__ void load_a(const Source<kBits>& s, int kt, uint32_t 
                                            s.a_off[j] | past, kt * BK, 0, 0);
 }
 
-template <int S, int kBits>
+template <int S, int kPolicy, int kBits>
 __device__ __forceinline__ void load_b(const Source<kBits>& s, int kt, uint32_t past, uint32_t step, int wave, int j) {
   uint32_t off = s.b_off;
   if constexpr (kBits == 8) {
@@ -154,7 +154,7 @@ __device__ __forceinline__ void load_b(const Source<kBits>& s, int kt, uint32_t 
   }
   off = j < s.b_pieces ? off + j * step : kPast;
   __builtin_amdgcn_raw_ptr_buffer_load_lds(s.b, (lds_void*)(stage_b<S>() + wave * (64 * kBits) + j * 64), 16,
-                                           off | past, kt * (BK * kBits / 8), 0, 0);
+                                           off | past, kt * (BK * kBits / 8), 0, kPolicy);
 }
 
 // Eight scale bytes of a row, blocks at .. at + 7, as they lie in memory (at least 8
@@ -234,7 +234,7 @@ __device__ __forceinline__ void mma(Frags<kBits>& f, int m) {
 // registers. `src`, `kt`: what comes into this stage next; `buf`: the scale buffer of the
 // next k-tile. kScales (the first step of a pair): the next pair's scales are loaded, and
 // written to buffer `into`. `active`: row blocks with rows.
-template <int S, bool kScales, int kBits>
+template <int S, bool kScales, int kPolicy, int kBits>
 __device__ __forceinline__ void step(Frags<kBits>& f, const Geo& g, const Source<kBits>& src, int kt, int K,
                                      int a_chunk, int b_chunk, uint32_t b_step, int buf, int into, int active,
                                      int wave, int lane) {
@@ -277,7 +277,7 @@ __device__ __forceinline__ void step(Frags<kBits>& f, const Geo& g, const Source
     }
     const int n = m - kFree;
     if (n >= 0 && n < 8) load_a<S>(src, kt, past_a, wave, n);
-    else if (n >= 8 && n < kLoads) load_b<S>(src, kt, past_b, b_step, wave, n - 8);
+    else if (n >= 8 && n < kLoads) load_b<S, kPolicy>(src, kt, past_b, b_step, wave, n - 8);
     __builtin_amdgcn_sched_barrier(0);
   }
 }
@@ -365,7 +365,7 @@ __device__ __forceinline__ void store_block(const MxArgs& a, int64_t row, bool i
 
 #endif  // __HIP_DEVICE_COMPILE__
 
-template <int kBits, bool kSwiglu, bool kMxOut>
+template <int kBits, bool kSwiglu, bool kMxOut, int kPolicy>
 __global__ __launch_bounds__(kThreads) void mx_tiles(MxArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int kOuts = kSwiglu ? BN / 2 : BN;   // of a tile
@@ -446,8 +446,8 @@ __global__ __launch_bounds__(kThreads) void mx_tiles(MxArgs a) {
       }
 #pragma unroll
       for (int j = 0; j < Source<kBits>::kBPieces; ++j) {
-        if (q == 0) load_b<0>(s0, q, past_b, b_step, wave, j);
-        else load_b<1>(s0, q, past_b, b_step, wave, j);
+        if (q == 0) load_b<0, kPolicy>(s0, q, past_b, b_step, wave, j);
+        else load_b<1, kPolicy>(s0, q, past_b, b_step, wave, j);
       }
     }
     g_sa[0][wave * 64 + lane] = load_scale8(s0.sa, 0, a.K / kMxBlock);
@@ -486,8 +486,8 @@ __global__ __launch_bounds__(kThreads) void mx_tiles(MxArgs a) {
         s0 = source<kBits, kSwiglu>(a, tn, rn, wave, lane);
         kt = 0;
       }
-      step<0, true>(f, g, s0, kt, a.K, a_chunk, b_chunk, b_step, buf, buf ^ 1, active, wave, lane);
-      step<1, false>(f, g, s0, kt + 1, a.K, a_chunk, b_chunk, b_step, buf ^ 1, 0, active, wave, lane);
+      step<0, true, kPolicy>(f, g, s0, kt, a.K, a_chunk, b_chunk, b_step, buf, buf ^ 1, active, wave, lane);
+      step<1, false, kPolicy>(f, g, s0, kt + 1, a.K, a_chunk, b_chunk, b_step, buf ^ 1, 0, active, wave, lane);
       buf ^= 1;
     } while (p++ < pairs);
 
@@ -536,7 +536,7 @@ constexpr int kMidN = 128;
 
 #endif
 
-template <int kBits, int kBM, int kStages, bool kSwiglu, bool kMxOut>
+template <int kBits, int kBM, int kStages, bool kSwiglu, bool kMxOut, int kPolicy>
 __global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int kOuts = kSwiglu ? kMidN / 2 : kMidN;
@@ -564,35 +564,26 @@ __global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
     else return b2;
   };
   __shared__ uint32_t sc[kStages][(kBM + kMidN) * kSub];
-  __shared__ int pre[kMaxE + 1], tmp[kThreads / kWave];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int No = kSwiglu ? a.N / 2 : a.N;
   const int NT = (No + kOuts - 1) / kOuts;
-  // the experts' m-tiles
-  int total_m;
-  {
-    const int per = (a.E + kThreads - 1) / kThreads;
-    int sum = 0, mine[4];
+  // The experts' m-tiles, each wave for itself: lane l has experts l per .. l per + per - 1.
+  const int per = (a.E + kWave - 1) / kWave;
+  auto segment = [&](int i, int* begin, int* end) {
+    const int e = lane * per + i;
+    *begin = max(0, min(a.offsets[min(e, a.E)], a.R));
+    *end = max(*begin, min(a.offsets[min(e + 1, a.E)], a.R));
+    return (*end - *begin + kBM - 1) / kBM;
+  };
+  int begin, end, mine = 0;
+  for (int i = 0; i < per; ++i) mine += segment(i, &begin, &end);
+  int upto = mine;      // m-tiles of this lane's and all lower lanes' experts
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = tid * per + i;
-      mine[i] = 0;
-      if (i < per && e < a.E) {
-        const int begin = max(0, min(a.offsets[e], a.R)), end = max(begin, min(a.offsets[e + 1], a.R));
-        mine[i] = (end - begin + kBM - 1) / kBM;
-      }
-      sum += mine[i];
-    }
-    int at = block_exclusive_scan<kThreads>(sum, tmp, &total_m);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = tid * per + i;
-      if (i < per && e < a.E) pre[e] = at;
-      at += mine[i];
-    }
-    if (tid == 0) pre[a.E] = total_m;
-    __syncthreads();
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int o = __shfl_up(upto, d, kWave);
+    if (lane >= d) upto += o;
   }
+  const int total_m = __builtin_amdgcn_readlane(upto, kWave - 1);
   // contiguous tiles for each XCD; an expert's m-tiles of one n-tile one after another
   const int total = total_m * NT;
   const int share = (total + 7) / 8;
@@ -601,20 +592,23 @@ __global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
   if (idx >= share || L >= total) return;
   Tile t;
   {
-    int lo = 0, hi = a.E;
     const int gm = L / NT;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pre[mid] <= gm) lo = mid; else hi = mid;
+    const int who = __builtin_amdgcn_readfirstlane(__popcll(__ballot(upto <= gm)));   // the lane that has it
+    int first = upto - mine, mts = 1, id = 0, at = 0, last = 0;
+    for (int i = 0, next = first; i < per; ++i) {
+      const int m = segment(i, &begin, &end);
+      if (next <= gm && gm < next + m) first = next, mts = m, id = lane * per + i, at = begin, last = end;
+      next += m;
     }
-    t.e = __builtin_amdgcn_readfirstlane(lo);
-    const int first = __builtin_amdgcn_readfirstlane(pre[t.e]);
-    const int mts = __builtin_amdgcn_readfirstlane(pre[t.e + 1]) - first;
+    t.e = __builtin_amdgcn_readlane(id, who);
+    first = __builtin_amdgcn_readlane(first, who);
+    mts = __builtin_amdgcn_readlane(mts, who);
+    at = __builtin_amdgcn_readlane(at, who);
+    last = __builtin_amdgcn_readlane(last, who);
     const int within = L - first * NT;
-    const int begin = max(0, min(a.offsets[t.e], a.R)), end = max(begin, min(a.offsets[t.e + 1], a.R));
     t.n0 = within / mts * kOuts;
-    t.row0 = begin + within % mts * kBM;
-    t.valid = min(kBM, end - t.row0);
+    t.row0 = at + within % mts * kBM;
+    t.valid = min(kBM, last - t.row0);
   }
   const int blocks = a.K / kMxBlock;
   const int64_t kb = static_cast<int64_t>(a.K) * kBits / 8;
@@ -625,26 +619,40 @@ __global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
       __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(abase), 0, static_cast<int>(a_bytes), kRawBuffer);
   const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(a.w + static_cast<int64_t>(t.e) * a.N * kb), 0, static_cast<int>(a.N * kb), kRawBuffer);
-  uint32_t a_off[kAPieces], b_off[kBPieces];
-#pragma unroll
-  for (int j = 0; j < kAPieces; ++j) {
-    const int lr = wave * (kBM / 4) + j * 8 + (lane >> 3);
-    uint32_t row = lr;
-    if (a.rows) row = max(0, min(a.rows[min(t.row0 + lr, a.R - 1)], static_cast<int>(a.T) - 1));
-    a_off[j] = lr < t.valid ? row * static_cast<uint32_t>(a.K) + (chunk ^ ((lr >> 3) & 1)) * 16 : kPast;
-  }
   // a row of the tile of w: outputs, for SwiGLU gate and then up
   auto w_row = [&](int lr, bool* in) {
     const int n = t.n0 + (kSwiglu ? lr & 63 : lr);
     *in = n < No;
     return min(n, No - 1) + (kSwiglu && lr >= 64 ? No : 0);
   };
+  uint32_t b_off[kBPieces];
 #pragma unroll
   for (int j = 0; j < kBPieces; ++j) {
     const int lr = wave * 32 + j * 8 + (lane >> 3);
     bool in;
     const uint32_t row = w_row(lr, &in);
     b_off[j] = in ? row * static_cast<uint32_t>(kb) + (chunk ^ (j & 1)) * 16 : kPast;
+  }
+  const int steps = (a.K + BK * kSub - 1) / (BK * kSub);
+  auto load_b = [&](u32x4* sb, int kt) {
+    const int b_at = __builtin_amdgcn_readfirstlane(kt * 128);
+#pragma unroll
+    for (int j = 0; j < kBPieces; ++j) {
+      const uint32_t past = kt * 8 + (chunk ^ (j & 1)) < a.K / (kBits == 8 ? 16 : 32) ? 0 : kPast;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(sb + wave * 256 + j * 64), 16, b_off[j] | past, b_at, 0,
+                                               kPolicy);
+    }
+  };
+  // (w's rows are known before x's, which are looked up)
+  load_b(b0, 0);
+  asm volatile("" ::: "memory");
+  uint32_t a_off[kAPieces];
+#pragma unroll
+  for (int j = 0; j < kAPieces; ++j) {
+    const int lr = wave * (kBM / 4) + j * 8 + (lane >> 3);
+    uint32_t row = lr;
+    if (a.rows) row = max(0, min(a.rows[min(t.row0 + lr, a.R - 1)], static_cast<int>(a.T) - 1));
+    a_off[j] = lr < t.valid ? row * static_cast<uint32_t>(a.K) + (chunk ^ ((lr >> 3) & 1)) * 16 : kPast;
   }
   // this thread's row of scales: of x, then of w
   const uint8_t* sp;
@@ -658,10 +666,8 @@ __global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
       sp = a.ws + (static_cast<int64_t>(t.e) * a.N + w_row(min(tid - kBM, kMidN - 1), &in)) * blocks;
     }
   }
-  const int steps = (a.K + BK * kSub - 1) / (BK * kSub);
-  auto load = [&](u32x4* sa, u32x4* sb, int kt) {
-    // (the scalar offsets stay scalar)
-    const int a_at = __builtin_amdgcn_readfirstlane(kt * (BK * kSub)), b_at = __builtin_amdgcn_readfirstlane(kt * 128);
+  auto load_a = [&](u32x4* sa, int kt) {
+    const int a_at = __builtin_amdgcn_readfirstlane(kt * (BK * kSub));   // (the scalar offset stays scalar)
 #pragma unroll
     for (int u = 0; u < kSub; ++u) {
       // (chunks c and c ^ 1 are past K together: K is a multiple of 32)
@@ -670,12 +676,6 @@ __global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
       for (int j = 0; j < kAPieces; ++j)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(sa + u * (kBM * 8) + wave * (kBM * 2) + j * 64), 16,
                                                  a_off[j] | past, a_at + u * BK, 0, 0);
-    }
-#pragma unroll
-    for (int j = 0; j < kBPieces; ++j) {
-      const uint32_t past = kt * 8 + (chunk ^ (j & 1)) < a.K / (kBits == 8 ? 16 : 32) ? 0 : kPast;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(sb + wave * 256 + j * 64), 16, b_off[j] | past, b_at, 0,
-                                               0);
     }
   };
   const int h = lane >> 5, l31 = lane & 31;
@@ -748,7 +748,8 @@ __global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
     constexpr int k = decltype(i)::value;
     if constexpr (k + 1 < kStages) {
       v[k + 1].load(sp, k + 1, blocks);
-      load(sa_of(i), sb_of(i), k);
+      if constexpr (k > 0) load_b(sb_of(i), k);
+      load_a(sa_of(i), k);
       asm volatile("" ::: "memory");
     }
   };
@@ -762,7 +763,8 @@ __global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
       lds_barrier();
       v[k].load(sp, kt + kStages, blocks);
       constexpr int next = (k + kStages - 1) % kStages;
-      load(sa_of(Index<next>{}), sb_of(Index<next>{}), kt + kStages - 1);
+      load_b(sb_of(Index<next>{}), kt + kStages - 1);
+      load_a(sa_of(Index<next>{}), kt + kStages - 1);
       multiply(sa_of(i), sb_of(i), sc[k]);
     }
   };
@@ -829,24 +831,44 @@ __global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
-template <int kBits, int kBM, int kStages>
+template <int kBits, int kBM, int kStages, int kPolicy>
 void launch_mid(const tr_expert_desc& d, const MxArgs& a, hipStream_t st) {
   const int64_t outs = d.swiglu ? d.N / 2 : d.N;
   const int64_t tiles = (d.R / kBM + d.E) * cdiv(outs, d.swiglu ? 64 : 128);   // at most
   const uint32_t blocks = static_cast<uint32_t>(cdiv(tiles, 8) * 8);
-  if (d.swiglu && d.out) mx_mid<kBits, kBM, kStages, true, true><<<blocks, kThreads, 0, st>>>(a);
-  else if (d.swiglu) mx_mid<kBits, kBM, kStages, true, false><<<blocks, kThreads, 0, st>>>(a);
-  else if (d.out) mx_mid<kBits, kBM, kStages, false, true><<<blocks, kThreads, 0, st>>>(a);
-  else mx_mid<kBits, kBM, kStages, false, false><<<blocks, kThreads, 0, st>>>(a);
+  if (d.swiglu && d.out) mx_mid<kBits, kBM, kStages, true, true, kPolicy><<<blocks, kThreads, 0, st>>>(a);
+  else if (d.swiglu) mx_mid<kBits, kBM, kStages, true, false, kPolicy><<<blocks, kThreads, 0, st>>>(a);
+  else if (d.out) mx_mid<kBits, kBM, kStages, false, true, kPolicy><<<blocks, kThreads, 0, st>>>(a);
+  else mx_mid<kBits, kBM, kStages, false, false, kPolicy><<<blocks, kThreads, 0, st>>>(a);
 }
 
-template <int kBits>
+template <int kBits, int kPolicy>
 void launch(const tr_expert_desc& d, const MxArgs& a, hipStream_t st) {
   const uint32_t blocks = static_cast<uint32_t>(device_cu_count());
-  if (d.swiglu && d.out) mx_tiles<kBits, true, true><<<blocks, kThreads, 0, st>>>(a);
-  else if (d.swiglu) mx_tiles<kBits, true, false><<<blocks, kThreads, 0, st>>>(a);
-  else if (d.out) mx_tiles<kBits, false, true><<<blocks, kThreads, 0, st>>>(a);
-  else mx_tiles<kBits, false, false><<<blocks, kThreads, 0, st>>>(a);
+  if (d.swiglu && d.out) mx_tiles<kBits, true, true, kPolicy><<<blocks, kThreads, 0, st>>>(a);
+  else if (d.swiglu) mx_tiles<kBits, true, false, kPolicy><<<blocks, kThreads, 0, st>>>(a);
+  else if (d.out) mx_tiles<kBits, false, true, kPolicy><<<blocks, kThreads, 0, st>>>(a);
+  else mx_tiles<kBits, false, false, kPolicy><<<blocks, kThreads, 0, st>>>(a);
+}
+
+// The kernel's form by the weights' bits, and whether they are read once (kOnce). Measured,
+// us a pass, read so against not: 32 experts, 7168 x 4096, 32 / 256 / 1024 rows 121 / 172 / 191
+// against 128 / 183 / 201, in 4 bits 64 / 91 / 109 against 68 / 98 / 118; 2048 x 7168, 64 rows 68
+// against 76. 51 MB of weights, which are there from the call before, 40 against 26.
+// 256-row tiles, 2048 / 4096 / 16384 rows: 178 / 192 / 506 against 199 / 212 / 477 (more rows
+// read them more than once), in 4 bits (half a line a load) 153 against 139.
+template <int kBM, int k8Stages, int k4Stages>
+void launch_mid(const tr_expert_desc& d, const MxArgs& a, hipStream_t st) {
+  const bool once = read_once(d.E * d.N * d.K * d.bits / 8);
+  if (d.bits == 4) once ? launch_mid<4, kBM, k4Stages, kOnce>(d, a, st) : launch_mid<4, kBM, k4Stages, kKept>(d, a, st);
+  else once ? launch_mid<8, kBM, k8Stages, kOnce>(d, a, st) : launch_mid<8, kBM, k8Stages, kKept>(d, a, st);
+}
+
+void launch(const tr_expert_desc& d, const MxArgs& a, hipStream_t st) {
+  const int64_t experts = d.R < d.E ? d.R : d.E;
+  if (d.bits == 4) launch<4, kKept>(d, a, st);
+  else if (read_once(d.E * d.N * d.K) && d.R <= 192 * experts) launch<8, kOnce>(d, a, st);
+  else launch<8, kKept>(d, a, st);
 }
 
 }  // namespace
@@ -891,10 +913,9 @@ hipError_t expert_tiles(const tr_expert_desc& d, tr_expert_kernel kernel, const 
                  static_cast<uint8_t*>(ys), d.T, static_cast<int>(d.R), static_cast<int>(d.K),
                  static_cast<int>(d.N), d.E};
   // (stages: as many as leave room for two blocks on a CU)
-  const bool four = d.bits == 4;
-  if (kernel == TR_EXPERT_TILE32) four ? launch_mid<4, 32, 3>(d, a, st) : launch_mid<8, 32, 3>(d, a, st);
-  else if (kernel == TR_EXPERT_TILE64) four ? launch_mid<4, 64, 2>(d, a, st) : launch_mid<8, 64, 3>(d, a, st);
-  else four ? launch<4>(d, a, st) : launch<8>(d, a, st);
+  if (kernel == TR_EXPERT_TILE32) launch_mid<32, 3, 3>(d, a, st);
+  else if (kernel == TR_EXPERT_TILE64) launch_mid<64, 3, 2>(d, a, st);
+  else launch(d, a, st);
   return hipGetLastError();
 }
 

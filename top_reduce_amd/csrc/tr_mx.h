@@ -66,6 +66,11 @@ __device__ __forceinline__ floatx2 mx_pair_f32(uint32_t v, float scale) {
     return __builtin_bit_cast(floatx2, __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(v, scale, kI != 0));
 }
 
+// Cache policies of loads to LDS: the ordinary one, and that of what is read once. Weights
+// that the 256 MiB behind the L2s cannot hold from call to call are read so.
+constexpr int kKept = 0, kOnce = 2;
+inline bool read_once(int64_t weight_bytes) { return weight_bytes > (int64_t{256} << 20); }
+
 #if defined(__HIP_DEVICE_COMPILE__)
 constexpr int kRawBuffer = 0x00020000;        // word 3 of a buffer resource: raw, 32-bit data
 constexpr uint32_t kPast = 0x80000000u;       // an offset past every buffer here: reads 0
