@@ -43,7 +43,7 @@ def test_quantize_refusals():
     for kw, status in ((dict(rows=-1), -1), (dict(K=0), -1), (dict(K=48), -2), (dict(K=(1 << 22) + 32), -2),
                        (dict(dtype=2), -1), (dict(bits=6), -1), (dict(rows=1 << 35), -2), (dict(x=None), -1),
                        (dict(x=FAKE + 8), -1), (dict(q=None), -1), (dict(q=FAR + 4), -1), (dict(s=None), -1),
-                       (dict(q=FAKE + 496), -1), (dict(s=FAKE + 511), -1)):
+                       (dict(q=FAKE + 496), -1), (dict(s=FAKE + 511), -1), (dict(s=FAR + 255), -1)):
         a = {**ok, **kw}
         assert lib.moe_quantize_mx(*a.values(), None) == status, kw
         assert lib.moe_last_error()
@@ -66,7 +66,9 @@ def test_norm_refusals():
     for a in (dict(x=None), dict(weight=None), dict(y=None, q=None, s=None), dict(q=None), dict(s=None),
               dict(x=FAKE + 8), dict(residual=FAKE + 8), dict(weight=FAKE + 2), dict(y=FAR + 4), dict(q=FAR + 8),
               dict(residual_out=FAR + 2), dict(y=FAKE + 16), dict(residual_out=FAKE + 496),
-              dict(q=FAKE), dict(s=FAKE + (1 << 20) + 511), dict(residual_out=FAR + 256)):
+              dict(q=FAKE), dict(s=FAKE + (1 << 20) + 511), dict(residual_out=FAR + 256), dict(q=FAR + 496),
+              dict(s=FAR), dict(s=FAR + (1 << 20) + 511), dict(s=FAR + (2 << 20) + 255),
+              dict(y=FAKE + (2 << 20) + 112), dict(s=FAKE + (2 << 20))):
         assert call({}, a) == -1, a
         assert lib.moe_last_error()
     assert lib.moe_rms_norm(None, *a0.values(), None) == -1
@@ -92,10 +94,15 @@ def test_expert_refusals():
         assert lib.moe_last_error()
     for a in (dict(x=None), dict(xs=None), dict(w=None), dict(ws=None), dict(offsets=None), dict(y=None),
               dict(ys=None), dict(x=FAKE + 8), dict(w=FAKE + 4), dict(y=FAR + 8), dict(offsets=FAKE + 2),
-              dict(rows=FAKE + 1), dict(y=FAKE + 496), dict(ys=FAKE + 511), dict(y=FAKE + (1 << 20))):
+              dict(rows=FAKE + 1), dict(y=FAKE + 496), dict(ys=FAKE + 511), dict(y=FAKE + (1 << 20)),
+              dict(ys=FAR + 511)):
         assert call({}, a) == -1, a
     assert call(dict(out=0), {}) == -1              # scales given, and none asked for
     assert call(dict(T=7), dict(rows=None)) == -1   # a row of x for each of the result's
+    # a block for each tile: too many for a launch
+    most = dict(T=1, R=1 << 22, K=256, N=1 << 16, out=0, swiglu=0)
+    for kernel in (2, 3):
+        assert call(dict(most, kernel=kernel), dict(y=FAR * 2, ys=None)) == -2
     assert lib.moe_expert_linear(None, *a0.values(), None) == -1
     assert call(dict(R=0, T=0), {k: None for k in a0}) == 0
 

@@ -762,6 +762,7 @@ tr_status moe_quantize_mx(int64_t rows, int64_t K, tr_dtype dtype, int32_t bits,
   const int64_t n = rows * K, xb = n * (dtype == TR_BF16 ? 2 : 4);
   if (overlap(x, xb, q, n * bits / 8) || overlap(x, xb, s, n / 32))
     return fail(TR_EINVAL, "q and s must not overlap x");
+  if (overlap(q, n * bits / 8, s, n / 32)) return fail(TR_EINVAL, "q and s overlap");
   return hip_status(tr::quantize_mx(rows, K, dtype == TR_F32, bits, x, q, s, stream), "moe_quantize_mx launch");
 }
 
@@ -794,7 +795,13 @@ tr_status moe_rms_norm(const tr_norm_desc* desc, const void* x, const void* resi
         overlap(q, n, p, b) || overlap(s, n / 32, p, b))
       return fail(TR_EINVAL, "an output overlaps x or residual without being it");
   }
-  if (overlap(y, b, residual_out, b)) return fail(TR_EINVAL, "y and residual_out overlap");
+  const struct { const void* p; int64_t n; } out[4] = {{y, b}, {residual_out, b}, {q, n}, {s, n / 32}};
+  const int64_t wb = d.H * (d.dtype == TR_BF16 ? 2 : 4);
+  for (int i = 0; i < 4; ++i) {
+    if (overlap(out[i].p, out[i].n, weight, wb)) return fail(TR_EINVAL, "an output overlaps weight");
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return fail(TR_EINVAL, "the outputs overlap");
+  }
   return hip_status(tr::rms_norm(d, x, residual, weight, y, residual_out, q, s, stream), "moe_rms_norm launch");
 }
 
@@ -818,6 +825,7 @@ tr_status moe_expert_linear(const tr_expert_desc* desc, const void* x, const voi
   if (overlap(y, yb, x, d.T * d.K) || overlap(y, yb, xs, d.T * d.K / 32) ||
       overlap(ys, d.R * No / 32, x, d.T * d.K) || overlap(ys, d.R * No / 32, xs, d.T * d.K / 32))
     return fail(TR_EINVAL, "y and ys must not overlap x or xs");
+  if (overlap(y, yb, ys, d.R * No / 32)) return fail(TR_EINVAL, "y and ys overlap");
   const tr_expert_kernel k = tr::expert_kernel(d, rows != nullptr);
   if (k == TR_EXPERT_AUTO) return fail(TR_EUNSUPPORTED, "kernel %d does not take these sizes", d.kernel);
   const hipError_t h = k == TR_EXPERT_ROWS ? tr::expert_few(d, x, xs, w, ws, offsets, rows, y, ys, stream)

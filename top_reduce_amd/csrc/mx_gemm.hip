@@ -888,11 +888,15 @@ void launch(const tr_expert_desc& d, const MxArgs& a, hipStream_t st) {
 //    184 / 200 with 64-row tiles; 1 expert of 64 rows, 7168 x 7168: 26, against 31.
 tr_expert_kernel expert_kernel(const tr_expert_desc& d, bool gather) {
   const int64_t outs = d.swiglu ? d.N / 2 : d.N;
-  // (gathered rows are addressed with 31 bits, tiles are numbered with 31)
+  // (gathered rows are addressed with 31 bits, tiles are numbered with 31; a block each, a
+  // launch has fewer than 2^32 threads)
   const int64_t most = (cdiv(d.R, 32) + d.E) * cdiv(outs, d.swiglu ? 64 : 128);
   const bool tiles = d.K >= 256 && (!gather || d.T * d.K < (int64_t{1} << 31)) && most < (int64_t{1} << 30);
+  const bool blocks = most < (int64_t{1} << 24) - 8;
   if (d.kernel == TR_EXPERT_ROWS || (d.kernel == TR_EXPERT_AUTO && !tiles)) return TR_EXPERT_ROWS;
   if (!tiles) return TR_EXPERT_AUTO;
+  if (d.kernel == TR_EXPERT_TILE256 || (d.kernel == TR_EXPERT_AUTO && !blocks)) return TR_EXPERT_TILE256;
+  if (!blocks) return TR_EXPERT_AUTO;
   if (d.kernel != TR_EXPERT_AUTO) return static_cast<tr_expert_kernel>(d.kernel);
   const int64_t cus = device_cu_count(), experts = d.R < d.E ? d.R : d.E;
   if (d.R <= 16 && experts * cdiv(outs, d.swiglu && !d.out ? 16 : 32) <= cus) return TR_EXPERT_ROWS;
