@@ -157,19 +157,6 @@ __device__ __forceinline__ void load_b(const Source<kBits>& s, int kt, uint32_t 
                                            off | past, kt * (BK * kBits / 8), 0, kPolicy);
 }
 
-// Eight scale bytes of a row, blocks at .. at + 7, as they lie in memory (at least 8
-// blocks: the row's last eight at most), and with 0 for those past the last.
-__device__ __forceinline__ uint2 load_scale8(const uint8_t* p, int at, int blocks) {
-  typedef uint32_t Odd __attribute__((ext_vector_type(2), aligned(1)));
-  const Odd v = *reinterpret_cast<const Odd*>(p + min(at, blocks - 8));
-  return uint2{v[0], v[1]};
-}
-__device__ __forceinline__ uint2 scale8(uint2 v, int at, int blocks) {
-  const int over = at - min(at, blocks - 8);
-  const uint64_t all = (static_cast<uint64_t>(v.y) << 32 | v.x) >> (8 * over & 63);
-  return over < 8 ? uint2{static_cast<uint32_t>(all), static_cast<uint32_t>(all >> 32)} : uint2{0, 0};
-}
-
 template <int kBits>
 struct Frags {
   intx8 a[2][4], b[2][4];   // of a step's two halves: rows of x, rows of w
@@ -563,7 +550,8 @@ __global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
     else if constexpr (k == 1) return b1;
     else return b2;
   };
-  __shared__ uint32_t sc[kStages][(kBM + kMidN) * kSub];
+  using Ring = ScaleRing<kSub, kBM + kMidN, 4>;
+  __shared__ __align__(16) uint32_t sc[Ring::kSize];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int No = kSwiglu ? a.N / 2 : a.N;
   const int NT = (No + kOuts - 1) / kOuts;
@@ -596,7 +584,7 @@ __global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
     const int who = __builtin_amdgcn_readfirstlane(__popcll(__ballot(upto <= gm)));   // the lane that has it
     int first = upto - mine, mts = 1, id = 0, at = 0, last = 0;
     for (int i = 0, next = first; i < per; ++i) {
-      const int m = segment(i, &begin, &end);
+      const int m = per == 1 ? mine : segment(i, &begin, &end);
       if (next <= gm && gm < next + m) first = next, mts = m, id = lane * per + i, at = begin, last = end;
       next += m;
     }
@@ -643,28 +631,44 @@ __global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
                                                kPolicy);
     }
   };
-  // (w's rows are known before x's, which are looked up)
-  load_b(b0, 0);
+  // x's rows: of this lane's pieces, and of its turns of scales. They are looked up while w's
+  // first k-tile comes.
+  int a_row_of[kAPieces], s_row_of[Ring::kTurns];
+#pragma unroll
+  for (int j = 0; j < kAPieces; ++j) a_row_of[j] = min(wave * (kBM / 4) + j * 8 + (lane >> 3), t.valid - 1);
+#pragma unroll
+  for (int i = 0; i < Ring::kTurns; ++i) s_row_of[i] = min(Ring::row_of(i, wave, lane), t.valid - 1);
+  if (a.rows) {
+#pragma unroll
+    for (int j = 0; j < kAPieces; ++j) a_row_of[j] = a.rows[t.row0 + a_row_of[j]];
+#pragma unroll
+    for (int i = 0; i < Ring::kTurns; ++i)
+      if (Ring::row_of(i, 0, 0) < kBM) s_row_of[i] = a.rows[t.row0 + s_row_of[i]];
+  }
   asm volatile("" ::: "memory");
+  load_b(b0, 0);
+#pragma unroll
+  for (int j = 0; j < kAPieces; ++j) asm volatile("" : "+v"(a_row_of[j]));   // (waited for from here on)
+#pragma unroll
+  for (int i = 0; i < Ring::kTurns; ++i) asm volatile("" : "+v"(s_row_of[i]));
   uint32_t a_off[kAPieces];
 #pragma unroll
   for (int j = 0; j < kAPieces; ++j) {
     const int lr = wave * (kBM / 4) + j * 8 + (lane >> 3);
-    uint32_t row = lr;
-    if (a.rows) row = max(0, min(a.rows[min(t.row0 + lr, a.R - 1)], static_cast<int>(a.T) - 1));
+    uint32_t row = a_row_of[j];
+    if (a.rows) row = max(0, min(a_row_of[j], static_cast<int>(a.T) - 1));
     a_off[j] = lr < t.valid ? row * static_cast<uint32_t>(a.K) + (chunk ^ ((lr >> 3) & 1)) * 16 : kPast;
   }
-  // this thread's row of scales: of x, then of w
-  const uint8_t* sp;
-  {
-    if (tid < kBM) {
-      int64_t row = t.row0 + min(tid, t.valid - 1);
-      if (a.rows) row = max(0, min(a.rows[row], static_cast<int>(a.T) - 1));
-      sp = a.xs + row * blocks;
-    } else {
-      bool in;
-      sp = a.ws + (static_cast<int64_t>(t.e) * a.N + w_row(min(tid - kBM, kMidN - 1), &in)) * blocks;
-    }
+  // scales: rows of x, then of w
+  Ring ring;
+  ring.blocks = blocks, ring.first = wave * Ring::kPart, ring.lane = lane;
+#pragma unroll
+  for (int i = 0; i < Ring::kTurns; ++i) {
+    const int lr = Ring::row_of(i, wave, lane);
+    const int64_t xr = a.rows ? max(0, min(s_row_of[i], static_cast<int>(a.T) - 1)) : static_cast<int64_t>(t.row0) + s_row_of[i];
+    bool in;
+    const int64_t wr = static_cast<int64_t>(t.e) * a.N + w_row(max(lr - kBM, 0), &in);
+    ring.row[i] = lr < kBM ? a.xs + xr * blocks : a.ws + wr * blocks;
   }
   auto load_a = [&](u32x4* sa, int kt) {
     const int a_at = __builtin_amdgcn_readfirstlane(kt * (BK * kSub));   // (the scalar offset stays scalar)
@@ -739,33 +743,37 @@ __global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
                                                                         gs[i][j], 2, fs[i][m]);
         }
   };
-  // Step kt, in stage kt % kStages: its scales (loaded kStages steps before) go to LDS, its
+  // Step kt, in stage kt % kStages: scales loaded kStages steps before go to LDS, its
   // operands have landed; then the loads of step kt + kStages - 1, into the stage that the
   // step before has read.
-  Scales<kSub> v[kStages];
-  v[0].load(sp, 0, blocks);
+  typename Ring::Window v[kStages], all[Ring::kTurns];
+#pragma unroll
+  for (int i = 0; i < Ring::kTurns; ++i) ring.load_from(all[i], ring.row[i], 0);
+  ring.load(v[0], 0);
   auto fill = [&](auto i) {
     constexpr int k = decltype(i)::value;
     if constexpr (k + 1 < kStages) {
-      v[k + 1].load(sp, k + 1, blocks);
+      ring.load(v[k + 1], k + 1);
       if constexpr (k > 0) load_b(sb_of(i), k);
       load_a(sa_of(i), k);
       asm volatile("" ::: "memory");
     }
   };
   fill(Index<0>{}), fill(Index<1>{});
+#pragma unroll
+  for (int i = 0; i < Ring::kTurns; ++i) ring.store_to(all[i], sc, i, 0);
   auto stage = [&](auto i, int kt) {
     constexpr int k = decltype(i)::value;
     if constexpr (k < kStages) {
-      if (tid < kBM + kMidN) v[k].store(sc[k] + tid * kSub, kt, blocks);
+      ring.store(v[k], sc, kt);
       // sent since this step's operands: scales and operands of kStages - 2 steps
-      __builtin_amdgcn_s_waitcnt(waitcnt_vm((kLoads + 1) * (kStages - 2), true));
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm((kLoads + 2) * (kStages - 2), true));
       lds_barrier();
-      v[k].load(sp, kt + kStages, blocks);
+      ring.load(v[k], kt + kStages);
       constexpr int next = (k + kStages - 1) % kStages;
       load_b(sb_of(Index<next>{}), kt + kStages - 1);
       load_a(sa_of(Index<next>{}), kt + kStages - 1);
-      multiply(sa_of(i), sb_of(i), sc[k]);
+      multiply(sa_of(i), sb_of(i), Ring::slot(sc, kt));
     }
   };
   int kt = 0;
@@ -775,9 +783,7 @@ __global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
   // The last steps, fewer than kStages: everything they need has been sent.
   auto put = [&](auto i) {
     constexpr int k = decltype(i)::value;
-    if constexpr (k + 1 < kStages) {
-      if (kt + k < steps && tid < kBM + kMidN) v[k].store(sc[k] + tid * kSub, kt + k, blocks);
-    }
+    if constexpr (k + 1 < kStages) ring.store(v[k], sc, kt + k);
   };
   put(Index<0>{}), put(Index<1>{});
   __builtin_amdgcn_s_waitcnt(waitcnt_vm(0, true));   // (loads past the last k-tile, too)
@@ -785,7 +791,7 @@ __global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
   auto rest = [&](auto i) {
     constexpr int k = decltype(i)::value;
     if constexpr (k + 1 < kStages) {
-      if (kt + k < steps) multiply(sa_of(i), sb_of(i), sc[k]);
+      if (kt + k < steps) multiply(sa_of(i), sb_of(i), Ring::slot(sc, kt + k));
     }
   };
   rest(Index<0>{}), rest(Index<1>{});

@@ -90,6 +90,19 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// Eight scale bytes of a row, blocks at .. at + 7, as they lie in memory (at least 8
+// blocks: the row's last eight at most), and with 0 for those past the last.
+__device__ __forceinline__ uint2 load_scale8(const uint8_t* p, int at, int blocks) {
+  typedef uint32_t Odd __attribute__((ext_vector_type(2), aligned(1)));
+  const Odd v = *(const __attribute__((address_space(1))) Odd*)(p + min(at, blocks - 8));
+  return uint2{v[0], v[1]};
+}
+__device__ __forceinline__ uint2 scale8(uint2 v, int at, int blocks) {
+  const int over = at - min(at, blocks - 8);
+  const uint64_t all = (static_cast<uint64_t>(v.y) << 32 | v.x) >> (8 * over & 63);
+  return over < 8 ? uint2{static_cast<uint32_t>(all), static_cast<uint32_t>(all >> 32)} : uint2{0, 0};
+}
+
 // The scales of a row's k-tile, kWords times four, as they lie in memory (the row has as
 // many: its last ones at most), and with 0 for the blocks past the last.
 template <int kWords>
@@ -108,6 +121,67 @@ struct Scales {
     all = over < 4 * kWords ? all >> (8 * over & 63) : 0;
     to[0] = static_cast<uint32_t>(all);
     if constexpr (kWords == 2) to[1] = static_cast<uint32_t>(all >> 32);
+  }
+};
+
+// The scales of kRows rows, 4 kWords bytes of each a k-tile, for a block of kWaves waves: in
+// LDS for the k-tiles next to come. A load of a few bytes costs a CU about as much as one of
+// a line of 128, which it is one of, and brings that line along: so a turn's rows, one of
+// kTurns in order, get 16 bytes each, for kTurns k-tiles. Against every row's own bytes at
+// every k-tile: 8 experts of a row, 7168 x 4096, 46 -> 39 us (38 with one row's scales for
+// all); 32 of 32 rows 191 -> 158. 32 bytes a turn took more than they saved (42).
+template <int kWords, int kRows, int kWaves>
+struct ScaleRing {
+  static constexpr int kBytes = 4 * kWords, kTurns = 16 / kBytes, kSlots = 2 * kTurns;
+  static constexpr int kPart = kRows / (kTurns * kWaves);      // rows of a wave's turn
+  static constexpr int kSize = kSlots * kRows * kWords;        // words of LDS
+  static_assert(kRows % (kTurns * kWaves) == 0 && kPart <= kWave, "turns");
+  struct Window {
+    uint2 lo, hi;
+  };
+  const uint8_t* row[kTurns];      // scales of this lane's row of each turn
+  int blocks, first, lane;         // first: of a wave's rows in a turn
+
+  __device__ __forceinline__ static int row_of(int turn, int wave, int lane) {
+    return turn * (kRows / kTurns) + wave * kPart + min(lane, kPart - 1);
+  }
+  // of the rows whose turn k-tile kt is, for k-tiles kt .. kt + kTurns - 1
+  __device__ __forceinline__ void load(Window& w, int kt) const {
+    const int t = kt & (kTurns - 1);
+    const uint8_t* p = row[0];
+#pragma unroll
+    for (int i = 1; i < kTurns; ++i) {
+      const uint8_t* q = row[i];
+      asm("" : "+v"(q));      // (chosen among registers, not by an index into memory)
+      p = t == i ? q : p;
+    }
+    load_from(w, p, kt);
+  }
+  __device__ __forceinline__ void store(const Window& w, uint32_t* ring, int kt) const {
+    store_to(w, ring, kt & (kTurns - 1), kt);
+  }
+  // of a row of turn t (before its first turn, too)
+  __device__ __forceinline__ void load_from(Window& w, const uint8_t* p, int kt) const {
+    w.lo = load_scale8(p, kt * kBytes, blocks);
+    w.hi = load_scale8(p, kt * kBytes + 8, blocks);
+  }
+  __device__ __forceinline__ void store_to(const Window& w, uint32_t* ring, int t, int kt) const {
+    if (lane >= kPart) return;
+    const int r = t * (kRows / kTurns) + first + lane;
+    uint2 lo = w.lo, hi = w.hi;
+    if (kt * kBytes + 16 > blocks) lo = scale8(lo, kt * kBytes, blocks), hi = scale8(hi, kt * kBytes + 8, blocks);
+    if constexpr (kWords == 1) {
+      const uint32_t v[4] = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) slot(ring, kt + i)[r] = v[i];
+    } else {
+      reinterpret_cast<uint2*>(slot(ring, kt))[r] = lo;
+      reinterpret_cast<uint2*>(slot(ring, kt + 1))[r] = hi;
+    }
+  }
+  // kWords words of every row for k-tile kt
+  __device__ __forceinline__ static uint32_t* slot(uint32_t* ring, int kt) {
+    return ring + (kt & (kSlots - 1)) * (kRows * kWords);
   }
 };
 #endif
