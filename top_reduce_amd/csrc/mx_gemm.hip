@@ -883,15 +883,17 @@ void launch(const tr_expert_desc& d, const MxArgs& a, hipStream_t st) {
 // min(E, R), and have some R / min(E, R) rows each (tiles: half an m-tile of each expert is
 // empty; an n-tile is 128 or 256 rows of w). Measured, us a pass:
 //  - ROWS (a CU's weights in one burst, K shared by its waves) where one block a CU has all:
-//    1 expert of 8 rows, 7168 x 7168: 12.5 (8 bits), 10.0 (4), against 23.8 and 15.7 with 32-row
-//    tiles; 8 experts of a row, 7168 x 4096: 55, against 50.
-//  - 256-row tiles from 48 rows an expert, with tiles for half the CUs: 32 experts, 7168 x
-//    4096, 1024 / 2048 / 4096 rows: 200 / 205 / 226, against 200 / 278 / 380 with 64-row tiles;
-//    2 experts, 4096 x 4096, 1000 / 2000 / 4000 rows (80, 144, 272 tiles): 59 / 60 / 82, against
-//    34 / 62 / 129.
+//    1 expert of 16 rows, 7168 x 7168: 12.7 (8 bits), 10.2 (4), against 24.8 and 16.0 with
+//    32-row tiles; 8 experts of a row, 7168 x 4096: 53, against 38.
+//  - 256-row tiles from 56 rows an expert, with tiles for half the CUs: 32 experts, 7168 x
+//    4096, 1024 / 1536 / 2048 rows: 176 / 177 / 178 (in 4 bits 134 / 136 / 139), against 157 /
+//    184 / 258 (97 / 120 / 154) with 64-row tiles; 2048 x 7168, 1536 / 2048 rows: 112 / 115,
+//    against 97 / 138; 4 experts, 4096 x 4096, 1000 / 2000 rows: 54 / 58, against 46 / 70.
 //  - of the others 32-row tiles for up to 20 rows an expert, or where 64-row tiles are for
-//    less than half the CUs: 32 experts, 7168 x 4096, 256 / 1024 rows: 181 / 250, against
-//    184 / 200 with 64-row tiles; 1 expert of 64 rows, 7168 x 7168: 26, against 31.
+//    three quarters of the CUs at most (two of them run on one): 32 experts, 7168 x 4096, 640 / 1024 rows:
+//    157 / 215 (in 4 bits 94 / 130), against 151 / 157 (94 / 97) with 64-row tiles; 1 expert of
+//    64 / 128 / 256 rows, 7168 x 7168: 28 / 29 / 40 (17 / 18 / 27), against 30 / 33 / 35 (28 / 28
+//    / 29).
 tr_expert_kernel expert_kernel(const tr_expert_desc& d, bool gather) {
   const int64_t outs = d.swiglu ? d.N / 2 : d.N;
   // (gathered rows are addressed with 31 bits, tiles are numbered with 31; a block each, a
@@ -910,8 +912,8 @@ tr_expert_kernel expert_kernel(const tr_expert_desc& d, bool gather) {
     const int64_t m = d.R / rows + (experts + 1) / 2;
     return m > experts ? m : experts;
   };
-  if (d.R >= 48 * experts && m_tiles(256) * cdiv(outs, d.swiglu ? 128 : 256) * 2 >= cus) return TR_EXPERT_TILE256;
-  if (d.R <= 20 * experts || m_tiles(64) * cdiv(outs, d.swiglu ? 64 : 128) * 2 <= cus) return TR_EXPERT_TILE32;
+  if (d.R >= 56 * experts && m_tiles(256) * cdiv(outs, d.swiglu ? 128 : 256) * 2 >= cus) return TR_EXPERT_TILE256;
+  if (d.R <= 20 * experts || m_tiles(64) * cdiv(outs, d.swiglu ? 64 : 128) * 4 <= cus * 3) return TR_EXPERT_TILE32;
   return TR_EXPERT_TILE64;
 }
 
