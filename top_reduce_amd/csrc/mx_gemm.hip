@@ -5,11 +5,11 @@
 //
 // 256 x 256 block tiles with k-tiles of 128 on the matrix instructions that take such
 // blocks (v_mfma_scale_f32_32x32x64_f8f6f4, twice the bf16 rate): four waves, each 128 x
-// 128 in 256 accumulation registers, every other 32 rows by 128 neighbouring rows of w. A row of a k-tile is 128 bytes (64 for
-// weights in 4 bits), so bytes, LDS reads and instruction times are those of bf16 tiles
-// with k-tiles of 64, and twice the numbers. The instruction's operands: lane 32 h + r
-// holds of row r the 16-byte chunks h and 2 + h of a step's four (in 4 bits the one chunk
-// h of two), and the scale of the row's block h.
+// 128 in 256 accumulation registers, every other 32 rows by 128 neighbouring rows of w. A
+// row of a k-tile is 128 bytes (64 for weights in 4 bits), so bytes, LDS reads and
+// instruction times are those of bf16 tiles with k-tiles of 64, and twice the numbers. The
+// instruction's operands: lane 32 h + r holds of row r the 16-byte chunks h and 2 + h of a
+// step's four (in 4 bits the one chunk h of two), and the scale of the row's block h.
 //
 // Both operands go from memory to LDS without registers, into the stage of two that the
 // step before has finished reading. A step (k-tile) is 32 matrix instructions a wave, 64
@@ -34,6 +34,10 @@
 // in contiguous runs for each of the 8 XCDs, whose L2s then hold a group's rows and
 // weights. Rows past a segment and chunks past K are loads from past the buffer: zeros
 // without an access.
+//
+// Bound by the matrix instructions and the power they take: 8192^3 in 8 bits 421-430 us (2.6
+// PFLOP/s, the library's product 2.65; of zeros 3.8), 16384 rows over 32 experts with uneven
+// counts 477-508 at 7168 x 4096 with SwiGLU and 265-288 at 2048 x 7168 (1.7-2.0 PFLOP/s).
 #include "tr_internal.h"
 #include "tr_mx.h"
 
@@ -518,6 +522,10 @@ __global__ __launch_bounds__(kThreads) void mx_tiles(MxArgs a) {
 // flight. Wave (m, n) of 2 x 2 has kBM / 2 rows by 64, for SwiGLU 32 gate and the matching
 // 32 up; with 32 rows wave (p, n) has them all and half p of every k-tile, and the halves'
 // sums are added in LDS.
+//
+// Bound by reading the weights, two blocks a CU, 64 to 80 KiB in flight on it: 8 experts of a
+// row, 7168 x 4096, 8 bits 39 us (6.2 TB/s); 64 rows over 32 of them, 4 bits 76 (5.7), 2048 x
+// 7168 in 8 bits 68 (6.2); 256 rows, 8 bits 143 (6.8).
 #if defined(__HIP_DEVICE_COMPILE__)
 constexpr int kMidN = 128;
 
@@ -665,7 +673,8 @@ __global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
 #pragma unroll
   for (int i = 0; i < Ring::kTurns; ++i) {
     const int lr = Ring::row_of(i, wave, lane);
-    const int64_t xr = a.rows ? max(0, min(s_row_of[i], static_cast<int>(a.T) - 1)) : static_cast<int64_t>(t.row0) + s_row_of[i];
+    const int64_t xr =
+        a.rows ? max(0, min(s_row_of[i], static_cast<int>(a.T) - 1)) : static_cast<int64_t>(t.row0) + s_row_of[i];
     bool in;
     const int64_t wr = static_cast<int64_t>(t.e) * a.N + w_row(max(lr - kBM, 0), &in);
     ring.row[i] = lr < kBM ? a.xs + xr * blocks : a.ws + wr * blocks;
@@ -924,7 +933,8 @@ hipError_t expert_tiles(const tr_expert_desc& d, tr_expert_kernel kernel, const 
                  static_cast<const uint8_t*>(w), static_cast<const uint8_t*>(ws), offsets, rows, y,
                  static_cast<uint8_t*>(ys), d.T, static_cast<int>(d.R), static_cast<int>(d.K),
                  static_cast<int>(d.N), d.E};
-  // (stages: as many as leave room for two blocks on a CU)
+  // (stages: as many as leave room for two blocks on a CU; six and one block: one token's
+  // experts 50 -> 52 us, 64 tokens' in 4 bits 90 -> 103)
   if (kernel == TR_EXPERT_TILE32) launch_mid<32, 3, 3>(d, a, st);
   else if (kernel == TR_EXPERT_TILE64) launch_mid<64, 3, 2>(d, a, st);
   else launch(d, a, st);

@@ -1,4 +1,4 @@
-// x w^T for more than a few rows of x in bf16 and weights w in 4 bits, in blocks of 32 with
+// x w^T for few rows of x in bf16 and weights w in 4 bits, in blocks of 32 with
 // scales (tr_mx.h).
 //
 // Elements times scales are bf16 numbers (exact): they are widened in registers, two by
@@ -12,7 +12,8 @@
 //
 // Bound by what a CU loads: a line of 128 bytes takes it about four cycles, of a k-tile 128
 // of w and 4 kBM of x. So a tile is as wide as LDS allows, and K is shared rather than the
-// rows of w.
+// rows of w. 64 rows, 7168 x 7168: 14.6 us, of which the sums' launch 2.4 to 4.8; 1 / 64 rows,
+// 7168 x 131072: 100 / 158 (5.0 / 3.2 TB/s).
 #include "tr_internal.h"
 #include "tr_mx.h"
 
