@@ -442,7 +442,8 @@ tr_status moe_rms_norm(const tr_norm_desc* desc, const void* x, const void* resi
 
 /* Kernel of moe_expert_linear. AUTO goes by the sizes; the others are for testing, and
  * TR_EUNSUPPORTED where the sizes do not fit: ROWS multiplies in bf16 and takes any size,
- * the TILEs (32, 64 and 256 rows) take K of 256 and more. */
+ * the TILEs (32, 64 and 256 rows) take K of 256 and more, and with `rows` T * K < 2^31
+ * (AUTO, too: gathered rows of a larger x take the slower ROWS). */
 typedef enum {
     TR_EXPERT_AUTO = 0, TR_EXPERT_ROWS = 1, TR_EXPERT_TILE32 = 2, TR_EXPERT_TILE64 = 3, TR_EXPERT_TILE256 = 4
 } tr_expert_kernel;

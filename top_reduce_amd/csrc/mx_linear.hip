@@ -41,7 +41,7 @@ __global__ __launch_bounds__(8 * kBM) void linear_tiles(LinearArgs a) {
   constexpr int kA = kBM * 32, kB = kBN * 8;                                    // chunks of 16 bytes
   // distinct objects: an access to one stage does not wait for loads into another
   __shared__ u32x4 a0[kA], a1[kA], a2[kA], b0[kB], b1[kB], b2[kB];
-  __shared__ uint32_t sc[3][kBN * 2];
+  __shared__ uint2 sc[3][kBN];      // scales of a row's eight blocks
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5, l31 = lane & 31;
   const int n0 = blockIdx.x * kBN;
@@ -94,9 +94,9 @@ __global__ __launch_bounds__(8 * kBM) void linear_tiles(LinearArgs a) {
 #pragma unroll
   for (int c = 0; c < 16; ++c) acc[c] = 0.0f;
   const int wr = (wave & 3) * 32 + l31, xr = (wave >> 2) * 32 + l31;     // this lane's rows
-  auto multiply = [&](const u32x4* sx, const u32x4* sw, const uint32_t* s) {
+  auto multiply = [&](const u32x4* sx, const u32x4* sw, const uint2* s) {
     const int swz = (l31 & 7) ^ ((l31 >> 3) & 1);
-    const uint32_t s0 = s[wr * 2], s1 = s[wr * 2 + 1];
+    const uint32_t s0 = s[wr].x, s1 = s[wr].y;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       // this lane's chunk of w: block 2 q + h
@@ -114,19 +114,17 @@ __global__ __launch_bounds__(8 * kBM) void linear_tiles(LinearArgs a) {
   };
   // Step kt: its scales (loaded three steps before) go to LDS, its operands have landed;
   // then the loads of the step after next, into the stage that the step before has read.
-  Scales<2> v0, v1, v2;
-  v0.load(sp, k0, blocks);
-  v1.load(sp, k0 + 1, blocks);
+  uint2 v0 = load_scale8(sp, k0 * 8, blocks), v1 = load_scale8(sp, k0 * 8 + 8, blocks);
   load(a0, b0, k0);
   asm volatile("" ::: "memory");
-  v2.load(sp, k0 + 2, blocks);
+  uint2 v2 = load_scale8(sp, k0 * 8 + 16, blocks);
   load(a1, b1, k0 + 1);
-  auto step = [&](int kt, u32x4* sx, u32x4* sw, u32x4* nx, u32x4* nw, uint32_t* s, Scales<2>& v) {
-    if (tid < kBN) v.store(s + tid * 2, kt, blocks);
+  auto step = [&](int kt, u32x4* sx, u32x4* sw, u32x4* nx, u32x4* nw, uint2* s, uint2& v) {
+    if (tid < kBN) s[tid] = scale8(v, kt * 8, blocks);
     // sent since: the scales and operands of one step
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(kLoads + 1, true));
     lds_barrier();
-    v.load(sp, kt + 3, blocks);
+    v = load_scale8(sp, (kt + 3) * 8, blocks);
     load(nx, nw, kt + 2);
     multiply(sx, sw, s);
   };
@@ -139,8 +137,8 @@ __global__ __launch_bounds__(8 * kBM) void linear_tiles(LinearArgs a) {
   }
   // The last, at most two: all has been sent.
   if (tid < kBN) {
-    v0.store(sc[0] + tid * 2, kt, blocks);
-    v1.store(sc[1] + tid * 2, kt + 1, blocks);
+    sc[0][tid] = scale8(v0, kt * 8, blocks);
+    sc[1][tid] = scale8(v1, kt * 8 + 8, blocks);
   }
   __builtin_amdgcn_s_waitcnt(waitcnt_vm(0, true));
   lds_barrier();

@@ -103,27 +103,6 @@ __device__ __forceinline__ uint2 scale8(uint2 v, int at, int blocks) {
   return over < 8 ? uint2{static_cast<uint32_t>(all), static_cast<uint32_t>(all >> 32)} : uint2{0, 0};
 }
 
-// The scales of a row's k-tile, kWords times four, as they lie in memory (the row has as
-// many: its last ones at most), and with 0 for the blocks past the last.
-template <int kWords>
-struct Scales {
-  uint32_t v[kWords];
-  __device__ __forceinline__ void load(const uint8_t* row, int kt, int blocks) {
-    typedef uint32_t Odd __attribute__((ext_vector_type(kWords), aligned(1)));
-    const Odd d = *reinterpret_cast<const Odd*>(row + min(kt * 4 * kWords, blocks - 4 * kWords));
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) v[i] = d[i];
-  }
-  __device__ __forceinline__ void store(uint32_t* to, int kt, int blocks) const {
-    const int over = kt * 4 * kWords - min(kt * 4 * kWords, blocks - 4 * kWords);
-    uint64_t all = v[0];
-    if constexpr (kWords == 2) all |= static_cast<uint64_t>(v[1]) << 32;
-    all = over < 4 * kWords ? all >> (8 * over & 63) : 0;
-    to[0] = static_cast<uint32_t>(all);
-    if constexpr (kWords == 2) to[1] = static_cast<uint32_t>(all >> 32);
-  }
-};
-
 // The scales of kRows rows, 4 kWords bytes of each a k-tile, for a block of kWaves waves: in
 // LDS for the k-tiles next to come. A load of a few bytes costs a CU about as much as one of
 // a line of 128, which it is one of, and brings that line along: so a turn's rows, one of
