@@ -79,6 +79,25 @@ def test_it_is_its_parts(T):
                        tr.combine_reduce(p, None, expert_out=o))
 
 
+@pytest.mark.parametrize("G,kernel", [(128, "tile64"), (16, "tile256"), (4, "tile256")])
+@pytest.mark.parametrize("bits", [8, 4])
+def test_the_rows_there_choose_the_kernel(G, kernel, bits):
+    """4 of G experts here: 32, 256 and 1024 rows each of the 1024 that the plan has room for."""
+    say(f"forward {G} {bits}")
+    T, H, I, E, K = 512, 256, 2048, 4, 8 if G > 8 else 4
+    g = torch.Generator().manual_seed(G + bits)
+    w1, w2 = weights(g, E, 2 * I, H, bits), weights(g, E, H, I, bits)
+    x = tuple(t.cuda() for t in M.quantize(torch.randn(2 * T, H, generator=g, dtype=torch.float64)))
+    idx = torch.stack([torch.randperm(G, generator=g)[:K] for _ in range(2 * T)]).cuda()
+    w = torch.rand(2 * T, K, generator=g).cuda()
+    p = tr.plan(idx, E=E, H=H, I=I)
+    y = tr.forward_mx(p, x, w, w1, w2)
+    v = p.views()
+    h = tr.expert_linear(x, w1, v["offsets"], rows=v["row_src"], swiglu=True, out="mx8", kernel=kernel)
+    o = tr.expert_linear(h, w2, v["offsets"])
+    assert torch.equal(tr.combine_reduce(p, w, expert_out=o), y)
+
+
 @pytest.mark.parametrize("T", [1, 40, 300])
 def test_captured_and_replayed(T):
     b = block(T, 256, 64, 4, 8, 2, 4)

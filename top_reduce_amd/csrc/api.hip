@@ -805,9 +805,9 @@ tr_status moe_rms_norm(const tr_norm_desc* desc, const void* x, const void* resi
   return hip_status(tr::rms_norm(d, x, residual, weight, y, residual_out, q, s, stream), "moe_rms_norm launch");
 }
 
-tr_status moe_expert_linear(const tr_expert_desc* desc, const void* x, const void* xs, const void* w,
-                            const void* ws, const int32_t* offsets, const int32_t* rows, void* y, void* ys,
-                            hipStream_t stream) {
+static tr_status expert_linear(const tr_expert_desc* desc, const void* x, const void* xs, const void* w,
+                               const void* ws, const int32_t* offsets, const int32_t* rows, void* y, void* ys,
+                               bool bound, hipStream_t stream) {
   tr_status e = check_expert_desc(desc);
   if (e != TR_OK) return e;
   const tr_expert_desc& d = *desc;
@@ -829,8 +829,14 @@ tr_status moe_expert_linear(const tr_expert_desc* desc, const void* x, const voi
   const tr_expert_kernel k = tr::expert_kernel(d, rows != nullptr);
   if (k == TR_EXPERT_AUTO) return fail(TR_EUNSUPPORTED, "kernel %d does not take these sizes", d.kernel);
   const hipError_t h = k == TR_EXPERT_ROWS ? tr::expert_few(d, x, xs, w, ws, offsets, rows, y, ys, stream)
-                                           : tr::expert_tiles(d, k, x, xs, w, ws, offsets, rows, y, ys, stream);
+                                           : tr::expert_tiles(d, k, x, xs, w, ws, offsets, rows, y, ys, bound, stream);
   return hip_status(h, "moe_expert_linear launch");
+}
+
+tr_status moe_expert_linear(const tr_expert_desc* desc, const void* x, const void* xs, const void* w,
+                            const void* ws, const int32_t* offsets, const int32_t* rows, void* y, void* ys,
+                            hipStream_t stream) {
+  return expert_linear(desc, x, xs, w, ws, offsets, rows, y, ys, false, stream);
 }
 
 size_t moe_linear_mx4_workspace(const tr_linear4_desc* desc) {
@@ -877,8 +883,11 @@ tr_status moe_forward_mx(const tr_moe_plan* plan, const void* x, const void* xs,
   // h: R_cap rows of I bytes, then their scales (the plan holds two bytes a number)
   char* h = static_cast<char*>(plan->h);
   char* hs = h + up(static_cast<size_t>(plan->R_cap) * d.I);
-  if ((e = moe_expert_linear(&gate_up, x, xs, w1, w1s, plan->offsets, plan->row_src, h, hs, stream)) != TR_OK) return e;
-  if ((e = moe_expert_linear(&down, h, hs, w2, w2s, plan->offsets, nullptr, plan->O, nullptr, stream)) != TR_OK)
+  // (tokens that name one expert each fill R_cap, but for those of other GPUs)
+  const bool bound = d.K > 1;
+  if ((e = expert_linear(&gate_up, x, xs, w1, w1s, plan->offsets, plan->row_src, h, hs, bound, stream)) != TR_OK)
+    return e;
+  if ((e = expert_linear(&down, h, hs, w2, w2s, plan->offsets, nullptr, plan->O, nullptr, bound, stream)) != TR_OK)
     return e;
   return moe_combine_reduce(plan, nullptr, topk_weights, y, stream);
 }

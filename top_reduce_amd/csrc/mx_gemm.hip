@@ -47,6 +47,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int BM = 256, BN = 256, BK = 128;
 constexpr int kGroupM = 4;
+constexpr int kShare = 56;     // rows an expert from which 256-row tiles are faster than 64-row ones
 
 struct MxArgs {
   const uint8_t* x;        // [T, K]
@@ -59,6 +60,7 @@ struct MxArgs {
   uint8_t* ys;             // [R, No / 32]
   int64_t T;
   int R, K, N, E;
+  int share;               // rows an expert from which mx_tiles takes a call, and below mx_mid; 0: no other is launched
 };
 
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -364,7 +366,7 @@ __global__ __launch_bounds__(kThreads) void mx_tiles(MxArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // the experts' m-tiles
   constexpr int kPer = kMaxE / kThreads;
-  int mine[kPer], sum = 0;
+  int mine[kPer], sum = 0, rows = 0, some = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = tid * kPer + i;
@@ -374,8 +376,16 @@ __global__ __launch_bounds__(kThreads) void mx_tiles(MxArgs a) {
       off[e] = begin;
       cnt[e] = end - begin;
       mine[i] = (end - begin + BM - 1) / BM;
+      rows += end - begin;
+      some += end > begin ? 1 : 0;
     }
     sum += mine[i];
+  }
+  if (a.share > 0) {
+    int all, experts;
+    block_exclusive_scan<kThreads>(rows, tmp, &all);
+    block_exclusive_scan<kThreads>(some, tmp, &experts);
+    if (all < a.share * experts) return;
   }
   int total_m;
   int at = block_exclusive_scan<kThreads>(sum, tmp, &total_m);
@@ -571,8 +581,17 @@ __global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
     *end = max(*begin, min(a.offsets[min(e + 1, a.E)], a.R));
     return (*end - *begin + kBM - 1) / kBM;
   };
-  int begin, end, mine = 0;
-  for (int i = 0; i < per; ++i) mine += segment(i, &begin, &end);
+  int begin, end, mine = 0, rows = 0, some = 0;
+  for (int i = 0; i < per; ++i) {
+    mine += segment(i, &begin, &end);
+    rows += end - begin;
+    some += end > begin ? 1 : 0;
+  }
+  if (a.share > 0) {
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) rows += __shfl_xor(rows, d, kWave), some += __shfl_xor(some, d, kWave);
+    if (rows >= a.share * some) return;
+  }
   int upto = mine;      // m-tiles of this lane's and all lower lanes' experts
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) {
@@ -849,7 +868,8 @@ __global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
 template <int kBits, int kBM, int kStages, int kPolicy>
 void launch_mid(const tr_expert_desc& d, const MxArgs& a, hipStream_t st) {
   const int64_t outs = d.swiglu ? d.N / 2 : d.N;
-  const int64_t tiles = (d.R / kBM + d.E) * cdiv(outs, d.swiglu ? 64 : 128);   // at most
+  const int64_t rows = a.share > 0 ? int64_t{a.share} * d.E : d.R;              // at most
+  const int64_t tiles = (rows / kBM + d.E) * cdiv(outs, d.swiglu ? 64 : 128);   // at most
   const uint32_t blocks = static_cast<uint32_t>(cdiv(tiles, 8) * 8);
   if (d.swiglu && d.out) mx_mid<kBits, kBM, kStages, true, true, kPolicy><<<blocks, kThreads, 0, st>>>(a);
   else if (d.swiglu) mx_mid<kBits, kBM, kStages, true, false, kPolicy><<<blocks, kThreads, 0, st>>>(a);
@@ -921,23 +941,31 @@ tr_expert_kernel expert_kernel(const tr_expert_desc& d, bool gather) {
     const int64_t m = d.R / rows + (experts + 1) / 2;
     return m > experts ? m : experts;
   };
-  if (d.R >= 56 * experts && m_tiles(256) * cdiv(outs, d.swiglu ? 128 : 256) * 2 >= cus) return TR_EXPERT_TILE256;
+  if (d.R >= kShare * experts && m_tiles(256) * cdiv(outs, d.swiglu ? 128 : 256) * 2 >= cus) return TR_EXPERT_TILE256;
   if (d.R <= 20 * experts || m_tiles(64) * cdiv(outs, d.swiglu ? 64 : 128) * 4 <= cus * 3) return TR_EXPERT_TILE32;
   return TR_EXPERT_TILE64;
 }
 
 hipError_t expert_tiles(const tr_expert_desc& d, tr_expert_kernel kernel, const void* x, const void* xs,
                         const void* w, const void* ws, const int* offsets, const int* rows, void* y, void* ys,
-                        hipStream_t st) {
-  const MxArgs a{static_cast<const uint8_t*>(x), static_cast<const uint8_t*>(xs),
-                 static_cast<const uint8_t*>(w), static_cast<const uint8_t*>(ws), offsets, rows, y,
-                 static_cast<uint8_t*>(ys), d.T, static_cast<int>(d.R), static_cast<int>(d.K),
-                 static_cast<int>(d.N), d.E};
+                        bool bound, hipStream_t st) {
+  MxArgs a{static_cast<const uint8_t*>(x), static_cast<const uint8_t*>(xs),
+           static_cast<const uint8_t*>(w), static_cast<const uint8_t*>(ws), offsets, rows, y,
+           static_cast<uint8_t*>(ys), d.T, static_cast<int>(d.R), static_cast<int>(d.K),
+           static_cast<int>(d.N), d.E, 0};
   // (stages: as many as leave room for two blocks on a CU; six and one block: one token's
   // experts 50 -> 52 us, 64 tokens' in 4 bits 90 -> 103)
   if (kernel == TR_EXPERT_TILE32) launch_mid<32, 3, 3>(d, a, st);
   else if (kernel == TR_EXPERT_TILE64) launch_mid<64, 3, 2>(d, a, st);
-  else launch(d, a, st);
+  else if (!bound) launch(d, a, st);
+  else {
+    // With the rows that the segments do hold, the kernels themselves say which of the two
+    // takes the call. R 8192, 32 experts, 7168 x 4096, 8 and 4 bits, 1365 rows there: 198, 138
+    // -> 168, 106 us; the launch that does nothing costs 4 to 7.
+    a.share = kShare;
+    launch_mid<64, 3, 2>(d, a, st);
+    launch(d, a, st);
+  }
   return hipGetLastError();
 }
 

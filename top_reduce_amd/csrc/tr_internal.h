@@ -130,9 +130,11 @@ tr_expert_kernel expert_kernel(const tr_expert_desc& d, bool gather);
 // TR_EXPERT_ROWS, and the others.
 hipError_t expert_few(const tr_expert_desc& d, const void* x, const void* xs, const void* w, const void* ws,
                       const int* offsets, const int* rows, void* y, void* ys, hipStream_t st);
+// bound: the segments may hold far fewer rows than R (those of a plan, which has a slot for
+// every expert that a token names, on this GPU or not).
 hipError_t expert_tiles(const tr_expert_desc& d, tr_expert_kernel kernel, const void* x, const void* xs,
                         const void* w, const void* ws, const int* offsets, const int* rows, void* y, void* ys,
-                        hipStream_t st);
+                        bool bound, hipStream_t st);
 size_t linear4_workspace(const tr_linear4_desc& d);
 hipError_t linear_mx4(const tr_linear4_desc& d, const void* x, const void* w, const void* ws, void* y, void* scratch,
                       hipStream_t st);
