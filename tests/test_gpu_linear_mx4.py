@@ -74,3 +74,29 @@ def test_a_workspace_of_the_callers():
         tr.linear_mx4(x, w, ws=ws[:256])
     # one that is not needed may be there all the same
     assert torch.equal(tr.linear_mx4(x[:3].contiguous(), w, ws=ws), tr.linear_mx4(x[:3].contiguous(), w))
+
+
+@pytest.mark.parametrize("T,K", [(3, 512), (3, 4096), (20, 512), (20, 4096), (9, 64)])
+def test_fp32_rows_of_any_size(T, K):
+    """Numbers near both ends of fp32, infinities and signalling NaN: what fp32 products give."""
+    g = torch.Generator().manual_seed(T + K)
+    w = M.quantize(torch.randint(1, 7, (48, K), generator=g).double() * 0.5, 4)      # no zeros
+    x = torch.randn(T, K, generator=g) * torch.tensor([2.0 ** 60, 2.0 ** -60, 1.0])[torch.arange(T) % 3, None]
+    x[1] = torch.randn(K, generator=g) * 2.0 ** -100
+    y = tr.linear_mx4(x.cuda(), (w[0].cuda(), w[1].cuda()))
+    xv, wv = S.f64(x), M.value(*w)
+    # (products below 2^-126 may be lost)
+    S.check(y, xv @ wv.t(), S.U[F32] * (xv @ wv.t()).abs() + (K + 64) * (S.EPS * (xv.abs() @ wv.abs().t()) + 2.0 ** -126), "y")
+    top = torch.zeros(T, K)
+    top[0, 5] = torch.finfo(F32).max / 8
+    y = tr.linear_mx4(top.cuda(), (w[0].cuda(), w[1].cuda()))
+    want = S.f64(top) @ wv.t()
+    assert ((S.f64(y) - want).abs() <= 2.0 ** -23 * want.abs()).all() and torch.isfinite(y).all()
+    odd = x.clone()
+    odd[0, 7] = float("inf")
+    odd[2, K - 1] = float("-inf")
+    odd.view(torch.int32)[1, 3] = 0x7f800001
+    y = tr.linear_mx4(odd.cuda(), (w[0].cuda(), w[1].cuda()))
+    assert (y[0] == float("inf")).all() and (y[2] == float("-inf")).all() and torch.isnan(y[1]).all()
+    odd[0, 8] = float("-inf")
+    assert torch.isnan(tr.linear_mx4(odd.cuda(), (w[0].cuda(), w[1].cuda()))[0]).all()

@@ -10,7 +10,8 @@
 // matrix instructions: every product is exact and the sums are fp32 (the matrix
 // instructions that take the blocks as they are drop what is 2^-13 below the largest of
 // eight products; here, where the weights' bytes take the time, they would save nothing).
-// With x in fp32 the weights are widened to fp32.
+// A number of x in fp32 is three of bf16 (split_bf16) in stream_products; few_products widens
+// the weights to fp32.
 //
 // A block takes 16 kGroups rows of w; its waves share K and add their sums in LDS in a
 // fixed order. Lane l = 16 g + r of a wave multiplies row r of w by row r of x, of which it
@@ -462,14 +463,15 @@ __global__ __launch_bounds__(kWaves* kWave) void stream_products(FewArgs a) {
 #pragma unroll
         for (int o = 0; o < kPer / 8; ++o) {      // eight numbers of the chunk
           if constexpr (kRows == kRowsF32) {
-            const u32x4 x0 = sx[(8 * c + 2 * o) ^ xf], x1 = sx[(8 * c + 2 * o + 1) ^ xf];
+            const Split x = split_bf16(sx[(8 * c + 2 * o) ^ xf], sx[(8 * c + 2 * o + 1) ^ xf]);
 #pragma unroll
             for (int m = 0; m < kGroups; ++m) {
               const uint32_t d = w[m][o];
-              const floatx2 p = mx_pair_f32<4, 0>(d, wf[m]), q = mx_pair_f32<4, 1>(d, wf[m]);
-              const floatx2 s = mx_pair_f32<4, 2>(d, wf[m]), t = mx_pair_f32<4, 3>(d, wf[m]);
-              acc[m] = mma16<true>(__builtin_bit_cast(u32x4, (floatx4){p[0], p[1], q[0], q[1]}), x0, acc[m]);
-              acc[m] = mma16<true>(__builtin_bit_cast(u32x4, (floatx4){s[0], s[1], t[0], t[1]}), x1, acc[m]);
+              const u32x4 v = {mx_pair_bf16<4, 0>(d, wf[m]), mx_pair_bf16<4, 1>(d, wf[m]),
+                               mx_pair_bf16<4, 2>(d, wf[m]), mx_pair_bf16<4, 3>(d, wf[m])};
+              acc[m] = mma16<false>(v, x.low, acc[m]);
+              acc[m] = mma16<false>(v, x.mid, acc[m]);
+              acc[m] = mma16<false>(v, x.top, acc[m]);
             }
           } else {
             u32x4 x;
@@ -554,7 +556,7 @@ struct Launch {
   // waves by what a stage of each takes of LDS: 4 KiB of w (8 with four groups) and x
   static void any(const FewArgs& a, int E, hipStream_t st) {
     if (a.R > 16) few<4>(a, E, st);
-    else if (a.K < 256 || (kRows == kRowsF32 && a.R > 4)) few<1>(a, E, st);
+    else if (a.K < 256 || (kRows == kRowsF32 && a.R > 4)) few<1>(a, E, st);   // (16 rows of fp32 are too much LDS)
     else if constexpr (kRows == kRowsF32) stream<4, 6, 3>(a, E, st);
     else if constexpr (kRows == kRowsBf16) {
       if (a.R <= 4) stream<4, 8, 3>(a, E, st);

@@ -90,6 +90,37 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// Eight floats as three times eight bf16 that add up to them: their upper 16 bits, the upper 16
+// of what is left, and the rest (24 significant bits are 8, 8 and 8). Beside bf16 weights three
+// matrix instructions count every product in full, at five times the rate of the fp32 ones.
+// What is not finite is the first part alone.
+struct Split {
+  u32x4 top, mid, low;
+};
+__device__ __forceinline__ Split split_bf16(const u32x4& lo, const u32x4& hi) {
+  typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
+  typedef float floatx8 __attribute__((ext_vector_type(8)));
+  u32x8 a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  const floatx8 x = __builtin_bit_cast(floatx8, a);
+  u32x8 b = __builtin_bit_cast(u32x8, x - __builtin_bit_cast(floatx8, a & 0xffff0000u));
+  u32x8 c = __builtin_bit_cast(u32x8, __builtin_bit_cast(floatx8, b) - __builtin_bit_cast(floatx8, b & 0xffff0000u));
+  float odd = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) odd = __builtin_fmaf(x[i], 0.0f, odd);
+  if (__any(odd != odd)) {
+    const u32x8 size = a & 0x7fffffffu;
+    const u32x8 finite = __builtin_bit_cast(u32x8, size < 0x7f800000u), nan = __builtin_bit_cast(u32x8, size > 0x7f800000u);
+    a |= nan & 0x00400000u;
+    b &= finite;
+    c &= finite;
+  }
+  auto upper = [](const u32x8& v) {
+    return u32x4{__builtin_amdgcn_perm(v[1], v[0], 0x07060302u), __builtin_amdgcn_perm(v[3], v[2], 0x07060302u),
+                 __builtin_amdgcn_perm(v[5], v[4], 0x07060302u), __builtin_amdgcn_perm(v[7], v[6], 0x07060302u)};
+  };
+  return {upper(a), upper(b), upper(c)};
+}
+
 // Eight scale bytes of a row, blocks at .. at + 7, as they lie in memory (at least 8
 // blocks: the row's last eight at most), and with 0 for those past the last.
 __device__ __forceinline__ uint2 load_scale8(const uint8_t* p, int at, int blocks) {
