@@ -282,7 +282,7 @@ void launch(const tr_linear4_desc& d, const void* x, const void* w, const void* 
 }  // namespace
 
 size_t linear4_workspace(const tr_linear4_desc& d) {
-  if (by_rows(d)) return 0;
+  if (d.T == 0 || by_rows(d)) return 0;   // (no rows have no tiles to share K among)
   const int parts = parts_of(d);
   return parts > 1 ? static_cast<size_t>(parts) * d.T * d.N * 4 : 0;
 }
