@@ -487,8 +487,8 @@ typedef struct tr_linear4_desc {
     int32_t reserved;      /* 0 */
 } tr_linear4_desc;
 
-/* Bytes of device workspace of moe_linear_mx4, 256 where it needs none (ws may then be
- * NULL). 0 and the last error if desc is invalid. */
+/* Bytes of device workspace of moe_linear_mx4: 256 where it needs none (ws may then be
+ * NULL), else 512 or more. 0 and the last error if desc is invalid. */
 size_t moe_linear_mx4_workspace(const tr_linear4_desc* desc);
 
 /* y[t][n] = sum over k of x[t][k] w[n][k], weights in 4 bits. x: device [T, K] of dtype;

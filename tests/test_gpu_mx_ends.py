@@ -1,0 +1,41 @@
+"""linear_mx4 and expert_linear at the ends of their sizes and numbers."""
+
+import pytest
+import torch
+
+import top_reduce_amd as tr
+from tests import _mx as M
+from tests import _serving as S
+from tests._gpu import say
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def pair(p):
+    return tuple(t.cuda() for t in p)
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 4096, 16), (2, 4096, 8), (16, 4096, 1), (1, 8192, 8), (4, 16384, 1), (1, 4096, 1),
+                                   (1, 16384, 33)])
+def test_the_smallest_shared_sums(T, K, N):
+    """Parts of K whose sums are 256 bytes and less: with a workspace of the call's and of the caller's."""
+    say(f"linear4 T={T} K={K} N={N}")
+    g = torch.Generator().manual_seed(T + N)
+    x = S.inputs(g, T, K, dtype=F32)
+    w = M.quantize(torch.randn(N, K, generator=g, dtype=torch.float64), 4)
+    n = tr.linear_mx4_workspace_size(T, K, N, F32)
+    assert n > 256
+    y = tr.linear_mx4(x.cuda(), pair(w))
+    assert torch.equal(y, tr.linear_mx4(x.cuda(), pair(w), ws=torch.full((n,), 255, dtype=torch.uint8, device="cuda")))
+    xv, wv = S.f64(x), M.value(*w)
+    want = xv @ wv.t()
+    S.check(y, want, S.U[F32] * want.abs() + (K + 64) * S.EPS * (xv.abs() @ wv.abs().t()), "y")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("K,N", [(4096, 16), (7168, 7168), (256, 16384)])
+def test_no_rows(K, N, dtype):
+    w = (torch.zeros(N, K // 2, dtype=torch.uint8, device="cuda"),
+         torch.zeros(N, K // 32, dtype=torch.uint8, device="cuda").view(M.E8M0))
+    assert tr.linear_mx4(torch.empty(0, K, dtype=dtype, device="cuda"), w).shape == (0, N)

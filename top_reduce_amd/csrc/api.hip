@@ -842,8 +842,9 @@ tr_status moe_expert_linear(const tr_expert_desc* desc, const void* x, const voi
 size_t moe_linear_mx4_workspace(const tr_linear4_desc* desc) {
   if (check_linear4_desc(desc) != TR_OK) return 0;
   ok();
+  // kAlign says that none is needed: one that is needed is larger
   const size_t n = tr::linear4_workspace(*desc);
-  return n ? n : kAlign;
+  return !n ? kAlign : n > 2 * kAlign ? n : 2 * kAlign;
 }
 
 tr_status moe_linear_mx4(const tr_linear4_desc* desc, const void* x, const void* wq, const void* wscale, void* y,
