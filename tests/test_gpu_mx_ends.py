@@ -39,3 +39,27 @@ def test_no_rows(K, N, dtype):
     w = (torch.zeros(N, K // 2, dtype=torch.uint8, device="cuda"),
          torch.zeros(N, K // 32, dtype=torch.uint8, device="cuda").view(M.E8M0))
     assert tr.linear_mx4(torch.empty(0, K, dtype=dtype, device="cuda"), w).shape == (0, N)
+
+
+@pytest.mark.parametrize("kernel", ["rows", "tile256", "auto"])
+def test_as_many_rows_as_there_may_be(kernel):
+    """2^31 - 1 gathered rows: segments that begin off a tile and end at the last row, whose strips and
+    counts of tiles pass 2^31 on the way."""
+    T, K, R = 64, 256, (1 << 31) - 1
+    say(f"experts {R} rows {kernel}")
+    g = torch.Generator().manual_seed(5)
+    x = pair(M.quantize(torch.randn(T, K, generator=g, dtype=torch.float64)))
+    w = pair(M.quantize(torch.randn(2, 1, K, generator=g, dtype=torch.float64)))
+    rows = torch.randint(0, T, (R,), dtype=torch.int32, device="cuda")
+    each = torch.arange(T, dtype=torch.int32, device="cuda").repeat(2)
+    table = tr.expert_linear(x, w, torch.tensor([0, T, 2 * T], dtype=torch.int32, device="cuda"), rows=each,
+                             kernel="tile256" if kernel == "auto" else kernel).reshape(2, T)
+    assert len(table.unique()) > T
+    y = torch.full((R, 1), 7.0, dtype=BF, device="cuda")
+    tr.expert_linear(x, w, torch.tensor([5, 70, R], dtype=torch.int32, device="cuda"), rows=rows, y=y, kernel=kernel)
+    assert (y[:5] == 7).all() and torch.equal(y[5:70, 0], table[0][rows[5:70].long()])
+    step = 1 << 27
+    for a in range(70, R, step):
+        assert torch.equal(y[a:a + step, 0], table[1][rows[a:a + step].long()]), a
+    del y, rows
+    torch.cuda.empty_cache()

@@ -185,7 +185,7 @@ __device__ __forceinline__ void finish(const FewArgs& a, const float* part, int 
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = swiglu<false>(v[j], u[j]);
     }
-    const int64_t out = first + row;
+    const int64_t out = static_cast<int64_t>(first) + row;      // (a strip may end past 2^31)
     if constexpr (kMxOut) {
       float top = 0.0f;
 #pragma unroll
@@ -235,7 +235,7 @@ __device__ __forceinline__ void few_strip(const FewArgs& a, int e, int first, in
   const uint8_t* xsc[kNT];
 #pragma unroll
   for (int n = 0; n < kNT; ++n) {
-    int64_t row = min(first + n * 16 + r, end - 1);
+    int64_t row = min(static_cast<int64_t>(first) + n * 16 + r, static_cast<int64_t>(end - 1));
     if (a.rows) row = a.rows[row];
     row = max(int64_t{0}, min(row, a.T - 1));
     xq[n] = a.x + row * a.K * kXBytes + (kBits == 8 ? 16 : 32 * kXBytes) * g;

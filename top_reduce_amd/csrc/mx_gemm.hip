@@ -296,7 +296,7 @@ __device__ __forceinline__ Tile tile_of(const int* pre, const int* cnt, const in
   // an expert's rows, in units of 64, as evenly over its m-tiles as they go
   const int mt = __builtin_amdgcn_readfirstlane(gm - pre[t.e]);
   const int count = __builtin_amdgcn_readfirstlane(cnt[t.e]);
-  const int units = (count + 63) / 64, mts = (units + 3) / 4;
+  const int units = static_cast<int>((static_cast<uint32_t>(count) + 63) / 64), mts = (units + 3) / 4;
   const int per = units / mts, more = units - per * mts;
   const int at = 64 * (mt * per + min(mt, more));
   t.row0 = __builtin_amdgcn_readfirstlane(off[t.e]) + at;
@@ -378,7 +378,7 @@ __global__ __launch_bounds__(kThreads) void mx_tiles(MxArgs a) {
       const int begin = max(0, min(a.offsets[e], a.R)), end = max(begin, min(a.offsets[e + 1], a.R));
       off[e] = begin;
       cnt[e] = end - begin;
-      mine[i] = (end - begin + BM - 1) / BM;
+      mine[i] = static_cast<int>((static_cast<uint32_t>(end - begin) + BM - 1) / BM);   // (unsigned: up to 2^31 - 1 rows)
       rows += end - begin;
       some += end > begin ? 1 : 0;
     }
@@ -503,7 +503,7 @@ __global__ __launch_bounds__(kThreads) void mx_tiles(MxArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int lr = g.a_row + i * 64 + (lane & 31);
-      const int64_t row = t.row0 + lr;
+      const int64_t row = static_cast<int64_t>(t.row0) + lr;
 #pragma unroll
       for (int j = 0; j < (kSwiglu ? 2 : 4); ++j) {
         floatx16 v = f.acc[i][j];
