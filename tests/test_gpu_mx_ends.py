@@ -1,5 +1,7 @@
 """linear_mx4 and expert_linear at the ends of their sizes and numbers."""
 
+import ctypes as C
+
 import pytest
 import torch
 
@@ -7,6 +9,7 @@ import top_reduce_amd as tr
 from tests import _mx as M
 from tests import _serving as S
 from tests._gpu import say
+from top_reduce_amd import _binding as B
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -62,4 +65,25 @@ def test_as_many_rows_as_there_may_be(kernel):
     for a in range(70, R, step):
         assert torch.equal(y[a:a + step, 0], table[1][rows[a:a + step].long()]), a
     del y, rows
+    torch.cuda.empty_cache()
+
+
+def test_a_plan_with_tiles_past_a_launch():
+    """Sizes whose 64-row tiles are more than a launch has blocks for, 254 GB in earnest: here the plan
+    holds no rows, so that neither weights nor rows of h are read or written."""
+    T, K, E, H, I = 14336, 2, 1024, 256, 563200
+    say(f"forward T={T} E={E} H={H} I={I}")
+    lib = tr.load_library()
+    p = tr.plan(torch.full((T, K), -1, dtype=torch.int64, device="cuda"), E=E, H=H, I=I, flags=tr.FLAG_NO_XE)
+    assert int(p.views()["offsets"].max()) == 0
+    x = torch.zeros(T, H, dtype=torch.uint8, device="cuda")
+    y = torch.full((T, H), 7.0, dtype=BF, device="cuda")
+    a = x.data_ptr()
+    for bits in (4, 8):
+        status = lib.moe_forward_mx(C.byref(p.struct), a, a, None, bits, a, a, a, a, y.data_ptr(), B._raw_stream(y.device))
+        assert status == 0, lib.moe_last_error()
+        torch.cuda.synchronize()
+        assert (y == 0).all()
+        y.fill_(7)
+    del p
     torch.cuda.empty_cache()

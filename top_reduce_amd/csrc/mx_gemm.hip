@@ -868,11 +868,16 @@ __global__ __launch_bounds__(kThreads) void mx_mid(MxArgs a) {
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
+// Tiles of kBM rows of `rows` rows, at most.
+int64_t mid_tiles(const tr_expert_desc& d, int64_t rows, int bm) {
+  return (rows / bm + d.E) * cdiv(d.swiglu ? d.N / 2 : d.N, d.swiglu ? 64 : 128);
+}
+// (a block each: a launch has fewer than 2^32 threads)
+constexpr int64_t kMostTiles = (int64_t{1} << 24) - 8;
+
 template <int kBits, int kBM, int kStages, int kPolicy>
 void launch_mid(const tr_expert_desc& d, const MxArgs& a, hipStream_t st) {
-  const int64_t outs = d.swiglu ? d.N / 2 : d.N;
-  const int64_t rows = a.share > 0 ? int64_t{a.share} * d.E : d.R;              // at most
-  const int64_t tiles = (rows / kBM + d.E) * cdiv(outs, d.swiglu ? 64 : 128);   // at most
+  const int64_t tiles = mid_tiles(d, a.share > 0 ? int64_t{a.share} * d.E : d.R, kBM);
   const uint32_t blocks = static_cast<uint32_t>(cdiv(tiles, 8) * 8);
   if (d.swiglu && d.out) mx_mid<kBits, kBM, kStages, true, true, kPolicy><<<blocks, kThreads, 0, st>>>(a);
   else if (d.swiglu) mx_mid<kBits, kBM, kStages, true, false, kPolicy><<<blocks, kThreads, 0, st>>>(a);
@@ -928,11 +933,10 @@ void launch(const tr_expert_desc& d, const MxArgs& a, hipStream_t st) {
 //    / 29).
 tr_expert_kernel expert_kernel(const tr_expert_desc& d, bool gather) {
   const int64_t outs = d.swiglu ? d.N / 2 : d.N;
-  // (gathered rows are addressed with 31 bits, tiles are numbered with 31; a block each, a
-  // launch has fewer than 2^32 threads)
+  // (gathered rows are addressed with 31 bits, tiles are numbered with 31)
   const int64_t most = (cdiv(d.R, 32) + d.E) * cdiv(outs, d.swiglu ? 64 : 128);
   const bool tiles = d.K >= 256 && (!gather || d.T * d.K < (int64_t{1} << 31)) && most < (int64_t{1} << 30);
-  const bool blocks = most < (int64_t{1} << 24) - 8;
+  const bool blocks = most < kMostTiles;
   if (d.kernel == TR_EXPERT_ROWS || (d.kernel == TR_EXPERT_AUTO && !tiles)) return TR_EXPERT_ROWS;
   if (!tiles) return TR_EXPERT_AUTO;
   if (d.kernel == TR_EXPERT_TILE256 || (d.kernel == TR_EXPERT_AUTO && !blocks)) return TR_EXPERT_TILE256;
@@ -960,7 +964,7 @@ hipError_t expert_tiles(const tr_expert_desc& d, tr_expert_kernel kernel, const 
   // experts 50 -> 52 us, 64 tokens' in 4 bits 90 -> 103)
   if (kernel == TR_EXPERT_TILE32) launch_mid<32, 3, 3>(d, a, st);
   else if (kernel == TR_EXPERT_TILE64) launch_mid<64, 3, 2>(d, a, st);
-  else if (!bound) launch(d, a, st);
+  else if (!bound || mid_tiles(d, int64_t{kShare} * d.E, 64) >= kMostTiles) launch(d, a, st);
   else {
     // With the rows that the segments do hold, the kernels themselves say which of the two
     // takes the call. R 8192, 32 experts, 7168 x 4096, 8 and 4 bits, 1365 rows there: 198, 138
