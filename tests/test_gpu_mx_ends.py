@@ -1,11 +1,12 @@
 """linear_mx4 and expert_linear at the ends of their sizes and numbers."""
 
-import ctypes as C
+import ctypes
 
 import pytest
 import torch
 
 import top_reduce_amd as tr
+from tests import _close as C
 from tests import _mx as M
 from tests import _serving as S
 from tests._gpu import say
@@ -80,10 +81,45 @@ def test_a_plan_with_tiles_past_a_launch():
     y = torch.full((T, H), 7.0, dtype=BF, device="cuda")
     a = x.data_ptr()
     for bits in (4, 8):
-        status = lib.moe_forward_mx(C.byref(p.struct), a, a, None, bits, a, a, a, a, y.data_ptr(), B._raw_stream(y.device))
+        status = lib.moe_forward_mx(ctypes.byref(p.struct), a, a, None, bits, a, a, a, a, y.data_ptr(), B._raw_stream(y.device))
         assert status == 0, lib.moe_last_error()
         torch.cuda.synchronize()
         assert (y == 0).all()
         y.fill_(7)
     del p
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T,K", [(3, 64), (3, 512), (1, 4096), (4, 4096), (20, 512), (20, 4096), (16, 256), (40, 1056)])
+@pytest.mark.parametrize("low", [100, 112, 120, 126, 134, 140])
+def test_small_numbers_count_in_full(T, K, low):
+    """Rows in fp32 down to the smallest, beside weights that bring the products back: fp32's own 24
+    bits (fewer below 2^-126, exact there), whatever the kernel. Rows of large ones among them."""
+    say(f"linear4 T={T} K={K} x near 2^-{low}")
+    g = torch.Generator().manual_seed(T + K + low)
+    q, s = M.quantize(torch.randn(48, K, generator=g, dtype=torch.float64), 4)
+    s = (s.view(torch.uint8) + 100).view(M.E8M0)
+    x = torch.ldexp(torch.randn(T, K, generator=g, dtype=torch.float64),
+                    torch.randint(-low - 4, -low + 1, (T, K), generator=g).double()).float()
+    x[T // 2, ::3] = 0.0
+    if T > 1:
+        x[0] *= 2.0 ** 90
+    y = tr.linear_mx4(x.cuda(), pair((q, s)))
+    xv, wv = S.f64(x), M.value(q, s)
+    want = xv @ wv.t()
+    S.check(y, want, S.U[F32] * want.abs() + (K + 64) * S.EPS * (xv.abs() @ wv.abs().t()), "y")
+    C.check(y, want, K, F32, "y")
+    # and of single numbers: no sum to hide in, each product rounded once
+    one = torch.zeros(T, K)
+    at = torch.arange(T) * 7 % K
+    one[torch.arange(T), at] = x[torch.arange(T), at]
+    want = S.f64(one) @ wv.t()
+    y = S.f64(tr.linear_mx4(one.cuda(), pair((q, s))))
+    assert ((y - want).abs() <= 2.0 ** -23 * want.abs()).all() and ((want != 0).any() or T == 1)
+    # what is not finite among them stays in its row
+    bad = x.clone()
+    bad[T - 1, 5], bad[T // 2, 6] = float("inf"), float("nan")
+    z = tr.linear_mx4(bad.cuda(), pair((q, s))).cpu()
+    hit = torch.zeros(T, dtype=torch.bool)
+    hit[T - 1] = hit[T // 2] = True
+    assert not z[hit].isfinite().any() and torch.equal(z[~hit], tr.linear_mx4(x.cuda(), pair((q, s))).cpu()[~hit])

@@ -447,6 +447,7 @@ __global__ __launch_bounds__(kWaves* kWave) void stream_products(FewArgs a) {
       const u32x4* sx = st + kWUnits + rx * kXPer;
       const int xf = swizzle(rx);
       const int b0 = kt * (kUnit / kMxBlock) - p0 / kMxBlock;     // its first block in the phase
+      uint32_t below = 0;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int c = 4 * u + g;       // this lane's chunk of w: its block's scale is
@@ -466,13 +467,12 @@ __global__ __launch_bounds__(kWaves* kWave) void stream_products(FewArgs a) {
             const Split x = split_bf16(sx[(8 * c + 2 * o) ^ xf], sx[(8 * c + 2 * o + 1) ^ xf]);
 #pragma unroll
             for (int m = 0; m < kGroups; ++m) {
-              const uint32_t d = w[m][o];
-              const u32x4 v = {mx_pair_bf16<4, 0>(d, wf[m]), mx_pair_bf16<4, 1>(d, wf[m]),
-                               mx_pair_bf16<4, 2>(d, wf[m]), mx_pair_bf16<4, 3>(d, wf[m])};
+              const u32x4 v = widen4(w[m][o], wf[m]);
               acc[m] = mma16<false>(v, x.low, acc[m]);
               acc[m] = mma16<false>(v, x.mid, acc[m]);
               acc[m] = mma16<false>(v, x.top, acc[m]);
             }
+            below |= x.below;
           } else {
             u32x4 x;
             if constexpr (kRows == kRowsBf16) {
@@ -487,15 +487,30 @@ __global__ __launch_bounds__(kWaves* kWave) void stream_products(FewArgs a) {
             for (int m = 0; m < kGroups; ++m) {
               u32x4 v;
               if constexpr (kBits == 4) {
-                const uint32_t d = w[m][o];
-                v = u32x4{mx_pair_bf16<4, 0>(d, wf[m]), mx_pair_bf16<4, 1>(d, wf[m]), mx_pair_bf16<4, 2>(d, wf[m]),
-                          mx_pair_bf16<4, 3>(d, wf[m])};
+                v = widen4(w[m][o], wf[m]);
               } else {
                 const uint32_t d = w[m][2 * o], f = w[m][2 * o + 1];
                 v = u32x4{mx_pair_bf16<8, 0>(d, wf[m]), mx_pair_bf16<8, 1>(d, wf[m]), mx_pair_bf16<8, 0>(f, wf[m]),
                           mx_pair_bf16<8, 1>(f, wf[m])};
               }
               acc[m] = mma16<false>(v, x, acc[m]);
+            }
+          }
+        }
+      }
+      if constexpr (kRows == kRowsF32) {
+        if (any_below(below)) {
+          // what the three parts could not hold (numbers below 2^-110)
+#pragma clang loop unroll(disable)
+          for (int i = 0; i < 8; ++i) {
+            const int c = (i & 4) + g, o = i & 3;
+            const Split x = split_rest(sx[(8 * c + 2 * o) ^ xf], sx[(8 * c + 2 * o + 1) ^ xf]);
+#pragma unroll
+            for (int m = 0; m < kGroups; ++m) {
+              const uint32_t d = reinterpret_cast<const uint32_t*>(st + (m * 16 + r) * 8 + (c ^ swz))[o];
+              const u32x4 v = widen4(d, scale_down(mx_scale(scale[(m * 16 + r) * kScalePitch + b0 + c])));
+              acc[m] = mma16<false>(v, x.mid, acc[m]);
+              acc[m] = mma16<false>(v, x.top, acc[m]);
             }
           }
         }

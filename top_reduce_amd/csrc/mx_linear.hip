@@ -36,6 +36,12 @@ struct LinearArgs {
   int K, N;
 };
 
+#if defined(__HIP_DEVICE_COMPILE__)
+__device__ __forceinline__ floatx16 mma32(const u32x4& w, const u32x4& x, const floatx16& acc) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x), acc, 0, 0, 0);
+}
+#endif
+
 // Four waves for 32 rows of x.
 template <bool kF32, int kBM>
 __global__ __launch_bounds__(8 * kBM) void linear_tiles(LinearArgs a) {
@@ -105,9 +111,10 @@ __global__ __launch_bounds__(8 * kBM) void linear_tiles(LinearArgs a) {
 #pragma unroll
     for (int c = 0; c < 16; ++c) acc[j][c] = 0.0f;
   const int xr = (kF32 ? 0 : wave >> 2) * 32 + l31;     // this lane's row of x
-  auto multiply = [&](const u32x4* sx, const u32x4* sw, const uint2* s) {
+  auto multiply = [&](const u32x4* sx, const u32x4* sw, const uint2* s) __attribute__((always_inline)) {
     const int swz = (l31 & 7) ^ ((l31 >> 3) & 1);
     const u32x4* x = sx + xr * kChunks;
+    uint32_t below = 0;
 #pragma unroll
     for (int i = 0; i < (kF32 ? 1 : 4); ++i) {
       const int q = kF32 ? wave : i;
@@ -128,14 +135,32 @@ __global__ __launch_bounds__(8 * kBM) void linear_tiles(LinearArgs a) {
         else p.top = x[c ^ (l31 & 15)];
 #pragma unroll
         for (int j = 0; j < kJ; ++j) {
-          const u32x4 v = {mx_pair_bf16<4, 0>(w[j][o], f[j]), mx_pair_bf16<4, 1>(w[j][o], f[j]),
-                           mx_pair_bf16<4, 2>(w[j][o], f[j]), mx_pair_bf16<4, 3>(w[j][o], f[j])};
-          auto mma = [&](const u32x4& part) {
-            acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v),
-                                                             __builtin_bit_cast(bf16x8, part), acc[j], 0, 0, 0);
-          };
-          if constexpr (kF32) mma(p.low), mma(p.mid);
-          mma(p.top);
+          const u32x4 v = widen4(w[j][o], f[j]);
+          if constexpr (kF32) {
+            acc[j] = mma32(v, p.low, acc[j]);
+            acc[j] = mma32(v, p.mid, acc[j]);
+          }
+          acc[j] = mma32(v, p.top, acc[j]);
+        }
+        if constexpr (kF32) below |= p.below;
+      }
+    }
+    if constexpr (kF32) {
+      if (any_below(below)) {
+        // what the three parts could not hold (numbers below 2^-110)
+        const int b = 2 * wave + h;     // this lane's block
+#pragma clang loop unroll(disable)
+        for (int o = 0; o < 4; ++o) {
+          const int c = 4 * b + o;
+          const Split r = split_rest(x[(2 * c) ^ (l31 & 15)], x[(2 * c + 1) ^ (l31 & 15)]);
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) {
+            const int wr = j * 32 + l31;
+            const uint32_t d = reinterpret_cast<const uint32_t*>(sw + wr * 8 + (b ^ swz))[o];
+            const u32x4 v = widen4(d, scale_down(mx_scale(reinterpret_cast<const uint8_t*>(s + wr)[b])));
+            acc[j] = mma32(v, r.mid, acc[j]);
+            acc[j] = mma32(v, r.top, acc[j]);
+          }
         }
       }
     }

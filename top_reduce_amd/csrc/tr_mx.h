@@ -58,6 +58,11 @@ __device__ __forceinline__ uint32_t mx_pair_bf16(uint32_t v, float scale) {
   else
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, scale, kI != 0));
 }
+// Eight elements of 4 bits.
+__device__ __forceinline__ u32x4 widen4(uint32_t v, float scale) {
+  return u32x4{mx_pair_bf16<4, 0>(v, scale), mx_pair_bf16<4, 1>(v, scale), mx_pair_bf16<4, 2>(v, scale),
+               mx_pair_bf16<4, 3>(v, scale)};
+}
 template <int kBits, int kI>
 __device__ __forceinline__ floatx2 mx_pair_f32(uint32_t v, float scale) {
   if constexpr (kBits == 4)
@@ -93,32 +98,58 @@ __device__ __forceinline__ void lds_barrier() {
 // Eight floats as three times eight bf16 that add up to them: their upper 16 bits, the upper 16
 // of what is left, and the rest (24 significant bits are 8, 8 and 8). Beside bf16 weights three
 // matrix instructions count every product in full, at five times the rate of the fp32 ones.
-// What is not finite is the first part alone.
+// What is not finite is the first part alone. A number below 2^-110 may have bits below the
+// smallest bf16, 2^-133, which its third part cannot hold: they are in the lower halves of the
+// remainders' words (`below`), which are 0 otherwise; split_rest makes numbers of them.
 struct Split {
   u32x4 top, mid, low;
+  uint32_t below;
 };
+// Whether a number of the wave's has bits left, by what its lanes have of `below`.
+__device__ __forceinline__ bool any_below(uint32_t below) { return __any((below & 0xffffu) != 0) != 0; }
+typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
+typedef float floatx8 __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ u32x4 upper_halves(const u32x8& v) {
+  return u32x4{__builtin_amdgcn_perm(v[1], v[0], 0x07060302u), __builtin_amdgcn_perm(v[3], v[2], 0x07060302u),
+               __builtin_amdgcn_perm(v[5], v[4], 0x07060302u), __builtin_amdgcn_perm(v[7], v[6], 0x07060302u)};
+}
 __device__ __forceinline__ Split split_bf16(const u32x4& lo, const u32x4& hi) {
-  typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
-  typedef float floatx8 __attribute__((ext_vector_type(8)));
   u32x8 a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   const floatx8 x = __builtin_bit_cast(floatx8, a);
   u32x8 b = __builtin_bit_cast(u32x8, x - __builtin_bit_cast(floatx8, a & 0xffff0000u));
   u32x8 c = __builtin_bit_cast(u32x8, __builtin_bit_cast(floatx8, b) - __builtin_bit_cast(floatx8, b & 0xffff0000u));
-  float odd = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) odd = __builtin_fmaf(x[i], 0.0f, odd);
-  if (__any(odd != odd)) {
+  auto all = [](const u32x8& v) { return (v[0] | v[1] | v[2]) | (v[3] | v[4] | v[5]) | (v[6] | v[7]); };
+  uint32_t below = all(c);
+  // What is not finite has NaN as its remainder. (Of finite numbers of 2^16 and more, too, the
+  // remainders' exponents may come to all ones together: nothing changes for them.)
+  if (__any((below & 0x7f800000u) == 0x7f800000u)) {
     const u32x8 size = a & 0x7fffffffu;
     const u32x8 finite = __builtin_bit_cast(u32x8, size < 0x7f800000u), nan = __builtin_bit_cast(u32x8, size > 0x7f800000u);
     a |= nan & 0x00400000u;
     b &= finite;
     c &= finite;
+    below = all(c);
   }
-  auto upper = [](const u32x8& v) {
-    return u32x4{__builtin_amdgcn_perm(v[1], v[0], 0x07060302u), __builtin_amdgcn_perm(v[3], v[2], 0x07060302u),
-                 __builtin_amdgcn_perm(v[5], v[4], 0x07060302u), __builtin_amdgcn_perm(v[7], v[6], 0x07060302u)};
-  };
-  return {upper(a), upper(b), upper(c)};
+  return {upper_halves(a), upper_halves(b), upper_halves(c), below};
+}
+
+// What split_bf16 leaves of the same eight floats, 16 bits at most each, times 2^64: `top` and
+// `mid` (low is 0). Their weights are scaled by scale_down's 2^-64; where a scale is too small for
+// that, the products are below 2^-190.
+__device__ __forceinline__ Split split_rest(const u32x4& lo, const u32x4& hi) {
+  const u32x8 a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  const u32x8 b = __builtin_bit_cast(u32x8, __builtin_bit_cast(floatx8, a) - __builtin_bit_cast(floatx8, a & 0xffff0000u));
+  const u32x8 c = __builtin_bit_cast(u32x8, __builtin_bit_cast(floatx8, b) - __builtin_bit_cast(floatx8, b & 0xffff0000u));
+  const u32x8 finite = __builtin_bit_cast(u32x8, (a & 0x7fffffffu) < 0x7f800000u);
+  const floatx8 d = __builtin_bit_cast(floatx8, c & 0x8000ffffu & finite) * 0x1p64f;
+  const u32x8 e = __builtin_bit_cast(u32x8, d);
+  const floatx8 f = d - __builtin_bit_cast(floatx8, e & 0xffff0000u);
+  return {upper_halves(e), upper_halves(__builtin_bit_cast(u32x8, f)), u32x4{0, 0, 0, 0}, 0};
+}
+// A block's scale (mx_scale) times 2^-64, 2^-127 at least.
+__device__ __forceinline__ float scale_down(float scale) {
+  const int u = static_cast<int>(__float_as_uint(scale));
+  return __uint_as_float(u >= 0x7f800000 ? u : max(u - (64 << 23), 0x00400000));
 }
 
 // Eight scale bytes of a row, blocks at .. at + 7, as they lie in memory (at least 8
