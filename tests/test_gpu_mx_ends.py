@@ -123,3 +123,65 @@ def test_small_numbers_count_in_full(T, K, low):
     hit = torch.zeros(T, dtype=torch.bool)
     hit[T - 1] = hit[T // 2] = True
     assert not z[hit].isfinite().any() and torch.equal(z[~hit], tr.linear_mx4(x.cuda(), pair((q, s))).cpu()[~hit])
+
+
+def ends(bits, E, N, K, scale, code):
+    """[E, N, K] numbers, all of one element and one scale."""
+    q = torch.full((E, N, K * bits // 8), code, dtype=torch.uint8)
+    return (q.view(M.E4M3) if bits == 8 else q), torch.full((E, N, K // 32), scale, dtype=torch.uint8).view(M.E8M0)
+
+
+@pytest.mark.parametrize("bits,code,scale", [(8, 0x7e, 254), (8, 0x7e, 247), (4, 0x77, 254), (8, 0x38, 254), (4, 0x22, 254)])
+@pytest.mark.parametrize("kernel", ["rows", "tile32", "tile64", "tile256"])
+@pytest.mark.parametrize("n", [3, 40])
+def test_weights_past_fp32(bits, code, scale, kernel, n):
+    """Weights of 2^128 and more, which the format has and fp32 has not: the tiles multiply blocks as
+    they are, the kernel of rows takes such a number as infinite."""
+    K = 256
+    w = ends(bits, 1, 32, K, scale, code)
+    x = torch.zeros(n, K, dtype=torch.uint8)
+    x[:, 9] = 0x38                                       # 1, scaled
+    x = (x.view(M.E4M3), torch.full((n, K // 32), 127 - 60, dtype=torch.uint8).view(M.E8M0))
+    off = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    y = S.f64(tr.expert_linear(pair(x), pair(w), off, kernel=kernel))
+    v = M.value(*w)[0, 0, 0]
+    if kernel == "rows" and v >= 2.0 ** 128:
+        assert not y.isfinite().any()
+    else:
+        want = v * 2.0 ** -60
+        assert ((y - want).abs() <= 2.0 ** -8 * want).all()
+
+
+@pytest.mark.parametrize("scale", [0, 1, 3, 8, 20])
+@pytest.mark.parametrize("kernel", ["rows", "tile32", "tile64", "tile256"])
+@pytest.mark.parametrize("n", [3, 40])
+def test_weights_below_bf16(scale, kernel, n):
+    """Weights of 8 bits down to 2^-136: in the kernel of rows those below 2^-133 go by bf16's steps."""
+    K = 256
+    g = torch.Generator().manual_seed(scale)
+    q = torch.randint(1, 0x78, (1, 32, K), generator=g, dtype=torch.uint8).view(M.E4M3)
+    w = (q, torch.full((1, 32, K // 32), scale, dtype=torch.uint8).view(M.E8M0))
+    x = M.quantize(torch.rand(n, K, generator=g, dtype=torch.float64) + 0.5)
+    x = (x[0], (x[1].view(torch.uint8) + 110).view(M.E8M0))
+    off = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    y = S.f64(tr.expert_linear(pair(x), pair(w), off, kernel=kernel))
+    xv, wv = M.value(*x), M.value(*w)[0]
+    want, size = xv @ wv.t(), xv.abs() @ wv.abs().t()
+    step = 2.0 ** -134 * xv.abs().sum(1, keepdim=True) if kernel == "rows" else 0.0      # half of bf16's smallest
+    assert ((y - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -10 * size + step).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,K", [(2, 64), (2, 512), (20, 512), (2, 4096), (20, 4096)])
+def test_projection_weights_past_fp32(T, K, dtype):
+    """Infinite, as in a weight matrix of fp32; the largest below it is not."""
+    x = torch.zeros(T, K, dtype=dtype, device="cuda")
+    x[:, 9] = 2.0 ** -60
+    for code, scale in ((0x77, 254), (0x66, 254), (0x55, 254), (0x77, 252), (0x22, 254)):
+        q, s = ends(4, 1, 16, K, scale, code)
+        v = M.value(q, s)[0, 0, 0]
+        y = S.f64(tr.linear_mx4(x, pair((q[0], s[0]))))
+        if v >= 2.0 ** 128:
+            assert not y.isfinite().any(), (code, scale)
+        else:
+            assert (y == v * 2.0 ** -60).all(), (code, scale)

@@ -7,7 +7,8 @@
 //
 // Bound by reading the weights. An element times its block's scale is a bf16 number, so
 // both operands are widened in registers, two by one conversion, and multiplied by bf16
-// matrix instructions: every product is exact and the sums are fp32 (the matrix
+// matrix instructions: every product is exact and the sums are fp32 (numbers of 2^128 and more
+// are infinite, those of 8 bits below 2^-133 go by bf16's steps; the matrix
 // instructions that take the blocks as they are drop what is 2^-13 below the largest of
 // eight products; here, where the weights' bytes take the time, they would save nothing).
 // A number of x in fp32 is three of bf16 (split_bf16) in stream_products; few_products widens

@@ -50,7 +50,8 @@ __device__ __forceinline__ float mx_scale(uint32_t byte) {
 typedef float floatx2 __attribute__((ext_vector_type(2)));
 
 // Elements 2 i, 2 i + 1 of a dword of e2m1 (i < 4) or e4m3 (i < 2), scaled, as two bf16
-// (exact: at most 4 significant bits) or two floats.
+// (exact: at most 4 significant bits; infinite from 2^128 on, below 2^-133 by bf16's steps) or
+// two floats.
 template <int kBits, int kI>
 __device__ __forceinline__ uint32_t mx_pair_bf16(uint32_t v, float scale) {
   if constexpr (kBits == 4)
