@@ -5,7 +5,9 @@ weights in 4 bits, the residual's addition and the norm, the router, this GPU's 
     y = this GPU's share of the experts' outputs for n
 
 The same calls (linear_mx4, rms_norm, route_topk, plan, forward_mx) take a decode batch,
-captured once into a HIP graph and replayed with the next tokens, and a prompt.
+captured once into a HIP graph and replayed with the next tokens, and a prompt, whose
+projection is a product in 8 bits (quantize_mx, expert_linear with one expert): linear_mx4
+is for few rows.
 
     python examples/serving_block_mx.py                        # decode of 64 and a prompt of 4096
     python examples/serving_block_mx.py --T 1 --prompt 0 --bits 4 --steps 100
@@ -20,6 +22,11 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import top_reduce_amd as tr  # noqa: E402
 from examples.serving_block import timed  # noqa: E402
+
+
+# Rows of x up to which linear_mx4 is the faster one. 256 / 512 / 4096 rows, 7168 x 7168: 33 / 67 /
+# 470 us, against 33 / 41 / 185 with x in 8 bits.
+FEW = 256
 
 
 class Block:
@@ -38,13 +45,19 @@ class Block:
 
         self.H, self.I, self.K, self.E, self.begin = H, I, K, E, begin
         self.w = tr.quantize_mx(normal(H, H, std=H ** -0.5), 4)
+        self.all = torch.tensor([0, 2 ** 31 - 1], dtype=torch.int32, device="cuda")     # one expert's: every row
         self.norm = normal(H, std=0.2) + 1
         self.gate = normal(G, H, std=1.5 * H ** -0.5)
         self.w1, self.w2 = experts(2 * I, H), experts(H, I)
 
+    def project(self, x):
+        if x.shape[0] <= FEW:
+            return tr.linear_mx4(x, self.w)
+        return tr.expert_linear(tr.quantize_mx(x), tuple(t[None] for t in self.w), self.all)
+
     def __call__(self, x, residual):
         """(y, next residual, idx, weights) of rows x [T, H] and their residuals."""
-        n = tr.rms_norm(tr.linear_mx4(x, self.w), self.norm, residual=residual, out="both")
+        n = tr.rms_norm(self.project(x), self.norm, residual=residual, out="both")
         idx, weights = tr.route_topk(n.y, self.gate, self.K)
         p = tr.plan(idx, E=self.E, H=self.H, I=self.I, expert_begin=self.begin, flags=tr.FLAG_NO_XE)
         return tr.forward_mx(p, (n.q, n.s), weights, self.w1, self.w2), n.residual, idx, weights
