@@ -10,14 +10,14 @@
 // stages of LDS, filled without registers by whole lines, two in flight while one is
 // multiplied. A wave has 32 rows of w, which it widens, and 32 rows of x; in fp32 all rows and
 // a quarter of the k-tile, so that x is split once (by four waves: 31 us for 32 rows of 7168 x
-// 7168, so 19.8; with the fp32 matrix instructions, by lanes, 107). Where the
+// 7168, so 18.6; with the fp32 matrix instructions, by lanes, 107). Where the
 // tiles are fewer than the CUs, K is shared among `parts` blocks, whose fp32 sums a second
 // launch adds in order.
 //
 // Bound by what a CU loads: a line of 128 bytes takes it about four cycles, of a k-tile 128
 // of w and 4 kBM of x. So a tile is as wide as LDS allows, and K is shared rather than the
-// rows of w. 64 rows, 7168 x 7168: 14.6 us, of which the sums' launch 2.4 to 4.8, in
-// fp32 30.6; 1 / 64 rows, 7168 x 131072: 100 / 158 (5.0 / 3.2 TB/s).
+// rows of w. 64 rows, 7168 x 7168: 14.6 us, of which the sums' launch 2.4, in
+// fp32 28.7; 1 / 64 rows, 7168 x 131072: 100 / 158 (5.0 / 3.2 TB/s).
 #include "tr_internal.h"
 #include "tr_mx.h"
 
@@ -111,6 +111,7 @@ __global__ __launch_bounds__(8 * kBM) void linear_tiles(LinearArgs a) {
 #pragma unroll
     for (int c = 0; c < 16; ++c) acc[j][c] = 0.0f;
   const int xr = (kF32 ? 0 : wave >> 2) * 32 + l31;     // this lane's row of x
+  // (inlined by force: as a function of its own it has the accumulators in memory, 310 us for 18)
   auto multiply = [&](const u32x4* sx, const u32x4* sw, const uint2* s) __attribute__((always_inline)) {
     const int swz = (l31 & 7) ^ ((l31 >> 3) & 1);
     const u32x4* x = sx + xr * kChunks;
