@@ -505,7 +505,8 @@ tr_status moe_linear_mx4(const tr_linear4_desc* desc, const void* x, const void*
 /* The whole layer of a plan, as moe_forward, with rows and weights in 8 bits (or weights
  * in 4): moe_expert_linear with swiglu over the plan's segments, its result in 8 bits in
  * the plan's h; moe_expert_linear into the plan's O; moe_combine_reduce. Both with the kernel
- * that AUTO takes, or, by the rows that the segments hold, smaller tiles. plan: of dtype
+ * that AUTO takes, or, by the rows that the segments hold, smaller tiles (for another one
+ * call the three parts, over the plan's offsets and row_src). plan: of dtype
  * TR_BF16, H and I multiples of 32. x: device [T, H] in 8 bits, xs its scales; w1: device
  * [E, 2I, H], w2: device [E, H, I], of bits, and their scales; topk_weights, y: as
  * moe_forward (y may not overlap x). */
