@@ -471,12 +471,13 @@ typedef struct tr_expert_desc {
  * (where a sum cancels, that may be more than the rounding of its result). The kernel for few
  * rows (ROWS) counts every product in full, of numbers that bf16 holds: one of 2^128 and
  * more is infinite there, and one of 8 bits below 2^-133 goes by steps of that. A row's
- * result does not hang on the other rows, but for that choice. x: device [T, K] in 8 bits, xs its scales; w: device [E, N, K], ws its
- * scales; offsets: device int32 [E + 1], ascending, those below 0 or past R taken as 0 and
- * R (the plan's offsets); rows: device int32 [R], or NULL for r itself, which needs T >= R
- * (the plan's row_src); entries outside [0, T) are taken as the nearest row; y: device
- * [R, N or N/2]; ys: its scales where out is 1, else NULL. Rows outside every segment are
- * left as they are. y and ys must not overlap x or xs. */
+ * result does not hang on the other rows, but for that choice. x: device [T, K] in 8 bits,
+ * xs its scales; w: device [E, N, K], ws its scales; offsets: device int32 [E + 1],
+ * ascending, those below 0 or past R taken as 0 and R (the plan's offsets); rows: device
+ * int32 [R], or NULL for r itself, which needs T >= R (the plan's row_src); entries
+ * outside [0, T) are taken as the nearest row; y: device [R, N or N/2]; ys: its scales
+ * where out is 1, else NULL. Rows outside every segment are left as they are. y and ys
+ * must not overlap x or xs. */
 tr_status moe_expert_linear(const tr_expert_desc* desc, const void* x, const void* xs, const void* w,
                             const void* ws, const int32_t* offsets, const int32_t* rows, void* y, void* ys,
                             hipStream_t stream);
